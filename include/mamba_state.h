@@ -464,6 +464,88 @@ int mamba1_state_update(const mamba1_layer_desc *desc, void *ssm_pool, int64_t s
                         const float *dt_bias, int32_t dt_softplus, const void *z, void *y,
                         int32_t *err_word, void *stream);
 
+/* ---------------------------------------------------------------------------------------- */
+/* gated delta rule layers                                                                   */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * A gated delta rule layer keeps, like a Mamba2 layer, one (head_dim, d_state) state a head in a
+ * slot of the same pool, and is described by the same mamba_layer_desc: head_dim is the length of
+ * a value, d_state the length of a key and query, and the n_groups groups hold the keys and
+ * queries, each shared by nheads / n_groups heads.  Its conv channels are [v | k | q] where a
+ * Mamba2 layer has [x | B | C].  So mamba_conv_update, mamba_conv_varlen, mamba_spec_commit,
+ * mamba_slot_copy and the int8 store serve it as they are.  Per head h (group g = h / (H / G))
+ * and token:
+ *     a = exp(Delta * A[h]),  Delta = softplus(dt + dt_bias[h])   (dt + dt_bias if !dt_softplus)
+ *     b = sigmoid(beta)                                           (beta itself if !beta_sigmoid)
+ *     k, q divided by sqrt(|.|^2 + 1e-6) if qk_l2norm
+ *     u = b * (v - a * S k),   S <- a * S + u k^T,   y = scale * S q      (S k sums over d_state)
+ * The method's domain is A <= 0, Delta >= 0 and b * |k|^2 <= 2, where the state cannot grow by its
+ * own (qk_l2norm gives |k| <= 1, and the sigmoid b < 1).
+ *
+ * Arguments common to the three calls:
+ *   dt, beta         (batch, ntok, nheads) or (total_tokens, nheads), both dt_dtype.
+ *   A                (nheads) fp32, required.   dt_bias: (nheads) fp32 or NULL.
+ *   scale            factor of the output (d_state^-1/2 in the method).
+ * Compiled shapes: those of mamba_decode_supported; state, activations and dt each f32 or bf16.
+ * Alignment: the pool, the workspace, xbc, v, k and q (and the y of gdn_chunk_scan) 16 bytes, the
+ * slot stride in bytes a multiple of 16, the y of a step its element size.
+ */
+
+/*
+ * gdn_state_update -- the recurrent step of ntok tokens a request, in order, in place on the pool.
+ * Slot ids, scratch_slots, batch, ntok, xbc and y as in mamba_state_update, with xbc already
+ * convolved (mamba_conv_update); a row one of whose slot ids is out of range is left untouched.
+ * Limits: 1 <= ntok <= 8, batch <= 65535.
+ */
+int gdn_state_update(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,
+                     int64_t num_slots, const int32_t *slot_ids, const int32_t *scratch_slots,
+                     int32_t batch, int32_t ntok, const void *xbc, const void *dt, const void *beta,
+                     const float *A, const float *dt_bias, int32_t dt_softplus, int32_t beta_sigmoid,
+                     int32_t qk_l2norm, float scale, void *y, int32_t *err_word, void *stream);
+
+/*
+ * gdn_state_update_int8 -- the recurrent step of one token a request on a cache held in 8 bits: row
+ * i's state is entry entries[i] of `store`, in the layout of mamba_ckpt_store_int8 (which makes
+ * an entry of a slot, as mamba_ckpt_load_int8 makes a slot of an entry).  The state is read as
+ * code * scale, updated in fp32, y taken from it, and then written as fresh codes and scales: the
+ * same symmetric grid per (head, d_state channel).  The entry's conv window is not touched; to
+ * convolve on it, give mamba_conv_update the address of the first entry's window as conv_pool and
+ * the entry's size as slot stride.
+ *   entries (batch) int32, -1 = padding; out of range: MAMBA_ERR_SLOT_RANGE, row left untouched.
+ *   Entries must be distinct.  xbc (batch, conv_dim), y (batch, nheads*head_dim).
+ * Every step rounds the state to half a grid step (max over head_dim / 254) at most; where the
+ * decay alone acts it only scales, so codes do not drift under it.
+ * Limits: batch <= 65535.
+ */
+int gdn_state_update_int8(const mamba_layer_desc *desc, void *store, int64_t num_entries,
+                          const int32_t *entries, int32_t batch, const void *xbc, const void *dt,
+                          const void *beta, const float *A, const float *dt_bias,
+                          int32_t dt_softplus, int32_t beta_sigmoid, int32_t qk_l2norm, float scale,
+                          void *y, int32_t *err_word, void *stream);
+
+/* Bytes of device workspace gdn_chunk_scan needs for these sizes (0 on a bad argument). */
+size_t gdn_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total_tokens, int32_t nseq);
+
+/*
+ * gdn_chunk_scan -- the gated delta rule over a varlen prefill batch.  Sequences, slot ids, initial
+ * states, final states and checkpoints as in mamba_chunk_scan; ckpt_interval is a positive
+ * multiple of 64 when ckpt_slots is given.
+ *   v                (total_tokens, nheads, head_dim) act_dtype.
+ *   k, q             (total_tokens, n_groups, d_state) act_dtype.
+ *   y                (total_tokens, nheads, head_dim) act_dtype.
+ *   workspace        at least gdn_chunk_scan_workspace_bytes(...) bytes (MAMBA_ENOSPACE otherwise).
+ * Limits: nseq <= 65535.
+ */
+int gdn_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,
+                   int64_t num_slots, const int32_t *cu_seqlens, int32_t nseq, int32_t total_tokens,
+                   const int32_t *slot_ids, const uint8_t *has_initial_state,
+                   const int32_t *ckpt_slots, int32_t max_ckpt, int32_t ckpt_interval, const void *v,
+                   const void *k, const void *q, const void *dt, const void *beta, const float *A,
+                   const float *dt_bias, int32_t dt_softplus, int32_t beta_sigmoid,
+                   int32_t qk_l2norm, float scale, void *y, void *workspace, size_t workspace_bytes,
+                   int32_t *err_word, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -63,6 +63,7 @@ def layer_desc(shape: "wl.LayerShape", state: str = wl.BF16, act: str = wl.BF16,
 _lock = threading.Lock()
 _lib = None
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 _dp = ctypes.POINTER(LayerDesc)
 _d1 = ctypes.POINTER(Mamba1Desc)
 
@@ -92,6 +93,13 @@ SIGNATURES = {
     "mamba_chunk_scan_noalloc": (ctypes.c_int, [_dp, _vp, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
                                                 _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]),
     "mamba_chunk_scan_static_scratch_bytes": (_sz, []),
+    "gdn_state_update": (ctypes.c_int, [_dp, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
+                                        _i32, _f32, _vp, _vp, _vp]),
+    "gdn_state_update_int8": (ctypes.c_int, [_dp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32,
+                                             _vp, _vp, _vp]),
+    "gdn_chunk_scan_workspace_bytes": (_sz, [_dp, _i32, _i32]),
+    "gdn_chunk_scan": (ctypes.c_int, [_dp, _vp, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _vp, _vp]),
     "mamba_check_slot_ids": (ctypes.c_int, [_vp, _i32, _vp, _i32, _i64, ctypes.POINTER(_i64)]),
     "mamba_selftest_wait_timeout": (ctypes.c_int, [_vp, _vp, _vp]),
 }
@@ -408,3 +416,89 @@ def mamba_chunk_scan_noalloc(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, x,
                                         _cptr(dt), _cptr(A), _cptr(B), _cptr(C), _cptr(D), _cptr(dt_bias),
                                         int(bool(dt_softplus)), _cptr(z), _cptr(y), _ptr(err_word), _stream(stream))
     _check(rc, "mamba_chunk_scan_noalloc")
+
+
+# ------------------------------------------------------------------------------------------
+# gated delta rule layers
+# ------------------------------------------------------------------------------------------
+
+def _elements(what, **tensors):
+    """Raises ValueError when a tensor has fewer elements than the call reads or writes."""
+    for name, (t, want) in tensors.items():
+        if t is not None and t.numel() < want:
+            raise ValueError(f"{what}: {name} needs {want} elements, got {t.numel()}")
+
+
+def _out_scale(desc, scale):
+    return desc.d_state ** -0.5 if scale is None else float(scale)
+
+
+def gdn_state_update(desc: LayerDesc, ssm_pool, slot_ids, xbc, dt, beta, A, y, *, scratch_slots=None, dt_bias=None,
+                     dt_softplus=True, beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
+    """The gated delta rule's step over (batch, ntok, conv_dim) convolved channels v | k | q, in
+    place on the pool (or into ``scratch_slots``).  ``scale`` defaults to d_state ** -0.5."""
+    st, _, act, dtt, f32, i32, _ = _layer_dtypes(desc)
+    _expect("gdn_state_update", ssm_pool=(ssm_pool, st), slot_ids=(slot_ids, i32), xbc=(xbc, act), dt=(dt, dtt),
+            beta=(beta, dtt), A=(A, f32), y=(y, act), scratch_slots=(scratch_slots, i32), dt_bias=(dt_bias, f32),
+            err_word=(err_word, i32))
+    batch, ntok = int(slot_ids.shape[0]), int(xbc.shape[1])
+    rows, H = batch * ntok, desc.nheads
+    _elements("gdn_state_update", xbc=(xbc, rows * (H * desc.head_dim + 2 * desc.n_groups * desc.d_state)),
+              dt=(dt, rows * H), beta=(beta, rows * H), A=(A, H), y=(y, rows * H * desc.head_dim),
+              scratch_slots=(scratch_slots, rows), dt_bias=(dt_bias, H))
+    rc = lib().gdn_state_update(ctypes.byref(desc), _ptr(ssm_pool), ssm_pool.stride(0), ssm_pool.shape[0],
+                                _cptr(slot_ids), _cptr(scratch_slots), batch, ntok, _cptr(xbc), _cptr(dt), _cptr(beta),
+                                _cptr(A), _cptr(dt_bias), int(bool(dt_softplus)), int(bool(beta_sigmoid)),
+                                int(bool(qk_l2norm)), _out_scale(desc, scale), _cptr(y), _ptr(err_word),
+                                _stream(stream))
+    _check(rc, "gdn_state_update")
+
+
+def gdn_state_update_int8(desc: LayerDesc, store, entries, xbc, dt, beta, A, y, *, dt_bias=None, dt_softplus=True,
+                          beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
+    """The gated delta rule's step of one token on int8 entries (the layout of mamba_ckpt_store_int8),
+    read, updated and requantised in place.  ``scale`` defaults to d_state ** -0.5."""
+    _, _, act, dtt, f32, i32, _ = _layer_dtypes(desc)
+    _expect("gdn_state_update_int8", entries=(entries, i32), xbc=(xbc, act), dt=(dt, dtt), beta=(beta, dtt), A=(A, f32),
+            y=(y, act), dt_bias=(dt_bias, f32), err_word=(err_word, i32))
+    batch, H = int(entries.shape[0]), desc.nheads
+    _elements("gdn_state_update_int8", xbc=(xbc, batch * (H * desc.head_dim + 2 * desc.n_groups * desc.d_state)),
+              dt=(dt, batch * H), beta=(beta, batch * H), A=(A, H), y=(y, batch * H * desc.head_dim),
+              dt_bias=(dt_bias, H))
+    eb = mamba_int8_entry_bytes(desc)
+    rc = lib().gdn_state_update_int8(ctypes.byref(desc), _cptr(store), (store.numel() * store.element_size()) // max(1, eb),
+                                     _cptr(entries), batch, _cptr(xbc), _cptr(dt), _cptr(beta), _cptr(A),
+                                     _cptr(dt_bias), int(bool(dt_softplus)), int(bool(beta_sigmoid)),
+                                     int(bool(qk_l2norm)), _out_scale(desc, scale), _cptr(y), _ptr(err_word),
+                                     _stream(stream))
+    _check(rc, "gdn_state_update_int8")
+
+
+def gdn_chunk_scan_workspace_bytes(desc: LayerDesc, total_tokens: int, nseq: int) -> int:
+    return lib().gdn_chunk_scan_workspace_bytes(ctypes.byref(desc), total_tokens, nseq)
+
+
+def gdn_chunk_scan(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, v, k, q, dt, beta, A, y, workspace, *,
+                   has_initial_state=None, ckpt_slots=None, ckpt_interval=0, dt_bias=None, dt_softplus=True,
+                   beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
+    """The gated delta rule over a varlen prefill batch; final states and checkpoints written into the
+    pool.  ``scale`` defaults to d_state ** -0.5."""
+    st, _, act, dtt, f32, i32, u8 = _layer_dtypes(desc)
+    _expect("gdn_chunk_scan", ssm_pool=(ssm_pool, st), cu_seqlens=(cu_seqlens, i32), slot_ids=(slot_ids, i32), v=(v, act),
+            k=(k, act), q=(q, act), dt=(dt, dtt), beta=(beta, dtt), A=(A, f32), y=(y, act),
+            has_initial_state=(has_initial_state, u8), ckpt_slots=(ckpt_slots, i32), dt_bias=(dt_bias, f32),
+            err_word=(err_word, i32))
+    nseq, total = int(cu_seqlens.shape[0]) - 1, int(v.shape[0])
+    H, GN = desc.nheads, desc.n_groups * desc.d_state
+    _elements("gdn_chunk_scan", v=(v, total * H * desc.head_dim), k=(k, total * GN), q=(q, total * GN),
+              dt=(dt, total * H), beta=(beta, total * H), A=(A, H), y=(y, total * H * desc.head_dim),
+              slot_ids=(slot_ids, nseq), has_initial_state=(has_initial_state, nseq), dt_bias=(dt_bias, H))
+    max_ckpt = int(ckpt_slots.shape[1]) if ckpt_slots is not None else 0
+    rc = lib().gdn_chunk_scan(ctypes.byref(desc), _ptr(ssm_pool), ssm_pool.stride(0), ssm_pool.shape[0],
+                              _cptr(cu_seqlens), nseq, total, _cptr(slot_ids), _cptr(has_initial_state),
+                              _cptr(ckpt_slots), max_ckpt, int(ckpt_interval), _cptr(v), _cptr(k), _cptr(q), _cptr(dt),
+                              _cptr(beta), _cptr(A), _cptr(dt_bias), int(bool(dt_softplus)), int(bool(beta_sigmoid)),
+                              int(bool(qk_l2norm)), _out_scale(desc, scale), _cptr(y), _ptr(workspace),
+                              0 if workspace is None else workspace.numel() * workspace.element_size(),
+                              _ptr(err_word), _stream(stream))
+    _check(rc, "gdn_chunk_scan")

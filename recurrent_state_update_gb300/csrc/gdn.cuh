@@ -1,0 +1,162 @@
+// gdn.cuh -- what the kernels of the gated delta rule share: the layout of a head's state over a
+// warp, the reductions along its rows, the gates, and 8-element loads and stores.
+//
+// The operation, per head h of group g with the state S (head_dim x d_state, d_state contiguous):
+//   a = exp(Delta * A),  Delta = softplus(dt + dt_bias),  b = sigmoid(beta)
+//   u = b * (v - a * S k),   S <- a * S + u k^T,   y = scale * S q
+// with k and q scaled to unit length.  A row of S needs nothing of the other rows, so rows are
+// spread over warps and blocks at will; each row needs two sums over its d_state values, S k and
+// S q of the OLD state, because S q of the new one is a * (S q) + u * (k . q).
+#pragma once
+
+#include "common.cuh"
+
+namespace ms {
+namespace gdn {
+
+constexpr float kNormEps = 1e-6f;  // added to the squared length of k and q before the root
+constexpr int kMaxTok = 8;         // tokens of one decode call
+
+// The gates' and scalings' switches of a call.
+struct Gates {
+    const float *A, *dt_bias;
+    int dt_bf16, dt_softplus, beta_sigmoid, l2norm;
+    float scale;
+};
+
+// log of the decay a of one token and head (<= 0 for A <= 0), from the raw step.
+__device__ __forceinline__ float log_decay(const Gates &g, float dt, int h) {
+    const float s = dt + (g.dt_bias ? g.dt_bias[h] : 0.0f);
+    return (g.dt_softplus ? softplus_f(s) : s) * g.A[h];
+}
+__device__ __forceinline__ float write_gate(const Gates &g, float beta) {
+    return g.beta_sigmoid ? 1.0f / (1.0f + expf(-beta)) : beta;
+}
+// The factor that scales a key or query of squared length ss.
+__device__ __forceinline__ float unit_factor(const Gates &g, float ss) {
+    return g.l2norm ? 1.0f / sqrtf(ss + kNormEps) : 1.0f;
+}
+
+// Eight consecutive values <-> fp32, past L1 (each state byte is used once per call).
+__device__ __forceinline__ void load8_stream(const bf16 *p, float (&f)[8]) {
+    unpack16(__ldcs(reinterpret_cast<const uint4 *>(p)), f);
+}
+__device__ __forceinline__ void load8_stream(const float *p, float (&f)[8]) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p)), b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+}
+__device__ __forceinline__ void store8_stream(bf16 *p, const float (&f)[8]) {
+    __stcs(reinterpret_cast<uint4 *>(p), pack16(f));
+}
+__device__ __forceinline__ void store8_stream(float *p, const float (&f)[8]) {
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                                    __float_as_uint(f[3])));
+    __stcs(reinterpret_cast<uint4 *>(p) + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
+                                                        __float_as_uint(f[6]), __float_as_uint(f[7])));
+}
+// The same through the caches (keys and queries, which every block of a head reads).
+__device__ __forceinline__ void load8(const bf16 *p, float (&f)[8]) {
+    unpack16(*reinterpret_cast<const uint4 *>(p), f);
+}
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// How a warp holds rows of S: LPR lanes a row with 8 consecutive values each, RPW rows side by
+// side, RT rows a lane (row r * RPW + lane / LPR of the warp's RPW * RT).
+template <int N, int RT_>
+struct RowMap {
+    static constexpr int LPR = N / 8, RPW = 32 / LPR, RT = RT_, ROWS = RPW * RT;
+    static constexpr int NV = 2 * RT;        // sums a lane has: S k and S q of each of its rows
+    static constexpr int SHARE = LPR / NV;   // lanes that end up with the same sum
+    static_assert(LPR >= NV, "more sums than lanes of a row");
+};
+
+// Sums val[0..NV) over the M*2 lanes that differ in the lane bits 2M-1 .. 0.  Halves the number of
+// sums with each exchange while there is more than one (NV - 1 exchanges, where a butterfly of each
+// sum would take NV * log2): lane l ends with the sum of index l / (2M / NV).
+template <int NV, int M>
+__device__ __forceinline__ float reduce_rows(float (&val)[NV], int lane) {
+    if constexpr (M == 0) {
+        static_assert(NV == 1, "as many lanes as sums");
+        return val[0];
+    } else if constexpr (NV == 1) {
+        val[0] += __shfl_xor_sync(0xffffffffu, val[0], M);
+        return reduce_rows<1, M / 2>(val, lane);
+    } else {
+        float half[NV / 2];
+        const bool up = lane & M;
+#pragma unroll
+        for (int j = 0; j < NV / 2; ++j) {
+            const float keep = up ? val[NV / 2 + j] : val[j], send = up ? val[j] : val[NV / 2 + j];
+            half[j] = keep + __shfl_xor_sync(0xffffffffu, send, M);
+        }
+        return reduce_rows<NV / 2, M / 2>(half, lane);
+    }
+}
+
+// Sum over the LPR lanes of a row, in every one of them.
+template <int LPR>
+__device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+    for (int m = LPR / 2; m; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
+// One token on the rows a warp holds: S <- a S + u k^T with u = b (v - a S k), and scale * S q.
+// k, q: this lane's 8 values, unscaled; rk, rq: their factors (rq with the output scale); kq: their
+// scaled product k . q without the output scale.  vrow: the value of row (index % RT), where index
+// = this lane's sum.  Returns y of that row in the lanes of index >= RT.
+template <typename Map>
+__device__ __forceinline__ float token_rows(float (&S)[Map::RT][8], const float (&k)[8], const float (&q)[8], float rk,
+                                            float rq, float ukq, float a, float b, float vrow, int lane) {
+    constexpr int RT = Map::RT;
+    float val[Map::NV];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        float p = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p = fmaf(S[r][e], k[e], p);
+            o = fmaf(S[r][e], q[e], o);
+        }
+        val[r] = p;
+        val[RT + r] = o;
+    }
+    const float sum = reduce_rows<Map::NV, Map::LPR / 2>(val, lane);
+    const float u_own = b * (vrow - a * rk * sum);  // meaningful in the lanes that hold S k
+    const int base = lane & ~(Map::LPR - 1), idx = (lane & (Map::LPR - 1)) / Map::SHARE;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const float uk = __shfl_sync(0xffffffffu, u_own, base + r * Map::SHARE) * rk;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) S[r][e] = fmaf(a, S[r][e], uk * k[e]);
+    }
+    const float u = __shfl_sync(0xffffffffu, u_own, base + (idx % RT) * Map::SHARE);
+    return fmaf(a * rq, sum, u * ukq);
+}
+
+// Checks that hold for every call on a layer; the state shapes are those of the decode kernels.
+inline int check_layer(const mamba_layer_desc *d) {
+    const int rc = check_desc(d);
+    if (rc != MAMBA_OK) return rc;
+    return mamba_decode_supported(d);
+}
+inline Gates make_gates(const mamba_layer_desc *d, const float *A, const float *dt_bias, int dt_softplus,
+                        int beta_sigmoid, int qk_l2norm, float scale) {
+    Gates g;
+    g.A = A;
+    g.dt_bias = dt_bias;
+    g.dt_bf16 = d->dt_dtype == MAMBA_BF16;
+    g.dt_softplus = dt_softplus != 0;
+    g.beta_sigmoid = beta_sigmoid != 0;
+    g.l2norm = qk_l2norm != 0;
+    g.scale = scale;
+    return g;
+}
+
+}  // namespace gdn
+}  // namespace ms

@@ -19,6 +19,7 @@
 // rows), each issuing all of its rows' code loads before converting any; 16-byte accesses,
 // every row read or written as one contiguous run.
 #include "common.cuh"
+#include "int8_entry.h"
 #include "umma.cuh"
 
 namespace ms {
@@ -31,24 +32,6 @@ constexpr int kQThreads = 128;
 constexpr int kStoreHeads = 1;           // heads quantised by one store block (more blocks in flight)
 constexpr int kLoadRows = 8;             // rows per thread and pass of the load
 constexpr uint32_t kQPolls = umma::kWaitPolls;  // bound on the wait for a staged tile
-
-inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
-
-struct EntryLayout {
-    size_t q, scales, conv, total;  // section offsets and entry size in bytes
-};
-
-inline EntryLayout entry_layout(const mamba_layer_desc *d) {
-    EntryLayout L;
-    const size_t q = (size_t)d->nheads * d->head_dim * d->d_state;
-    const size_t sc = (size_t)d->nheads * d->d_state * sizeof(float);
-    const size_t cv = (size_t)mamba_conv_dim(d) * (d->conv_kernel - 1 + d->num_spec) * dtype_bytes(d->conv_dtype);
-    L.q = 0;
-    L.scales = align256(q);
-    L.conv = L.scales + align256(sc);
-    L.total = L.conv + align256(cv);
-    return L;
-}
 
 struct CopyArgs {
     unsigned char *ssm;
