@@ -7,7 +7,7 @@
 // bounds the call while there are fewer warps than the SMs hold.  Keys and queries of 16 tokens are
 // scaled once and staged in shared memory in fp32 for all warps of the block, the next 16 tokens'
 // loads being in flight meanwhile.
-#include "gdn_scan.h"
+#include "gdn_scan_tc.h"
 
 namespace ms {
 
@@ -199,7 +199,7 @@ using namespace ms;
 
 extern "C" size_t gdn_chunk_scan_workspace_bytes(const mamba_layer_desc *d, int32_t total_tokens, int32_t nseq) {
     if (check_layer(d) != MAMBA_OK || total_tokens < 0 || nseq < 0) return 0;
-    return scan_meta_bytes(nseq);
+    return scan_meta_bytes(nseq) + (chunked_eligible(d) ? chunked_workspace_bytes(d, total_tokens, nseq) : 0);
 }
 
 extern "C" int gdn_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t ssm_slot_stride, int64_t num_slots,
@@ -237,6 +237,7 @@ extern "C" int gdn_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (launch_pdl(k_gdn_plan, dim3(1), dim3(256), 0, st, p) != cudaSuccess) return MAMBA_ECUDA;
     if (total_tokens == 0) return launch_status();  // only empty sequences
+    if (chunked_eligible(d)) return chunked_launch(p, st);
     const bool sbf = d->state_dtype == MAMBA_BF16, abf = d->act_dtype == MAMBA_BF16;
     if (sbf && abf) return dispatch_tokens<bf16, bf16>(p, P, N, st);
     if (sbf) return dispatch_tokens<bf16, float>(p, P, N, st);

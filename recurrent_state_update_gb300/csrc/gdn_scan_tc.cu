@@ -1,0 +1,757 @@
+// gdn_scan_tc.cu -- the chunked gated delta rule on the tcgen05 tensor cores.
+//
+// For a chunk of 64 tokens and a head with the state S (P x N) before it, with c_i the running sum
+// of the log decays, unit keys and queries k_i, q_i of lengths |k_i|, |q_i| (after any scaling):
+//   (I + L) U = diag(b) R,   L_ij = b_i |k_i||k_j| (k_i . k_j) e^(c_i - c_j), j < i
+//   R = V - diag(e^c |k|) K S^T            the values, less what the decayed state already returns
+//   U = T R,  T = (I + L)^-1 diag(b)       what is written
+//   Y = |q| (diag(e^c) Q S^T + A U),       A_ij = |k_j| (q_i . k_j) e^(c_i - c_j), j <= i
+//   S <- e^(c_64) S + (diag(e^(c_64 - c) |k|) U)^T K
+// T and A need no state, so k_gdn_prep forms them for all chunks of the batch at once; the chain
+// from chunk to chunk, k_gdn_chain, has four products left, all of them transposed so that the
+// value index is the row: its left operands S, R^T, U^T are the accumulators of the product
+// before, rounded to 16 bits, and never leave tensor memory; T, A, K, Q are tiles in shared
+// memory in the form the products read them.
+//
+// Number formats: the products run on fp16 operands (11 bits; bf16's 8 would put four times the
+// output's own rounding into y), sums in fp32, and the state itself stays in fp32 in registers.
+// Keys and queries are of unit length before they are rounded.  Values have bf16's range, so every
+// row of the state (one value index) has a power of two that brings its values and state to a few
+// units, taken anew every 16 chunks and whenever a value outgrows it; the rule cannot grow the state
+// past sqrt(tokens) times the largest value, far inside the 2^12 left.
+#include <mutex>
+
+#include <cuda_fp16.h>
+
+#include "gdn_scan_tc.h"
+#include "umma.cuh"
+
+namespace ms {
+namespace gdn {
+
+using namespace umma;
+
+namespace {
+
+constexpr int C = kChunk, TN = 128, TP = 128;
+constexpr uint32_t kPolls = umma::kWaitPolls;
+constexpr float LOG2E = 1.4426950408889634f;
+
+// Workspace of one chunk.  Per group the tiles of unit keys and queries, 64 rows x 128 fp16 in two
+// 128-byte-swizzled blocks each, interleaved [K 0..63 | Q 0..63 | K 64..127 | Q 64..127] so that keys
+// and queries stacked are one operand of 128 rows; per head T, A (64 x 64, swizzled) and the gates.
+constexpr uint32_t kBlk = 64 * 128;          // one swizzled block of 64 rows
+constexpr uint32_t kKqBytes = 4 * kBlk;
+struct HeadGates {
+    float rk[C];   // e^c |k|
+    float ek[C];   // e^(c_64 - c) |k|
+    float g[C];    // e^c
+    float oq[C];   // |q| * scale
+    float last, pad[3];  // e^(c_64)
+};
+constexpr uint32_t kGateBytes = sizeof(HeadGates);
+constexpr uint32_t kHeadBytes = 2 * kBlk + kGateBytes;
+static_assert(kGateBytes % 16 == 0, "bulk copy size");
+
+struct WsLayout {
+    unsigned char *base;
+    int H, G;
+    __host__ __device__ int64_t chunk_bytes() const { return (int64_t)G * kKqBytes + (int64_t)H * kHeadBytes; }
+    __device__ unsigned char *kq(int chunk, int g) const { return base + chunk * chunk_bytes() + (int64_t)g * kKqBytes; }
+    __device__ unsigned char *head(int chunk, int h) const {
+        return base + chunk * chunk_bytes() + (int64_t)G * kKqBytes + (int64_t)h * kHeadBytes;
+    }
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+    return idesc_bf16(M, N, false, b_mn_major) & ~((7u << 7) | (7u << 10));  // A and B format: fp16
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The swizzled tiles want 1024-byte boundaries; the launches ask for that much more.
+template <typename T>
+__device__ __forceinline__ T *align1024(unsigned char *p) {
+    return reinterpret_cast<T *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
+// ---------------------------------------------------------------------------------------
+// what needs no state: unit keys and queries, T, A and the gates of every chunk
+// ---------------------------------------------------------------------------------------
+
+constexpr int kPrepThreads = 256;
+constexpr int LP = C + 4;  // row pitch of the fp32 matrices: rows 16 bytes apart modulo a bank row
+
+struct PrepSmem {
+    union {
+        unsigned char kq[kKqBytes];  // until its product and its copy to the workspace are done
+        struct {
+            float L[C][LP];       // L, and then its lower left quarter times T's upper left one
+            float t[2][32][36];   // the diagonal 32 x 32 blocks of (I + L)^-1
+        } m;
+    };
+    unsigned char out[2 * kBlk];  // T | A
+    HeadGates gates;
+    float cum[C], b[C], nk[C], nq[C];
+    uint64_t bar;
+    uint32_t tmem;
+    float half_sum;
+};
+
+// Sequence of a chunk: the last one whose first chunk is not past it.
+__device__ __forceinline__ int chunk_sequence(const int32_t *first, int nseq, int chunk) {
+    int lo = 0, hi = nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= chunk) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Block (chunk, group and share of its heads).
+__global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, const WsLayout ws, int heads_per_block) {
+    extern __shared__ __align__(1024) unsigned char prep_smem[];
+    PrepSmem &sm = *align1024<PrepSmem>(prep_smem);
+    pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
+    pdl_launch_dependents();
+    const int chunk = blockIdx.x;
+    if (p.meta[0] == 0 || chunk >= p.meta[1]) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int s = chunk_sequence(meta_chunks(p), p.nseq, chunk);
+    const int at = (chunk - meta_chunks(p)[s]) * C;
+    const int64_t t0 = (int64_t)p.cu[s] + at;
+    const int L = min(C, p.cu[s + 1] - p.cu[s] - at);
+    const int shares = p.HG / heads_per_block;
+    const int g = blockIdx.y / shares, h0 = g * p.HG + (blockIdx.y % shares) * heads_per_block;
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem, 64);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(&sm.bar, 1);
+        fence_mbar_init();
+    }
+    // unit keys (rows 0..63) and queries (64..127): 16 lanes a row, 16 rows a pass
+    {
+        const int r0 = tid >> 4, col = (tid & 15) * 8;
+        uint4 raw[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = (i * 16 + r0) & (C - 1);
+            const bf16 *src = static_cast<const bf16 *>(i < 4 ? p.k : p.q) + ((t0 + row) * p.G + g) * TN + col;
+            raw[i] = row < L ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float f[8];
+            unpack16(raw[i], f);
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+            ss = sum_lanes<16>(ss);
+            const float inv = ss > 0.0f ? 1.0f / sqrtf(ss) : 0.0f;
+            const int row = i * 16 + r0;  // of the stacked tile
+            uint4 u;
+            u.x = pack_f16x2(f[0] * inv, f[1] * inv);
+            u.y = pack_f16x2(f[2] * inv, f[3] * inv);
+            u.z = pack_f16x2(f[4] * inv, f[5] * inv);
+            u.w = pack_f16x2(f[6] * inv, f[7] * inv);
+            *reinterpret_cast<uint4 *>(sm.kq + (col >> 6) * 2 * kBlk + swz128_chunk(row, (col & 63) >> 3)) = u;
+            if (col == 0) {
+                const float len = sqrtf(ss) * unit_factor(p.gates, ss);
+                if (i < 4) sm.nk[row] = len;
+                else sm.nq[row - C] = len * p.gates.scale;
+            }
+        }
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;
+    if (tid == 0) {
+        const uint32_t kq = smem_u32(sm.kq);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // rows 0..63: k_i . k_j, rows 64..127: q_i . k_j
+            mma_bf16(tm, desc_kmajor(kq, 2 * kBlk, kk), desc_kmajor(kq, 2 * kBlk, kk), idesc_f16(128, C, false), kk > 0);
+        mma_commit(&sm.bar);
+        if (blockIdx.y % shares == 0) {
+            bulk_s2g(ws.kq(chunk, g), sm.kq, kKqBytes);
+            bulk_commit();
+            bulk_wait_read<0>();  // the tile's memory is reused below
+        }
+    }
+    int bad = mbar_wait(&sm.bar, 0, kPolls) ? 0 : 1;
+    tc_fence_after();
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            flag_error(p.err, MAMBA_ERR_TIMEOUT);
+            mbar_wait(&sm.bar, 0, kPolls);
+        }
+    } else {
+        const int q = warp & 3, hf = warp >> 2, i = (q & 1) * 32 + lane;  // row i of K K^T (q < 2) or Q K^T
+        float dots[32];
+        tmem_ld32(tm + ((uint32_t)(q * 32) << 16) + hf * 32, dots);
+        for (int h = h0; h < h0 + heads_per_block; ++h) {
+            // running sums of the log decays (base 2) over the chunk's two warps of tokens; no step and
+            // no write past the sequence's end
+            float run = 0.0f, b = 0.0f;
+            if (tid < C) {
+                if (tid < L) {
+                    const int64_t th = (t0 + tid) * p.H + h;
+                    run = log_decay(p.gates, load_scalar(p.dt, th, p.gates.dt_bf16), h) * LOG2E;
+                    b = write_gate(p.gates, load_scalar(p.beta, th, p.gates.dt_bf16));
+                }
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float v = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += v;
+                }
+                if (tid == 31) sm.half_sum = run;
+            }
+            __syncthreads();  // (also: the last head's T and A have been copied out)
+            if (tid < C) {
+                if (warp == 1) run += sm.half_sum;
+                sm.cum[tid] = run;
+                sm.b[tid] = b;
+            }
+            __syncthreads();
+            if (tid < C) {
+                const float last = sm.cum[C - 1], nk = sm.nk[tid], e = exp2f(run);
+                sm.gates.rk[tid] = e * nk;
+                sm.gates.ek[tid] = exp2f(last - run) * nk;
+                sm.gates.g[tid] = e;
+                sm.gates.oq[tid] = sm.nq[tid];
+                if (tid == 0) sm.gates.last = exp2f(last);
+            }
+            // L in fp32, A rounded to its tile
+            const float ci = sm.cum[i];
+            if (q < 2) {
+                const float bi = sm.b[i] * sm.nk[i];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    float4 w;
+                    float *wp = &w.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int jj = hf * 32 + j + e;
+                        wp[e] = jj < i ? dots[j + e] * bi * sm.nk[jj] * exp2f(ci - sm.cum[jj]) : 0.0f;
+                    }
+                    *reinterpret_cast<float4 *>(&sm.m.L[i][hf * 32 + j]) = w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    float w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int jj = hf * 32 + j + e;
+                        w[e] = jj <= i ? dots[j + e] * sm.nk[jj] * exp2f(ci - sm.cum[jj]) : 0.0f;
+                    }
+                    uint4 u = make_uint4(pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3]), pack_f16x2(w[4], w[5]),
+                                         pack_f16x2(w[6], w[7]));
+                    *reinterpret_cast<uint4 *>(sm.out + kBlk + swz128_chunk(i, hf * 4 + j / 8)) = u;
+                }
+            }
+            __syncthreads();
+            // (I + L)^-1 of the two diagonal 32 x 32 blocks, a column a thread, by forward substitution
+            if (warp < 2) {
+                float x[32];
+#pragma unroll
+                for (int r = 0; r < 32; ++r) {
+                    float acc[4] = {r == lane ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int m = 0; m < r; m += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(&sm.m.L[warp * 32 + r][warp * 32 + m]);
+                        const float *lp = &l.x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (m + e < r) acc[e] = fmaf(-lp[e], x[m + e], acc[e]);
+                    }
+                    x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                    sm.m.t[warp][r][lane] = x[r];
+                }
+            }
+            __syncthreads();
+            // lower left block: -T22 (L21 T11), four columns a thread
+            const int mi = tid >> 3, mc = (tid & 7) * 4;
+            {
+                float acc[4] = {};
+#pragma unroll
+                for (int m = 0; m < 32; ++m) {
+                    const float l = sm.m.L[32 + mi][m];
+                    const float4 t = *reinterpret_cast<const float4 *>(&sm.m.t[0][m][mc]);
+                    acc[0] = fmaf(l, t.x, acc[0]);
+                    acc[1] = fmaf(l, t.y, acc[1]);
+                    acc[2] = fmaf(l, t.z, acc[2]);
+                    acc[3] = fmaf(l, t.w, acc[3]);
+                }
+                *reinterpret_cast<float4 *>(&sm.m.L[mi][mc]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            }
+            __syncthreads();
+            {
+                float acc[4] = {};
+#pragma unroll
+                for (int m = 0; m < 32; ++m) {
+                    const float l = sm.m.t[1][mi][m];
+                    const float4 t = *reinterpret_cast<const float4 *>(&sm.m.L[m][mc]);
+                    acc[0] = fmaf(l, t.x, acc[0]);
+                    acc[1] = fmaf(l, t.y, acc[1]);
+                    acc[2] = fmaf(l, t.z, acc[2]);
+                    acc[3] = fmaf(l, t.w, acc[3]);
+                }
+                // T diag(b), rounded: this thread's four columns of the lower left block and of the others
+                auto put = [&](int row, int c, float v0, float v1, float v2, float v3) {
+                    const uint2 u = make_uint2(pack_f16x2(v0 * sm.b[c], v1 * sm.b[c + 1]),
+                                               pack_f16x2(v2 * sm.b[c + 2], v3 * sm.b[c + 3]));
+                    *reinterpret_cast<uint2 *>(sm.out + swz128_offset(row, c)) = u;
+                };
+                put(32 + mi, mc, -acc[0], -acc[1], -acc[2], -acc[3]);
+                const float4 a = *reinterpret_cast<const float4 *>(&sm.m.t[0][mi][mc]);
+                const float4 d = *reinterpret_cast<const float4 *>(&sm.m.t[1][mi][mc]);
+                put(mi, mc, a.x, a.y, a.z, a.w);
+                put(mi, 32 + mc, 0.0f, 0.0f, 0.0f, 0.0f);
+                put(32 + mi, 32 + mc, d.x, d.y, d.z, d.w);
+            }
+            fence_async_smem();
+            __syncthreads();
+            if (tid == 0) {
+                unsigned char *dst = ws.head(chunk, h);
+                bulk_s2g(dst, sm.out, 2 * kBlk);
+                bulk_s2g(dst + 2 * kBlk, &sm.gates, kGateBytes);
+                bulk_commit();
+                bulk_wait_read<0>();
+            }
+        }
+        if (tid == 0) bulk_wait_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tm, 64);
+}
+
+// ---------------------------------------------------------------------------------------
+// the chain over a sequence's chunks
+// ---------------------------------------------------------------------------------------
+
+constexpr int kChainThreads = 256;
+constexpr int kRescale = 16;  // chunks between two choices of the rows' powers of two
+
+// What the block waits for: a stage (two), T, A, the values; the products X, U, Q S^T, the increment
+// and Y.
+enum { B_KQ = 0, B_T = 2, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, kBars };
+
+struct ChainSmem {
+    unsigned char k[2][2 * kBlk], q[2][2 * kBlk], T[kBlk], A[kBlk];
+    bf16 v[C][TP];
+    HeadGates gates[4];
+    float row_max[2][TP];
+    uint64_t bar[kBars];
+    uint32_t tmem;
+};
+
+// Tensor-memory columns: the state's 16-bit copy and X (or R^T over X) make way for the new state's
+// increment, which is as wide as both.
+constexpr uint32_t T_S = 0, T_X = 64, T_D = 0, T_U = 128, T_Y = 192;
+
+// The stage (keys, queries, gates) of chunk c of the sequence; completes on barrier B_KQ + (c & 1).
+__device__ __forceinline__ void load_stage(ChainSmem &sm, const WsLayout &ws, int first, int c, int g, int h) {
+    uint64_t *bar = &sm.bar[B_KQ + (c & 1)];
+    mbar_arrive_expect_tx(bar, kKqBytes + kGateBytes);
+    const unsigned char *kq = ws.kq(first + c, g);
+    bulk_g2s(sm.k[c & 1], kq, kBlk, bar);
+    bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, bar);
+    bulk_g2s(sm.k[c & 1] + kBlk, kq + 2 * kBlk, kBlk, bar);
+    bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, bar);
+    bulk_g2s(&sm.gates[c & 3], ws.head(first + c, h) + 2 * kBlk, kGateBytes, bar);
+}
+__device__ __forceinline__ void load_tile(void *dst, const unsigned char *src, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, kBlk);
+    bulk_g2s(dst, src, kBlk, bar);
+}
+__device__ __forceinline__ void load_values(ChainSmem &sm, const CUtensorMap *map, int h, int t) {
+    mbar_arrive_expect_tx(&sm.bar[B_V], sizeof(sm.v));
+    tma_load_2d(sm.v, map, h * TP, t, &sm.bar[B_V]);
+}
+
+__device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(q + 1) : "memory"); }
+
+// Block (sequence in the plan's order, head).  Warp w works on tensor-memory lanes 32 (w % 4) .. + 31,
+// the value indices, and on half w / 4 of the columns: of the tokens, or of the state's.
+__global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,
+                                                                const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) unsigned char chain_smem[];
+    ChainSmem &sm = *align1024<ChainSmem>(chain_smem);
+    pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
+    pdl_launch_dependents();
+    if (p.meta[0] == 0) return;  // bad cu_seqlens (flagged): nothing is done
+    const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, g = h / p.HG;
+    const int t0 = p.cu[s], len = p.cu[s + 1] - t0, first = meta_chunks(p)[s];
+    const int32_t slot = p.slot[s];
+    if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, hf = warp >> 2;
+    const int row = q * 32 + lane;  // value index
+    const int nc = (len + C - 1) / C;
+    bf16 *pool = static_cast<bf16 *>(p.pool);
+    const int64_t off = ((int64_t)h * TP + row) * TN + hf * 64;
+
+    if (tid == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&vmap);
+        load_stage(sm, ws, first, 0, g, h);
+        load_tile(sm.T, ws.head(first, h), &sm.bar[B_T]);
+        load_tile(sm.A, ws.head(first, h) + kBlk, &sm.bar[B_A]);
+        load_values(sm, &vmap, h, t0);
+    }
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem, 256);
+        tmem_relinquish();
+    }
+    // this thread's half row of the state, times the row's power of two
+    float S[64];
+    if (slot >= 0 && p.has_init && p.has_init[s]) {
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+            float f[8];
+            load8_stream(pool + slot * p.stride + off + e, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) S[e + i] = f[i];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) S[e] = 0.0f;
+    }
+    float sigma = 1.0f, inv_sigma = 1.0f;
+    uint32_t limit = 0;  // largest bf16 magnitude (as bits) that fits the row's power of two
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem, lanes = tm + ((uint32_t)(q * 32) << 16);
+    bool failed = false;
+    uint32_t x_phase = 0;
+    uint32_t armed = 0, parity = 0;  // thread 0: the barriers with something in flight, ever, and its phase
+    auto arm = [&](int i, uint32_t phase) {
+        armed |= 1u << i;
+        parity = (parity & ~(1u << i)) | phase << i;
+    };
+    if (tid == 0) arm(B_KQ, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
+
+    auto store_state16 = [&] {  // the state's copy for the products; the pair's columns are consumed
+#pragma unroll
+        for (int e = 0; e < 64; e += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(S[e + 2 * i], S[e + 2 * i + 1]);
+            tmem_st16(lanes + T_S + hf * 32 + e / 2, pk);
+        }
+    };
+    auto issue_x = [&](int c) {  // X = S K^T
+        const uint32_t k = smem_u32(sm.k[c & 1]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tm + T_X, tm + T_S + 8 * kk, desc_kmajor(k, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+        mma_commit(&sm.bar[B_X]);
+        arm(B_X, x_phase);
+    };
+    // outputs of chunk c: lane = value index, 32 tokens a thread
+    auto write_outputs = [&](int c) {
+        float y[32];
+        tmem_ld32(lanes + T_Y + hf * 32, y);
+        const int L = min(C, len - c * C);
+        const HeadGates &gt = sm.gates[c & 3];
+        bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(t0 + c * C + hf * 32) * p.H + h) * TP + row;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (hf * 32 + j < L) dst[(int64_t)j * p.H * TP] = __float2bfloat16_rn(y[j] * gt.oq[hf * 32 + j] * inv_sigma);
+    };
+    auto write_state = [&](int32_t to) {
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = S[e + i] * inv_sigma;
+            store8_stream(pool + to * p.stride + off + e, f);
+        }
+    };
+
+    for (int c = 0; c < nc; ++c) {
+        const uint32_t ph = c & 1;
+        const int L = min(C, len - c * C);
+        int bad = 0;
+        const bool fresh = c % kRescale == 0;  // this chunk starts from a new power of two
+        // 1. X = S K^T, while the next stage's loads start and the last chunk's outputs are written
+        if (!mbar_wait(&sm.bar[B_KQ + ph], (c >> 1) & 1, kPolls)) bad = 1;
+        if (tid == 0 && !bad) {
+            tc_fence_after();
+            if (!fresh) issue_x(c);
+            if (c > 0 && !mbar_wait(&sm.bar[B_Y], ph ^ 1, kPolls)) bad = 1;
+            if (!bad) {
+                if (c > 0) {
+                    load_tile(sm.A, ws.head(first + c, h) + kBlk, &sm.bar[B_A]);
+                    arm(B_A, ph);
+                }
+                if (c + 1 < nc) {
+                    load_stage(sm, ws, first, c + 1, g, h);
+                    arm(B_KQ + (ph ^ 1), ((c + 1) >> 1) & 1);
+                }
+            }
+        }
+        if (c > 0) {
+            if (!mbar_wait(&sm.bar[B_Y], ph ^ 1, kPolls)) bad = 1;
+            tc_fence_after();
+            if (!bad) write_outputs(c - 1);
+        }
+        // 2. queries times e^c in place; this thread's 32 values of its row
+        const HeadGates &gt = sm.gates[c & 3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int cidx = tid + kChainThreads * i;  // 16-byte chunk of the tile: row of 128 bytes = token
+            uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[ph] + cidx * 16);
+            const __half2 w = __float2half2_rn(gt.g[(cidx >> 3) & (C - 1)]);
+            uint4 u = *ptr;
+            __half2 *hp = reinterpret_cast<__half2 *>(&u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w);
+            *ptr = u;
+        }
+        fence_async_smem();
+        if (!mbar_wait(&sm.bar[B_V], ph, kPolls)) bad = 1;
+        uint32_t vals[16];
+        uint32_t vmax = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int t = hf * 32 + 2 * j;
+            const uint32_t lo = t < L ? __bfloat16_as_ushort(sm.v[t][row]) : 0u;
+            const uint32_t hi = t + 1 < L ? __bfloat16_as_ushort(sm.v[t + 1][row]) : 0u;
+            vals[j] = lo | hi << 16;
+            vmax = max(vmax, max(lo & 0x7fffu, hi & 0x7fffu));
+        }
+        // a value outgrew its row's power of two, or it is time to choose anew (a wait that gave up goes
+        // the same way and ends the block below)
+        if (__syncthreads_or(bad || vmax > limit) || fresh) {
+            if (!fresh) {  // X of the old power is not used
+                if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
+                x_phase ^= 1;
+            }
+            // the largest magnitude in the row of the state (unscaled) and of the values
+            float top = __uint_as_float(vmax << 16);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) top = fmaxf(top, fabsf(S[e]) * inv_sigma);
+            sm.row_max[hf][row] = top;
+            __syncthreads();
+            top = fmaxf(sm.row_max[0][row], sm.row_max[1][row]);
+            // power of two that brings the largest to [2, 4); values may grow to 16 before the next choice
+            int ex = (int)(__float_as_uint(top) >> 23) - 127;
+            ex = max(-120, min(120, ex));
+            if (!(top < INFINITY)) ex = 0;
+            const float next = __uint_as_float((uint32_t)(127 + 1 - ex) << 23);
+            const float ratio = next * inv_sigma;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) S[e] *= ratio;
+            sigma = next;
+            inv_sigma = __uint_as_float((uint32_t)(127 - 1 + ex) << 23);
+            limit = top < INFINITY ? (uint32_t)(127 + ex + 3) << 7 : 0xffffu;
+            store_state16();
+            tc_fence_before();
+            if (__syncthreads_or(bad)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after();
+            if (tid == 0) issue_x(c);
+        }
+        // 3. R = V - e^c |k| X, rounded, over X; then U^T = R^T T^T and the state's part of Y
+        if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
+        x_phase ^= 1;
+        tc_fence_after();
+        {
+            float x[32];
+            tmem_ld32(lanes + T_X + hf * 32, x);
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int t = hf * 32 + 2 * j;
+                const float v0 = __uint_as_float(vals[j] << 16) * sigma, v1 = __uint_as_float(vals[j] & 0xffff0000u) * sigma;
+                const float r0 = t < L ? fmaf(-gt.rk[t], x[2 * j], v0) : 0.0f;
+                const float r1 = t + 1 < L ? fmaf(-gt.rk[t + 1], x[2 * j + 1], v1) : 0.0f;
+                pk[j] = pack_f16x2(r0, r1);
+            }
+            tmem_st16(lanes + T_X + hf * 32, pk);
+        }
+        if (!mbar_wait(&sm.bar[B_T], ph, kPolls)) bad = 1;
+        tc_fence_before();
+        if (__syncthreads_or(bad)) {
+            failed = true;
+            break;
+        }
+        tc_fence_after();
+        if (tid == 0) {
+            const uint32_t T = smem_u32(sm.T), qq = smem_u32(sm.q[ph]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ts(tm + T_U, tm + T_X + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(T, kBlk, kk),
+                            idesc_f16(128, C, false), kk > 0);
+            mma_commit(&sm.bar[B_U]);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(qq, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+            mma_commit(&sm.bar[B_OI]);
+            arm(B_U, ph), arm(B_OI, ph);
+            if (c + 1 < nc) {
+                load_values(sm, &vmap, h, t0 + (c + 1) * C);
+                arm(B_V, ph ^ 1);
+            }
+        }
+        // 4. U^T rounded, as it is and times e^(c_64 - c) |k|; then the state's increment and A's part of Y
+        if (!mbar_wait(&sm.bar[B_U], ph, kPolls)) bad = 1;
+        tc_fence_after();
+        {
+            float u[32];
+            tmem_ld32(lanes + T_U + hf * 32, u);
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = pack_f16x2(u[2 * j], u[2 * j + 1]);
+            tmem_st16(lanes + T_U + hf * 32, pk);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int t = hf * 32 + 2 * j;
+                pk[j] = pack_f16x2(u[2 * j] * gt.ek[t], u[2 * j + 1] * gt.ek[t + 1]);
+            }
+            tmem_st16(lanes + T_U + hf * 32 + 16, pk);
+        }
+        if (!mbar_wait(&sm.bar[B_OI], ph, kPolls)) bad = 1;  // the state's copy is read: its columns are free
+        if (!mbar_wait(&sm.bar[B_A], ph, kPolls)) bad = 1;
+        tc_fence_before();
+        if (__syncthreads_or(bad)) {
+            failed = true;
+            break;
+        }
+        tc_fence_after();
+        if (tid == 0) {
+            const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ts(tm + T_D, tm + T_U + (kk >> 1) * 32 + 16 + (kk & 1) * 8, desc_mnmajor(k, kBlk, kk),
+                            idesc_f16(128, TN, true), kk > 0);
+            mma_commit(&sm.bar[B_S]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ts(tm + T_Y, tm + T_U + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(A, kBlk, kk),
+                            idesc_f16(128, C, false), 1);
+            mma_commit(&sm.bar[B_Y]);
+            arm(B_S, ph), arm(B_Y, ph);
+            if (c + 1 < nc) {
+                load_tile(sm.T, ws.head(first + c + 1, h), &sm.bar[B_T]);
+                arm(B_T, ph ^ 1);
+            }
+        }
+        // 5. the new state, and its copy
+        if (!mbar_wait(&sm.bar[B_S], ph, kPolls)) bad = 1;
+        tc_fence_after();
+        const float last = gt.last;
+#pragma unroll
+        for (int e = 0; e < 64; e += 32) {
+            float d[32];
+            tmem_ld32(lanes + T_D + hf * 64 + e, d);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[e + i] = fmaf(last, S[e + i], d[i]);
+        }
+        const int32_t cs = ckpt_slot(p, s, c * C + L, tid == 0 && h == 0);
+        if (cs >= 0) write_state(cs);
+        if (c + 1 < nc && (c + 1) % kRescale != 0) {
+            tc_fence_before();
+            pair_sync(q);  // both halves of the row have read the increment
+            tc_fence_after();
+            store_state16();
+        }
+        tc_fence_before();
+        if (__syncthreads_or(bad)) {
+            failed = true;
+            break;
+        }
+        tc_fence_after();
+    }
+    if (!failed) {
+        if (slot >= 0) write_state(slot);
+        failed = !mbar_wait(&sm.bar[B_Y], (nc - 1) & 1, kPolls);
+        tc_fence_after();
+        if (!failed) write_outputs(nc - 1);
+    }
+    if (__syncthreads_or(failed)) {
+        // an operation did not complete in time: report it, and give what this block still has in flight
+        // the same bounded time to finish before its memory is released
+        if (tid == 0) {
+            flag_error(p.err, MAMBA_ERR_TIMEOUT);
+            for (int i = 0; i < kBars; ++i)
+                if (armed >> i & 1) mbar_wait(&sm.bar[i], parity >> i & 1, kPolls);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tm, 256);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    return fn;
+}
+
+// Rows of tokens x (heads * 128) values, in boxes of 64 tokens x 128 values; rows past the end read as zero.
+bool value_map(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+    cuuint32_t box[2] = {TP, C}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool chunked_eligible(const mamba_layer_desc *d) {
+    return d->act_dtype == MAMBA_BF16 && d->state_dtype == MAMBA_BF16 && d->head_dim == TP && d->d_state == TN;
+}
+
+size_t chunked_workspace_bytes(const mamba_layer_desc *d, int T, int nseq) {
+    const WsLayout ws = {nullptr, d->nheads, d->n_groups};
+    return (size_t)(scan_max_chunks(T, nseq) * ws.chunk_bytes());
+}
+
+int chunked_launch(const ScanParams &p, cudaStream_t st) {
+    const WsLayout ws = {p.ws, p.H, p.G};
+    CUtensorMap vmap;
+    if (!value_map(&vmap, p.v, (uint64_t)p.H * TP, (uint64_t)p.T)) return MAMBA_ECUDA;
+    const size_t prep = sizeof(PrepSmem) + 1024, chain = sizeof(ChainSmem) + 1024;
+    if (cudaFuncSetAttribute(k_gdn_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep) != cudaSuccess ||
+        cudaFuncSetAttribute(k_gdn_chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain) != cudaSuccess)
+        return MAMBA_ECUDA;
+    const int hpb = p.HG % 2 == 0 ? 2 : 1;
+    const dim3 grid((unsigned)scan_max_chunks(p.T, p.nseq), (unsigned)(p.G * (p.HG / hpb)));
+    if (launch_pdl(k_gdn_prep, grid, dim3(kPrepThreads), prep, st, p, ws, hpb) != cudaSuccess) return MAMBA_ECUDA;
+    if (launch_pdl(k_gdn_chain, dim3((unsigned)((int64_t)p.nseq * p.H)), dim3(kChainThreads), chain, st, p, ws, vmap) != cudaSuccess)
+        return MAMBA_ECUDA;
+    return launch_status();
+}
+
+}  // namespace gdn
+}  // namespace ms
