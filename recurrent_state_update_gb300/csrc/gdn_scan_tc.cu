@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // The swizzled tiles want 1024-byte boundaries; the launches ask for that much more.
 template <typename T>
 __device__ __forceinline__ T *align1024(unsigned char *p) {
-    return reinterpret_cast<T *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
+    return reinterpret_cast<T *>(p + (-smem_u32(p) & 1023u));  // (an offset, so that accesses stay shared-memory ones)
 }
 
 // ---------------------------------------------------------------------------------------
@@ -85,6 +85,7 @@ __device__ __forceinline__ T *align1024(unsigned char *p) {
 constexpr int kPrepThreads = 256;
 constexpr int LP = C + 4;  // row pitch of the fp32 matrices: rows 16 bytes apart modulo a bank row
 
+template <int HEADS>
 struct PrepSmem {
     union {
         unsigned char kq[kKqBytes];  // until its product and its copy to the workspace are done
@@ -95,10 +96,10 @@ struct PrepSmem {
     };
     unsigned char out[2 * kBlk];  // T | A
     HeadGates gates;
-    float cum[C], b[C], nk[C], nq[C];
+    float cum[HEADS][C], b[HEADS][C], nk[C], nq[C];
     uint64_t bar;
     uint32_t tmem;
-    float half_sum;
+    float half_sum[HEADS];
 };
 
 // Sequence of a chunk: the last one whose first chunk is not past it.
@@ -113,9 +114,10 @@ __device__ __forceinline__ int chunk_sequence(const int32_t *first, int nseq, in
 }
 
 // Block (chunk, group and share of its heads).
-__global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, const WsLayout ws, int heads_per_block) {
+template <int HEADS>
+__global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p, const WsLayout ws) {
     extern __shared__ __align__(1024) unsigned char prep_smem[];
-    PrepSmem &sm = *align1024<PrepSmem>(prep_smem);
+    PrepSmem<HEADS> &sm = *align1024<PrepSmem<HEADS>>(prep_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     const int chunk = blockIdx.x;
@@ -125,8 +127,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, c
     const int at = (chunk - meta_chunks(p)[s]) * C;
     const int64_t t0 = (int64_t)p.cu[s] + at;
     const int L = min(C, p.cu[s + 1] - p.cu[s] - at);
-    const int shares = p.HG / heads_per_block;
-    const int g = blockIdx.y / shares, h0 = g * p.HG + (blockIdx.y % shares) * heads_per_block;
+    const int shares = p.HG / HEADS;
+    const int g = blockIdx.y / shares, h0 = g * p.HG + (blockIdx.y % shares) * HEADS;
     if (warp == 0) {
         tmem_alloc(&sm.tmem, 64);
         tmem_relinquish();
@@ -134,6 +136,13 @@ __global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, c
     if (tid == 0) {
         mbar_init(&sm.bar, 1);
         fence_mbar_init();
+    }
+    // a token of a head a thread: its raw step and gate; no step and no write past the sequence's end
+    float run = 0.0f, b = 0.0f;
+    if (tid < HEADS * C && (tid & (C - 1)) < L) {
+        const int64_t th = (t0 + (tid & (C - 1))) * p.H + h0 + tid / C;
+        run = load_scalar(p.dt, th, p.gates.dt_bf16);
+        b = load_scalar(p.beta, th, p.gates.dt_bf16);
     }
     // unit keys (rows 0..63) and queries (64..127): 16 lanes a row, 16 rows a pass
     {
@@ -168,10 +177,28 @@ __global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, c
             }
         }
     }
+    // running sums of the log decays (base 2) over each head's two warps of tokens
+    if (tid < HEADS * C) {
+        if ((tid & (C - 1)) < L) {
+            run = log_decay(p.gates, run, h0 + tid / C) * LOG2E;
+            b = write_gate(p.gates, b);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+        }
+        if ((tid & (C - 1)) == 31) sm.half_sum[tid / C] = run;
+        sm.b[tid / C][tid & (C - 1)] = b;
+    }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid < HEADS * C) {
+        if (warp & 1) run += sm.half_sum[tid / C];
+        sm.cum[tid / C][tid & (C - 1)] = run;
+    }
     const uint32_t tm = sm.tmem;
     if (tid == 0) {
         const uint32_t kq = smem_u32(sm.kq);
@@ -196,66 +223,47 @@ __global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, c
         const int q = warp & 3, hf = warp >> 2, i = (q & 1) * 32 + lane;  // row i of K K^T (q < 2) or Q K^T
         float dots[32];
         tmem_ld32(tm + ((uint32_t)(q * 32) << 16) + hf * 32, dots);
-        for (int h = h0; h < h0 + heads_per_block; ++h) {
-            // running sums of the log decays (base 2) over the chunk's two warps of tokens; no step and
-            // no write past the sequence's end
-            float run = 0.0f, b = 0.0f;
+        for (int hh = 0; hh < HEADS; ++hh) {
+            const float *cum = sm.cum[hh], *bb = sm.b[hh];
+            if (hh) __syncthreads();  // the last head's T and A have been copied out
             if (tid < C) {
-                if (tid < L) {
-                    const int64_t th = (t0 + tid) * p.H + h;
-                    run = log_decay(p.gates, load_scalar(p.dt, th, p.gates.dt_bf16), h) * LOG2E;
-                    b = write_gate(p.gates, load_scalar(p.beta, th, p.gates.dt_bf16));
-                }
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float v = __shfl_up_sync(0xffffffffu, run, o);
-                    if (lane >= o) run += v;
-                }
-                if (tid == 31) sm.half_sum = run;
-            }
-            __syncthreads();  // (also: the last head's T and A have been copied out)
-            if (tid < C) {
-                if (warp == 1) run += sm.half_sum;
-                sm.cum[tid] = run;
-                sm.b[tid] = b;
-            }
-            __syncthreads();
-            if (tid < C) {
-                const float last = sm.cum[C - 1], nk = sm.nk[tid], e = exp2f(run);
+                const float c = cum[tid], last = cum[C - 1], nk = sm.nk[tid], e = exp2f(c);
                 sm.gates.rk[tid] = e * nk;
-                sm.gates.ek[tid] = exp2f(last - run) * nk;
+                sm.gates.ek[tid] = exp2f(last - c) * nk;
                 sm.gates.g[tid] = e;
                 sm.gates.oq[tid] = sm.nq[tid];
                 if (tid == 0) sm.gates.last = exp2f(last);
             }
-            // L in fp32, A rounded to its tile
-            const float ci = sm.cum[i];
-            if (q < 2) {
-                const float bi = sm.b[i] * sm.nk[i];
+            // L in fp32, A rounded to its tile; a block of columns past the rows is zero
+            const float ci = cum[i], wi = q < 2 ? bb[i] * sm.nk[i] : 1.0f;
+            const int edge = q < 2 ? i : i + 1;  // columns below it count
+            float w[32];
+            if (hf <= (q & 1)) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    float4 w;
-                    float *wp = &w.x;
+                    const float4 cj = *reinterpret_cast<const float4 *>(cum + hf * 32 + j);
+                    const float4 nj = *reinterpret_cast<const float4 *>(sm.nk + hf * 32 + j);
+                    const float *cp = &cj.x, *np = &nj.x;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int jj = hf * 32 + j + e;
-                        wp[e] = jj < i ? dots[j + e] * bi * sm.nk[jj] * exp2f(ci - sm.cum[jj]) : 0.0f;
+                        const float v = dots[j + e] * wi * np[e] * exp2f(ci - cp[e]);
+                        w[j + e] = hf * 32 + j + e < edge ? v : 0.0f;
                     }
-                    *reinterpret_cast<float4 *>(&sm.m.L[i][hf * 32 + j]) = w;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    float w[8];
+                for (int j = 0; j < 32; ++j) w[j] = 0.0f;
+            }
+            if (q < 2) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int jj = hf * 32 + j + e;
-                        w[e] = jj <= i ? dots[j + e] * sm.nk[jj] * exp2f(ci - sm.cum[jj]) : 0.0f;
-                    }
-                    uint4 u = make_uint4(pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3]), pack_f16x2(w[4], w[5]),
-                                         pack_f16x2(w[6], w[7]));
-                    *reinterpret_cast<uint4 *>(sm.out + kBlk + swz128_chunk(i, hf * 4 + j / 8)) = u;
-                }
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4 *>(&sm.m.L[i][hf * 32 + j]) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8)
+                    *reinterpret_cast<uint4 *>(sm.out + kBlk + swz128_chunk(i, hf * 4 + j / 8)) =
+                        make_uint4(pack_f16x2(w[j], w[j + 1]), pack_f16x2(w[j + 2], w[j + 3]), pack_f16x2(w[j + 4], w[j + 5]),
+                                   pack_f16x2(w[j + 6], w[j + 7]));
             }
             __syncthreads();
             // (I + L)^-1 of the two diagonal 32 x 32 blocks, a column a thread, by forward substitution
@@ -306,8 +314,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, c
                 }
                 // T diag(b), rounded: this thread's four columns of the lower left block and of the others
                 auto put = [&](int row, int c, float v0, float v1, float v2, float v3) {
-                    const uint2 u = make_uint2(pack_f16x2(v0 * sm.b[c], v1 * sm.b[c + 1]),
-                                               pack_f16x2(v2 * sm.b[c + 2], v3 * sm.b[c + 3]));
+                    const float4 w = *reinterpret_cast<const float4 *>(bb + c);
+                    const uint2 u = make_uint2(pack_f16x2(v0 * w.x, v1 * w.y), pack_f16x2(v2 * w.z, v3 * w.w));
                     *reinterpret_cast<uint2 *>(sm.out + swz128_offset(row, c)) = u;
                 };
                 put(32 + mi, mc, -acc[0], -acc[1], -acc[2], -acc[3]);
@@ -320,7 +328,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_gdn_prep(const ScanParams p, c
             fence_async_smem();
             __syncthreads();
             if (tid == 0) {
-                unsigned char *dst = ws.head(chunk, h);
+                unsigned char *dst = ws.head(chunk, h0 + hh);
                 bulk_s2g(dst, sm.out, 2 * kBlk);
                 bulk_s2g(dst + 2 * kBlk, &sm.gates, kGateBytes);
                 bulk_commit();
@@ -463,12 +471,20 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     auto write_outputs = [&](int c) {
         float y[32];
         tmem_ld32(lanes + T_Y + hf * 32, y);
-        const int L = min(C, len - c * C);
-        const HeadGates &gt = sm.gates[c & 3];
+        const int L = min(C, len - c * C) - hf * 32;
+        const float4 *oq = reinterpret_cast<const float4 *>(sm.gates[c & 3].oq + hf * 32);
         bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(t0 + c * C + hf * 32) * p.H + h) * TP + row;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (hf * 32 + j < L) dst[(int64_t)j * p.H * TP] = __float2bfloat16_rn(y[j] * gt.oq[hf * 32 + j] * inv_sigma);
+        for (int j = 0; j < 32; j += 4) {
+            const float4 w = oq[j / 4];
+            const float *wp = &w.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bf16 v = __float2bfloat16_rn(y[j + e] * (wp[e] * inv_sigma));
+                if (j + e < L) *dst = v;
+                dst += (int64_t)p.H * TP;
+            }
+        }
     };
     auto write_state = [&](int32_t to) {
 #pragma unroll
@@ -527,11 +543,18 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const int t = hf * 32 + 2 * j;
-            const uint32_t lo = t < L ? __bfloat16_as_ushort(sm.v[t][row]) : 0u;
-            const uint32_t hi = t + 1 < L ? __bfloat16_as_ushort(sm.v[t + 1][row]) : 0u;
-            vals[j] = lo | hi << 16;
-            vmax = max(vmax, max(lo & 0x7fffu, hi & 0x7fffu));
+            vals[j] = __bfloat16_as_ushort(sm.v[t][row]) | (uint32_t)__bfloat16_as_ushort(sm.v[t + 1][row]) << 16;
         }
+        if (L < C) {  // rows past the sequence's end hold another sequence's values
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int t = hf * 32 + 2 * j;
+                vals[j] = t + 1 < L ? vals[j] : (t < L ? vals[j] & 0xffffu : 0u);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) vmax = __vmaxu2(vmax, vals[j] & 0x7fff7fffu);
+        vmax = max(vmax & 0xffffu, vmax >> 16);
         // a value outgrew its row's power of two, or it is time to choose anew (a wait that gave up goes
         // the same way and ends the block below)
         if (__syncthreads_or(bad || vmax > limit) || fresh) {
@@ -574,13 +597,14 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             float x[32];
             tmem_ld32(lanes + T_X + hf * 32, x);
             uint32_t pk[16];
+            const float4 *rk = reinterpret_cast<const float4 *>(gt.rk + hf * 32);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int t = hf * 32 + 2 * j;
-                const float v0 = __uint_as_float(vals[j] << 16) * sigma, v1 = __uint_as_float(vals[j] & 0xffff0000u) * sigma;
-                const float r0 = t < L ? fmaf(-gt.rk[t], x[2 * j], v0) : 0.0f;
-                const float r1 = t + 1 < L ? fmaf(-gt.rk[t + 1], x[2 * j + 1], v1) : 0.0f;
-                pk[j] = pack_f16x2(r0, r1);
+            for (int j = 0; j < 16; j += 2) {  // (past the end the values, the keys and so X are zero)
+                const float4 w = rk[j / 2];
+                pk[j] = pack_f16x2(fmaf(-w.x, x[2 * j], __uint_as_float(vals[j] << 16) * sigma),
+                                   fmaf(-w.y, x[2 * j + 1], __uint_as_float(vals[j] & 0xffff0000u) * sigma));
+                pk[j + 1] = pack_f16x2(fmaf(-w.z, x[2 * j + 2], __uint_as_float(vals[j + 1] << 16) * sigma),
+                                       fmaf(-w.w, x[2 * j + 3], __uint_as_float(vals[j + 1] & 0xffff0000u) * sigma));
             }
             tmem_st16(lanes + T_X + hf * 32, pk);
         }
@@ -618,10 +642,12 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
 #pragma unroll
             for (int j = 0; j < 16; ++j) pk[j] = pack_f16x2(u[2 * j], u[2 * j + 1]);
             tmem_st16(lanes + T_U + hf * 32, pk);
+            const float4 *ek = reinterpret_cast<const float4 *>(gt.ek + hf * 32);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int t = hf * 32 + 2 * j;
-                pk[j] = pack_f16x2(u[2 * j] * gt.ek[t], u[2 * j + 1] * gt.ek[t + 1]);
+            for (int j = 0; j < 16; j += 2) {
+                const float4 w = ek[j / 2];
+                pk[j] = pack_f16x2(u[2 * j] * w.x, u[2 * j + 1] * w.y);
+                pk[j + 1] = pack_f16x2(u[2 * j + 2] * w.z, u[2 * j + 3] * w.w);
             }
             tmem_st16(lanes + T_U + hf * 32 + 16, pk);
         }
@@ -741,13 +767,14 @@ int chunked_launch(const ScanParams &p, cudaStream_t st) {
     const WsLayout ws = {p.ws, p.H, p.G};
     CUtensorMap vmap;
     if (!value_map(&vmap, p.v, (uint64_t)p.H * TP, (uint64_t)p.T)) return MAMBA_ECUDA;
-    const size_t prep = sizeof(PrepSmem) + 1024, chain = sizeof(ChainSmem) + 1024;
-    if (cudaFuncSetAttribute(k_gdn_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep) != cudaSuccess ||
+    const bool pairs = p.HG % 2 == 0;  // heads of a group share its products, two a block
+    auto prep = pairs ? k_gdn_prep<2> : k_gdn_prep<1>;
+    const size_t prep_smem = (pairs ? sizeof(PrepSmem<2>) : sizeof(PrepSmem<1>)) + 1024, chain = sizeof(ChainSmem) + 1024;
+    if (cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem) != cudaSuccess ||
         cudaFuncSetAttribute(k_gdn_chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain) != cudaSuccess)
         return MAMBA_ECUDA;
-    const int hpb = p.HG % 2 == 0 ? 2 : 1;
-    const dim3 grid((unsigned)scan_max_chunks(p.T, p.nseq), (unsigned)(p.G * (p.HG / hpb)));
-    if (launch_pdl(k_gdn_prep, grid, dim3(kPrepThreads), prep, st, p, ws, hpb) != cudaSuccess) return MAMBA_ECUDA;
+    const dim3 grid((unsigned)scan_max_chunks(p.T, p.nseq), (unsigned)(pairs ? p.H / 2 : p.H));
+    if (launch_pdl(prep, grid, dim3(kPrepThreads), prep_smem, st, p, ws) != cudaSuccess) return MAMBA_ECUDA;
     if (launch_pdl(k_gdn_chain, dim3((unsigned)((int64_t)p.nseq * p.H)), dim3(kChainThreads), chain, st, p, ws, vmap) != cudaSuccess)
         return MAMBA_ECUDA;
     return launch_status();
