@@ -17,20 +17,35 @@ namespace {
 
 constexpr int kStage = 16;  // tokens staged in shared memory at a time
 
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxOrdered = 4096;  // sequences up to which the longest go first (the order is found by counting)
+
 // Checks cu_seqlens and the slot ids, orders the sequences longest first (the longest chains start
-// first) and numbers the chunks.
-__global__ void __launch_bounds__(256) k_gdn_plan(const ScanParams p) {
+// first), numbers the chunks and notes where each begins.
+__global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const ScanParams p) {
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
-    __shared__ int ok, sums[256];
-    const int tid = threadIdx.x;
+    __shared__ int ok, sums[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) ok = p.cu[0] == 0 && p.cu[p.nseq] == p.T;
     __syncthreads();
-    for (int s = tid; s < p.nseq; s += 256) {
-        if (p.cu[s + 1] < p.cu[s]) ok = 0;
+    // each thread numbers a run of sequences, from the sum of the runs before it
+    const int run = (p.nseq + kPlanThreads - 1) / kPlanThreads, lo = min(p.nseq, tid * run), hi = min(p.nseq, lo + run);
+    int n = 0;
+    for (int s = lo; s < hi; ++s) {
+        const int len = p.cu[s + 1] - p.cu[s];
+        if (len < 0) ok = 0;
         const int32_t sl = p.slot[s];
         if (sl < -1 || sl >= p.num_slots) flag_error(p.err, MAMBA_ERR_SLOT_RANGE);
+        n += (len + kChunk - 1) / kChunk;
     }
+    int at = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+    }
+    if (lane == 31) sums[warp] = at;
     __syncthreads();
     if (!ok) {
         if (tid == 0) {
@@ -40,30 +55,45 @@ __global__ void __launch_bounds__(256) k_gdn_plan(const ScanParams p) {
         }
         return;
     }
-    int32_t *order = p.meta + 4, *first = p.meta + 4 + p.nseq;
-    // each thread numbers a run of sequences, from the sum of the runs before it
-    const int run = (p.nseq + 255) / 256, lo = min(p.nseq, tid * run), hi = min(p.nseq, lo + run);
-    int n = 0;
-    for (int s = lo; s < hi; ++s) n += (p.cu[s + 1] - p.cu[s] + kChunk - 1) / kChunk;
-    sums[tid] = n;
-    __syncthreads();
-    int at = 0;
-    for (int t = 0; t < tid; ++t) at += sums[t];
+    int32_t *order = meta_order(p), *first = meta_chunks(p);
+    int total = 0;
+    at -= n;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) at += sums[w];
+        total += sums[w];
+    }
     for (int s = lo; s < hi; ++s) {
         first[s] = at;
         at += (p.cu[s + 1] - p.cu[s] + kChunk - 1) / kChunk;
     }
-    if (tid == 255) first[p.nseq] = at, p.meta[1] = at;
-    for (int s = tid; s < p.nseq; s += 256) {
-        const int len = p.cu[s + 1] - p.cu[s];
-        int r = 0;
-        for (int s2 = 0; s2 < p.nseq; ++s2) {
-            const int l2 = p.cu[s2 + 1] - p.cu[s2];
-            r += (l2 > len) || (l2 == len && s2 < s);
+    if (tid == 0) {
+        first[p.nseq] = total;
+        p.meta[0] = 1;
+        p.meta[1] = total;
+    }
+    __syncthreads();
+    for (int c = tid; c < total; c += kPlanThreads) {  // a chunk's sequence: the last whose first chunk is not past it
+        int a = 0, b = p.nseq - 1;
+        while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            if (first[mid] <= c) a = mid;
+            else b = mid - 1;
+        }
+        const int t0 = p.cu[a] + (c - first[a]) * kChunk;
+        meta_table(p)[c] = make_int2(t0, min(kChunk, p.cu[a + 1] - t0));
+    }
+    for (int s = tid; s < p.nseq; s += kPlanThreads) {
+        int r = s;
+        if (p.nseq <= kMaxOrdered) {
+            const int len = p.cu[s + 1] - p.cu[s];
+            r = 0;
+            for (int s2 = 0; s2 < p.nseq; ++s2) {
+                const int l2 = p.cu[s2 + 1] - p.cu[s2];
+                r += (l2 > len) || (l2 == len && s2 < s);
+            }
         }
         order[r] = s;
     }
-    if (tid == 0) p.meta[0] = 1;
 }
 
 // Block (head and share of its rows, sequence in the plan's order).
@@ -199,7 +229,7 @@ using namespace ms;
 
 extern "C" size_t gdn_chunk_scan_workspace_bytes(const mamba_layer_desc *d, int32_t total_tokens, int32_t nseq) {
     if (check_layer(d) != MAMBA_OK || total_tokens < 0 || nseq < 0) return 0;
-    return scan_meta_bytes(nseq) + (chunked_eligible(d) ? chunked_workspace_bytes(d, total_tokens, nseq) : 0);
+    return scan_meta_bytes(total_tokens, nseq) + (chunked_eligible(d) ? chunked_workspace_bytes(d, total_tokens, nseq) : 0);
 }
 
 extern "C" int gdn_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t ssm_slot_stride, int64_t num_slots,
@@ -233,9 +263,9 @@ extern "C" int gdn_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t
     p.gates = make_gates(d, A, dt_bias, dt_softplus, beta_sigmoid, qk_l2norm, scale);
     p.y = y; p.err = err_word;
     p.meta = static_cast<int32_t *>(workspace);
-    p.ws = static_cast<unsigned char *>(workspace) + scan_meta_bytes(nseq);
+    p.ws = static_cast<unsigned char *>(workspace) + scan_meta_bytes(total_tokens, nseq);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_pdl(k_gdn_plan, dim3(1), dim3(256), 0, st, p) != cudaSuccess) return MAMBA_ECUDA;
+    if (launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, st, p) != cudaSuccess) return MAMBA_ECUDA;
     if (total_tokens == 0) return launch_status();  // only empty sequences
     if (chunked_eligible(d)) return chunked_launch(p, st);
     const bool sbf = d->state_dtype == MAMBA_BF16, abf = d->act_dtype == MAMBA_BF16;

@@ -20,16 +20,19 @@ struct ScanParams {
     Gates gates;
     void *y;
     int32_t *err;
-    int32_t *meta;  // workspace: [valid, chunks, pad x2, order[nseq], first chunk of each sequence[nseq + 1]]
+    int32_t *meta;  // workspace: [valid, chunks, pad x2, (first token, tokens) of each chunk, order[nseq], first chunk of each
+                    // sequence[nseq + 1]]
     unsigned char *ws;  // workspace of the chunked form, past meta
 };
 
-__device__ __forceinline__ const int32_t *meta_order(const ScanParams &p) { return p.meta + 4; }
-__device__ __forceinline__ const int32_t *meta_chunks(const ScanParams &p) { return p.meta + 4 + p.nseq; }
-
-inline size_t scan_meta_bytes(int nseq) { return ((size_t)(5 + 2 * (int64_t)nseq) * sizeof(int32_t) + 1023) / 1024 * 1024; }
 // Chunks of the whole batch, at most.
-inline int64_t scan_max_chunks(int T, int nseq) { return (int64_t)T / kChunk + nseq; }
+__host__ __device__ inline int64_t scan_max_chunks(int T, int nseq) { return (int64_t)T / kChunk + nseq; }
+inline size_t scan_meta_bytes(int T, int nseq) {
+    return ((size_t)(5 + 2 * (int64_t)nseq + 2 * scan_max_chunks(T, nseq)) * sizeof(int32_t) + 1023) / 1024 * 1024;
+}
+__device__ __forceinline__ int2 *meta_table(const ScanParams &p) { return reinterpret_cast<int2 *>(p.meta + 4); }
+__device__ __forceinline__ int32_t *meta_order(const ScanParams &p) { return p.meta + 4 + 2 * scan_max_chunks(p.T, p.nseq); }
+__device__ __forceinline__ int32_t *meta_chunks(const ScanParams &p) { return meta_order(p) + p.nseq; }
 
 // Slot of the checkpoint due after `done` tokens of sequence s, or -1 (an id outside the pool is
 // flagged by the one thread that passes flag).

@@ -83,39 +83,164 @@ __device__ __forceinline__ T *align1024(unsigned char *p) {
 // ---------------------------------------------------------------------------------------
 
 constexpr int kPrepThreads = 256;
-constexpr int LP = C + 4;  // row pitch of the fp32 matrices: rows 16 bytes apart modulo a bank row
+constexpr float kSpan = 96.0f;  // largest base-2 exponent span of a block whose decays are factored
+
+// T of one head on the way: L's diagonal 16 x 16 blocks in fp32 (two blocks start 16 banks apart), the
+// rest of L and (I + L)^-1 in fp16, rows 144 bytes apart so that eight rows' 16 bytes miss one another's
+// banks.
+struct Inverse {
+    float diag[4][16 * 20 + 16];
+    __half L[C][72], t[C][72];
+};
+// Decays within a 32-token half of the chunk and from the first half to the second, as a factor of the
+// row times one of the column (with the key's length); see decay_factors.
+struct Decays {
+    float cum[C], b[C], near[C], far[32];
+};
 
 template <int HEADS>
 struct PrepSmem {
     union {
         unsigned char kq[kKqBytes];  // until its product and its copy to the workspace are done
-        struct {
-            float L[C][LP];       // L, and then its lower left quarter times T's upper left one
-            float t[2][32][36];   // the diagonal 32 x 32 blocks of (I + L)^-1
-        } m;
+        Inverse inv[HEADS];
     };
-    unsigned char out[2 * kBlk];  // T | A
-    HeadGates gates;
-    float cum[HEADS][C], b[HEADS][C], nk[C], nq[C];
+    unsigned char out[HEADS][2 * kBlk];  // T | A
+    HeadGates gates[HEADS];
+    Decays dec[HEADS];
+    float ss[2 * C];  // squared lengths of keys and queries
+    float nk[C];
     uint64_t bar;
     uint32_t tmem;
     float half_sum[HEADS];
 };
 
-// Sequence of a chunk: the last one whose first chunk is not past it.
-__device__ __forceinline__ int chunk_sequence(const int32_t *first, int nseq, int chunk) {
-    int lo = 0, hi = nseq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= chunk) lo = mid;
-        else hi = mid - 1;
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 8 x 8 matrices of 16-bit elements from shared memory, as fragments (thread T: row T / 4, elements
+// 2 (T % 4) and the next), or transposed; lane l points at row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// A 16 x 16 (row-major fragments) times B 16 x 8, added to D 16 x 8: for the blocks of 16 and 32 rows
+// of (I + L)^-1, below the 64 rows of a tcgen05 tile.
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Address of this lane's row for a 16 x 16 block of a matrix with 72-element rows: fragments in the
+// order of an A operand, and (transposed) of two B operands side by side.
+__device__ __forceinline__ uint32_t block16(const __half (*m)[72], int row, int col, int lane) {
+    return smem_u32(&m[row + (lane & 15)][col + (lane >> 4) * 8]);
+}
+
+// -T22 (L21 T11) as (T22 L21) T11 for 16 rows and 16 K columns: rows row.. of T22 at columns mid.., L21 in
+// rows mid.., columns left.., T11 at (left, left).  The first product's sums are the second's left
+// operand as they lie in the registers.
+template <int K>
+__device__ __forceinline__ void lower_left(const Inverse &v, int row, int mid, int left, float (&out)[2 * K][4], int lane) {
+    uint32_t a[K][4], b[4];
+#pragma unroll
+    for (int k = 0; k < K; ++k) ldmatrix4(a[k], block16(v.t, row, mid + 16 * k, lane));
+    float x[2 * K][4] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int n = 0; n < K; ++n) {
+            ldmatrix4_trans(b, block16(v.L, mid + 16 * k, left + 16 * n, lane));
+            mma16(x[2 * n], a[k], b[0], b[1]);
+            mma16(x[2 * n + 1], a[k], b[2], b[3]);
+        }
+#pragma unroll
+    for (int n = 0; n < 2 * K; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[n][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t xa[4] = {pack_f16x2(-x[2 * k][0], -x[2 * k][1]), pack_f16x2(-x[2 * k][2], -x[2 * k][3]),
+                                pack_f16x2(-x[2 * k + 1][0], -x[2 * k + 1][1]),
+                                pack_f16x2(-x[2 * k + 1][2], -x[2 * k + 1][3])};
+#pragma unroll
+        for (int n = 0; n < K; ++n) {
+            ldmatrix4_trans(b, block16(v.t, left + 16 * k, left + 16 * n, lane));
+            mma16(out[2 * n], xa, b[0], b[1]);
+            mma16(out[2 * n + 1], xa, b[2], b[3]);
+        }
     }
-    return lo;
+}
+
+// T = (I + L)^-1 diag(b) of one head by a pair of warps (w = 0, 1 of the pair).  The diagonal blocks of
+// 16 by forward substitution in fp32, a column a thread; the blocks below them by products.
+__device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float *b, int w, int lane, int pair) {
+    const int d = 2 * w + (lane >> 4), c = lane & 15;  // diagonal block and its column
+    {
+        float x[16];
+        const float bc = b[16 * d + c];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float acc[2] = {r == c ? 1.0f : 0.0f, 0.0f};
+#pragma unroll
+            for (int m = 0; m < r; m += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(&v.diag[d][r * 20 + m]);
+                const float *lp = &l.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (m + e < r) acc[e & 1] = fmaf(-lp[e], x[m + e], acc[e & 1]);
+            }
+            x[r] = acc[0] + acc[1];
+            const int row = 16 * d + r, col = 16 * d + c;
+            v.t[row][col] = __float2half_rn(x[r]);
+            *reinterpret_cast<__half *>(T + swz128_offset(row, col)) = __float2half_rn(x[r] * bc);
+        }
+        // the block right of the first of the pair's two diagonal blocks
+        *reinterpret_cast<uint4 *>(&v.t[32 * w + c][32 * w + 16 + (lane >> 4) * 8]) = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    const int fr = lane >> 2, fc = (lane & 3) * 2;
+    auto put = [&](int row, int col, float v0, float v1) {
+        const float2 w2 = *reinterpret_cast<const float2 *>(b + col);
+        *reinterpret_cast<uint32_t *>(T + swz128_offset(row, col)) = pack_f16x2(v0 * w2.x, v1 * w2.y);
+    };
+    {
+        float o[2][4];
+        const int left = 32 * w, mid = left + 16;
+        lower_left<1>(v, mid, mid, left, o, lane);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = mid + fr + 8 * e, col = left + 8 * n + fc;
+                *reinterpret_cast<uint32_t *>(&v.t[row][col]) = pack_f16x2(o[n][2 * e], o[n][2 * e + 1]);
+                put(row, col, o[n][2 * e], o[n][2 * e + 1]);
+            }
+    }
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+    {
+        float o[4][4];
+        lower_left<2>(v, 32 + 16 * w, 32, 0, o, lane);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) put(32 + 16 * w + fr + 8 * e, 8 * n + fc, o[n][2 * e], o[n][2 * e + 1]);
+    }
 }
 
 // Block (chunk, group and share of its heads).
 template <int HEADS>
-__global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p, const WsLayout ws) {
+__global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p, const WsLayout ws) {
     extern __shared__ __align__(1024) unsigned char prep_smem[];
     PrepSmem<HEADS> &sm = *align1024<PrepSmem<HEADS>>(prep_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -123,24 +248,16 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
     const int chunk = blockIdx.x;
     if (p.meta[0] == 0 || chunk >= p.meta[1]) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int s = chunk_sequence(meta_chunks(p), p.nseq, chunk);
-    const int at = (chunk - meta_chunks(p)[s]) * C;
-    const int64_t t0 = (int64_t)p.cu[s] + at;
-    const int L = min(C, p.cu[s + 1] - p.cu[s] - at);
+    const int2 where = meta_table(p)[chunk];
+    const int64_t t0 = where.x;
+    const int L = where.y;
     const int shares = p.HG / HEADS;
     const int g = blockIdx.y / shares, h0 = g * p.HG + (blockIdx.y % shares) * HEADS;
-    if (warp == 0) {
-        tmem_alloc(&sm.tmem, 64);
-        tmem_relinquish();
-    }
-    if (tid == 0) {
-        mbar_init(&sm.bar, 1);
-        fence_mbar_init();
-    }
     // a token of a head a thread: its raw step and gate; no step and no write past the sequence's end
     float run = 0.0f, b = 0.0f;
-    if (tid < HEADS * C && (tid & (C - 1)) < L) {
-        const int64_t th = (t0 + (tid & (C - 1))) * p.H + h0 + tid / C;
+    const int hh = tid / C, tok = tid & (C - 1);
+    if (hh < HEADS && tok < L) {
+        const int64_t th = (t0 + tok) * p.H + h0 + hh;
         run = load_scalar(p.dt, th, p.gates.dt_bf16);
         b = load_scalar(p.beta, th, p.gates.dt_bf16);
     }
@@ -154,6 +271,18 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
             const bf16 *src = static_cast<const bf16 *>(i < 4 ? p.k : p.q) + ((t0 + row) * p.G + g) * TN + col;
             raw[i] = row < L ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
         }
+        if (warp == 0) {
+            tmem_alloc(&sm.tmem, 64);
+            tmem_relinquish();
+        }
+        if (tid == 0) {
+            mbar_init(&sm.bar, 1);
+            fence_mbar_init();
+        }
+#pragma unroll
+        for (int e = tid * 16; e < (int)kBlk; e += kPrepThreads * 16)  // T above its diagonal blocks
+#pragma unroll
+            for (int x = 0; x < HEADS; ++x) *reinterpret_cast<uint4 *>(sm.out[x] + e) = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float f[8];
@@ -162,7 +291,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
             ss = sum_lanes<16>(ss);
-            const float inv = ss > 0.0f ? 1.0f / sqrtf(ss) : 0.0f;
+            const float inv = ss > 0.0f ? rsqrtf(ss) : 0.0f;
             const int row = i * 16 + r0;  // of the stacked tile
             uint4 u;
             u.x = pack_f16x2(f[0] * inv, f[1] * inv);
@@ -170,17 +299,13 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
             u.z = pack_f16x2(f[4] * inv, f[5] * inv);
             u.w = pack_f16x2(f[6] * inv, f[7] * inv);
             *reinterpret_cast<uint4 *>(sm.kq + (col >> 6) * 2 * kBlk + swz128_chunk(row, (col & 63) >> 3)) = u;
-            if (col == 0) {
-                const float len = sqrtf(ss) * unit_factor(p.gates, ss);
-                if (i < 4) sm.nk[row] = len;
-                else sm.nq[row - C] = len * p.gates.scale;
-            }
+            if (col == 0) sm.ss[row] = ss;
         }
     }
     // running sums of the log decays (base 2) over each head's two warps of tokens
-    if (tid < HEADS * C) {
-        if ((tid & (C - 1)) < L) {
-            run = log_decay(p.gates, run, h0 + tid / C) * LOG2E;
+    if (hh < HEADS) {
+        if (tok < L) {
+            run = log_decay(p.gates, run, h0 + hh) * LOG2E;
             b = write_gate(p.gates, b);
         }
 #pragma unroll
@@ -188,19 +313,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
             const float v = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += v;
         }
-        if ((tid & (C - 1)) == 31) sm.half_sum[tid / C] = run;
-        sm.b[tid / C][tid & (C - 1)] = b;
+        if (tok == 31) sm.half_sum[hh] = run;
+        sm.dec[hh].b[tok] = b;
     }
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid < HEADS * C) {
-        if (warp & 1) run += sm.half_sum[tid / C];
-        sm.cum[tid / C][tid & (C - 1)] = run;
-    }
     const uint32_t tm = sm.tmem;
-    if (tid == 0) {
+    if (warp == 7 && elect_one()) {
         const uint32_t kq = smem_u32(sm.kq);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // rows 0..63: k_i . k_j, rows 64..127: q_i . k_j
@@ -212,7 +333,28 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
             bulk_wait_read<0>();  // the tile's memory is reused below
         }
     }
-    int bad = mbar_wait(&sm.bar, 0, kPolls) ? 0 : 1;
+    // The decay e^(c_i - c_j), j <= i, is a row factor times a column factor.  From the first half of the
+    // chunk to the second both are taken to the first half's last token, so both are at most 1; within a
+    // half to its first token, where the column's is at least 1 and is used only while the half spans at
+    // most 2^96 (wider ones form each decay from its own difference, below).
+    if (hh < HEADS) {
+        Decays &dec = sm.dec[hh];
+        if (tok >= 32) run += sm.half_sum[hh];
+        dec.cum[tok] = run;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + hh) : "memory");
+        const float kk = sm.ss[tok], qq = sm.ss[C + tok], last = dec.cum[C - 1], e = exp2f(run);
+        const float nk = sqrtf(kk) * unit_factor(p.gates, kk);
+        HeadGates &gt = sm.gates[hh];
+        gt.rk[tok] = e * nk;
+        gt.ek[tok] = exp2f(last - run) * nk;
+        gt.g[tok] = e;
+        gt.oq[tok] = sqrtf(qq) * unit_factor(p.gates, qq) * p.gates.scale;
+        if (tok == 0) gt.last = exp2f(last);
+        dec.near[tok] = exp2f(fminf(dec.cum[tok & 32] - run, kSpan)) * nk;
+        if (tok < 32) dec.far[tok] = exp2f(dec.cum[31] - run) * nk;
+        if (hh == 0) sm.nk[tok] = nk;
+    }
+    const int bad = mbar_wait(&sm.bar, 0, kPolls) ? 0 : 1;
     tc_fence_after();
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
@@ -223,31 +365,39 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
         const int q = warp & 3, hf = warp >> 2, i = (q & 1) * 32 + lane;  // row i of K K^T (q < 2) or Q K^T
         float dots[32];
         tmem_ld32(tm + ((uint32_t)(q * 32) << 16) + hf * 32, dots);
-        for (int hh = 0; hh < HEADS; ++hh) {
-            const float *cum = sm.cum[hh], *bb = sm.b[hh];
-            if (hh) __syncthreads();  // the last head's T and A have been copied out
-            if (tid < C) {
-                const float c = cum[tid], last = cum[C - 1], nk = sm.nk[tid], e = exp2f(c);
-                sm.gates.rk[tid] = e * nk;
-                sm.gates.ek[tid] = exp2f(last - c) * nk;
-                sm.gates.g[tid] = e;
-                sm.gates.oq[tid] = sm.nq[tid];
-                if (tid == 0) sm.gates.last = exp2f(last);
-            }
-            // L in fp32, A rounded to its tile; a block of columns past the rows is zero
-            const float ci = cum[i], wi = q < 2 ? bb[i] * sm.nk[i] : 1.0f;
-            const int edge = q < 2 ? i : i + 1;  // columns below it count
+        // L (what T needs of it) and A of this thread's 32 columns
+#pragma unroll 1
+        for (int x = 0; x < HEADS; ++x) {
+            const Decays &dec = sm.dec[x];
+            const float ci = dec.cum[i], wi = q < 2 ? dec.b[i] * sm.nk[i] : 1.0f;
             float w[32];
-            if (hf <= (q & 1)) {
+            if (hf < (q & 1)) {  // from the first half to the second
+                const float f = exp2f(ci - dec.cum[31]) * wi;
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    const float4 cj = *reinterpret_cast<const float4 *>(cum + hf * 32 + j);
-                    const float4 nj = *reinterpret_cast<const float4 *>(sm.nk + hf * 32 + j);
-                    const float *cp = &cj.x, *np = &nj.x;
+                    const float4 u = *reinterpret_cast<const float4 *>(dec.far + j);
+                    w[j] = dots[j] * (f * u.x);
+                    w[j + 1] = dots[j + 1] * (f * u.y);
+                    w[j + 2] = dots[j + 2] * (f * u.z);
+                    w[j + 3] = dots[j + 3] * (f * u.w);
+                }
+            } else if (hf == (q & 1)) {  // within a half
+                const int lim = q < 2 ? lane : lane + 1;  // columns below it count
+                if (dec.cum[hf * 32] - dec.cum[hf * 32 + 31] <= kSpan) {
+                    const float f = exp2f(ci - dec.cum[hf * 32]) * wi;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = dots[j + e] * wi * np[e] * exp2f(ci - cp[e]);
-                        w[j + e] = hf * 32 + j + e < edge ? v : 0.0f;
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(dec.near + hf * 32 + j);
+                        w[j] = j < lim ? dots[j] * (f * u.x) : 0.0f;
+                        w[j + 1] = j + 1 < lim ? dots[j + 1] * (f * u.y) : 0.0f;
+                        w[j + 2] = j + 2 < lim ? dots[j + 2] * (f * u.z) : 0.0f;
+                        w[j + 3] = j + 3 < lim ? dots[j + 3] * (f * u.w) : 0.0f;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float v = dots[j] * wi * sm.nk[hf * 32 + j] * exp2_approx(ci - dec.cum[hf * 32 + j]);
+                        w[j] = j < lim ? v : 0.0f;
                     }
                 }
             } else {
@@ -255,87 +405,47 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
                 for (int j = 0; j < 32; ++j) w[j] = 0.0f;
             }
             if (q < 2) {
+                if (hf <= (q & 1)) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4 *>(&sm.m.L[i][hf * 32 + j]) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                    for (int j = 0; j < 32; j += 8)
+                        *reinterpret_cast<uint4 *>(&sm.inv[x].L[i][hf * 32 + j]) =
+                            make_uint4(pack_f16x2(w[j], w[j + 1]), pack_f16x2(w[j + 2], w[j + 3]),
+                                       pack_f16x2(w[j + 4], w[j + 5]), pack_f16x2(w[j + 6], w[j + 7]));
+                }
+                if (hf == (q & 1)) {  // this row's part of its diagonal block of 16
+                    float *dst = &sm.inv[x].diag[i >> 4][(i & 15) * 20];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4 *>(dst + j) =
+                            make_float4(lane & 16 ? w[j + 16] : w[j], lane & 16 ? w[j + 17] : w[j + 1],
+                                        lane & 16 ? w[j + 18] : w[j + 2], lane & 16 ? w[j + 19] : w[j + 3]);
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; j += 8)
-                    *reinterpret_cast<uint4 *>(sm.out + kBlk + swz128_chunk(i, hf * 4 + j / 8)) =
+                    *reinterpret_cast<uint4 *>(sm.out[x] + kBlk + swz128_chunk(i, hf * 4 + j / 8)) =
                         make_uint4(pack_f16x2(w[j], w[j + 1]), pack_f16x2(w[j + 2], w[j + 3]), pack_f16x2(w[j + 4], w[j + 5]),
                                    pack_f16x2(w[j + 6], w[j + 7]));
             }
-            __syncthreads();
-            // (I + L)^-1 of the two diagonal 32 x 32 blocks, a column a thread, by forward substitution
-            if (warp < 2) {
-                float x[32];
-#pragma unroll
-                for (int r = 0; r < 32; ++r) {
-                    float acc[4] = {r == lane ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int m = 0; m < r; m += 4) {
-                        const float4 l = *reinterpret_cast<const float4 *>(&sm.m.L[warp * 32 + r][warp * 32 + m]);
-                        const float *lp = &l.x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (m + e < r) acc[e] = fmaf(-lp[e], x[m + e], acc[e]);
-                    }
-                    x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                    sm.m.t[warp][r][lane] = x[r];
-                }
-            }
-            __syncthreads();
-            // lower left block: -T22 (L21 T11), four columns a thread
-            const int mi = tid >> 3, mc = (tid & 7) * 4;
-            {
-                float acc[4] = {};
-#pragma unroll
-                for (int m = 0; m < 32; ++m) {
-                    const float l = sm.m.L[32 + mi][m];
-                    const float4 t = *reinterpret_cast<const float4 *>(&sm.m.t[0][m][mc]);
-                    acc[0] = fmaf(l, t.x, acc[0]);
-                    acc[1] = fmaf(l, t.y, acc[1]);
-                    acc[2] = fmaf(l, t.z, acc[2]);
-                    acc[3] = fmaf(l, t.w, acc[3]);
-                }
-                *reinterpret_cast<float4 *>(&sm.m.L[mi][mc]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            }
-            __syncthreads();
-            {
-                float acc[4] = {};
-#pragma unroll
-                for (int m = 0; m < 32; ++m) {
-                    const float l = sm.m.t[1][mi][m];
-                    const float4 t = *reinterpret_cast<const float4 *>(&sm.m.L[m][mc]);
-                    acc[0] = fmaf(l, t.x, acc[0]);
-                    acc[1] = fmaf(l, t.y, acc[1]);
-                    acc[2] = fmaf(l, t.z, acc[2]);
-                    acc[3] = fmaf(l, t.w, acc[3]);
-                }
-                // T diag(b), rounded: this thread's four columns of the lower left block and of the others
-                auto put = [&](int row, int c, float v0, float v1, float v2, float v3) {
-                    const float4 w = *reinterpret_cast<const float4 *>(bb + c);
-                    const uint2 u = make_uint2(pack_f16x2(v0 * w.x, v1 * w.y), pack_f16x2(v2 * w.z, v3 * w.w));
-                    *reinterpret_cast<uint2 *>(sm.out + swz128_offset(row, c)) = u;
-                };
-                put(32 + mi, mc, -acc[0], -acc[1], -acc[2], -acc[3]);
-                const float4 a = *reinterpret_cast<const float4 *>(&sm.m.t[0][mi][mc]);
-                const float4 d = *reinterpret_cast<const float4 *>(&sm.m.t[1][mi][mc]);
-                put(mi, mc, a.x, a.y, a.z, a.w);
-                put(mi, 32 + mc, 0.0f, 0.0f, 0.0f, 0.0f);
-                put(32 + mi, 32 + mc, d.x, d.y, d.z, d.w);
-            }
-            fence_async_smem();
-            __syncthreads();
-            if (tid == 0) {
-                unsigned char *dst = ws.head(chunk, h0 + hh);
-                bulk_s2g(dst, sm.out, 2 * kBlk);
-                bulk_s2g(dst + 2 * kBlk, &sm.gates, kGateBytes);
-                bulk_commit();
-                bulk_wait_read<0>();
-            }
         }
-        if (tid == 0) bulk_wait_all();
+        __syncthreads();
+        if (warp < 2 * HEADS) {
+            const int x = warp >> 1;
+            invert(sm.inv[x], sm.out[x], sm.dec[x].b, warp & 1, lane, x);
+        }
+        fence_async_smem();
+        __syncthreads();
+        if (warp == 0 && elect_one()) {
+#pragma unroll
+            for (int x = 0; x < HEADS; ++x) {
+                unsigned char *dst = ws.head(chunk, h0 + x);
+                bulk_s2g(dst, sm.out[x], 2 * kBlk);
+                bulk_s2g(dst + 2 * kBlk, &sm.gates[x], kGateBytes);
+            }
+            bulk_commit();
+            bulk_wait_all();
+        }
+        if (warp == 7 && elect_one()) bulk_wait_all();
     }
     tc_fence_before();
     __syncthreads();
@@ -408,7 +518,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     bf16 *pool = static_cast<bf16 *>(p.pool);
     const int64_t off = ((int64_t)h * TP + row) * TN + hf * 64;
 
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
         for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], 1);
         fence_mbar_init();
         tma_prefetch_desc(&vmap);
@@ -443,12 +553,12 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     const uint32_t tm = sm.tmem, lanes = tm + ((uint32_t)(q * 32) << 16);
     bool failed = false;
     uint32_t x_phase = 0;
-    uint32_t armed = 0, parity = 0;  // thread 0: the barriers with something in flight, ever, and its phase
+    uint32_t armed = 0, parity = 0;  // of the issuing thread: the barriers with something in flight, ever, and its phase
     auto arm = [&](int i, uint32_t phase) {
         armed |= 1u << i;
         parity = (parity & ~(1u << i)) | phase << i;
     };
-    if (tid == 0) arm(B_KQ, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
+    arm(B_KQ, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
 
     auto store_state16 = [&] {  // the state's copy for the products; the pair's columns are consumed
 #pragma unroll
@@ -503,7 +613,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         const bool fresh = c % kRescale == 0;  // this chunk starts from a new power of two
         // 1. X = S K^T, while the next stage's loads start and the last chunk's outputs are written
         if (!mbar_wait(&sm.bar[B_KQ + ph], (c >> 1) & 1, kPolls)) bad = 1;
-        if (tid == 0 && !bad) {
+        if (warp == 0 && elect_one() && !bad) {
             tc_fence_after();
             if (!fresh) issue_x(c);
             if (c > 0 && !mbar_wait(&sm.bar[B_Y], ph ^ 1, kPolls)) bad = 1;
@@ -587,7 +697,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
                 break;
             }
             tc_fence_after();
-            if (tid == 0) issue_x(c);
+            if (warp == 0 && elect_one()) issue_x(c);
         }
         // 3. R = V - e^c |k| X, rounded, over X; then U^T = R^T T^T and the state's part of Y
         if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
@@ -615,7 +725,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             break;
         }
         tc_fence_after();
-        if (tid == 0) {
+        if (warp == 0 && elect_one()) {
             const uint32_t T = smem_u32(sm.T), qq = smem_u32(sm.q[ph]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -659,7 +769,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             break;
         }
         tc_fence_after();
-        if (tid == 0) {
+        if (warp == 0 && elect_one()) {
             const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -712,7 +822,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
         // the same bounded time to finish before its memory is released
-        if (tid == 0) {
+        if (warp == 0 && elect_one()) {
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
             for (int i = 0; i < kBars; ++i)
                 if (armed >> i & 1) mbar_wait(&sm.bar[i], parity >> i & 1, kPolls);
