@@ -457,18 +457,19 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
 // the chain over a sequence's chunks
 // ---------------------------------------------------------------------------------------
 
-constexpr int kChainThreads = 256;
+constexpr int kChainThreads = 512;
 constexpr int kRescale = 16;  // chunks between two choices of the rows' powers of two
 
-// What the block waits for: a stage (two), T, A, the values; the products X, U, Q S^T, the increment
-// and Y.
-enum { B_KQ = 0, B_T = 2, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, kBars };
+// What the block waits for: keys with gates (two stages), queries, T, A, the values; the products X, U,
+// Q S^T, the increment and Y.
+enum { B_K = 0, B_Q = 2, B_T, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, kBars };
 
 struct ChainSmem {
-    unsigned char k[2][2 * kBlk], q[2][2 * kBlk], T[kBlk], A[kBlk];
-    bf16 v[C][TP];
+    // q: a chunk's queries, and once they are used its outputs on their way to memory; v: values, 64 of
+    // them in a swizzled block of 64 tokens
+    unsigned char k[2][2 * kBlk], q[2][2 * kBlk], T[kBlk], A[kBlk], v[2 * kBlk];
     HeadGates gates[4];
-    float row_max[2][TP];
+    float row_max[4][TP];
     uint64_t bar[kBars];
     uint32_t tmem;
 };
@@ -477,30 +478,67 @@ struct ChainSmem {
 // increment, which is as wide as both.
 constexpr uint32_t T_S = 0, T_X = 64, T_D = 0, T_U = 128, T_Y = 192;
 
-// The stage (keys, queries, gates) of chunk c of the sequence; completes on barrier B_KQ + (c & 1).
-__device__ __forceinline__ void load_stage(ChainSmem &sm, const WsLayout &ws, int first, int c, int g, int h) {
-    uint64_t *bar = &sm.bar[B_KQ + (c & 1)];
-    mbar_arrive_expect_tx(bar, kKqBytes + kGateBytes);
+// The accumulators' 32 lanes of a warp as matrix fragments: two loads of 16 lanes each, 8 NC fp32
+// columns; element [half][4 n + 2 r + e] is lane 16 half + 8 r + T / 4, column 8 n + 2 (T % 4) + e.
+__device__ __forceinline__ void tmem_frag2(uint32_t a, float (&v)[2][8]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a), "r"(a + (16u << 16))
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __uint_as_float(r[i]);
+}
+// Their 16-bit counterpart: element [half][2 n + r] holds columns 8 n + 2 (T % 4) and the next.
+__device__ __forceinline__ void tmem_put2(uint32_t a, const uint32_t (&v)[2][4]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%2,%3,%4,%5};\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x2.b32 [%1], {%6,%7,%8,%9};\n\t" ::"r"(a),
+        "r"(a + (16u << 16)), "r"(v[0][0]), "r"(v[0][1]), "r"(v[0][2]), "r"(v[0][3]), "r"(v[1][0]), "r"(v[1][1]),
+        "r"(v[1][2]), "r"(v[1][3])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+// Keys and gates of chunk c of the sequence.
+__device__ __forceinline__ void load_keys(ChainSmem &sm, const WsLayout &ws, int first, int c, int g, int h) {
+    uint64_t *bar = &sm.bar[B_K + (c & 1)];
+    mbar_arrive_expect_tx(bar, 2 * kBlk + kGateBytes);
     const unsigned char *kq = ws.kq(first + c, g);
     bulk_g2s(sm.k[c & 1], kq, kBlk, bar);
-    bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, bar);
     bulk_g2s(sm.k[c & 1] + kBlk, kq + 2 * kBlk, kBlk, bar);
-    bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, bar);
     bulk_g2s(&sm.gates[c & 3], ws.head(first + c, h) + 2 * kBlk, kGateBytes, bar);
+}
+__device__ __forceinline__ void load_queries(ChainSmem &sm, const WsLayout &ws, int first, int c, int g) {
+    mbar_arrive_expect_tx(&sm.bar[B_Q], 2 * kBlk);
+    const unsigned char *kq = ws.kq(first + c, g);
+    bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, &sm.bar[B_Q]);
+    bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, &sm.bar[B_Q]);
 }
 __device__ __forceinline__ void load_tile(void *dst, const unsigned char *src, uint64_t *bar) {
     mbar_arrive_expect_tx(bar, kBlk);
     bulk_g2s(dst, src, kBlk, bar);
 }
 __device__ __forceinline__ void load_values(ChainSmem &sm, const CUtensorMap *map, int h, int t) {
-    mbar_arrive_expect_tx(&sm.bar[B_V], sizeof(sm.v));
+    mbar_arrive_expect_tx(&sm.bar[B_V], 2 * kBlk);
     tma_load_2d(sm.v, map, h * TP, t, &sm.bar[B_V]);
+    tma_load_2d(sm.v + kBlk, map, h * TP + 64, t, &sm.bar[B_V]);
 }
 
-__device__ __forceinline__ void pair_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(q + 1) : "memory"); }
-
-// Block (sequence in the plan's order, head).  Warp w works on tensor-memory lanes 32 (w % 4) .. + 31,
-// the value indices, and on half w / 4 of the columns: of the tokens, or of the state's.
+// Block (sequence in the plan's order, head) of 16 warps.  Warp w works on tensor-memory lanes
+// 32 (w % 4) .. + 31, the value indices, and on quarter w / 4 of the columns: 16 tokens, or 32 of the
+// state's.  A thread holds its rows 8 i + T / 4 and columns 8 n + 2 (T % 4) + {0, 1} as fragments, which
+// is how ldmatrix and stmatrix turn values and outputs between (token, value) and (value, token).
 __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,
                                                                 const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char chain_smem[];
@@ -512,41 +550,45 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     const int t0 = p.cu[s], len = p.cu[s + 1] - t0, first = meta_chunks(p)[s];
     const int32_t slot = p.slot[s];
     if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, hf = warp >> 2;
-    const int row = q * 32 + lane;  // value index
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, Q = warp >> 2;
+    const int fr = lane >> 2, fc = (lane & 3) * 2;
     const int nc = (len + C - 1) / C;
     bf16 *pool = static_cast<bf16 *>(p.pool);
-    const int64_t off = ((int64_t)h * TP + row) * TN + hf * 64;
+    const int64_t off = ((int64_t)h * TP + 32 * q + fr) * TN + 32 * Q + fc;  // of this thread's first state element
 
     if (warp == 0 && elect_one()) {
         for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], 1);
         fence_mbar_init();
         tma_prefetch_desc(&vmap);
-        load_stage(sm, ws, first, 0, g, h);
+        load_keys(sm, ws, first, 0, g, h);
+        load_values(sm, &vmap, h, t0);
+        load_queries(sm, ws, first, 0, g);
         load_tile(sm.T, ws.head(first, h), &sm.bar[B_T]);
         load_tile(sm.A, ws.head(first, h) + kBlk, &sm.bar[B_A]);
-        load_values(sm, &vmap, h, t0);
     }
     if (warp == 0) {
         tmem_alloc(&sm.tmem, 256);
         tmem_relinquish();
     }
-    // this thread's half row of the state, times the row's power of two
-    float S[64];
+    // this thread's part of the state, each row times its power of two: S[i / 2][4 n + 2 (i % 2) + e]
+    float S[2][16];
     if (slot >= 0 && p.has_init && p.has_init[s]) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {
-            float f[8];
-            load8_stream(pool + slot * p.stride + off + e, f);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) S[e + i] = f[i];
-        }
+            for (int n = 0; n < 4; ++n) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(pool + slot * p.stride + off + i * 8 * TN + 8 * n);
+                S[i >> 1][4 * n + 2 * (i & 1)] = __uint_as_float(w << 16);
+                S[i >> 1][4 * n + 2 * (i & 1) + 1] = __uint_as_float(w & 0xffff0000u);
+            }
     } else {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) S[e] = 0.0f;
+        for (int n = 0; n < 32; ++n) S[n >> 4][n & 15] = 0.0f;
     }
-    float sigma = 1.0f, inv_sigma = 1.0f;
-    uint32_t limit = 0;  // largest bf16 magnitude (as bits) that fits the row's power of two
+    // row i's power of two, 2^(128 - E_i), by the byte E_i: its inverse 2^(E_i - 128)
+    uint32_t powers = 0x80808080u;
+    auto scale_of = [&](int i) { return __uint_as_float((255u - (powers >> (8 * i) & 0xffu)) << 23); };
+    auto unscale_of = [&](int i) { return __uint_as_float(((powers >> (8 * i) & 0xffu) - 1u) << 23); };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -558,16 +600,18 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         armed |= 1u << i;
         parity = (parity & ~(1u << i)) | phase << i;
     };
-    arm(B_KQ, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
+    arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
 
-    auto store_state16 = [&] {  // the state's copy for the products; the pair's columns are consumed
+    auto store_state16 = [&] {  // the state's copy for the products; the lanes' increment is consumed
 #pragma unroll
-        for (int e = 0; e < 64; e += 32) {
-            uint32_t pk[16];
+        for (int n = 0; n < 2; ++n) {
+            uint32_t pk[2][4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(S[e + 2 * i], S[e + 2 * i + 1]);
-            tmem_st16(lanes + T_S + hf * 32 + e / 2, pk);
+            for (int i = 0; i < 8; ++i)
+                pk[i >> 2][i & 3] = pack_f16x2(S[i >> 2][8 * n + 2 * (i & 3)], S[i >> 2][8 * n + 2 * (i & 3) + 1]);
+            tmem_put2(lanes + T_S + Q * 16 + n * 8, pk);
         }
+        tmem_put_wait();
     };
     auto issue_x = [&](int c) {  // X = S K^T
         const uint32_t k = smem_u32(sm.k[c & 1]);
@@ -577,32 +621,50 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         mma_commit(&sm.bar[B_X]);
         arm(B_X, x_phase);
     };
-    // outputs of chunk c: lane = value index, 32 tokens a thread
-    auto write_outputs = [&](int c) {
-        float y[32];
-        tmem_ld32(lanes + T_Y + hf * 32, y);
-        const int L = min(C, len - c * C) - hf * 32;
-        const float4 *oq = reinterpret_cast<const float4 *>(sm.gates[c & 3].oq + hf * 32);
-        bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(t0 + c * C + hf * 32) * p.H + h) * TP + row;
+    // this lane's row of 16 bytes (8 values of a token) in a swizzled tile of tokens, for the fragments of
+    // 8 tokens from 16 Q + 8 n and this warp's 32 values
+    auto value_row = [&](const unsigned char *tile, int n) {
+        return smem_u32(tile) + (q >> 1) * kBlk + swz128_chunk(16 * Q + 8 * n + (lane & 7), 4 * (q & 1) + (lane >> 3));
+    };
+    // outputs of chunk c into its queries' place
+    auto stage_outputs = [&](int c) {
+        float y[2][8];
+        tmem_frag2(lanes + T_Y + Q * 16, y);
+        const float *oq = sm.gates[c & 3].oq + 16 * Q + fc;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 w = oq[j / 4];
-            const float *wp = &w.x;
+        for (int n = 0; n < 2; ++n) {
+            const float2 w = *reinterpret_cast<const float2 *>(oq + 8 * n);
+            uint32_t pk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bf16 v = __float2bfloat16_rn(y[j + e] * (wp[e] * inv_sigma));
-                if (j + e < L) *dst = v;
-                dst += (int64_t)p.H * TP;
+            for (int i = 0; i < 4; ++i) {
+                const float u = unscale_of(i);
+                const __nv_bfloat162 v = __floats2bfloat162_rn(y[i >> 1][4 * n + 2 * (i & 1)] * (w.x * u),
+                                                               y[i >> 1][4 * n + 2 * (i & 1) + 1] * (w.y * u));
+                pk[i] = *reinterpret_cast<const uint32_t *>(&v);
             }
+            stmatrix4_trans(value_row(sm.q[c & 1], n), pk[0], pk[1], pk[2], pk[3]);
+        }
+    };
+    auto write_outputs = [&](int c) {  // from there to memory, 16 bytes a thread
+        const int L = min(C, len - c * C);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = (tid >> 4) + 32 * i, ch = tid & 15;
+            if (t < L)
+                *reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + ((int64_t)(t0 + c * C + t) * p.H + h) * TP + ch * 8) =
+                    *reinterpret_cast<const uint4 *>(sm.q[c & 1] + (ch >> 3) * kBlk + swz128_chunk(t, ch & 7));
         }
     };
     auto write_state = [&](int32_t to) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 8) {
-            float f[8];
+        for (int i = 0; i < 4; ++i) {
+            const float u = unscale_of(i);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = S[e + i] * inv_sigma;
-            store8_stream(pool + to * p.stride + off + e, f);
+            for (int n = 0; n < 4; ++n) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(S[i >> 1][4 * n + 2 * (i & 1)] * u,
+                                                               S[i >> 1][4 * n + 2 * (i & 1) + 1] * u);
+                *reinterpret_cast<__nv_bfloat162 *>(pool + to * p.stride + off + i * 8 * TN + 8 * n) = v;
+            }
         }
     };
 
@@ -610,33 +672,31 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         const uint32_t ph = c & 1;
         const int L = min(C, len - c * C);
         int bad = 0;
-        const bool fresh = c % kRescale == 0;  // this chunk starts from a new power of two
-        // 1. X = S K^T, while the next stage's loads start and the last chunk's outputs are written
-        if (!mbar_wait(&sm.bar[B_KQ + ph], (c >> 1) & 1, kPolls)) bad = 1;
+        const bool fresh = c % kRescale == 0;  // this chunk starts from new powers of two
+        const HeadGates &gt = sm.gates[c & 3];
+        // 1. X = S K^T, while the last chunk's outputs leave tensor memory
+        if (!mbar_wait(&sm.bar[B_K + ph], (c >> 1) & 1, kPolls)) bad = 1;
         if (warp == 0 && elect_one() && !bad) {
             tc_fence_after();
             if (!fresh) issue_x(c);
-            if (c > 0 && !mbar_wait(&sm.bar[B_Y], ph ^ 1, kPolls)) bad = 1;
-            if (!bad) {
-                if (c > 0) {
-                    load_tile(sm.A, ws.head(first + c, h) + kBlk, &sm.bar[B_A]);
-                    arm(B_A, ph);
-                }
-                if (c + 1 < nc) {
-                    load_stage(sm, ws, first, c + 1, g, h);
-                    arm(B_KQ + (ph ^ 1), ((c + 1) >> 1) & 1);
-                }
+            if (c + 1 < nc) {
+                load_keys(sm, ws, first, c + 1, g, h);
+                arm(B_K + (ph ^ 1), ((c + 1) >> 1) & 1);
             }
         }
         if (c > 0) {
             if (!mbar_wait(&sm.bar[B_Y], ph ^ 1, kPolls)) bad = 1;
             tc_fence_after();
-            if (!bad) write_outputs(c - 1);
+            if (warp == 0 && elect_one() && !bad) {
+                load_tile(sm.A, ws.head(first + c, h) + kBlk, &sm.bar[B_A]);
+                arm(B_A, ph);
+            }
+            stage_outputs(c - 1);
         }
-        // 2. queries times e^c in place; this thread's 32 values of its row
-        const HeadGates &gt = sm.gates[c & 3];
+        // 2. queries times e^c in place; this thread's values
+        if (!mbar_wait(&sm.bar[B_Q], ph, kPolls)) bad = 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int cidx = tid + kChainThreads * i;  // 16-byte chunk of the tile: row of 128 bytes = token
             uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[ph] + cidx * 16);
             const __half2 w = __float2half2_rn(gt.g[(cidx >> 3) & (C - 1)]);
@@ -648,48 +708,60 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         }
         fence_async_smem();
         if (!mbar_wait(&sm.bar[B_V], ph, kPolls)) bad = 1;
-        uint32_t vals[16];
-        uint32_t vmax = 0;
+        uint32_t vals[2][4];  // [n][i]: two tokens of row i
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int t = hf * 32 + 2 * j;
-            vals[j] = __bfloat16_as_ushort(sm.v[t][row]) | (uint32_t)__bfloat16_as_ushort(sm.v[t + 1][row]) << 16;
-        }
+        for (int n = 0; n < 2; ++n) ldmatrix4_trans(vals[n], value_row(sm.v, n));
         if (L < C) {  // rows past the sequence's end hold another sequence's values
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int t = hf * 32 + 2 * j;
-                vals[j] = t + 1 < L ? vals[j] : (t < L ? vals[j] & 0xffffu : 0u);
+            for (int n = 0; n < 2; ++n) {
+                const int t = 16 * Q + 8 * n + fc;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vals[n][i] = t + 1 < L ? vals[n][i] : (t < L ? vals[n][i] & 0xffffu : 0u);
             }
         }
+        uint32_t vmax[4], over = 0;  // largest magnitudes as bf16 bits; whether one outgrew 2^4 units of its row
 #pragma unroll
-        for (int j = 0; j < 16; ++j) vmax = __vmaxu2(vmax, vals[j] & 0x7fff7fffu);
-        vmax = max(vmax & 0xffffu, vmax >> 16);
-        // a value outgrew its row's power of two, or it is time to choose anew (a wait that gave up goes
-        // the same way and ends the block below)
-        if (__syncthreads_or(bad || vmax > limit) || fresh) {
-            if (!fresh) {  // X of the old power is not used
+        for (int i = 0; i < 4; ++i) {
+            vmax[i] = __vmaxu2(vals[0][i] & 0x7fff7fffu, vals[1][i] & 0x7fff7fffu);
+            const uint32_t lim = ((powers >> (8 * i) & 0xffu) + 3u) << 7;
+            over |= __vcmpgtu2(vmax[i], lim | lim << 16);
+        }
+        // (a wait that gave up goes the same way and ends the block below)
+        if (__syncthreads_or(bad || over) || fresh) {
+            if (!fresh) {  // X of the old powers is not used
                 if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
                 x_phase ^= 1;
             }
-            // the largest magnitude in the row of the state (unscaled) and of the values
-            float top = __uint_as_float(vmax << 16);
+            // the largest magnitude in each row of the state (unscaled) and of the values
 #pragma unroll
-            for (int e = 0; e < 64; ++e) top = fmaxf(top, fabsf(S[e]) * inv_sigma);
-            sm.row_max[hf][row] = top;
+            for (int i = 0; i < 4; ++i) {
+                float top = __uint_as_float(max(vmax[i] & 0xffffu, vmax[i] >> 16) << 16);
+                const float u = unscale_of(i);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    top = fmaxf(top, u * fmaxf(fabsf(S[i >> 1][4 * n + 2 * (i & 1)]), fabsf(S[i >> 1][4 * n + 2 * (i & 1) + 1])));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (fc == 0) sm.row_max[Q][32 * q + 8 * i + fr] = top;
+            }
             __syncthreads();
-            top = fmaxf(sm.row_max[0][row], sm.row_max[1][row]);
-            // power of two that brings the largest to [2, 4); values may grow to 16 before the next choice
-            int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            ex = max(-120, min(120, ex));
-            if (!(top < INFINITY)) ex = 0;
-            const float next = __uint_as_float((uint32_t)(127 + 1 - ex) << 23);
-            const float ratio = next * inv_sigma;
+            uint32_t next = 0;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) S[e] *= ratio;
-            sigma = next;
-            inv_sigma = __uint_as_float((uint32_t)(127 - 1 + ex) << 23);
-            limit = top < INFINITY ? (uint32_t)(127 + ex + 3) << 7 : 0xffffu;
+            for (int i = 0; i < 4; ++i) {
+                const int row = 32 * q + 8 * i + fr;
+                const float top = fmaxf(fmaxf(sm.row_max[0][row], sm.row_max[1][row]), fmaxf(sm.row_max[2][row], sm.row_max[3][row]));
+                // the power that brings the largest to [2, 4); values may grow to 16 before the next choice
+                int E = (int)(__float_as_uint(top) >> 23);
+                E = top < INFINITY ? max(7, min(247, E)) : 127;
+                next |= (uint32_t)E << (8 * i);
+                const float ratio = __uint_as_float((255u - E) << 23) * unscale_of(i);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    S[i >> 1][4 * n + 2 * (i & 1)] *= ratio;
+                    S[i >> 1][4 * n + 2 * (i & 1) + 1] *= ratio;
+                }
+            }
+            powers = next;
             store_state16();
             tc_fence_before();
             if (__syncthreads_or(bad)) {
@@ -704,19 +776,22 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         x_phase ^= 1;
         tc_fence_after();
         {
-            float x[32];
-            tmem_ld32(lanes + T_X + hf * 32, x);
-            uint32_t pk[16];
-            const float4 *rk = reinterpret_cast<const float4 *>(gt.rk + hf * 32);
+            float x[2][8];
+            tmem_frag2(lanes + T_X + Q * 16, x);
+            uint32_t pk[2][4];
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {  // (past the end the values, the keys and so X are zero)
-                const float4 w = rk[j / 2];
-                pk[j] = pack_f16x2(fmaf(-w.x, x[2 * j], __uint_as_float(vals[j] << 16) * sigma),
-                                   fmaf(-w.y, x[2 * j + 1], __uint_as_float(vals[j] & 0xffff0000u) * sigma));
-                pk[j + 1] = pack_f16x2(fmaf(-w.z, x[2 * j + 2], __uint_as_float(vals[j + 1] << 16) * sigma),
-                                       fmaf(-w.w, x[2 * j + 3], __uint_as_float(vals[j + 1] & 0xffff0000u) * sigma));
+            for (int n = 0; n < 2; ++n) {
+                const float2 w = *reinterpret_cast<const float2 *>(gt.rk + 16 * Q + 8 * n + fc);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // (past the end the values, the keys and so X are zero)
+                    const float sc = scale_of(i);
+                    const float *xi = &x[i >> 1][4 * n + 2 * (i & 1)];
+                    pk[i >> 1][2 * n + (i & 1)] = pack_f16x2(fmaf(-w.x, xi[0], __uint_as_float(vals[n][i] << 16) * sc),
+                                                             fmaf(-w.y, xi[1], __uint_as_float(vals[n][i] & 0xffff0000u) * sc));
+                }
             }
-            tmem_st16(lanes + T_X + hf * 32, pk);
+            tmem_put2(lanes + T_X + Q * 16, pk);
+            tmem_put_wait();
         }
         if (!mbar_wait(&sm.bar[B_T], ph, kPolls)) bad = 1;
         tc_fence_before();
@@ -729,8 +804,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             const uint32_t T = smem_u32(sm.T), qq = smem_u32(sm.q[ph]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(tm + T_U, tm + T_X + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(T, kBlk, kk),
-                            idesc_f16(128, C, false), kk > 0);
+                mma_bf16_ts(tm + T_U, tm + T_X + kk * 16, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
             mma_commit(&sm.bar[B_U]);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
@@ -742,24 +816,27 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
                 arm(B_V, ph ^ 1);
             }
         }
+        if (c > 0) write_outputs(c - 1);
         // 4. U^T rounded, as it is and times e^(c_64 - c) |k|; then the state's increment and A's part of Y
         if (!mbar_wait(&sm.bar[B_U], ph, kPolls)) bad = 1;
         tc_fence_after();
         {
-            float u[32];
-            tmem_ld32(lanes + T_U + hf * 32, u);
-            uint32_t pk[16];
+            float u[2][8];
+            tmem_frag2(lanes + T_U + Q * 16, u);
+            uint32_t pk[2][4], pe[2][4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = pack_f16x2(u[2 * j], u[2 * j + 1]);
-            tmem_st16(lanes + T_U + hf * 32, pk);
-            const float4 *ek = reinterpret_cast<const float4 *>(gt.ek + hf * 32);
+            for (int n = 0; n < 2; ++n) {
+                const float2 w = *reinterpret_cast<const float2 *>(gt.ek + 16 * Q + 8 * n + fc);
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                const float4 w = ek[j / 2];
-                pk[j] = pack_f16x2(u[2 * j] * w.x, u[2 * j + 1] * w.y);
-                pk[j + 1] = pack_f16x2(u[2 * j + 2] * w.z, u[2 * j + 3] * w.w);
+                for (int i = 0; i < 4; ++i) {
+                    const float *ui = &u[i >> 1][4 * n + 2 * (i & 1)];
+                    pk[i >> 1][2 * n + (i & 1)] = pack_f16x2(ui[0], ui[1]);
+                    pe[i >> 1][2 * n + (i & 1)] = pack_f16x2(ui[0] * w.x, ui[1] * w.y);
+                }
             }
-            tmem_st16(lanes + T_U + hf * 32 + 16, pk);
+            tmem_put2(lanes + T_U + Q * 16, pk);
+            tmem_put2(lanes + T_U + Q * 16 + 8, pe);
+            tmem_put_wait();
         }
         if (!mbar_wait(&sm.bar[B_OI], ph, kPolls)) bad = 1;  // the state's copy is read: its columns are free
         if (!mbar_wait(&sm.bar[B_A], ph, kPolls)) bad = 1;
@@ -773,18 +850,17 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(tm + T_D, tm + T_U + (kk >> 1) * 32 + 16 + (kk & 1) * 8, desc_mnmajor(k, kBlk, kk),
-                            idesc_f16(128, TN, true), kk > 0);
+                mma_bf16_ts(tm + T_D, tm + T_U + kk * 16 + 8, desc_mnmajor(k, kBlk, kk), idesc_f16(128, TN, true), kk > 0);
             mma_commit(&sm.bar[B_S]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(tm + T_Y, tm + T_U + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(A, kBlk, kk),
-                            idesc_f16(128, C, false), 1);
+                mma_bf16_ts(tm + T_Y, tm + T_U + kk * 16, desc_kmajor(A, kBlk, kk), idesc_f16(128, C, false), 1);
             mma_commit(&sm.bar[B_Y]);
             arm(B_S, ph), arm(B_Y, ph);
             if (c + 1 < nc) {
+                load_queries(sm, ws, first, c + 1, g);
                 load_tile(sm.T, ws.head(first + c + 1, h), &sm.bar[B_T]);
-                arm(B_T, ph ^ 1);
+                arm(B_Q, ph ^ 1), arm(B_T, ph ^ 1);
             }
         }
         // 5. the new state, and its copy
@@ -792,17 +868,17 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         tc_fence_after();
         const float last = gt.last;
 #pragma unroll
-        for (int e = 0; e < 64; e += 32) {
-            float d[32];
-            tmem_ld32(lanes + T_D + hf * 64 + e, d);
+        for (int n = 0; n < 2; ++n) {
+            float d[2][8];
+            tmem_frag2(lanes + T_D + Q * 32 + n * 16, d);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[e + i] = fmaf(last, S[e + i], d[i]);
+            for (int i = 0; i < 16; ++i) S[i >> 3][8 * n + (i & 7)] = fmaf(last, S[i >> 3][8 * n + (i & 7)], d[i >> 3][i & 7]);
         }
         const int32_t cs = ckpt_slot(p, s, c * C + L, tid == 0 && h == 0);
         if (cs >= 0) write_state(cs);
         if (c + 1 < nc && (c + 1) % kRescale != 0) {
             tc_fence_before();
-            pair_sync(q);  // both halves of the row have read the increment
+            asm volatile("bar.sync %0, 128;" ::"r"(q + 1) : "memory");  // these lanes' increment has been read
             tc_fence_after();
             store_state16();
         }
@@ -817,7 +893,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         if (slot >= 0) write_state(slot);
         failed = !mbar_wait(&sm.bar[B_Y], (nc - 1) & 1, kPolls);
         tc_fence_after();
-        if (!failed) write_outputs(nc - 1);
+        stage_outputs(nc - 1);
     }
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
@@ -827,6 +903,8 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             for (int i = 0; i < kBars; ++i)
                 if (armed >> i & 1) mbar_wait(&sm.bar[i], parity >> i & 1, kPolls);
         }
+    } else {
+        write_outputs(nc - 1);
     }
     tc_fence_before();
     __syncthreads();
@@ -851,14 +929,15 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Rows of tokens x (heads * 128) values, in boxes of 64 tokens x 128 values; rows past the end read as zero.
+// Rows of tokens x (heads * 128) values, in swizzled boxes of 64 tokens x 64 values; rows past the end
+// read as zero.
 bool value_map(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
-    cuuint32_t box[2] = {TP, C}, es[2] = {1, 1};
+    cuuint32_t box[2] = {64, C}, es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
