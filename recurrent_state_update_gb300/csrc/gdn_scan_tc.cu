@@ -457,88 +457,475 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
 // the chain over a sequence's chunks
 // ---------------------------------------------------------------------------------------
 
-constexpr int kChainThreads = 512;
-constexpr int kRescale = 16;  // chunks between two choices of the rows' powers of two
+constexpr int kChainThreads = 256;       // four warps on the chain, four beside it
+constexpr int kChainRegs = 200, kSideRegs = 56;  // (200 + 56) * 128 registers: what the block is launched with
+constexpr int kRescale = 16;             // chunks between two choices of the rows' powers of two
 
-// What the block waits for: keys with gates (two stages), queries, T, A, the values; the products X, U,
-// Q S^T, the increment and Y.
-enum { B_K = 0, B_Q = 2, B_T, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, kBars };
+// What the block waits for: a stage of keys, queries and gates (two), T, A and the values from memory;
+// the products X, U, Q S^T, the increment and Y; the values turned and the queries scaled, the values
+// taken, Y taken.
+enum { B_KQ = 0, B_T = 2, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, B_READY, B_TAKEN, B_YTAKEN, kBars };
 
 struct ChainSmem {
-    // q: a chunk's queries, and once they are used its outputs on their way to memory; v: values, 64 of
-    // them in a swizzled block of 64 tokens
+    // q: a chunk's queries, and once they are used its outputs on their way to memory; v: its values, first
+    // by token (64 values in a swizzled block of 64 tokens, twice), then by value (128 rows of 64 tokens)
     unsigned char k[2][2 * kBlk], q[2][2 * kBlk], T[kBlk], A[kBlk], v[2 * kBlk];
     HeadGates gates[4];
-    float row_max[4][TP];
+    float vmax[TP];          // largest magnitude among a chunk's values, by row
+    float unscale[2][TP];    // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
+    uint32_t armed[2], parity[2];  // of the issuing and the loading thread: barriers ever armed, the last phase of each
 };
 
 // Tensor-memory columns: the state's 16-bit copy and X (or R^T over X) make way for the new state's
 // increment, which is as wide as both.
 constexpr uint32_t T_S = 0, T_X = 64, T_D = 0, T_U = 128, T_Y = 192;
 
-// The accumulators' 32 lanes of a warp as matrix fragments: two loads of 16 lanes each, 8 NC fp32
-// columns; element [half][4 n + 2 r + e] is lane 16 half + 8 r + T / 4, column 8 n + 2 (T % 4) + e.
-__device__ __forceinline__ void tmem_frag2(uint32_t a, float (&v)[2][8]) {
-    uint32_t r[16];
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// Barrier of one half of the block (1: the chain, 2: the side); whether any thread passed a non-zero
+// value.
+__device__ __forceinline__ bool half_sync_or(int half, int v) {
+    uint32_t any;
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(any)
+        : "r"(v), "r"(half)
+        : "memory");
+    return any != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// 8 fp32 columns of a warp's 32 lanes as matrix fragments, 16 lanes a load: element [half][2 r + e] is
+// lane 16 half + 8 r + T / 4, column 2 (T % 4) + e.
+__device__ __forceinline__ void tmem_frag(uint32_t a, float (&v)[2][4]) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%4,%5,%6,%7}, [%9];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(a), "r"(a + (16u << 16))
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = __uint_as_float(r[i]);
 }
-// Their 16-bit counterpart: element [half][2 n + r] holds columns 8 n + 2 (T % 4) and the next.
-__device__ __forceinline__ void tmem_put2(uint32_t a, const uint32_t (&v)[2][4]) {
+// 16 32-bit columns (two 16-bit values each) of this warp's lanes; tmem_put_wait waits for all before it.
+__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%2,%3,%4,%5};\n\t"
-        "tcgen05.st.sync.aligned.16x128b.x2.b32 [%1], {%6,%7,%8,%9};\n\t" ::"r"(a),
-        "r"(a + (16u << 16)), "r"(v[0][0]), "r"(v[0][1]), "r"(v[0][2]), "r"(v[0][3]), "r"(v[1][0]), "r"(v[1][1]),
-        "r"(v[1][2]), "r"(v[1][3])
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
-                 "r"(r2), "r"(r3)
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
                  : "memory");
 }
-
-// Keys and gates of chunk c of the sequence.
-__device__ __forceinline__ void load_keys(ChainSmem &sm, const WsLayout &ws, int first, int c, int g, int h) {
-    uint64_t *bar = &sm.bar[B_K + (c & 1)];
-    mbar_arrive_expect_tx(bar, 2 * kBlk + kGateBytes);
-    const unsigned char *kq = ws.kq(first + c, g);
-    bulk_g2s(sm.k[c & 1], kq, kBlk, bar);
-    bulk_g2s(sm.k[c & 1] + kBlk, kq + 2 * kBlk, kBlk, bar);
-    bulk_g2s(&sm.gates[c & 3], ws.head(first + c, h) + 2 * kBlk, kGateBytes, bar);
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
-__device__ __forceinline__ void load_queries(ChainSmem &sm, const WsLayout &ws, int first, int c, int g) {
-    mbar_arrive_expect_tx(&sm.bar[B_Q], 2 * kBlk);
-    const unsigned char *kq = ws.kq(first + c, g);
-    bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, &sm.bar[B_Q]);
-    bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, &sm.bar[B_Q]);
-}
-__device__ __forceinline__ void load_tile(void *dst, const unsigned char *src, uint64_t *bar) {
-    mbar_arrive_expect_tx(bar, kBlk);
-    bulk_g2s(dst, src, kBlk, bar);
-}
-__device__ __forceinline__ void load_values(ChainSmem &sm, const CUtensorMap *map, int h, int t) {
-    mbar_arrive_expect_tx(&sm.bar[B_V], 2 * kBlk);
-    tma_load_2d(sm.v, map, h * TP, t, &sm.bar[B_V]);
-    tma_load_2d(sm.v + kBlk, map, h * TP + 64, t, &sm.bar[B_V]);
+__device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// Block (sequence in the plan's order, head) of 16 warps.  Warp w works on tensor-memory lanes
-// 32 (w % 4) .. + 31, the value indices, and on quarter w / 4 of the columns: 16 tokens, or 32 of the
-// state's.  A thread holds its rows 8 i + T / 4 and columns 8 n + 2 (T % 4) + {0, 1} as fragments, which
-// is how ldmatrix and stmatrix turn values and outputs between (token, value) and (value, token).
+// One sequence and head, as both halves of the block see it.
+struct ChainJob {
+    const ScanParams &p;
+    const WsLayout &ws;
+    const CUtensorMap &vmap;
+    ChainSmem &sm;
+    int s, h, t0, len, first, nc;
+
+    __device__ __forceinline__ const unsigned char *head(int c) const { return ws.head(first + c, h); }
+    __device__ __forceinline__ void arm(int who, int i, uint32_t phase) const {
+        sm.armed[who] |= 1u << i;
+        sm.parity[who] = (sm.parity[who] & ~(1u << i)) | phase << i;
+    }
+    __device__ __forceinline__ void load_stage(int c) const {
+        uint64_t *bar = &sm.bar[B_KQ + (c & 1)];
+        const unsigned char *kq = ws.kq(first + c, h / p.HG);
+        mbar_arrive_expect_tx(bar, kKqBytes + kGateBytes);
+        bulk_g2s(&sm.gates[c & 3], head(c) + 2 * kBlk, kGateBytes, bar);
+        bulk_g2s(sm.k[c & 1], kq, kBlk, bar);
+        bulk_g2s(sm.k[c & 1] + kBlk, kq + 2 * kBlk, kBlk, bar);
+        bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, bar);
+        bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, bar);
+        arm(1, B_KQ + (c & 1), c >> 1 & 1);
+    }
+    __device__ __forceinline__ void load_values(int c) const {
+        mbar_arrive_expect_tx(&sm.bar[B_V], 2 * kBlk);
+        tma_load_2d(sm.v, &vmap, h * TP, t0 + c * C, &sm.bar[B_V]);
+        tma_load_2d(sm.v + kBlk, &vmap, h * TP + 64, t0 + c * C, &sm.bar[B_V]);
+        arm(1, B_V, c & 1);
+    }
+    __device__ __forceinline__ void load_tile(int who, int c, int i, unsigned char *dst, uint32_t off) const {
+        mbar_arrive_expect_tx(&sm.bar[i], kBlk);
+        bulk_g2s(dst, head(c) + off, kBlk, &sm.bar[i]);
+        arm(who, i, c & 1);
+    }
+    // into L2, for loads that are needed within a thousand cycles of their issue
+    __device__ __forceinline__ void prefetch(int c) const {
+        bulk_prefetch(head(c), 2 * kBlk);
+        for (int i = 0; i < 2; ++i)
+            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&vmap)),
+                         "r"(h * TP + 64 * i), "r"(t0 + c * C)
+                         : "memory");
+    }
+};
+
+// The chain's four warps: warp w holds rows 32 w .. + 31 of the state, a row a thread.  Returns whether
+// a wait gave up.
+__device__ __forceinline__ bool chain_warps(const ChainJob &J) {
+    const ScanParams &p = J.p;
+    ChainSmem &sm = J.sm;
+    const int row = threadIdx.x, warp = threadIdx.x >> 5;
+    const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);  // (of warp 0: tensor memory's first lane)
+    const int32_t slot = p.slot[J.s];
+    auto pool_row = [&](int32_t to) {
+        return static_cast<bf16 *>(p.pool) + to * p.stride + ((int64_t)J.h * TP + row) * TN;
+    };
+    float S[TN];  // times the row's power of two
+    {
+        const bool seeded = slot >= 0 && p.has_init && p.has_init[J.s];
+        const bf16 *src = pool_row(seeded ? slot : 0);
+#pragma unroll
+        for (int e = 0; e < TN; e += 8) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (seeded)  // (volatile: one after the other, not all in registers at once)
+                asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(src + e));
+            float f[8];
+            unpack16(w, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) S[e + i] = f[i];
+        }
+    }
+    float scale = 1.0f, unscale = 1.0f, limit = 0.0f;  // the power of two, its inverse, the largest value it takes
+    uint32_t x_phase = 0;
+    int bad = 0;  // a wait gave up: all four warps leave at the next barrier
+
+    auto store_state16 = [&](int e) {  // 32 columns of the state's copy for the products
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(S[e + 2 * i], S[e + 2 * i + 1]);
+        tmem_put(lanes + T_S + e / 2, pk);
+    };
+    auto issue_x = [&](int c) {  // X = S K^T
+        const uint32_t k = smem_u32(sm.k[c & 1]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(lanes + T_X, lanes + T_S + 8 * kk, desc_kmajor(k, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+        mma_commit(&sm.bar[B_X]);
+        J.arm(0, B_X, x_phase);
+    };
+    auto write_state = [&](int32_t to) {
+        uint4 *dst = reinterpret_cast<uint4 *>(pool_row(to));
+#pragma unroll
+        for (int e = 0; e < TN; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = S[e + i] * unscale;
+            dst[e / 8] = pack16(f);
+        }
+    };
+
+    for (int c = 0; c < J.nc; ++c) {
+        const uint32_t ph = c & 1;
+        const HeadGates &gt = sm.gates[c & 3];
+        // 1. X = S K^T, its operand stored at the last chunk's end
+        bool rescale = c % kRescale == 0;  // this chunk starts from a new power of two
+        if (!mbar_wait(&sm.bar[B_KQ + ph], (c >> 1) & 1, kPolls)) bad = 1;
+        if (!rescale && warp == 0 && elect_one()) issue_x(c);
+        if (!mbar_wait(&sm.bar[B_READY], ph, kPolls)) bad = 1;
+        const float vmax = sm.vmax[row];
+        int over = vmax > limit;  // a value outgrew 2^4 units of its row
+        // 2. R = V - e^c |k| X, rounded, over X (past the sequence's end the values, the keys and so X are
+        // zero); if a power of two has to change, X and R again from the rescaled state
+        for (;;) {
+            if (rescale) {
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 0; e < TN; ++e) top = fmaxf(top, fabsf(S[e]));
+                top = fmaxf(top * unscale, vmax);
+                // the power that brings the largest to [2, 4); values may grow to 16 before the next choice
+                uint32_t E = __float_as_uint(top) >> 23;
+                E = top < INFINITY ? max(7u, min(247u, E)) : 127u;
+                scale = __uint_as_float((255u - E) << 23);
+                const float ratio = scale * unscale;
+                unscale = __uint_as_float((E - 1u) << 23);
+                limit = __uint_as_float((E + 3u) << 23);
+#pragma unroll
+                for (int e = 0; e < TN; ++e) S[e] *= ratio;
+#pragma unroll
+                for (int e = 0; e < TN; e += 32) store_state16(e);
+                tmem_put_wait();
+                tc_fence_before();
+                if (half_sync_or(1, bad)) return true;
+                tc_fence_after();
+                if (warp == 0 && elect_one()) issue_x(c);
+                over = 0;
+            }
+            if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
+            x_phase ^= 1;
+            tc_fence_after();
+#pragma unroll
+            for (int n = 0; n < 8; n += 4) {
+                float x[32];
+                tmem_ld32(lanes + T_X + 8 * n, x);
+                uint32_t pk[16];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint4 v8 = *reinterpret_cast<const uint4 *>(sm.v + swz128_chunk(row, n + m));  // 8 tokens' values
+                    const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
+                    const float4 r0 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m));
+                    const float4 r1 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m) + 4);
+                    const float rk[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        pk[4 * m + i] = pack_f16x2(fmaf(-rk[2 * i], x[8 * m + 2 * i], __uint_as_float(w[i] << 16) * scale),
+                                                   fmaf(-rk[2 * i + 1], x[8 * m + 2 * i + 1],
+                                                        __uint_as_float(w[i] & 0xffff0000u) * scale));
+                }
+                tmem_put(lanes + T_X + 4 * n, pk);
+            }
+            tmem_put_wait();
+            sm.unscale[ph][row] = unscale;
+            tc_fence_before();
+            const bool again = half_sync_or(1, bad || over);
+            tc_fence_after();
+            if (!again) break;
+            rescale = true;
+        }
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.bar[B_TAKEN]);  // (after the barrier: the warp has read its values)
+        // 3. U^T = R^T T^T, and the state's part of Y once the last one is taken
+        if (warp == 0) {
+            if (!mbar_wait(&sm.bar[B_T], ph, kPolls)) bad = 1;
+            if (elect_one() && !bad) {
+                const uint32_t T = smem_u32(sm.T);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_ts(lanes + T_U, lanes + T_X + kk * 8, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+                mma_commit(&sm.bar[B_U]);
+                J.arm(0, B_U, ph);
+            }
+            if (c > 0 && !mbar_wait(&sm.bar[B_YTAKEN], ph ^ 1, kPolls)) bad = 1;
+            tc_fence_after();
+            if (elect_one() && !bad) {
+                const uint32_t q = smem_u32(sm.q[ph]);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(lanes + T_Y, lanes + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+                mma_commit(&sm.bar[B_OI]);
+                J.arm(0, B_OI, ph);
+            }
+        }
+        // 4. U^T rounded, as it is and times e^(c_64 - c) |k|
+        if (!mbar_wait(&sm.bar[B_U], ph, kPolls)) bad = 1;
+        tc_fence_after();
+#pragma unroll
+        for (int n = 0; n < C; n += 32) {  // 32 tokens: both forms over their own columns
+            float u[32];
+            tmem_ld32(lanes + T_U + n, u);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(u[2 * i], u[2 * i + 1]);
+            tmem_put(lanes + T_U + n, pk);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float4 w = *reinterpret_cast<const float4 *>(gt.ek + n + 2 * i);
+                pk[i] = pack_f16x2(u[2 * i] * w.x, u[2 * i + 1] * w.y);
+                pk[i + 1] = pack_f16x2(u[2 * i + 2] * w.z, u[2 * i + 3] * w.w);
+            }
+            tmem_put(lanes + T_U + n + 16, pk);
+        }
+        tmem_put_wait();
+        tc_fence_before();
+        if (half_sync_or(1, bad)) return true;
+        tc_fence_after();
+        // 5. the state's increment, over the columns of its copy and of R (both are read), and A's part of Y
+        if (warp == 0) {
+            if (!mbar_wait(&sm.bar[B_OI], ph, kPolls) || !mbar_wait(&sm.bar[B_A], ph, kPolls)) bad = 1;
+            if (elect_one() && !bad) {
+                const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_ts(lanes + T_D, lanes + T_U + (kk >> 1) * 32 + 16 + (kk & 1) * 8, desc_mnmajor(k, kBlk, kk),
+                                idesc_f16(128, TN, true), kk > 0);
+                mma_commit(&sm.bar[B_S]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_ts(lanes + T_Y, lanes + T_U + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(A, kBlk, kk),
+                                idesc_f16(128, C, false), 1);
+                mma_commit(&sm.bar[B_Y]);
+                J.arm(0, B_S, ph), J.arm(0, B_Y, ph);
+                if (c + 1 < J.nc) J.load_tile(0, c + 1, B_T, sm.T, 0);
+            }
+        }
+        // 6. the new state, and its copy over the increment (a row's columns are its thread's own)
+        if (!mbar_wait(&sm.bar[B_S], ph, kPolls)) bad = 1;
+        tc_fence_after();
+        const float last = gt.last;
+#pragma unroll
+        for (int e = 0; e < TN; e += 32) {
+            float d[32];
+            tmem_ld32(lanes + T_D + e, d);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[e + i] = fmaf(last, S[e + i], d[i]);
+        }
+        if (p.ckpt_slots) {
+            const int32_t cs = ckpt_slot(p, J.s, min(J.len, (c + 1) * C), threadIdx.x == 0 && J.h == 0);
+            if (cs >= 0) write_state(cs);
+        }
+        if (c + 1 < J.nc && (c + 1) % kRescale != 0) {
+#pragma unroll
+            for (int e = 0; e < TN; e += 32) store_state16(e);
+            tmem_put_wait();
+        }
+        tc_fence_before();
+        if (half_sync_or(1, bad)) return true;
+        tc_fence_after();
+    }
+    if (slot >= 0) write_state(slot);
+    return false;
+}
+
+// The four warps beside the chain: they turn the values of the next chunk, scale its queries, take the
+// outputs of the last one to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31, the
+// fragments of 32 values by 8 tokens.  Returns whether a wait gave up.
+__device__ __forceinline__ bool side_warps(const ChainJob &J) {
+    const ScanParams &p = J.p;
+    ChainSmem &sm = J.sm;
+    const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
+    const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);
+    // this lane's 16 bytes (8 values of a token) of a tile by tokens, for 8 tokens from 8 n
+    auto token_row = [&](const unsigned char *tile, int n) {
+        return smem_u32(tile) + (warp >> 1) * kBlk + swz128_chunk(8 * n + (lane & 7), 4 * (warp & 1) + (lane >> 3));
+    };
+    int bad = 0;
+    for (int c = -1; c < J.nc; ++c) {
+        // the next chunk's values and queries
+        if (c + 1 < J.nc) {
+            const int c1 = c + 1;
+            if (warp == 1) {
+                if (c >= 0 && !mbar_wait(&sm.bar[B_TAKEN], c & 1, kPolls)) bad = 1;
+                if (elect_one() && !bad) {
+                    if (c >= 0) J.load_values(c1);
+                    if (c1 + 1 < J.nc) J.prefetch(c1 + 1);
+                }
+            }
+            if (!mbar_wait(&sm.bar[B_KQ + (c1 & 1)], (c1 >> 1) & 1, kPolls)) bad = 1;
+            const float *g = sm.gates[c1 & 3].g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // queries times e^c, 16 bytes each
+                const int cidx = tid + 128 * i;
+                uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1] + cidx * 16);
+                const __half2 w = __float2half2_rn(g[(cidx >> 3) & (C - 1)]);
+                uint4 u = *ptr;
+                __half2 *hp = reinterpret_cast<__half2 *>(&u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w);
+                *ptr = u;
+            }
+            if (!mbar_wait(&sm.bar[B_V], c1 & 1, kPolls)) bad = 1;
+            uint32_t v[8][4];  // [n][i]: rows 8 i + T / 4, tokens 8 n + 2 (T % 4) and the next
+#pragma unroll
+            for (int n = 0; n < 8; ++n) ldmatrix4_trans(v[n], token_row(sm.v, n));
+            const int L = J.len - c1 * C;
+            if (L < C) {  // rows past the sequence's end hold another sequence's values
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const int t = 8 * n + (lane & 3) * 2;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[n][i] = t + 1 < L ? v[n][i] : (t < L ? v[n][i] & 0xffffu : 0u);
+                }
+            }
+            if (half_sync_or(2, bad)) return true;  // all values are in registers
+#pragma unroll
+            for (int n = 0; n < 8; ++n) stmatrix4(smem_u32(sm.v) + swz128_chunk(32 * warp + lane, n), v[n]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const uint32_t a = v[n][i] & 0x7fff7fffu;
+                    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m2),
+                                                     *reinterpret_cast<const __nv_bfloat162 *>(&a));
+                    m2 = *reinterpret_cast<const uint32_t *>(&m);
+                }
+                float top = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if ((lane & 3) == 0) sm.vmax[32 * warp + 8 * i + (lane >> 2)] = top;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.bar[B_READY]);
+        }
+        // the last chunk's outputs, over its queries and from there to memory
+        if (c >= 0) {
+            if (!mbar_wait(&sm.bar[B_Y], c & 1, kPolls)) bad = 1;
+            tc_fence_after();
+            if (warp == 1 && c + 1 < J.nc && elect_one() && !bad) J.load_tile(1, c + 1, B_A, sm.A, kBlk);
+            const float *oq = sm.gates[c & 3].oq + (lane & 3) * 2;
+            float un[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                float y[2][4];
+                tmem_frag(lanes + T_Y + 8 * n, y);
+                const float2 w = *reinterpret_cast<const float2 *>(oq + 8 * n);
+                uint32_t pk[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 o = __floats2bfloat162_rn(y[i >> 1][2 * (i & 1)] * (w.x * un[i]),
+                                                                   y[i >> 1][2 * (i & 1) + 1] * (w.y * un[i]));
+                    pk[i] = *reinterpret_cast<const uint32_t *>(&o);
+                }
+                stmatrix4_trans(token_row(sm.q[c & 1], n), pk);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.bar[B_YTAKEN]);
+            if (half_sync_or(2, bad)) return true;
+            const int L = min(C, J.len - c * C), ch = tid & 15;
+            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C + (tid >> 4)) * p.H + J.h) * TP + ch * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = (tid >> 4) + 8 * i;
+                if (t < L)
+                    *reinterpret_cast<uint4 *>(dst + (int64_t)i * 8 * p.H * TP) =
+                        *reinterpret_cast<const uint4 *>(sm.q[c & 1] + (ch >> 3) * kBlk + swz128_chunk(t, ch & 7));
+            }
+            fence_async_smem();
+            if (c + 2 < J.nc) {
+                if (half_sync_or(2, bad)) return true;  // the queries' place is free
+                if (warp == 1 && elect_one()) J.load_stage(c + 2);
+            }
+        }
+    }
+    return half_sync_or(2, bad);
+}
+
+// Block (sequence in the plan's order, head).
 __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,
                                                                 const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char chain_smem[];
@@ -546,365 +933,47 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     if (p.meta[0] == 0) return;  // bad cu_seqlens (flagged): nothing is done
-    const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, g = h / p.HG;
-    const int t0 = p.cu[s], len = p.cu[s + 1] - t0, first = meta_chunks(p)[s];
+    const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, t0 = p.cu[s], len = p.cu[s + 1] - t0;
     const int32_t slot = p.slot[s];
     if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = warp & 3, Q = warp >> 2;
-    const int fr = lane >> 2, fc = (lane & 3) * 2;
-    const int nc = (len + C - 1) / C;
-    bf16 *pool = static_cast<bf16 *>(p.pool);
-    const int64_t off = ((int64_t)h * TP + 32 * q + fr) * TN + 32 * Q + fc;  // of this thread's first state element
-
-    if (warp == 0 && elect_one()) {
-        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], 1);
+    const ChainJob J = {p, ws, vmap, sm, s, h, t0, len, meta_chunks(p)[s], (len + C - 1) / C};
+    const int warp = threadIdx.x >> 5;
+    if (warp == 5 && elect_one()) {
+        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i >= B_READY ? 4 : 1);
         fence_mbar_init();
+        sm.armed[0] = sm.armed[1] = sm.parity[0] = sm.parity[1] = 0;
         tma_prefetch_desc(&vmap);
-        load_keys(sm, ws, first, 0, g, h);
-        load_values(sm, &vmap, h, t0);
-        load_queries(sm, ws, first, 0, g);
-        load_tile(sm.T, ws.head(first, h), &sm.bar[B_T]);
-        load_tile(sm.A, ws.head(first, h) + kBlk, &sm.bar[B_A]);
+        J.load_stage(0);
+        J.load_values(0);
+        J.load_tile(1, 0, B_T, sm.T, 0);
+        J.load_tile(1, 0, B_A, sm.A, kBlk);
+        if (J.nc > 1) J.load_stage(1);
     }
     if (warp == 0) {
         tmem_alloc(&sm.tmem, 256);
         tmem_relinquish();
     }
-    // this thread's part of the state, each row times its power of two: S[i / 2][4 n + 2 (i % 2) + e]
-    float S[2][16];
-    if (slot >= 0 && p.has_init && p.has_init[s]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(pool + slot * p.stride + off + i * 8 * TN + 8 * n);
-                S[i >> 1][4 * n + 2 * (i & 1)] = __uint_as_float(w << 16);
-                S[i >> 1][4 * n + 2 * (i & 1) + 1] = __uint_as_float(w & 0xffff0000u);
-            }
-    } else {
-#pragma unroll
-        for (int n = 0; n < 32; ++n) S[n >> 4][n & 15] = 0.0f;
-    }
-    // row i's power of two, 2^(128 - E_i), by the byte E_i: its inverse 2^(E_i - 128)
-    uint32_t powers = 0x80808080u;
-    auto scale_of = [&](int i) { return __uint_as_float((255u - (powers >> (8 * i) & 0xffu)) << 23); };
-    auto unscale_of = [&](int i) { return __uint_as_float(((powers >> (8 * i) & 0xffu) - 1u) << 23); };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = sm.tmem, lanes = tm + ((uint32_t)(q * 32) << 16);
-    bool failed = false;
-    uint32_t x_phase = 0;
-    uint32_t armed = 0, parity = 0;  // of the issuing thread: the barriers with something in flight, ever, and its phase
-    auto arm = [&](int i, uint32_t phase) {
-        armed |= 1u << i;
-        parity = (parity & ~(1u << i)) | phase << i;
-    };
-    arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
-
-    auto store_state16 = [&] {  // the state's copy for the products; the lanes' increment is consumed
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            uint32_t pk[2][4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                pk[i >> 2][i & 3] = pack_f16x2(S[i >> 2][8 * n + 2 * (i & 3)], S[i >> 2][8 * n + 2 * (i & 3) + 1]);
-            tmem_put2(lanes + T_S + Q * 16 + n * 8, pk);
-        }
-        tmem_put_wait();
-    };
-    auto issue_x = [&](int c) {  // X = S K^T
-        const uint32_t k = smem_u32(sm.k[c & 1]);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tm + T_X, tm + T_S + 8 * kk, desc_kmajor(k, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-        mma_commit(&sm.bar[B_X]);
-        arm(B_X, x_phase);
-    };
-    // this lane's row of 16 bytes (8 values of a token) in a swizzled tile of tokens, for the fragments of
-    // 8 tokens from 16 Q + 8 n and this warp's 32 values
-    auto value_row = [&](const unsigned char *tile, int n) {
-        return smem_u32(tile) + (q >> 1) * kBlk + swz128_chunk(16 * Q + 8 * n + (lane & 7), 4 * (q & 1) + (lane >> 3));
-    };
-    // outputs of chunk c into its queries' place
-    auto stage_outputs = [&](int c) {
-        float y[2][8];
-        tmem_frag2(lanes + T_Y + Q * 16, y);
-        const float *oq = sm.gates[c & 3].oq + 16 * Q + fc;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float2 w = *reinterpret_cast<const float2 *>(oq + 8 * n);
-            uint32_t pk[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = unscale_of(i);
-                const __nv_bfloat162 v = __floats2bfloat162_rn(y[i >> 1][4 * n + 2 * (i & 1)] * (w.x * u),
-                                                               y[i >> 1][4 * n + 2 * (i & 1) + 1] * (w.y * u));
-                pk[i] = *reinterpret_cast<const uint32_t *>(&v);
-            }
-            stmatrix4_trans(value_row(sm.q[c & 1], n), pk[0], pk[1], pk[2], pk[3]);
-        }
-    };
-    auto write_outputs = [&](int c) {  // from there to memory, 16 bytes a thread
-        const int L = min(C, len - c * C);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = (tid >> 4) + 32 * i, ch = tid & 15;
-            if (t < L)
-                *reinterpret_cast<uint4 *>(static_cast<bf16 *>(p.y) + ((int64_t)(t0 + c * C + t) * p.H + h) * TP + ch * 8) =
-                    *reinterpret_cast<const uint4 *>(sm.q[c & 1] + (ch >> 3) * kBlk + swz128_chunk(t, ch & 7));
-        }
-    };
-    auto write_state = [&](int32_t to) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = unscale_of(i);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(S[i >> 1][4 * n + 2 * (i & 1)] * u,
-                                                               S[i >> 1][4 * n + 2 * (i & 1) + 1] * u);
-                *reinterpret_cast<__nv_bfloat162 *>(pool + to * p.stride + off + i * 8 * TN + 8 * n) = v;
-            }
-        }
-    };
-
-    for (int c = 0; c < nc; ++c) {
-        const uint32_t ph = c & 1;
-        const int L = min(C, len - c * C);
-        int bad = 0;
-        const bool fresh = c % kRescale == 0;  // this chunk starts from new powers of two
-        const HeadGates &gt = sm.gates[c & 3];
-        // 1. X = S K^T, while the last chunk's outputs leave tensor memory
-        if (!mbar_wait(&sm.bar[B_K + ph], (c >> 1) & 1, kPolls)) bad = 1;
-        if (warp == 0 && elect_one() && !bad) {
-            tc_fence_after();
-            if (!fresh) issue_x(c);
-            if (c + 1 < nc) {
-                load_keys(sm, ws, first, c + 1, g, h);
-                arm(B_K + (ph ^ 1), ((c + 1) >> 1) & 1);
-            }
-        }
-        if (c > 0) {
-            if (!mbar_wait(&sm.bar[B_Y], ph ^ 1, kPolls)) bad = 1;
-            tc_fence_after();
-            if (warp == 0 && elect_one() && !bad) {
-                load_tile(sm.A, ws.head(first + c, h) + kBlk, &sm.bar[B_A]);
-                arm(B_A, ph);
-            }
-            stage_outputs(c - 1);
-        }
-        // 2. queries times e^c in place; this thread's values
-        if (!mbar_wait(&sm.bar[B_Q], ph, kPolls)) bad = 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int cidx = tid + kChainThreads * i;  // 16-byte chunk of the tile: row of 128 bytes = token
-            uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[ph] + cidx * 16);
-            const __half2 w = __float2half2_rn(gt.g[(cidx >> 3) & (C - 1)]);
-            uint4 u = *ptr;
-            __half2 *hp = reinterpret_cast<__half2 *>(&u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w);
-            *ptr = u;
-        }
-        fence_async_smem();
-        if (!mbar_wait(&sm.bar[B_V], ph, kPolls)) bad = 1;
-        uint32_t vals[2][4];  // [n][i]: two tokens of row i
-#pragma unroll
-        for (int n = 0; n < 2; ++n) ldmatrix4_trans(vals[n], value_row(sm.v, n));
-        if (L < C) {  // rows past the sequence's end hold another sequence's values
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int t = 16 * Q + 8 * n + fc;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vals[n][i] = t + 1 < L ? vals[n][i] : (t < L ? vals[n][i] & 0xffffu : 0u);
-            }
-        }
-        uint32_t vmax[4], over = 0;  // largest magnitudes as bf16 bits; whether one outgrew 2^4 units of its row
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            vmax[i] = __vmaxu2(vals[0][i] & 0x7fff7fffu, vals[1][i] & 0x7fff7fffu);
-            const uint32_t lim = ((powers >> (8 * i) & 0xffu) + 3u) << 7;
-            over |= __vcmpgtu2(vmax[i], lim | lim << 16);
-        }
-        // (a wait that gave up goes the same way and ends the block below)
-        if (__syncthreads_or(bad || over) || fresh) {
-            if (!fresh) {  // X of the old powers is not used
-                if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
-                x_phase ^= 1;
-            }
-            // the largest magnitude in each row of the state (unscaled) and of the values
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float top = __uint_as_float(max(vmax[i] & 0xffffu, vmax[i] >> 16) << 16);
-                const float u = unscale_of(i);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    top = fmaxf(top, u * fmaxf(fabsf(S[i >> 1][4 * n + 2 * (i & 1)]), fabsf(S[i >> 1][4 * n + 2 * (i & 1) + 1])));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (fc == 0) sm.row_max[Q][32 * q + 8 * i + fr] = top;
-            }
-            __syncthreads();
-            uint32_t next = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 32 * q + 8 * i + fr;
-                const float top = fmaxf(fmaxf(sm.row_max[0][row], sm.row_max[1][row]), fmaxf(sm.row_max[2][row], sm.row_max[3][row]));
-                // the power that brings the largest to [2, 4); values may grow to 16 before the next choice
-                int E = (int)(__float_as_uint(top) >> 23);
-                E = top < INFINITY ? max(7, min(247, E)) : 127;
-                next |= (uint32_t)E << (8 * i);
-                const float ratio = __uint_as_float((255u - E) << 23) * unscale_of(i);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    S[i >> 1][4 * n + 2 * (i & 1)] *= ratio;
-                    S[i >> 1][4 * n + 2 * (i & 1) + 1] *= ratio;
-                }
-            }
-            powers = next;
-            store_state16();
-            tc_fence_before();
-            if (__syncthreads_or(bad)) {
-                failed = true;
-                break;
-            }
-            tc_fence_after();
-            if (warp == 0 && elect_one()) issue_x(c);
-        }
-        // 3. R = V - e^c |k| X, rounded, over X; then U^T = R^T T^T and the state's part of Y
-        if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
-        x_phase ^= 1;
-        tc_fence_after();
-        {
-            float x[2][8];
-            tmem_frag2(lanes + T_X + Q * 16, x);
-            uint32_t pk[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 w = *reinterpret_cast<const float2 *>(gt.rk + 16 * Q + 8 * n + fc);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {  // (past the end the values, the keys and so X are zero)
-                    const float sc = scale_of(i);
-                    const float *xi = &x[i >> 1][4 * n + 2 * (i & 1)];
-                    pk[i >> 1][2 * n + (i & 1)] = pack_f16x2(fmaf(-w.x, xi[0], __uint_as_float(vals[n][i] << 16) * sc),
-                                                             fmaf(-w.y, xi[1], __uint_as_float(vals[n][i] & 0xffff0000u) * sc));
-                }
-            }
-            tmem_put2(lanes + T_X + Q * 16, pk);
-            tmem_put_wait();
-        }
-        if (!mbar_wait(&sm.bar[B_T], ph, kPolls)) bad = 1;
-        tc_fence_before();
-        if (__syncthreads_or(bad)) {
-            failed = true;
-            break;
-        }
-        tc_fence_after();
-        if (warp == 0 && elect_one()) {
-            const uint32_t T = smem_u32(sm.T), qq = smem_u32(sm.q[ph]);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(tm + T_U, tm + T_X + kk * 16, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-            mma_commit(&sm.bar[B_U]);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(qq, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-            mma_commit(&sm.bar[B_OI]);
-            arm(B_U, ph), arm(B_OI, ph);
-            if (c + 1 < nc) {
-                load_values(sm, &vmap, h, t0 + (c + 1) * C);
-                arm(B_V, ph ^ 1);
-            }
-        }
-        if (c > 0) write_outputs(c - 1);
-        // 4. U^T rounded, as it is and times e^(c_64 - c) |k|; then the state's increment and A's part of Y
-        if (!mbar_wait(&sm.bar[B_U], ph, kPolls)) bad = 1;
-        tc_fence_after();
-        {
-            float u[2][8];
-            tmem_frag2(lanes + T_U + Q * 16, u);
-            uint32_t pk[2][4], pe[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 w = *reinterpret_cast<const float2 *>(gt.ek + 16 * Q + 8 * n + fc);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float *ui = &u[i >> 1][4 * n + 2 * (i & 1)];
-                    pk[i >> 1][2 * n + (i & 1)] = pack_f16x2(ui[0], ui[1]);
-                    pe[i >> 1][2 * n + (i & 1)] = pack_f16x2(ui[0] * w.x, ui[1] * w.y);
-                }
-            }
-            tmem_put2(lanes + T_U + Q * 16, pk);
-            tmem_put2(lanes + T_U + Q * 16 + 8, pe);
-            tmem_put_wait();
-        }
-        if (!mbar_wait(&sm.bar[B_OI], ph, kPolls)) bad = 1;  // the state's copy is read: its columns are free
-        if (!mbar_wait(&sm.bar[B_A], ph, kPolls)) bad = 1;
-        tc_fence_before();
-        if (__syncthreads_or(bad)) {
-            failed = true;
-            break;
-        }
-        tc_fence_after();
-        if (warp == 0 && elect_one()) {
-            const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(tm + T_D, tm + T_U + kk * 16 + 8, desc_mnmajor(k, kBlk, kk), idesc_f16(128, TN, true), kk > 0);
-            mma_commit(&sm.bar[B_S]);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ts(tm + T_Y, tm + T_U + kk * 16, desc_kmajor(A, kBlk, kk), idesc_f16(128, C, false), 1);
-            mma_commit(&sm.bar[B_Y]);
-            arm(B_S, ph), arm(B_Y, ph);
-            if (c + 1 < nc) {
-                load_queries(sm, ws, first, c + 1, g);
-                load_tile(sm.T, ws.head(first + c + 1, h), &sm.bar[B_T]);
-                arm(B_Q, ph ^ 1), arm(B_T, ph ^ 1);
-            }
-        }
-        // 5. the new state, and its copy
-        if (!mbar_wait(&sm.bar[B_S], ph, kPolls)) bad = 1;
-        tc_fence_after();
-        const float last = gt.last;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float d[2][8];
-            tmem_frag2(lanes + T_D + Q * 32 + n * 16, d);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[i >> 3][8 * n + (i & 7)] = fmaf(last, S[i >> 3][8 * n + (i & 7)], d[i >> 3][i & 7]);
-        }
-        const int32_t cs = ckpt_slot(p, s, c * C + L, tid == 0 && h == 0);
-        if (cs >= 0) write_state(cs);
-        if (c + 1 < nc && (c + 1) % kRescale != 0) {
-            tc_fence_before();
-            asm volatile("bar.sync %0, 128;" ::"r"(q + 1) : "memory");  // these lanes' increment has been read
-            tc_fence_after();
-            store_state16();
-        }
-        tc_fence_before();
-        if (__syncthreads_or(bad)) {
-            failed = true;
-            break;
-        }
-        tc_fence_after();
-    }
-    if (!failed) {
-        if (slot >= 0) write_state(slot);
-        failed = !mbar_wait(&sm.bar[B_Y], (nc - 1) & 1, kPolls);
-        tc_fence_after();
-        stage_outputs(nc - 1);
+    const uint32_t tm = sm.tmem;
+    bool failed;
+    if (warp < 4) {
+        more_registers<kChainRegs>();
+        failed = chain_warps(J);
+    } else {
+        fewer_registers<kSideRegs>();
+        failed = side_warps(J);
     }
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
         // the same bounded time to finish before its memory is released
-        if (warp == 0 && elect_one()) {
+        if (warp == 4 && elect_one()) {
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
-            for (int i = 0; i < kBars; ++i)
-                if (armed >> i & 1) mbar_wait(&sm.bar[i], parity >> i & 1, kPolls);
+            for (int w = 0; w < 2; ++w)
+                for (int i = 0; i < kBars; ++i)
+                    if (sm.armed[w] >> i & 1) mbar_wait(&sm.bar[i], sm.parity[w] >> i & 1, kPolls);
         }
-    } else {
-        write_outputs(nc - 1);
     }
     tc_fence_before();
     __syncthreads();
