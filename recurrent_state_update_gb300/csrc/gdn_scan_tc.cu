@@ -72,6 +72,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// mbar_wait as a short loop: unrolled, the waits alone were a third of k_gdn_chain's instructions, and a
+// loop that does not stay in the instruction cache runs at the rate it is fetched.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPolls; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
 // The swizzled tiles want 1024-byte boundaries; the launches ask for that much more.
 template <typename T>
 __device__ __forceinline__ T *align1024(unsigned char *p) {
@@ -354,12 +363,12 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
         if (tok < 32) dec.far[tok] = exp2f(dec.cum[31] - run) * nk;
         if (hh == 0) sm.nk[tok] = nk;
     }
-    const int bad = mbar_wait(&sm.bar, 0, kPolls) ? 0 : 1;
+    const int bad = wait_for(&sm.bar, 0) ? 0 : 1;
     tc_fence_after();
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
-            mbar_wait(&sm.bar, 0, kPolls);
+            wait_for(&sm.bar, 0);
         }
     } else {
         const int q = warp & 3, hf = warp >> 2, i = (q & 1) * 32 + lane;  // row i of K K^T (q < 2) or Q K^T
@@ -475,7 +484,17 @@ struct ChainSmem {
     float unscale[2][TP];    // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
-    uint32_t armed[2], parity[2];  // of the issuing and the loading thread: barriers ever armed, the last phase of each
+    uint32_t armed[2], parity[2];  // what each half of the block leaves behind (Armed)
+};
+
+// The barriers ever armed with a copy or a product, and the last phase of each: what is waited for
+// before a block that gave up lets go of its memory.
+struct Armed {
+    uint32_t bars = 0, parity = 0;
+    __device__ __forceinline__ void operator()(int i, uint32_t phase) {
+        bars |= 1u << i;
+        parity = (parity & ~(1u << i)) | phase << i;
+    }
 };
 
 // Tensor-memory columns: the state's 16-bit copy and X (or R^T over X) make way for the new state's
@@ -509,19 +528,20 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 8 fp32 columns of a warp's 32 lanes as matrix fragments, 16 lanes a load: element [half][2 r + e] is
-// lane 16 half + 8 r + T / 4, column 2 (T % 4) + e.
-__device__ __forceinline__ void tmem_frag(uint32_t a, float (&v)[2][4]) {
-    uint32_t r[8];
+// 16 fp32 columns of a warp's 32 lanes as matrix fragments, 16 lanes a load: element
+// [half][4 n + 2 r + e] is lane 16 half + 8 r + T / 4, column 8 n + 2 (T % 4) + e.
+__device__ __forceinline__ void tmem_frag2(uint32_t a, float (&v)[2][8]) {
+    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%8];\n\t"
-        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%4,%5,%6,%7}, [%9];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(a), "r"(a + (16u << 16))
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __uint_as_float(r[i]);
 }
 // 16 32-bit columns (two 16-bit values each) of this warp's lanes; tmem_put_wait waits for all before it.
 __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&v)[16]) {
@@ -556,10 +576,6 @@ struct ChainJob {
     int s, h, t0, len, first, nc;
 
     __device__ __forceinline__ const unsigned char *head(int c) const { return ws.head(first + c, h); }
-    __device__ __forceinline__ void arm(int who, int i, uint32_t phase) const {
-        sm.armed[who] |= 1u << i;
-        sm.parity[who] = (sm.parity[who] & ~(1u << i)) | phase << i;
-    }
     __device__ __forceinline__ void load_stage(int c) const {
         uint64_t *bar = &sm.bar[B_KQ + (c & 1)];
         const unsigned char *kq = ws.kq(first + c, h / p.HG);
@@ -569,18 +585,15 @@ struct ChainJob {
         bulk_g2s(sm.k[c & 1] + kBlk, kq + 2 * kBlk, kBlk, bar);
         bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, bar);
         bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, bar);
-        arm(1, B_KQ + (c & 1), c >> 1 & 1);
     }
     __device__ __forceinline__ void load_values(int c) const {
         mbar_arrive_expect_tx(&sm.bar[B_V], 2 * kBlk);
         tma_load_2d(sm.v, &vmap, h * TP, t0 + c * C, &sm.bar[B_V]);
         tma_load_2d(sm.v + kBlk, &vmap, h * TP + 64, t0 + c * C, &sm.bar[B_V]);
-        arm(1, B_V, c & 1);
     }
-    __device__ __forceinline__ void load_tile(int who, int c, int i, unsigned char *dst, uint32_t off) const {
+    __device__ __forceinline__ void load_tile(int c, int i, unsigned char *dst, uint32_t off) const {
         mbar_arrive_expect_tx(&sm.bar[i], kBlk);
         bulk_g2s(dst, head(c) + off, kBlk, &sm.bar[i]);
-        arm(who, i, c & 1);
     }
     // into L2, for loads that are needed within a thousand cycles of their issue
     __device__ __forceinline__ void prefetch(int c) const {
@@ -594,7 +607,7 @@ struct ChainJob {
 
 // The chain's four warps: warp w holds rows 32 w .. + 31 of the state, a row a thread.  Returns whether
 // a wait gave up.
-__device__ __forceinline__ bool chain_warps(const ChainJob &J) {
+__device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
     const ScanParams &p = J.p;
     ChainSmem &sm = J.sm;
     const int row = threadIdx.x, warp = threadIdx.x >> 5;
@@ -634,7 +647,6 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
         for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ts(lanes + T_X, lanes + T_S + 8 * kk, desc_kmajor(k, kBlk, kk), idesc_f16(128, C, false), kk > 0);
         mma_commit(&sm.bar[B_X]);
-        J.arm(0, B_X, x_phase);
     };
     auto write_state = [&](int32_t to) {
         uint4 *dst = reinterpret_cast<uint4 *>(pool_row(to));
@@ -652,10 +664,12 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
         const HeadGates &gt = sm.gates[c & 3];
         // 1. X = S K^T, its operand stored at the last chunk's end
         bool rescale = c % kRescale == 0;  // this chunk starts from a new power of two
-        if (!mbar_wait(&sm.bar[B_KQ + ph], (c >> 1) & 1, kPolls)) bad = 1;
+        if (!wait_for(&sm.bar[B_KQ + ph], (c >> 1) & 1)) bad = 1;
+        if (!rescale) arm(B_X, x_phase);
         if (!rescale && warp == 0 && elect_one()) issue_x(c);
-        if (!mbar_wait(&sm.bar[B_READY], ph, kPolls)) bad = 1;
+        if (!wait_for(&sm.bar[B_READY], ph)) bad = 1;
         const float vmax = sm.vmax[row];
+        if (warp == 0 && !wait_for(&sm.bar[B_T], ph)) bad = 1;
         int over = vmax > limit;  // a value outgrew 2^4 units of its row
         // 2. R = V - e^c |k| X, rounded, over X (past the sequence's end the values, the keys and so X are
         // zero); if a power of two has to change, X and R again from the rescaled state
@@ -680,21 +694,24 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
                 tc_fence_before();
                 if (half_sync_or(1, bad)) return true;
                 tc_fence_after();
+                arm(B_X, x_phase);
                 if (warp == 0 && elect_one()) issue_x(c);
                 over = 0;
             }
-            if (!mbar_wait(&sm.bar[B_X], x_phase, kPolls)) bad = 1;
+            if (!wait_for(&sm.bar[B_X], x_phase)) bad = 1;
             x_phase ^= 1;
             tc_fence_after();
 #pragma unroll
             for (int n = 0; n < 8; n += 4) {
+                uint4 v8[4];  // 8 tokens' values each
+#pragma unroll
+                for (int m = 0; m < 4; ++m) v8[m] = *reinterpret_cast<const uint4 *>(sm.v + swz128_chunk(row, n + m));
                 float x[32];
                 tmem_ld32(lanes + T_X + 8 * n, x);
                 uint32_t pk[16];
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const uint4 v8 = *reinterpret_cast<const uint4 *>(sm.v + swz128_chunk(row, n + m));  // 8 tokens' values
-                    const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
+                    const uint32_t w[4] = {v8[m].x, v8[m].y, v8[m].z, v8[m].w};
                     const float4 r0 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m));
                     const float4 r1 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m) + 4);
                     const float rk[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
@@ -717,31 +734,34 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
         if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.bar[B_TAKEN]);  // (after the barrier: the warp has read its values)
         // 3. U^T = R^T T^T, and the state's part of Y once the last one is taken
         if (warp == 0) {
-            if (!mbar_wait(&sm.bar[B_T], ph, kPolls)) bad = 1;
+            if (!bad) arm(B_U, ph);
             if (elect_one() && !bad) {
                 const uint32_t T = smem_u32(sm.T);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16_ts(lanes + T_U, lanes + T_X + kk * 8, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
                 mma_commit(&sm.bar[B_U]);
-                J.arm(0, B_U, ph);
             }
-            if (c > 0 && !mbar_wait(&sm.bar[B_YTAKEN], ph ^ 1, kPolls)) bad = 1;
+            if (c > 0 && !wait_for(&sm.bar[B_YTAKEN], ph ^ 1)) bad = 1;
+            if (!wait_for(&sm.bar[B_A], ph)) bad = 1;
             tc_fence_after();
+            if (!bad) arm(B_OI, ph);
             if (elect_one() && !bad) {
                 const uint32_t q = smem_u32(sm.q[ph]);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_bf16_ts(lanes + T_Y, lanes + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
                 mma_commit(&sm.bar[B_OI]);
-                J.arm(0, B_OI, ph);
             }
         }
         // 4. U^T rounded, as it is and times e^(c_64 - c) |k|
-        if (!mbar_wait(&sm.bar[B_U], ph, kPolls)) bad = 1;
+        if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
         tc_fence_after();
 #pragma unroll
         for (int n = 0; n < C; n += 32) {  // 32 tokens: both forms over their own columns
+            float4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float4 *>(gt.ek + n + 4 * i);
             float u[32];
             tmem_ld32(lanes + T_U + n, u);
             uint32_t pk[16];
@@ -750,9 +770,8 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
             tmem_put(lanes + T_U + n, pk);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-                const float4 w = *reinterpret_cast<const float4 *>(gt.ek + n + 2 * i);
-                pk[i] = pack_f16x2(u[2 * i] * w.x, u[2 * i + 1] * w.y);
-                pk[i + 1] = pack_f16x2(u[2 * i + 2] * w.z, u[2 * i + 3] * w.w);
+                pk[i] = pack_f16x2(u[2 * i] * w[i / 2].x, u[2 * i + 1] * w[i / 2].y);
+                pk[i + 1] = pack_f16x2(u[2 * i + 2] * w[i / 2].z, u[2 * i + 3] * w[i / 2].w);
             }
             tmem_put(lanes + T_U + n + 16, pk);
         }
@@ -762,7 +781,8 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
         tc_fence_after();
         // 5. the state's increment, over the columns of its copy and of R (both are read), and A's part of Y
         if (warp == 0) {
-            if (!mbar_wait(&sm.bar[B_OI], ph, kPolls) || !mbar_wait(&sm.bar[B_A], ph, kPolls)) bad = 1;
+            if (!wait_for(&sm.bar[B_OI], ph)) bad = 1;
+            if (!bad) arm(B_S, ph), arm(B_Y, ph), arm(B_T, ph ^ (c + 1 < J.nc));
             if (elect_one() && !bad) {
                 const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
 #pragma unroll
@@ -775,14 +795,13 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
                     mma_bf16_ts(lanes + T_Y, lanes + T_U + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(A, kBlk, kk),
                                 idesc_f16(128, C, false), 1);
                 mma_commit(&sm.bar[B_Y]);
-                J.arm(0, B_S, ph), J.arm(0, B_Y, ph);
-                if (c + 1 < J.nc) J.load_tile(0, c + 1, B_T, sm.T, 0);
+                if (c + 1 < J.nc) J.load_tile(c + 1, B_T, sm.T, 0);
             }
         }
         // 6. the new state, and its copy over the increment (a row's columns are its thread's own)
-        if (!mbar_wait(&sm.bar[B_S], ph, kPolls)) bad = 1;
-        tc_fence_after();
         const float last = gt.last;
+        if (!wait_for(&sm.bar[B_S], ph)) bad = 1;
+        tc_fence_after();
 #pragma unroll
         for (int e = 0; e < TN; e += 32) {
             float d[32];
@@ -810,7 +829,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J) {
 // The four warps beside the chain: they turn the values of the next chunk, scale its queries, take the
 // outputs of the last one to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31, the
 // fragments of 32 values by 8 tokens.  Returns whether a wait gave up.
-__device__ __forceinline__ bool side_warps(const ChainJob &J) {
+__device__ __forceinline__ bool side_warps(const ChainJob &J, Armed &arm) {
     const ScanParams &p = J.p;
     ChainSmem &sm = J.sm;
     const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
@@ -825,26 +844,33 @@ __device__ __forceinline__ bool side_warps(const ChainJob &J) {
         if (c + 1 < J.nc) {
             const int c1 = c + 1;
             if (warp == 1) {
-                if (c >= 0 && !mbar_wait(&sm.bar[B_TAKEN], c & 1, kPolls)) bad = 1;
+                if (c >= 0 && !wait_for(&sm.bar[B_TAKEN], c & 1)) bad = 1;
+                if (!bad) arm(B_V, c1 & 1);
                 if (elect_one() && !bad) {
                     if (c >= 0) J.load_values(c1);
                     if (c1 + 1 < J.nc) J.prefetch(c1 + 1);
                 }
             }
-            if (!mbar_wait(&sm.bar[B_KQ + (c1 & 1)], (c1 >> 1) & 1, kPolls)) bad = 1;
+            if (!wait_for(&sm.bar[B_KQ + (c1 & 1)], (c1 >> 1) & 1)) bad = 1;
             const float *g = sm.gates[c1 & 3].g;
+            {  // queries times e^c, 16 bytes of a token each: tokens 16 apart, in both blocks of 64 elements
+                uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1]) + tid;
+                uint4 u[8];
+                float w[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // queries times e^c, 16 bytes each
-                const int cidx = tid + 128 * i;
-                uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1] + cidx * 16);
-                const __half2 w = __float2half2_rn(g[(cidx >> 3) & (C - 1)]);
-                uint4 u = *ptr;
-                __half2 *hp = reinterpret_cast<__half2 *>(&u);
+                for (int i = 0; i < 4; ++i) w[i] = g[16 * i + (tid >> 3)];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w);
-                *ptr = u;
+                for (int i = 0; i < 8; ++i) u[i] = ptr[128 * i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 w2 = __float2half2_rn(w[i & 3]);
+                    __half2 *hp = reinterpret_cast<__half2 *>(&u[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w2);
+                    ptr[128 * i] = u[i];
+                }
             }
-            if (!mbar_wait(&sm.bar[B_V], c1 & 1, kPolls)) bad = 1;
+            if (!wait_for(&sm.bar[B_V], c1 & 1)) bad = 1;
             uint32_t v[8][4];  // [n][i]: rows 8 i + T / 4, tokens 8 n + 2 (T % 4) and the next
 #pragma unroll
             for (int n = 0; n < 8; ++n) ldmatrix4_trans(v[n], token_row(sm.v, n));
@@ -881,26 +907,33 @@ __device__ __forceinline__ bool side_warps(const ChainJob &J) {
         }
         // the last chunk's outputs, over its queries and from there to memory
         if (c >= 0) {
-            if (!mbar_wait(&sm.bar[B_Y], c & 1, kPolls)) bad = 1;
+            if (!wait_for(&sm.bar[B_Y], c & 1)) bad = 1;
             tc_fence_after();
-            if (warp == 1 && c + 1 < J.nc && elect_one() && !bad) J.load_tile(1, c + 1, B_A, sm.A, kBlk);
+            if (warp == 1 && c + 1 < J.nc && !bad) {
+                arm(B_A, (c + 1) & 1);
+                if (elect_one()) J.load_tile(c + 1, B_A, sm.A, kBlk);
+            }
             const float *oq = sm.gates[c & 3].oq + (lane & 3) * 2;
             float un[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                float y[2][4];
-                tmem_frag(lanes + T_Y + 8 * n, y);
-                const float2 w = *reinterpret_cast<const float2 *>(oq + 8 * n);
-                uint32_t pk[4];
+            for (int n = 0; n < 8; n += 2) {
+                const float2 w0 = *reinterpret_cast<const float2 *>(oq + 8 * n), w1 = *reinterpret_cast<const float2 *>(oq + 8 * n + 8);
+                float y[2][8];
+                tmem_frag2(lanes + T_Y + 8 * n, y);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 o = __floats2bfloat162_rn(y[i >> 1][2 * (i & 1)] * (w.x * un[i]),
-                                                                   y[i >> 1][2 * (i & 1) + 1] * (w.y * un[i]));
-                    pk[i] = *reinterpret_cast<const uint32_t *>(&o);
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 w = m ? w1 : w0;
+                        const float *yi = &y[i >> 1][4 * m + 2 * (i & 1)];
+                        const __nv_bfloat162 o = __floats2bfloat162_rn(yi[0] * (w.x * un[i]), yi[1] * (w.y * un[i]));
+                        pk[i] = *reinterpret_cast<const uint32_t *>(&o);
+                    }
+                    stmatrix4_trans(token_row(sm.q[c & 1], n + m), pk);
                 }
-                stmatrix4_trans(token_row(sm.q[c & 1], n), pk);
             }
             tc_fence_before();
             __syncwarp();
@@ -908,17 +941,20 @@ __device__ __forceinline__ bool side_warps(const ChainJob &J) {
             if (half_sync_or(2, bad)) return true;
             const int L = min(C, J.len - c * C), ch = tid & 15;
             bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C + (tid >> 4)) * p.H + J.h) * TP + ch * 8;
+            uint4 o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = (tid >> 4) + 8 * i;
-                if (t < L)
-                    *reinterpret_cast<uint4 *>(dst + (int64_t)i * 8 * p.H * TP) =
-                        *reinterpret_cast<const uint4 *>(sm.q[c & 1] + (ch >> 3) * kBlk + swz128_chunk(t, ch & 7));
-            }
+            for (int i = 0; i < 8; ++i)  // (the swizzle repeats every 8 tokens)
+                o[i] = *reinterpret_cast<const uint4 *>(sm.q[c & 1] + (ch >> 3) * kBlk + swz128_chunk(tid >> 4, ch & 7) + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((tid >> 4) + 8 * i < L) *reinterpret_cast<uint4 *>(dst + (int64_t)i * 8 * p.H * TP) = o[i];
             fence_async_smem();
             if (c + 2 < J.nc) {
                 if (half_sync_or(2, bad)) return true;  // the queries' place is free
-                if (warp == 1 && elect_one()) J.load_stage(c + 2);
+                if (warp == 1) {
+                    arm(B_KQ + (c & 1), (c + 2) >> 1 & 1);
+                    if (elect_one()) J.load_stage(c + 2);
+                }
             }
         }
     }
@@ -941,12 +977,11 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     if (warp == 5 && elect_one()) {
         for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i >= B_READY ? 4 : 1);
         fence_mbar_init();
-        sm.armed[0] = sm.armed[1] = sm.parity[0] = sm.parity[1] = 0;
         tma_prefetch_desc(&vmap);
         J.load_stage(0);
         J.load_values(0);
-        J.load_tile(1, 0, B_T, sm.T, 0);
-        J.load_tile(1, 0, B_A, sm.A, kBlk);
+        J.load_tile(0, B_T, sm.T, 0);
+        J.load_tile(0, B_A, sm.A, kBlk);
         if (J.nc > 1) J.load_stage(1);
     }
     if (warp == 0) {
@@ -960,10 +995,16 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     bool failed;
     if (warp < 4) {
         more_registers<kChainRegs>();
-        failed = chain_warps(J);
+        Armed arm;
+        failed = chain_warps(J, arm);
+        if (threadIdx.x == 0) sm.armed[0] = arm.bars, sm.parity[0] = arm.parity;
     } else {
         fewer_registers<kSideRegs>();
-        failed = side_warps(J);
+        Armed arm;
+        arm(B_KQ, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
+        if (J.nc > 1) arm(B_KQ + 1, 0);
+        failed = side_warps(J, arm);
+        if (threadIdx.x == 160) sm.armed[1] = arm.bars, sm.parity[1] = arm.parity;
     }
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
@@ -972,7 +1013,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
             for (int w = 0; w < 2; ++w)
                 for (int i = 0; i < kBars; ++i)
-                    if (sm.armed[w] >> i & 1) mbar_wait(&sm.bar[i], sm.parity[w] >> i & 1, kPolls);
+                    if (sm.armed[w] >> i & 1) wait_for(&sm.bar[i], sm.parity[w] >> i & 1);
         }
     }
     tc_fence_before();
