@@ -30,11 +30,31 @@ __device__ __forceinline__ float log_decay(const Gates &g, float dt, int h) {
     return (g.dt_softplus ? softplus_f(s) : s) * g.A[h];
 }
 __device__ __forceinline__ float write_gate(const Gates &g, float beta) {
-    return g.beta_sigmoid ? 1.0f / (1.0f + expf(-beta)) : beta;
+    return g.beta_sigmoid ? __fdividef(1.0f, 1.0f + expf(-beta)) : beta;
 }
 // The factor that scales a key or query of squared length ss.
 __device__ __forceinline__ float unit_factor(const Gates &g, float ss) {
-    return g.l2norm ? 1.0f / sqrtf(ss + kNormEps) : 1.0f;
+    return g.l2norm ? rsqrtf(ss + kNormEps) : 1.0f;
+}
+
+// Two fp32 values in a register pair, for the two-wide multiply-add.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Eight consecutive values <-> fp32, past L1 (each state byte is used once per call).
@@ -63,6 +83,48 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
     const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_row(const T *p, uint64_t (&v)[4]) {
+    float f[8];
+    load8_stream(p, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+}
+// Eight state values on their way: loaded now, unpacked when they are needed.
+struct RawBf16 {
+    uint4 w;
+    __device__ __forceinline__ void load(const bf16 *p) { w = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void unpack(uint64_t (&v)[4]) const {
+        float f[8];
+        unpack16(w, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+    }
+};
+struct RawF32 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldcs(reinterpret_cast<const uint4 *>(p));
+        b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void unpack(uint64_t (&v)[4]) const {
+        v[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y));
+        v[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
+        v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
+        v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+};
+template <typename T> struct RawOf;
+template <> struct RawOf<bf16> { using type = RawBf16; };
+template <> struct RawOf<float> { using type = RawF32; };
+template <typename T>
+__device__ __forceinline__ void store_row(T *p, const uint64_t (&v)[4]) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) unpair(v[e], f[2 * e], f[2 * e + 1]);
+    store8_stream(p, f);
 }
 
 // How a warp holds rows of S: LPR lanes a row with 8 consecutive values each, RPW rows side by
@@ -107,33 +169,38 @@ __device__ __forceinline__ float sum_lanes(float v) {
 }
 
 // One token on the rows a warp holds: S <- a S + u k^T with u = b (v - a S k), and scale * S q.
-// k, q: this lane's 8 values, unscaled; rk, rq: their factors (rq with the output scale); kq: their
-// scaled product k . q without the output scale.  vrow: the value of row (index % RT), where index
-// = this lane's sum.  Returns y of that row in the lanes of index >= RT.
+// k, q: this lane's 8 values, unscaled; rk, rq: their factors (rq with the output scale); ukq: their
+// scaled product k . q with the output scale.  vrow: the value of row (index % RT), where index = this
+// lane's sum.  Returns y of that row in the lanes of index >= RT.
 template <typename Map>
-__device__ __forceinline__ float token_rows(float (&S)[Map::RT][8], const float (&k)[8], const float (&q)[8], float rk,
-                                            float rq, float ukq, float a, float b, float vrow, int lane) {
+__device__ __forceinline__ float token_rows(uint64_t (&S)[Map::RT][4], const uint64_t (&k)[4], const uint64_t (&q)[4],
+                                            float rk, float rq, float ukq, float a, float b, float vrow, int lane) {
     constexpr int RT = Map::RT;
     float val[Map::NV];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        float p = 0.0f, o = 0.0f;
+        uint64_t p = mul2(S[r][0], k[0]), o = mul2(S[r][0], q[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            p = fmaf(S[r][e], k[e], p);
-            o = fmaf(S[r][e], q[e], o);
+        for (int e = 1; e < 4; ++e) {
+            p = fma2(S[r][e], k[e], p);
+            o = fma2(S[r][e], q[e], o);
         }
-        val[r] = p;
-        val[RT + r] = o;
+        float lo, hi;
+        unpair(p, lo, hi);
+        val[r] = lo + hi;
+        unpair(o, lo, hi);
+        val[RT + r] = lo + hi;
     }
     const float sum = reduce_rows<Map::NV, Map::LPR / 2>(val, lane);
     const float u_own = b * (vrow - a * rk * sum);  // meaningful in the lanes that hold S k
     const int base = lane & ~(Map::LPR - 1), idx = (lane & (Map::LPR - 1)) / Map::SHARE;
+    const uint64_t a2 = pair(a, a);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const float uk = __shfl_sync(0xffffffffu, u_own, base + r * Map::SHARE) * rk;
+        const uint64_t uk2 = pair(uk, uk);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) S[r][e] = fmaf(a, S[r][e], uk * k[e]);
+        for (int e = 0; e < 4; ++e) S[r][e] = fma2(a2, S[r][e], mul2(uk2, k[e]));
     }
     const float u = __shfl_sync(0xffffffffu, u_own, base + (idx % RT) * Map::SHARE);
     return fmaf(a * rq, sum, u * ukq);

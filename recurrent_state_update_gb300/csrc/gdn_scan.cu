@@ -16,6 +16,7 @@ using namespace gdn;
 namespace {
 
 constexpr int kStage = 16;  // tokens staged in shared memory at a time
+constexpr int64_t kManyRows = 32768;  // rows of all states together from which a lane takes most of them
 
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxOrdered = 4096;  // sequences up to which the longest go first (the order is found by counting)
@@ -96,12 +97,18 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const ScanParams p) {
     }
 }
 
+// Eight staged values.
+__device__ __forceinline__ void stage_row(const float *p, uint64_t (&v)[4]) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
 // Block (head and share of its rows, sequence in the plan's order).
 template <typename StateT, typename ActT, int P, int N, int RT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
     using Map = RowMap<N, RT>;
     constexpr int ROWS = Map::ROWS * WARPS, SPLITS = P / ROWS, GROUPS = WARPS * Map::RPW;  // staging: a token a group of lanes
-    constexpr int PASS = (kStage + GROUPS - 1) / GROUPS;
+    constexpr int PASS = (kStage + GROUPS - 1) / GROUPS, VPASS = (kStage * ROWS + 32 * WARPS - 1) / (32 * WARPS);
     __shared__ __align__(16) float ks[kStage][N], qs[kStage][N];
     __shared__ float vs[kStage][ROWS];
     __shared__ float as[kStage], bs[kStage], kqs[kStage];
@@ -119,16 +126,17 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
     const int lrow = brow + (idx % RT) * Map::RPW + sub;  // the block's row whose sum this lane gets
     StateT *pool = static_cast<StateT *>(p.pool);
     const int64_t off = ((int64_t)h * P + row0 + sub) * N + col;
-    float S[RT][8] = {};
+    uint64_t S[RT][4] = {};  // (pairs of zeros)
     if (slot >= 0 && p.has_init && p.has_init[s]) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) load8_stream(pool + slot * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
+        for (int r = 0; r < RT; ++r) load_row(pool + slot * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
     }
     const ActT *v = static_cast<const ActT *>(p.v), *k = static_cast<const ActT *>(p.k), *q = static_cast<const ActT *>(p.q);
     ActT *y = static_cast<ActT *>(p.y);
     const int64_t rowk = (int64_t)p.G * N, rowv = (int64_t)p.H * P;
     const int group = tid / Map::LPR;
     float kr[PASS][8], qr[PASS][8], dtr[PASS], br[PASS];
+    ActT vr[VPASS];
     auto fetch = [&](int base) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
@@ -143,6 +151,12 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
                 for (int e = 0; e < 8; ++e) kr[i][e] = qr[i][e] = 0.0f;
                 dtr[i] = br[i] = 0.0f;
             }
+        }
+#pragma unroll
+        for (int x = 0; x < VPASS; ++x) {
+            const int c = tid + x * 32 * WARPS, j = base + c / ROWS;
+            vr[x] = c < kStage * ROWS && j < len ? v[(t0 + j) * rowv + (int64_t)h * P + split * ROWS + c % ROWS]
+                                                 : from_f32<ActT>(0.0f);
         }
     };
     fetch(0);
@@ -176,31 +190,49 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
                 }
             }
         }
-        for (int c = tid; c < kStage * ROWS; c += 32 * WARPS) {
-            const int j = c / ROWS, r = c % ROWS;
-            vs[j][r] = j < L ? to_f32(v[(t0 + base + j) * rowv + (int64_t)h * P + split * ROWS + r]) : 0.0f;
+#pragma unroll
+        for (int x = 0; x < VPASS; ++x) {
+            const int c = tid + x * 32 * WARPS;
+            if (c < kStage * ROWS) vs[c / ROWS][c % ROWS] = to_f32(vr[x]);
         }
         __syncthreads();
         fetch(base + kStage);
-        for (int j = 0; j < L; ++j) {
-            float kc[8], qc[8];
-            load8(&ks[j][col], kc);
-            load8(&qs[j][col], qc);
-            const float out = token_rows<Map>(S, kc, qc, 1.0f, 1.0f, kqs[j], as[j], bs[j], vs[j][lrow], lane);
-            const int t = t0 + base + j;
-            if (idx >= RT && (lane & (Map::SHARE - 1)) == 0)
-                y[(int64_t)t * rowv + (int64_t)h * P + split * ROWS + lrow] = from_f32<ActT>(out);
-            const int done = base + j + 1;
-            const int32_t cs = ckpt_slot(p, s, done, tid == 0 && blockIdx.x == 0);
-            if (cs >= 0) {
+        ActT *yt = y + (int64_t)(t0 + base) * rowv + (int64_t)h * P + split * ROWS + lrow;
+        // with few rows a lane the next token's operands wait in registers; with many, other warps hide them
+        constexpr bool AHEAD = RT <= 2;
+        uint64_t kc[4], qc[4];
+        float ac = as[0], bc = bs[0], kqc = kqs[0], vc = vs[0][lrow];
+        stage_row(&ks[0][col], kc);
+        stage_row(&qs[0][col], qc);
+#pragma unroll 1
+        for (int j = 0; j < L; ++j, yt += rowv) {
+            uint64_t kn[4], qn[4];
+            const int jn = min(j + 1, kStage - 1);
+            float an, bn, kqn, vn;
+            auto next = [&] {
+                an = as[jn], bn = bs[jn], kqn = kqs[jn], vn = vs[jn][lrow];
+                stage_row(&ks[jn][col], kn);
+                stage_row(&qs[jn][col], qn);
+            };
+            if (AHEAD) next();
+            const float out = token_rows<Map>(S, kc, qc, 1.0f, 1.0f, kqc, ac, bc, vc, lane);
+            if (!AHEAD) next();
+            if (idx >= RT && (lane & (Map::SHARE - 1)) == 0) *yt = from_f32<ActT>(out);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) store8_stream(pool + cs * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
+            for (int e = 0; e < 4; ++e) kc[e] = kn[e], qc[e] = qn[e];
+            ac = an, bc = bn, kqc = kqn, vc = vn;
+            if (p.ckpt_slots) {
+                const int32_t cs = ckpt_slot(p, s, base + j + 1, tid == 0 && blockIdx.x == 0);
+                if (cs >= 0) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) store_row(pool + cs * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
+                }
             }
         }
     }
     if (slot >= 0) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) store8_stream(pool + slot * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
+        for (int r = 0; r < RT; ++r) store_row(pool + slot * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
     }
 }
 
@@ -212,12 +244,30 @@ int launch_tokens(const ScanParams &p, cudaStream_t st) {
     return launch_status();
 }
 
+// Rows a lane: a token costs a warp about 90 instructions and 25 a row, so many rows keep the SMs' issue
+// slots for the rows and few make many warps.  Measured on 32 heads of 128 x 128 with fp32 states: 16
+// sequences of 500 tokens 1.02 ms with 8 rows, 1.23 with 4, 1.68 with 2; one of 1000 tokens 0.50, 0.43, 0.40.
 template <typename StateT, typename ActT>
 int dispatch_tokens(const ScanParams &p, int P, int N, cudaStream_t st) {
-    if (P == 128 && N == 128) return launch_tokens<StateT, ActT, 128, 128, 2, 4>(p, st);
-    if (P == 64 && N == 128) return launch_tokens<StateT, ActT, 64, 128, 2, 4>(p, st);
-    if (P == 64 && N == 64) return launch_tokens<StateT, ActT, 64, 64, 2, 4>(p, st);
-    if (P == 32 && N == 64) return launch_tokens<StateT, ActT, 32, 64, 2, 4>(p, st);
+    const int64_t rows = (int64_t)p.nseq * p.H * P;
+    if (P == 128 && N == 128) {
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 128, 128, 8, 4>(p, st);
+        if (rows >= kManyRows / 4) return launch_tokens<StateT, ActT, 128, 128, 4, 4>(p, st);
+        return launch_tokens<StateT, ActT, 128, 128, 2, 8>(p, st);
+    }
+    if (P == 64 && N == 128) {
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 128, 8, 4>(p, st);
+        if (rows >= kManyRows / 4) return launch_tokens<StateT, ActT, 64, 128, 4, 4>(p, st);
+        return launch_tokens<StateT, ActT, 64, 128, 2, 8>(p, st);
+    }
+    if (P == 64 && N == 64) {
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 64, 4, 4>(p, st);
+        return launch_tokens<StateT, ActT, 64, 64, 2, 4>(p, st);
+    }
+    if (P == 32 && N == 64) {
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 32, 64, 4, 2>(p, st);
+        return launch_tokens<StateT, ActT, 32, 64, 2, 4>(p, st);
+    }
     if (P == 16 && N == 16) return launch_tokens<StateT, ActT, 16, 16, 1, 1>(p, st);
     return MAMBA_EUNSUPPORTED;
 }
