@@ -422,56 +422,91 @@ def mamba_chunk_scan_noalloc(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, x,
 # gated delta rule layers
 # ------------------------------------------------------------------------------------------
 
-def _elements(what, **tensors):
-    """Raises ValueError when a tensor has fewer elements than the call reads or writes."""
-    for name, (t, want) in tensors.items():
-        if t is not None and t.numel() < want:
-            raise ValueError(f"{what}: {name} needs {want} elements, got {t.numel()}")
+_gdn_types = None  # torch dtypes by code, and the current stream's handle
 
 
-def _out_scale(desc, scale):
-    return desc.d_state ** -0.5 if scale is None else float(scale)
+def _gdn_setup():
+    global _gdn_types
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    now = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _gdn_types = ({MAMBA_F32: torch.float32, MAMBA_BF16: torch.bfloat16}, torch.int32, torch.uint8, now)
+    return _gdn_types
+
+
+def _gdn_refuse(what, tensors):
+    """Raises the ValueError of the first of (name, tensor or None, dtype, least elements or -1, contiguous)
+    that breaks its line.  Called when a call's quick checks have found that one does."""
+    for name, t, want, least, dense in tensors:
+        if t is None:
+            continue
+        _expect(what, **{name: (t, want)})
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name}: expected a CUDA tensor")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"{what}: {name}: expected a contiguous tensor")
+        if t.numel() < least:
+            raise ValueError(f"{what}: {name} needs {least} elements, got {t.numel()}")
+    raise ValueError(f"{what}: bad arguments")
+
+
+def _gdn_pointers(what, tensors):
+    """Device pointers of (name, tensor or None, dtype, least elements, contiguous), each checked.  A decode
+    step's kernel takes a few microseconds, so the checks of a good call are kept to attribute reads."""
+    out = []
+    for name, t, want, least, dense in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not want or not t.is_cuda or t.numel() < least or (dense and not t.is_contiguous()):
+            _gdn_refuse(what, tensors)
+        out.append(t.data_ptr())
+    return out
 
 
 def gdn_state_update(desc: LayerDesc, ssm_pool, slot_ids, xbc, dt, beta, A, y, *, scratch_slots=None, dt_bias=None,
                      dt_softplus=True, beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
     """The gated delta rule's step over (batch, ntok, conv_dim) convolved channels v | k | q, in
     place on the pool (or into ``scratch_slots``).  ``scale`` defaults to d_state ** -0.5."""
-    st, _, act, dtt, f32, i32, _ = _layer_dtypes(desc)
-    _expect("gdn_state_update", ssm_pool=(ssm_pool, st), slot_ids=(slot_ids, i32), xbc=(xbc, act), dt=(dt, dtt),
-            beta=(beta, dtt), A=(A, f32), y=(y, act), scratch_slots=(scratch_slots, i32), dt_bias=(dt_bias, f32),
-            err_word=(err_word, i32))
-    batch, ntok = int(slot_ids.shape[0]), int(xbc.shape[1])
-    rows, H = batch * ntok, desc.nheads
-    _elements("gdn_state_update", xbc=(xbc, rows * (H * desc.head_dim + 2 * desc.n_groups * desc.d_state)),
-              dt=(dt, rows * H), beta=(beta, rows * H), A=(A, H), y=(y, rows * H * desc.head_dim),
-              scratch_slots=(scratch_slots, rows), dt_bias=(dt_bias, H))
-    rc = lib().gdn_state_update(ctypes.byref(desc), _ptr(ssm_pool), ssm_pool.stride(0), ssm_pool.shape[0],
-                                _cptr(slot_ids), _cptr(scratch_slots), batch, ntok, _cptr(xbc), _cptr(dt), _cptr(beta),
-                                _cptr(A), _cptr(dt_bias), int(bool(dt_softplus)), int(bool(beta_sigmoid)),
-                                int(bool(qk_l2norm)), _out_scale(desc, scale), _cptr(y), _ptr(err_word),
-                                _stream(stream))
-    _check(rc, "gdn_state_update")
+    code, i32, _, now = _gdn_types or _gdn_setup()
+    H, P, N = desc.nheads, desc.head_dim, desc.d_state
+    act, dtt, f32 = code[desc.act_dtype], code[desc.dt_dtype], code[MAMBA_F32]
+    batch, ntok = slot_ids.shape[0], xbc.shape[1]
+    rows = batch * ntok
+    pool, ids, scr, xp, dp, bp, ap, bias, yp, err = _gdn_pointers("gdn_state_update", (
+        ("ssm_pool", ssm_pool, code[desc.state_dtype], -1, False), ("slot_ids", slot_ids, i32, -1, True),
+        ("scratch_slots", scratch_slots, i32, rows, True), ("xbc", xbc, act, rows * (H * P + 2 * desc.n_groups * N), True),
+        ("dt", dt, dtt, rows * H, True), ("beta", beta, dtt, rows * H, True), ("A", A, f32, H, True),
+        ("dt_bias", dt_bias, f32, H, True), ("y", y, act, rows * H * P, True), ("err_word", err_word, i32, 1, False)))
+    rc = (_lib or lib()).gdn_state_update(ctypes.byref(desc), pool, ssm_pool.stride(0), ssm_pool.shape[0], ids, scr, batch,
+                                          ntok, xp, dp, bp, ap, bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
+                                          1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, err,
+                                          now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "gdn_state_update")
 
 
 def gdn_state_update_int8(desc: LayerDesc, store, entries, xbc, dt, beta, A, y, *, dt_bias=None, dt_softplus=True,
                           beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
     """The gated delta rule's step of one token on int8 entries (the layout of mamba_ckpt_store_int8),
     read, updated and requantised in place.  ``scale`` defaults to d_state ** -0.5."""
-    _, _, act, dtt, f32, i32, _ = _layer_dtypes(desc)
-    _expect("gdn_state_update_int8", entries=(entries, i32), xbc=(xbc, act), dt=(dt, dtt), beta=(beta, dtt), A=(A, f32),
-            y=(y, act), dt_bias=(dt_bias, f32), err_word=(err_word, i32))
-    batch, H = int(entries.shape[0]), desc.nheads
-    _elements("gdn_state_update_int8", xbc=(xbc, batch * (H * desc.head_dim + 2 * desc.n_groups * desc.d_state)),
-              dt=(dt, batch * H), beta=(beta, batch * H), A=(A, H), y=(y, batch * H * desc.head_dim),
-              dt_bias=(dt_bias, H))
-    eb = mamba_int8_entry_bytes(desc)
-    rc = lib().gdn_state_update_int8(ctypes.byref(desc), _cptr(store), (store.numel() * store.element_size()) // max(1, eb),
-                                     _cptr(entries), batch, _cptr(xbc), _cptr(dt), _cptr(beta), _cptr(A),
-                                     _cptr(dt_bias), int(bool(dt_softplus)), int(bool(beta_sigmoid)),
-                                     int(bool(qk_l2norm)), _out_scale(desc, scale), _cptr(y), _ptr(err_word),
-                                     _stream(stream))
-    _check(rc, "gdn_state_update_int8")
+    code, i32, u8, now = _gdn_types or _gdn_setup()
+    H, P, N = desc.nheads, desc.head_dim, desc.d_state
+    act, dtt, f32 = code[desc.act_dtype], code[desc.dt_dtype], code[MAMBA_F32]
+    batch = entries.shape[0]
+    sp, ids, xp, dp, bp, ap, bias, yp, err = _gdn_pointers("gdn_state_update_int8", (
+        ("store", store, store.dtype, -1, True), ("entries", entries, i32, -1, True),
+        ("xbc", xbc, act, batch * (H * P + 2 * desc.n_groups * N), True), ("dt", dt, dtt, batch * H, True),
+        ("beta", beta, dtt, batch * H, True), ("A", A, f32, H, True), ("dt_bias", dt_bias, f32, H, True),
+        ("y", y, act, batch * H * P, True), ("err_word", err_word, i32, 1, False)))
+    h = _lib or lib()
+    ref = ctypes.byref(desc)
+    rc = h.gdn_state_update_int8(ref, sp, store.numel() * store.element_size() // (h.mamba_int8_entry_bytes(ref) or 1), ids,
+                                 batch, xp, dp, bp, ap, bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
+                                 1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, err,
+                                 now(store.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "gdn_state_update_int8")
 
 
 def gdn_chunk_scan_workspace_bytes(desc: LayerDesc, total_tokens: int, nseq: int) -> int:
@@ -483,22 +518,22 @@ def gdn_chunk_scan(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, v, k, q, dt,
                    beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
     """The gated delta rule over a varlen prefill batch; final states and checkpoints written into the
     pool.  ``scale`` defaults to d_state ** -0.5."""
-    st, _, act, dtt, f32, i32, u8 = _layer_dtypes(desc)
-    _expect("gdn_chunk_scan", ssm_pool=(ssm_pool, st), cu_seqlens=(cu_seqlens, i32), slot_ids=(slot_ids, i32), v=(v, act),
-            k=(k, act), q=(q, act), dt=(dt, dtt), beta=(beta, dtt), A=(A, f32), y=(y, act),
-            has_initial_state=(has_initial_state, u8), ckpt_slots=(ckpt_slots, i32), dt_bias=(dt_bias, f32),
-            err_word=(err_word, i32))
-    nseq, total = int(cu_seqlens.shape[0]) - 1, int(v.shape[0])
-    H, GN = desc.nheads, desc.n_groups * desc.d_state
-    _elements("gdn_chunk_scan", v=(v, total * H * desc.head_dim), k=(k, total * GN), q=(q, total * GN),
-              dt=(dt, total * H), beta=(beta, total * H), A=(A, H), y=(y, total * H * desc.head_dim),
-              slot_ids=(slot_ids, nseq), has_initial_state=(has_initial_state, nseq), dt_bias=(dt_bias, H))
-    max_ckpt = int(ckpt_slots.shape[1]) if ckpt_slots is not None else 0
-    rc = lib().gdn_chunk_scan(ctypes.byref(desc), _ptr(ssm_pool), ssm_pool.stride(0), ssm_pool.shape[0],
-                              _cptr(cu_seqlens), nseq, total, _cptr(slot_ids), _cptr(has_initial_state),
-                              _cptr(ckpt_slots), max_ckpt, int(ckpt_interval), _cptr(v), _cptr(k), _cptr(q), _cptr(dt),
-                              _cptr(beta), _cptr(A), _cptr(dt_bias), int(bool(dt_softplus)), int(bool(beta_sigmoid)),
-                              int(bool(qk_l2norm)), _out_scale(desc, scale), _cptr(y), _ptr(workspace),
-                              0 if workspace is None else workspace.numel() * workspace.element_size(),
-                              _ptr(err_word), _stream(stream))
-    _check(rc, "gdn_chunk_scan")
+    code, i32, u8, now = _gdn_types or _gdn_setup()
+    H, P, N = desc.nheads, desc.head_dim, desc.d_state
+    act, dtt, f32 = code[desc.act_dtype], code[desc.dt_dtype], code[MAMBA_F32]
+    nseq, total, GN = cu_seqlens.shape[0] - 1, v.shape[0], desc.n_groups * N
+    pool, cu, ids, init, ckpt, vp, kp, qp, dp, bp, ap, bias, yp, wp, err = _gdn_pointers("gdn_chunk_scan", (
+        ("ssm_pool", ssm_pool, code[desc.state_dtype], -1, False), ("cu_seqlens", cu_seqlens, i32, -1, True),
+        ("slot_ids", slot_ids, i32, nseq, True), ("has_initial_state", has_initial_state, u8, nseq, True),
+        ("ckpt_slots", ckpt_slots, i32, -1, True), ("v", v, act, total * H * P, True), ("k", k, act, total * GN, True),
+        ("q", q, act, total * GN, True), ("dt", dt, dtt, total * H, True), ("beta", beta, dtt, total * H, True),
+        ("A", A, f32, H, True), ("dt_bias", dt_bias, f32, H, True), ("y", y, act, total * H * P, True),
+        ("workspace", workspace, workspace.dtype, -1, True), ("err_word", err_word, i32, 1, False)))
+    rc = (_lib or lib()).gdn_chunk_scan(ctypes.byref(desc), pool, ssm_pool.stride(0), ssm_pool.shape[0], cu, nseq, total, ids,
+                                        init, ckpt, 0 if ckpt_slots is None else ckpt_slots.shape[1], ckpt_interval, vp, kp,
+                                        qp, dp, bp, ap, bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
+                                        1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, wp,
+                                        workspace.numel() * workspace.element_size(), err,
+                                        now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "gdn_chunk_scan")

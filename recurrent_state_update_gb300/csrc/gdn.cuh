@@ -92,6 +92,10 @@ __device__ __forceinline__ void load_row(const T *p, uint64_t (&v)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
 }
+__device__ __forceinline__ void load_row_shared(const float *p, uint64_t (&v)[4]) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
 // Eight state values on their way: loaded now, unpacked when they are needed.
 struct RawBf16 {
     uint4 w;
@@ -132,9 +136,8 @@ __device__ __forceinline__ void store_row(T *p, const uint64_t (&v)[4]) {
 template <int N, int RT_>
 struct RowMap {
     static constexpr int LPR = N / 8, RPW = 32 / LPR, RT = RT_, ROWS = RPW * RT;
-    static constexpr int NV = 2 * RT;        // sums a lane has: S k and S q of each of its rows
-    static constexpr int SHARE = LPR / NV;   // lanes that end up with the same sum
-    static_assert(LPR >= NV, "more sums than lanes of a row");
+    static constexpr int SHARE = LPR / RT;   // lanes of a row's that end up with the same row's sum
+    static_assert(LPR >= RT, "more sums than lanes of a row");
 };
 
 // Sums val[0..NV) over the M*2 lanes that differ in the lane bits 2M-1 .. 0.  Halves the number of
@@ -168,42 +171,47 @@ __device__ __forceinline__ float sum_lanes(float v) {
     return v;
 }
 
-// One token on the rows a warp holds: S <- a S + u k^T with u = b (v - a S k), and scale * S q.
-// k, q: this lane's 8 values, unscaled; rk, rq: their factors (rq with the output scale); ukq: their
-// scaled product k . q with the output scale.  vrow: the value of row (index % RT), where index = this
-// lane's sum.  Returns y of that row in the lanes of index >= RT.
+// S x of the rows a warp holds, that of row r in the lanes of index r, where a lane's index is (its place in
+// the row) / SHARE.
 template <typename Map>
-__device__ __forceinline__ float token_rows(uint64_t (&S)[Map::RT][4], const uint64_t (&k)[4], const uint64_t (&q)[4],
-                                            float rk, float rq, float ukq, float a, float b, float vrow, int lane) {
-    constexpr int RT = Map::RT;
-    float val[Map::NV];
+__device__ __forceinline__ float row_sum(const uint64_t (&S)[Map::RT][4], const uint64_t (&x)[4], int lane) {
+    float val[Map::RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        uint64_t p = mul2(S[r][0], k[0]), o = mul2(S[r][0], q[0]);
+    for (int r = 0; r < Map::RT; ++r) {
+        uint64_t p = mul2(S[r][0], x[0]);
 #pragma unroll
-        for (int e = 1; e < 4; ++e) {
-            p = fma2(S[r][e], k[e], p);
-            o = fma2(S[r][e], q[e], o);
-        }
+        for (int e = 1; e < 4; ++e) p = fma2(S[r][e], x[e], p);
         float lo, hi;
         unpair(p, lo, hi);
         val[r] = lo + hi;
-        unpair(o, lo, hi);
-        val[RT + r] = lo + hi;
     }
-    const float sum = reduce_rows<Map::NV, Map::LPR / 2>(val, lane);
-    const float u_own = b * (vrow - a * rk * sum);  // meaningful in the lanes that hold S k
-    const int base = lane & ~(Map::LPR - 1), idx = (lane & (Map::LPR - 1)) / Map::SHARE;
-    const uint64_t a2 = pair(a, a);
+    return reduce_rows<Map::RT, Map::LPR / 2>(val, lane);
+}
+// S <- a S + u (rk k)^T, u of row r from the lanes of index r; a may differ by column (int8 codes carry their
+// scale in it).
+template <typename Map>
+__device__ __forceinline__ void write_rows(uint64_t (&S)[Map::RT][4], const uint64_t (&a)[4], const uint64_t (&k)[4], float u,
+                                           float rk, int lane) {
+    const float own = u * rk;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const float uk = __shfl_sync(0xffffffffu, u_own, base + r * Map::SHARE) * rk;
+    for (int r = 0; r < Map::RT; ++r) {
+        const float uk = __shfl_sync(0xffffffffu, own, (lane & ~(Map::LPR - 1)) + r * Map::SHARE);
         const uint64_t uk2 = pair(uk, uk);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[r][e] = fma2(a2, S[r][e], mul2(uk2, k[e]));
+        for (int e = 0; e < 4; ++e) S[r][e] = fma2(a[e], S[r][e], mul2(uk2, k[e]));
     }
-    const float u = __shfl_sync(0xffffffffu, u_own, base + (idx % RT) * Map::SHARE);
-    return fmaf(a * rq, sum, u * ukq);
+}
+// One token on the rows a warp holds: the new states, and scale * S q of the row of this lane's index.  k, q:
+// this lane's 8 values, unscaled; rk, rq: their factors (rq with the output scale); ukq: their scaled
+// product k . q with the output scale (S q of the new state is a * (S q) + u * (k . q)); v: the row's value.
+template <typename Map>
+__device__ __forceinline__ float token_rows(uint64_t (&S)[Map::RT][4], const uint64_t (&k)[4], const uint64_t (&q)[4],
+                                            float rk, float rq, float ukq, float a, float b, float v, int lane) {
+    const float sq = row_sum<Map>(S, q, lane);
+    const float u = b * (v - a * rk * row_sum<Map>(S, k, lane));
+    const uint64_t a2 = pair(a, a), as[4] = {a2, a2, a2, a2};
+    write_rows<Map>(S, as, k, u, rk, lane);
+    return fmaf(a * rq, sq, u * ukq);
 }
 
 // Checks that hold for every call on a layer; the state shapes are those of the decode kernels.

@@ -97,12 +97,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const ScanParams p) {
     }
 }
 
-// Eight staged values.
-__device__ __forceinline__ void stage_row(const float *p, uint64_t (&v)[4]) {
-    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-}
-
 // Block (head and share of its rows, sequence in the plan's order).
 template <typename StateT, typename ActT, int P, int N, int RT, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
@@ -123,7 +117,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane / Map::LPR, col = (lane & (Map::LPR - 1)) * 8, idx = (lane & (Map::LPR - 1)) / Map::SHARE;
     const int brow = warp * Map::ROWS, row0 = split * ROWS + brow;
-    const int lrow = brow + (idx % RT) * Map::RPW + sub;  // the block's row whose sum this lane gets
+    const int lrow = brow + idx * Map::RPW + sub;  // the block's row whose sum this lane gets
     StateT *pool = static_cast<StateT *>(p.pool);
     const int64_t off = ((int64_t)h * P + row0 + sub) * N + col;
     uint64_t S[RT][4] = {};  // (pairs of zeros)
@@ -202,8 +196,8 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
         constexpr bool AHEAD = RT <= 2;
         uint64_t kc[4], qc[4];
         float ac = as[0], bc = bs[0], kqc = kqs[0], vc = vs[0][lrow];
-        stage_row(&ks[0][col], kc);
-        stage_row(&qs[0][col], qc);
+        load_row_shared(&ks[0][col], kc);
+        load_row_shared(&qs[0][col], qc);
 #pragma unroll 1
         for (int j = 0; j < L; ++j, yt += rowv) {
             uint64_t kn[4], qn[4];
@@ -211,13 +205,13 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
             float an, bn, kqn, vn;
             auto next = [&] {
                 an = as[jn], bn = bs[jn], kqn = kqs[jn], vn = vs[jn][lrow];
-                stage_row(&ks[jn][col], kn);
-                stage_row(&qs[jn][col], qn);
+                load_row_shared(&ks[jn][col], kn);
+                load_row_shared(&qs[jn][col], qn);
             };
             if (AHEAD) next();
             const float out = token_rows<Map>(S, kc, qc, 1.0f, 1.0f, kqc, ac, bc, vc, lane);
             if (!AHEAD) next();
-            if (idx >= RT && (lane & (Map::SHARE - 1)) == 0) *yt = from_f32<ActT>(out);
+            if ((lane & (Map::SHARE - 1)) == 0) *yt = from_f32<ActT>(out);
 #pragma unroll
             for (int e = 0; e < 4; ++e) kc[e] = kn[e], qc[e] = qn[e];
             ac = an, bc = bn, kqc = kqn, vc = vn;

@@ -37,9 +37,12 @@ struct TokenIn {
     float kk, qq, kq;  // this lane's parts of the lengths and of k . q
     __device__ __forceinline__ void load_vectors(const ActT *row, int HP, int GN, int grp, int N, int lane) {
         const int c = (lane & (Map::LPR - 1)) * 8;
+        unpack(row + HP + grp * N + c, row + HP + GN + grp * N + c);
+    }
+    __device__ __forceinline__ void unpack(const ActT *ksrc, const ActT *qsrc) {
         float kf[8], qf[8];
-        load8(row + HP + grp * N + c, kf);
-        load8(row + HP + GN + grp * N + c, qf);
+        load8(ksrc, kf);
+        load8(qsrc, qf);
         kk = qq = kq = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(64) k_gdn_step(const StepArgs p) {
     Raw raw[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) raw[r].load(state + r * Map::RPW * N);
-    const int vrow = row0 + (idx % RT) * Map::RPW + sub;
+    const int vrow = row0 + idx * Map::RPW + sub;
     const int64_t th = (int64_t)i * p.H + h;
     const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.Cd;
     const float v = to_f32(xbc[h * P + vrow]);
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(64) k_gdn_step(const StepArgs p) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) raw[r].unpack(S[r]);
     const float out = token_rows<Map>(S, in.k, in.q, in.rk, in.rq, in.ukq, in.a, in.b, v, lane);
-    if (idx >= RT && (lane & (Map::SHARE - 1)) == 0) static_cast<ActT *>(p.y)[th * P + vrow] = from_f32<ActT>(out);
+    if ((lane & (Map::SHARE - 1)) == 0) static_cast<ActT *>(p.y)[th * P + vrow] = from_f32<ActT>(out);
 #pragma unroll
     for (int r = 0; r < RT; ++r) store_row(state + r * Map::RPW * N, S[r]);
 }
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(64) k_gdn_tokens_step(const StepArgs p) {
     uint64_t S[RT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r) load_row(pool + s * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
-    const int vrow = row0 + (idx % RT) * Map::RPW + sub;
+    const int vrow = row0 + idx * Map::RPW + sub;
     const ActT *xbc = static_cast<const ActT *>(p.xbc);
     ActT *y = static_cast<ActT *>(p.y);
     for (int j = 0; j < p.ntok; ++j) {
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(64) k_gdn_tokens_step(const StepArgs p) {
         in.load_scalars(p.gates, h, p.dt, p.beta, t * p.H + h);
         const float v = to_f32(xbc[t * p.Cd + h * P + vrow]);
         const float out = token_rows<Map>(S, in.k, in.q, in.rk, in.rq, in.ukq, in.a, in.b, v, lane);
-        if (idx >= RT && (lane & (Map::SHARE - 1)) == 0) y[(t * p.H + h) * P + vrow] = from_f32<ActT>(out);
+        if ((lane & (Map::SHARE - 1)) == 0) y[(t * p.H + h) * P + vrow] = from_f32<ActT>(out);
         const int32_t d = p.scratch ? p.scratch[t] : (j == p.ntok - 1 ? s : -1);
         if (d >= 0) {
 #pragma unroll
@@ -162,25 +165,51 @@ struct Int8Args {
 // Codes to fp32 and back without conversion instructions, which run at a quarter of the rate: a byte
 // with its sign bit flipped, as the low mantissa bits of 2^23, is 2^23 + 128 + code; and a sum with 1.5 * 2^23
 // rounds to the nearest integer, ties to even, and holds it in its low bits.
-__device__ __forceinline__ void codes_to_f32(uint2 w, const uint64_t (&scale)[4], uint64_t (&v)[4]) {
+__device__ __forceinline__ void codes_to_f32(uint2 w, uint64_t (&v)[4]) {
     const uint32_t x[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
     const uint64_t bias = pair(-8388736.0f, -8388736.0f);  // -(2^23 + 128)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const uint32_t lo = __byte_perm(x[e >> 1], 0x4b000000u, 0x7440u | (e & 1) * 2);
         const uint32_t hi = __byte_perm(x[e >> 1], 0x4b000000u, 0x7441u + (e & 1) * 2);
-        uint64_t f = pair(__uint_as_float(lo), __uint_as_float(hi));
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(f) : "l"(bias));
-        v[e] = mul2(f, scale[e]);
+        v[e] = pair(__uint_as_float(lo), __uint_as_float(hi));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v[e]) : "l"(bias));
     }
+}
+// The step on codes: S holds them as fp32, sc their columns' scales, which go into the keys and queries of
+// the sums and into the decay.  (Reading sc and k twice leaves the registers to the sums.)
+template <typename Map, typename ActT>
+__device__ __forceinline__ float token_codes(uint64_t (&S)[Map::RT][4], const float *scales, const ActT *ksrc, const ActT *qsrc,
+                                             float rk, float rq, float ukq, float a, float b, float v, int lane) {
+    uint64_t x[4], sc[4];
+    float f[8];
+    auto scaled = [&](const ActT *src) {  // keys or queries times the columns' scales
+        load8(src, f);
+        load_row_shared(scales, sc);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(pair(f[2 * e], f[2 * e + 1]), sc[e]);
+    };
+    scaled(qsrc);
+    const float sq = row_sum<Map>(S, x, lane);
+    scaled(ksrc);
+    const float u = b * (v - a * rk * row_sum<Map>(S, x, lane));
+    load8(ksrc, f);
+    load_row_shared(scales, sc);
+    const uint64_t a2 = pair(a, a);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[e] = pair(f[2 * e], f[2 * e + 1]);
+        sc[e] = mul2(sc[e], a2);
+    }
+    write_rows<Map>(S, sc, x, u, rk, lane);
+    return fmaf(a * rq, sq, u * ukq);
 }
 __device__ __forceinline__ uint2 f32_to_codes(const uint64_t (&v)[4], const uint64_t (&inv)[4]) {
     const uint64_t round = pair(12582912.0f, 12582912.0f);
     uint32_t half[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        uint64_t f = mul2(v[e], inv[e]);  // at most 127 and its rounding error: the nearest integer needs no bound
-        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(f) : "l"(round));
+        const uint64_t f = fma2(v[e], inv[e], round);  // (at most 127 and a rounding error: the nearest integer needs no bound)
         float lo, hi;
         unpair(f, lo, hi);
         half[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
@@ -188,53 +217,12 @@ __device__ __forceinline__ uint2 f32_to_codes(const uint64_t (&v)[4], const uint
     return make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
 }
 
-// Block (head, batch row): all rows of the head, because a scale covers a column of it.  Codes
-// become fp32 on load; the new state is scaled by the new column maxima (a maximum over the warps
-// through shared memory: the order of its updates does not matter) and rounded to the grid of
-// step max/127, as the int8 store does.
-template <typename ActT, int P, int N, int RT>
-__global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(const Int8Args p) {
-    using Map = RowMap<N, RT>;
-    constexpr int WARPS = P / Map::ROWS;
-    __shared__ __align__(16) float top[WARPS][N], inv_s[N];
-    __shared__ float scalars[5];
-    pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
-    pdl_launch_dependents();
-    const int i = blockIdx.y, h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t e = p.entry[i];
-    if (e == -1) return;  // padding row
-    if (e < -1 || e >= p.num_entries) {
-        if (threadIdx.x == 0) flag_error(p.err, MAMBA_ERR_SLOT_RANGE);
-        return;
-    }
-    unsigned char *ent = p.store + e * p.entry_bytes;
-    const int col = (lane & (Map::LPR - 1)) * 8, sub = lane / Map::LPR, row0 = warp * Map::ROWS;
-    const int idx = (lane & (Map::LPR - 1)) / Map::SHARE, vrow = row0 + (idx % RT) * Map::RPW + sub;
-    unsigned char *codes = ent + ((int64_t)h * P + row0 + sub) * N + col;
-    float *scales = reinterpret_cast<float *>(ent + p.scale_off) + (int64_t)h * N + col;
-    uint2 raw[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) raw[r] = __ldcs(reinterpret_cast<const uint2 *>(codes + r * Map::RPW * N));
-    uint64_t sc[4];
-    load_row(scales, sc);
-    const int64_t th = (int64_t)i * p.H + h;
-    const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.Cd;
-    const float v = to_f32(xbc[h * P + vrow]);
-    TokenIn<Map, ActT> in;
-    in.load_vectors(xbc, p.H * P, p.G * N, h / p.HG, N, lane);
-    if (warp == 0) {  // the token's scalars, once for the block
-        in.load_scalars(p.gates, h, p.dt, p.beta, th);
-        if (lane == 0) scalars[0] = in.rk, scalars[1] = in.rq, scalars[2] = in.ukq, scalars[3] = in.a, scalars[4] = in.b;
-    }
-    uint64_t S[RT][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) codes_to_f32(raw[r], sc, S[r]);
-    __syncthreads();
-    const float out = token_rows<Map>(S, in.k, in.q, scalars[0], scalars[1], scalars[2], scalars[3], scalars[4], v, lane);
-    if (idx >= RT && (lane & (Map::SHARE - 1)) == 0) static_cast<ActT *>(p.y)[th * P + vrow] = from_f32<ActT>(out);
+// The largest magnitude in each of this lane's columns over its warp's rows.
+template <typename Map>
+__device__ __forceinline__ void column_maxima(const uint64_t (&S)[Map::RT][4], float *top, int sub) {
     float m[8] = {};
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < Map::RT; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             float lo, hi;
@@ -247,23 +235,78 @@ __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(
 #pragma unroll
         for (int o = Map::LPR; o < 32; o *= 2) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
     if (sub == 0) {
-        *reinterpret_cast<float4 *>(&top[warp][col]) = make_float4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<float4 *>(&top[warp][col + 4]) = make_float4(m[4], m[5], m[6], m[7]);
+        reinterpret_cast<float4 *>(top)[0] = make_float4(m[0], m[1], m[2], m[3]);
+        reinterpret_cast<float4 *>(top)[1] = make_float4(m[4], m[5], m[6], m[7]);
     }
-    __syncthreads();  // (every thread has its scales, too)
+}
+// From the warps' column maxima the new scales, a column a thread, and what codes are formed with.
+template <int WARPS, int N>
+__device__ __forceinline__ void new_scales(const float (*top)[N], float *inv, float *scales) {
     for (int c = threadIdx.x; c < N; c += 32 * WARPS) {
         float t = top[0][c];
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) t = fmaxf(t, top[w][c]);
-        inv_s[c] = t > kLeast ? 127.0f / t : 0.0f;
-        scales[c - col] = t / 127.0f;
+        inv[c] = t > kLeast ? 127.0f / t : 0.0f;
+        scales[c] = t / 127.0f;
     }
+}
+template <typename Map, int N>
+__device__ __forceinline__ void store_codes(unsigned char *codes, const uint64_t (&S)[Map::RT][4], const float *inv) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(inv)[0], b = reinterpret_cast<const ulonglong2 *>(inv)[1];
+    const uint64_t inv2[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int r = 0; r < Map::RT; ++r) __stcs(reinterpret_cast<uint2 *>(codes + r * Map::RPW * N), f32_to_codes(S[r], inv2));
+}
+
+// Block (head, batch row): all rows of the head, because a scale covers a column of it.  Codes
+// become fp32 on load; the new state is scaled by the new column maxima (a maximum over the warps
+// through shared memory) and rounded to the grid of step max/127, as the int8 store does.
+template <typename ActT, int P, int N, int RT>
+__global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(const Int8Args p) {
+    using Map = RowMap<N, RT>;
+    constexpr int WARPS = P / Map::ROWS;
+    __shared__ __align__(16) float top[WARPS][N], inv_s[N];  // inv_s: first the scales
+    __shared__ float scalars[5];
+    pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
+    pdl_launch_dependents();
+    const int i = blockIdx.y, h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t e = p.entry[i];
+    if (e == -1) return;  // padding row
+    if (e < -1 || e >= p.num_entries) {
+        if (threadIdx.x == 0) flag_error(p.err, MAMBA_ERR_SLOT_RANGE);
+        return;
+    }
+    unsigned char *ent = p.store + e * p.entry_bytes;
+    const int col = (lane & (Map::LPR - 1)) * 8, sub = lane / Map::LPR, row0 = warp * Map::ROWS;
+    const int idx = (lane & (Map::LPR - 1)) / Map::SHARE, vrow = row0 + idx * Map::RPW + sub;
+    unsigned char *codes = ent + ((int64_t)h * P + row0 + sub) * N + col;
+    float *scales = reinterpret_cast<float *>(ent + p.scale_off) + (int64_t)h * N + col;
+    uint2 raw[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) raw[r] = __ldcs(reinterpret_cast<const uint2 *>(codes + r * Map::RPW * N));
+    const int64_t th = (int64_t)i * p.H + h;
+    const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.Cd;
+    const ActT *ksrc = xbc + p.H * P + (h / p.HG) * N + col, *qsrc = ksrc + p.G * N;
+    const float v = to_f32(xbc[h * P + vrow]);
+    for (int c = threadIdx.x; c < N; c += 32 * WARPS) inv_s[c] = scales[c - col];
+    if (warp == 0) {  // the token's scalars, once for the block
+        TokenIn<Map, ActT> in;
+        in.unpack(ksrc, qsrc);
+        in.load_scalars(p.gates, h, p.dt, p.beta, th);
+        if (lane == 0) scalars[0] = in.rk, scalars[1] = in.rq, scalars[2] = in.ukq, scalars[3] = in.a, scalars[4] = in.b;
+    }
+    uint64_t S[RT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) codes_to_f32(raw[r], S[r]);
     __syncthreads();
-    uint64_t inv[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) inv[c] = pair(inv_s[col + 2 * c], inv_s[col + 2 * c + 1]);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) __stcs(reinterpret_cast<uint2 *>(codes + r * Map::RPW * N), f32_to_codes(S[r], inv));
+    const float out = token_codes<Map>(S, &inv_s[col], ksrc, qsrc, scalars[0], scalars[1], scalars[2], scalars[3], scalars[4], v,
+                                       lane);
+    if ((lane & (Map::SHARE - 1)) == 0) static_cast<ActT *>(p.y)[th * P + vrow] = from_f32<ActT>(out);
+    column_maxima<Map>(S, &top[warp][col], sub);
+    __syncthreads();  // (every thread has its scales, too)
+    new_scales<WARPS, N>(top, inv_s, scales - col);
+    __syncthreads();
+    store_codes<Map, N>(codes, S, &inv_s[col]);
 }
 
 // Blocks of two warps (P = 16: one) with as many rows a lane as have sums for its 16 lanes: measured at

@@ -310,6 +310,38 @@ def test_int8_step(shape, act, steps):
     assert torch.equal(held.t, want)  # other entries and every conv window are untouched
 
 
+@pytest.mark.parametrize("shape,batch", [(FULL, 330), (SHAPES[1], 200), (SHAPES[3], 450)], ids=ids)
+def test_int8_large_batches(shape, batch):
+    """Many rows: the same bytes as the rows' entries get in small calls, with padding rows and entries out
+    of range among them."""
+    import torch
+    desc = bd.layer_desc(shape)
+    n = batch + 5
+    g = np.random.default_rng(batch)
+    entries = g.permutation(n)[:batch].astype(np.int32)
+    entries[g.permutation(batch)[:9]] = -1
+    entries[g.permutation(batch)[:4]] = n + 3
+    store, codes, scales = _store_views(shape, desc, n)
+    codes.copy_(torch.randint(-127, 128, codes.shape, device="cuda"))
+    scales.copy_(torch.rand(scales.shape, device="cuda") / 1000)
+    A, bias = (to_dev(a, wl.F32) for a in ref.layer(23, shape))
+    x, r, b = (to_dev(a, d) for a, d in zip(ref.inputs(23, shape, (batch,), wl.BF16), (wl.BF16, wl.F32, wl.F32)))
+    outs = []
+    for step in (batch, 7):
+        held = guarded(store)
+        y = torch.full((batch, shape.nheads * shape.head_dim), 7.0, device="cuda", dtype=torch.bfloat16)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(0, batch, step):
+            bd.gdn_state_update_int8(desc, held.t, to_i32(entries[i:i + step]), x[i:i + step], r[i:i + step], b[i:i + step], A,
+                                     y[i:i + step], dt_bias=bias, err_word=err)
+        torch.cuda.synchronize()
+        held.check("store")
+        assert int(err.item()) == bd.MAMBA_ERR_SLOT_RANGE
+        outs.append((held.t.clone(), y))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert not torch.equal(outs[0][0], store)
+
+
 def test_int8_bad_entries_are_flagged():
     import torch
     desc = bd.layer_desc(FULL)
