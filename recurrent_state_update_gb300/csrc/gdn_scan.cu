@@ -311,7 +311,7 @@ extern "C" int gdn_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (launch_pdl(k_gdn_plan, dim3(1), dim3(kPlanThreads), 0, st, p) != cudaSuccess) return MAMBA_ECUDA;
     if (total_tokens == 0) return launch_status();  // only empty sequences
-    if (chunked_eligible(d)) return chunked_launch(p, st);
+    if (chunked_eligible(d)) return chunked_launch(p, P, st);
     const bool sbf = d->state_dtype == MAMBA_BF16, abf = d->act_dtype == MAMBA_BF16;
     if (sbf && abf) return dispatch_tokens<bf16, bf16>(p, P, N, st);
     if (sbf) return dispatch_tokens<bf16, float>(p, P, N, st);

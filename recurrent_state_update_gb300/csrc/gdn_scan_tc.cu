@@ -33,7 +33,7 @@ using namespace umma;
 
 namespace {
 
-constexpr int C = kChunk, TN = 128, TP = 128;
+constexpr int C = kChunk, TN = 128;
 constexpr uint32_t kPolls = umma::kWaitPolls;
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -44,9 +44,9 @@ constexpr uint32_t kBlk = 64 * 128;          // one swizzled block of 64 rows
 constexpr uint32_t kKqBytes = 4 * kBlk;
 struct HeadGates {
     float rk[C];   // e^c |k|
-    float ek[C];   // e^(c_64 - c) |k|
-    float g[C];    // e^c
     float oq[C];   // |q| * scale
+    __half ek[C];  // e^(c_64 - c) |k|, for operands of 11 bits
+    __half g[C];   // e^c, as well
     float last, pad[3];  // e^(c_64)
 };
 constexpr uint32_t kGateBytes = sizeof(HeadGates);
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
         const float nk = sqrtf(kk) * unit_factor(p.gates, kk);
         HeadGates &gt = sm.gates[hh];
         gt.rk[tok] = e * nk;
-        gt.ek[tok] = exp2f(last - run) * nk;
-        gt.g[tok] = e;
+        gt.ek[tok] = __float2half_rn(exp2f(last - run) * nk);
+        gt.g[tok] = __float2half_rn(e);
         gt.oq[tok] = sqrtf(qq) * unit_factor(p.gates, qq) * p.gates.scale;
         if (tok == 0) gt.last = exp2f(last);
         dec.near[tok] = exp2f(fminf(dec.cum[tok & 32] - run, kSpan)) * nk;
@@ -468,23 +468,23 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
 
 constexpr int kChainThreads = 256;       // four warps on the chain, four beside it
 constexpr int kChainRegs = 200, kSideRegs = 56;  // (200 + 56) * 128 registers: what the block is launched with
+constexpr int kRows = 128;               // rows of tensor memory; with head_dim 64 the upper half holds zeros
 constexpr int kRescale = 16;             // chunks between two choices of the rows' powers of two
 
-// What the block waits for: a stage of keys, queries and gates (two), T, A and the values from memory;
-// the products X, U, Q S^T, the increment and Y; the values turned and the queries scaled, the values
-// taken, Y taken.
-enum { B_KQ = 0, B_T = 2, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, B_READY, B_TAKEN, B_YTAKEN, kBars };
+// What the block waits for: keys and gates (two stages), queries, T, A and the values from memory; the
+// products X, U, Q S^T, the increment and Y; the values turned, and R formed of them.
+enum { B_K = 0, B_Q = 2, B_T, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, B_READY, B_TAKEN, kBars };
 
 struct ChainSmem {
     // q: a chunk's queries, and once they are used its outputs on their way to memory; v: its values, first
-    // by token (64 values in a swizzled block of 64 tokens, twice), then by value (128 rows of 64 tokens)
+    // by token (64 values in a swizzled block of 64 tokens, twice), then by value (kRows rows of 64 tokens)
     unsigned char k[2][2 * kBlk], q[2][2 * kBlk], T[kBlk], A[kBlk], v[2 * kBlk];
     HeadGates gates[4];
-    float vmax[TP];          // largest magnitude among a chunk's values, by row
-    float unscale[2][TP];    // a chunk's inverse powers of two, by row
+    float vmax[kRows];        // largest magnitude among a chunk's values, by row
+    float unscale[2][kRows];   // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
-    uint32_t armed[2], parity[2];  // what each half of the block leaves behind (Armed)
+    uint32_t armed[3], parity[3];  // what the issuing warps leave behind (Armed)
 };
 
 // The barriers ever armed with a copy or a product, and the last phase of each: what is waited for
@@ -568,6 +568,7 @@ __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
 }
 
 // One sequence and head, as both halves of the block see it.
+template <int P>
 struct ChainJob {
     const ScanParams &p;
     const WsLayout &ws;
@@ -576,20 +577,22 @@ struct ChainJob {
     int s, h, t0, len, first, nc;
 
     __device__ __forceinline__ const unsigned char *head(int c) const { return ws.head(first + c, h); }
-    __device__ __forceinline__ void load_stage(int c) const {
-        uint64_t *bar = &sm.bar[B_KQ + (c & 1)];
-        const unsigned char *kq = ws.kq(first + c, h / p.HG);
-        mbar_arrive_expect_tx(bar, kKqBytes + kGateBytes);
+    __device__ __forceinline__ const unsigned char *kq(int c) const { return ws.kq(first + c, h / p.HG); }
+    __device__ __forceinline__ void load_keys(int c) const {
+        uint64_t *bar = &sm.bar[B_K + (c & 1)];
+        mbar_arrive_expect_tx(bar, 2 * kBlk + kGateBytes);
+        bulk_g2s(sm.k[c & 1], kq(c), kBlk, bar);
+        bulk_g2s(sm.k[c & 1] + kBlk, kq(c) + 2 * kBlk, kBlk, bar);
         bulk_g2s(&sm.gates[c & 3], head(c) + 2 * kBlk, kGateBytes, bar);
-        bulk_g2s(sm.k[c & 1], kq, kBlk, bar);
-        bulk_g2s(sm.k[c & 1] + kBlk, kq + 2 * kBlk, kBlk, bar);
-        bulk_g2s(sm.q[c & 1], kq + kBlk, kBlk, bar);
-        bulk_g2s(sm.q[c & 1] + kBlk, kq + 3 * kBlk, kBlk, bar);
+    }
+    __device__ __forceinline__ void load_queries(int c) const {
+        mbar_arrive_expect_tx(&sm.bar[B_Q], 2 * kBlk);
+        bulk_g2s(sm.q[c & 1], kq(c) + kBlk, kBlk, &sm.bar[B_Q]);
+        bulk_g2s(sm.q[c & 1] + kBlk, kq(c) + 3 * kBlk, kBlk, &sm.bar[B_Q]);
     }
     __device__ __forceinline__ void load_values(int c) const {
-        mbar_arrive_expect_tx(&sm.bar[B_V], 2 * kBlk);
-        tma_load_2d(sm.v, &vmap, h * TP, t0 + c * C, &sm.bar[B_V]);
-        tma_load_2d(sm.v + kBlk, &vmap, h * TP + 64, t0 + c * C, &sm.bar[B_V]);
+        mbar_arrive_expect_tx(&sm.bar[B_V], P / 64 * kBlk);
+        for (int i = 0; i < P / 64; ++i) tma_load_2d(sm.v + i * kBlk, &vmap, h * P + 64 * i, t0 + c * C, &sm.bar[B_V]);
     }
     __device__ __forceinline__ void load_tile(int c, int i, unsigned char *dst, uint32_t off) const {
         mbar_arrive_expect_tx(&sm.bar[i], kBlk);
@@ -597,28 +600,30 @@ struct ChainJob {
     }
     // into L2, for loads that are needed within a thousand cycles of their issue
     __device__ __forceinline__ void prefetch(int c) const {
-        bulk_prefetch(head(c), 2 * kBlk);
-        for (int i = 0; i < 2; ++i)
+        bulk_prefetch(head(c), kHeadBytes);
+        bulk_prefetch(kq(c), kKqBytes);
+        for (int i = 0; i < P / 64; ++i)
             asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&vmap)),
-                         "r"(h * TP + 64 * i), "r"(t0 + c * C)
+                         "r"(h * P + 64 * i), "r"(t0 + c * C)
                          : "memory");
     }
 };
 
 // The chain's four warps: warp w holds rows 32 w .. + 31 of the state, a row a thread.  Returns whether
 // a wait gave up.
-__device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
+template <int P>
+__device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     const ScanParams &p = J.p;
     ChainSmem &sm = J.sm;
     const int row = threadIdx.x, warp = threadIdx.x >> 5;
     const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);  // (of warp 0: tensor memory's first lane)
     const int32_t slot = p.slot[J.s];
     auto pool_row = [&](int32_t to) {
-        return static_cast<bf16 *>(p.pool) + to * p.stride + ((int64_t)J.h * TP + row) * TN;
+        return static_cast<bf16 *>(p.pool) + to * p.stride + ((int64_t)J.h * P + row) * TN;
     };
     float S[TN];  // times the row's power of two
     {
-        const bool seeded = slot >= 0 && p.has_init && p.has_init[J.s];
+        const bool seeded = row < P && slot >= 0 && p.has_init && p.has_init[J.s];
         const bf16 *src = pool_row(seeded ? slot : 0);
 #pragma unroll
         for (int e = 0; e < TN; e += 8) {
@@ -649,6 +654,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
         mma_commit(&sm.bar[B_X]);
     };
     auto write_state = [&](int32_t to) {
+        if (row >= P) return;
         uint4 *dst = reinterpret_cast<uint4 *>(pool_row(to));
 #pragma unroll
         for (int e = 0; e < TN; e += 8) {
@@ -664,7 +670,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
         const HeadGates &gt = sm.gates[c & 3];
         // 1. X = S K^T, its operand stored at the last chunk's end
         bool rescale = c % kRescale == 0;  // this chunk starts from a new power of two
-        if (!wait_for(&sm.bar[B_KQ + ph], (c >> 1) & 1)) bad = 1;
+        if (!wait_for(&sm.bar[B_K + ph], (c >> 1) & 1)) bad = 1;
         if (!rescale) arm(B_X, x_phase);
         if (!rescale && warp == 0 && elect_one()) issue_x(c);
         if (!wait_for(&sm.bar[B_READY], ph)) bad = 1;
@@ -709,17 +715,20 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
                 float x[32];
                 tmem_ld32(lanes + T_X + 8 * n, x);
                 uint32_t pk[16];
+                const uint64_t sc = pair(scale, scale);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const uint32_t w[4] = {v8[m].x, v8[m].y, v8[m].z, v8[m].w};
                     const float4 r0 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m));
                     const float4 r1 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m) + 4);
-                    const float rk[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+                    const uint64_t rk[4] = {pair(-r0.x, -r0.y), pair(-r0.z, -r0.w), pair(-r1.x, -r1.y), pair(-r1.z, -r1.w)};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        pk[4 * m + i] = pack_f16x2(fmaf(-rk[2 * i], x[8 * m + 2 * i], __uint_as_float(w[i] << 16) * scale),
-                                                   fmaf(-rk[2 * i + 1], x[8 * m + 2 * i + 1],
-                                                        __uint_as_float(w[i] & 0xffff0000u) * scale));
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t v2 = mul2(pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), sc);
+                        float lo, hi;
+                        unpair(fma2(rk[i], pair(x[8 * m + 2 * i], x[8 * m + 2 * i + 1]), v2), lo, hi);
+                        pk[4 * m + i] = pack_f16x2(lo, hi);
+                    }
                 }
                 tmem_put(lanes + T_X + 4 * n, pk);
             }
@@ -732,7 +741,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
             rescale = true;
         }
         if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.bar[B_TAKEN]);  // (after the barrier: the warp has read its values)
-        // 3. U^T = R^T T^T, and the state's part of Y once the last one is taken
+        // 3. U^T = R^T T^T (the side issues the state's part of Y)
         if (warp == 0) {
             if (!bad) arm(B_U, ph);
             if (elect_one() && !bad) {
@@ -742,26 +751,17 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
                     mma_bf16_ts(lanes + T_U, lanes + T_X + kk * 8, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
                 mma_commit(&sm.bar[B_U]);
             }
-            if (c > 0 && !wait_for(&sm.bar[B_YTAKEN], ph ^ 1)) bad = 1;
             if (!wait_for(&sm.bar[B_A], ph)) bad = 1;
-            tc_fence_after();
-            if (!bad) arm(B_OI, ph);
-            if (elect_one() && !bad) {
-                const uint32_t q = smem_u32(sm.q[ph]);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(lanes + T_Y, lanes + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-                mma_commit(&sm.bar[B_OI]);
-            }
         }
-        // 4. U^T rounded, as it is and times e^(c_64 - c) |k|
+        // 4. U^T rounded, as it is and times e^(c_64 - c) |k| (a product of rounded numbers: a conversion from fp32
+        // takes four times as long)
         if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
         tc_fence_after();
 #pragma unroll
         for (int n = 0; n < C; n += 32) {  // 32 tokens: both forms over their own columns
-            float4 w[8];
+            uint4 w[4];  // 8 tokens' factors each
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float4 *>(gt.ek + n + 4 * i);
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(gt.ek + n + 8 * i);
             float u[32];
             tmem_ld32(lanes + T_U + n, u);
             uint32_t pk[16];
@@ -769,9 +769,10 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
             for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(u[2 * i], u[2 * i + 1]);
             tmem_put(lanes + T_U + n, pk);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                pk[i] = pack_f16x2(u[2 * i] * w[i / 2].x, u[2 * i + 1] * w[i / 2].y);
-                pk[i + 1] = pack_f16x2(u[2 * i + 2] * w[i / 2].z, u[2 * i + 3] * w[i / 2].w);
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t f = (&w[i / 4].x)[i & 3];
+                const __half2 e = __hmul2(*reinterpret_cast<const __half2 *>(&pk[i]), *reinterpret_cast<const __half2 *>(&f));
+                pk[i] = *reinterpret_cast<const uint32_t *>(&e);
             }
             tmem_put(lanes + T_U + n + 16, pk);
         }
@@ -826,54 +827,53 @@ __device__ __forceinline__ bool chain_warps(const ChainJob &J, Armed &arm) {
     return false;
 }
 
-// The four warps beside the chain: they turn the values of the next chunk, scale its queries, take the
-// outputs of the last one to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31, the
-// fragments of 32 values by 8 tokens.  Returns whether a wait gave up.
-__device__ __forceinline__ bool side_warps(const ChainJob &J, Armed &arm) {
+// The four warps beside the chain: they turn the values of the next chunk, scale its queries, issue the
+// state's part of Y, take the outputs to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31,
+// the fragments of 32 values by 8 tokens.  Returns whether a wait gave up.
+template <int P>
+__device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     const ScanParams &p = J.p;
     ChainSmem &sm = J.sm;
     const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
-    const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);
+    const bool live = 32 * warp < P;  // this warp's rows are values
+    const uint32_t tm = sm.tmem, lanes = tm + ((uint32_t)(warp * 32) << 16);
     // this lane's 16 bytes (8 values of a token) of a tile by tokens, for 8 tokens from 8 n
     auto token_row = [&](const unsigned char *tile, int n) {
         return smem_u32(tile) + (warp >> 1) * kBlk + swz128_chunk(8 * n + (lane & 7), 4 * (warp & 1) + (lane >> 3));
     };
     int bad = 0;
     for (int c = -1; c < J.nc; ++c) {
-        // the next chunk's values and queries
-        if (c + 1 < J.nc) {
-            const int c1 = c + 1;
-            if (warp == 1) {
-                if (c >= 0 && !wait_for(&sm.bar[B_TAKEN], c & 1)) bad = 1;
-                if (!bad) arm(B_V, c1 & 1);
-                if (elect_one() && !bad) {
-                    if (c >= 0) J.load_values(c1);
-                    if (c1 + 1 < J.nc) J.prefetch(c1 + 1);
+        const int c1 = c + 1;
+        // R of this chunk is formed: its values' place is free, and the state's part of Y can start
+        if (c >= 0 && warp < 2) {
+            if (!wait_for(&sm.bar[B_TAKEN], c & 1)) bad = 1;
+            if (warp == 0 && !bad) {
+                arm(B_OI, c & 1);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t q = smem_u32(sm.q[c & 1]);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+                    mma_commit(&sm.bar[B_OI]);
                 }
             }
-            if (!wait_for(&sm.bar[B_KQ + (c1 & 1)], (c1 >> 1) & 1)) bad = 1;
-            const float *g = sm.gates[c1 & 3].g;
-            {  // queries times e^c, 16 bytes of a token each: tokens 16 apart, in both blocks of 64 elements
-                uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1]) + tid;
-                uint4 u[8];
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = g[16 * i + (tid >> 3)];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = ptr[128 * i];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const __half2 w2 = __float2half2_rn(w[i & 3]);
-                    __half2 *hp = reinterpret_cast<__half2 *>(&u[i]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w2);
-                    ptr[128 * i] = u[i];
-                }
+        }
+        if (warp == 1 && c1 < J.nc && !bad) {
+            arm(B_V, c1 & 1);
+            if (elect_one()) {
+                if (c >= 0) J.load_values(c1);
+                if (c1 + 1 < J.nc) J.prefetch(c1 + 1);
             }
+        }
+        if (c1 < J.nc) {
+            // the next chunk's values, turned in place
             if (!wait_for(&sm.bar[B_V], c1 & 1)) bad = 1;
-            uint32_t v[8][4];  // [n][i]: rows 8 i + T / 4, tokens 8 n + 2 (T % 4) and the next
+            uint32_t v[8][4] = {};  // [n][i]: rows 8 i + T / 4, tokens 8 n + 2 (T % 4) and the next
+            if (live) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) ldmatrix4_trans(v[n], token_row(sm.v, n));
+                for (int n = 0; n < 8; ++n) ldmatrix4_trans(v[n], token_row(sm.v, n));
+            }
             const int L = J.len - c1 * C;
             if (L < C) {  // rows past the sequence's end hold another sequence's values
 #pragma unroll
@@ -904,57 +904,85 @@ __device__ __forceinline__ bool side_warps(const ChainJob &J, Armed &arm) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.bar[B_READY]);
+            // its queries times e^c, in place, 16 bytes of a token each: tokens 16 apart, in both blocks of 64
+            // elements
+            if (!wait_for(&sm.bar[B_K + (c1 & 1)], (c1 >> 1) & 1) || !wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
+            const __half *g = sm.gates[c1 & 3].g + (tid >> 3);
+            uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1]) + tid;
+            uint4 u[8];
+            __half2 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __half2half2(g[16 * i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = ptr[128 * i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                __half2 *hp = reinterpret_cast<__half2 *>(&u[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hp[e] = __hmul2(hp[e], w[i & 3]);
+                ptr[128 * i] = u[i];
+            }
+            fence_async_smem();
         }
-        // the last chunk's outputs, over its queries and from there to memory
+        // this chunk's outputs, over its queries and from there to memory
         if (c >= 0) {
             if (!wait_for(&sm.bar[B_Y], c & 1)) bad = 1;
             tc_fence_after();
-            if (warp == 1 && c + 1 < J.nc && !bad) {
-                arm(B_A, (c + 1) & 1);
-                if (elect_one()) J.load_tile(c + 1, B_A, sm.A, kBlk);
+            if (warp == 1 && !bad) {
+                if (c1 < J.nc) arm(B_A, c1 & 1);
+                if (c + 2 < J.nc) arm(B_K + (c & 1), (c + 2) >> 1 & 1);
+                if (elect_one()) {
+                    if (c1 < J.nc) J.load_tile(c1, B_A, sm.A, kBlk);
+                    if (c + 2 < J.nc) J.load_keys(c + 2);
+                }
             }
-            const float *oq = sm.gates[c & 3].oq + (lane & 3) * 2;
-            float un[4];
+            if (live) {
+                const float *oq = sm.gates[c & 3].oq + (lane & 3) * 2;
+                float un[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
+                for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
 #pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-                const float2 w0 = *reinterpret_cast<const float2 *>(oq + 8 * n), w1 = *reinterpret_cast<const float2 *>(oq + 8 * n + 8);
-                float y[2][8];
-                tmem_frag2(lanes + T_Y + 8 * n, y);
+                for (int n = 0; n < 8; n += 2) {
+                    const float2 w0 = *reinterpret_cast<const float2 *>(oq + 8 * n);
+                    const float2 w1 = *reinterpret_cast<const float2 *>(oq + 8 * n + 8);
+                    float y[2][8];
+                    tmem_frag2(lanes + T_Y + 8 * n, y);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t pk[4];
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t pk[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 w = m ? w1 : w0;
-                        const float *yi = &y[i >> 1][4 * m + 2 * (i & 1)];
-                        const __nv_bfloat162 o = __floats2bfloat162_rn(yi[0] * (w.x * un[i]), yi[1] * (w.y * un[i]));
-                        pk[i] = *reinterpret_cast<const uint32_t *>(&o);
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 w = m ? w1 : w0;
+                            const float *yi = &y[i >> 1][4 * m + 2 * (i & 1)];
+                            const __nv_bfloat162 o = __floats2bfloat162_rn(yi[0] * (w.x * un[i]), yi[1] * (w.y * un[i]));
+                            pk[i] = *reinterpret_cast<const uint32_t *>(&o);
+                        }
+                        stmatrix4_trans(token_row(sm.q[c & 1], n + m), pk);
                     }
-                    stmatrix4_trans(token_row(sm.q[c & 1], n + m), pk);
                 }
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.bar[B_YTAKEN]);
-            if (half_sync_or(2, bad)) return true;
-            const int L = min(C, J.len - c * C), ch = tid & 15;
-            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C + (tid >> 4)) * p.H + J.h) * TP + ch * 8;
-            uint4 o[8];
+        }
+        if (half_sync_or(2, bad)) return true;  // Y is taken, the outputs are staged, the next queries scaled
+        if (c >= 0) {
+            constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
+            const int L = min(C, J.len - c * C), ch = tid % CH, first = tid / CH;
+            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C + first) * p.H + J.h) * P + ch * 8;
+            const unsigned char *src = sm.q[c & 1] + (ch >> 3) * kBlk;
+            uint4 o[C * CH / 128];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)  // (the swizzle repeats every 8 tokens)
-                o[i] = *reinterpret_cast<const uint4 *>(sm.q[c & 1] + (ch >> 3) * kBlk + swz128_chunk(tid >> 4, ch & 7) + 1024 * i);
+            for (int i = 0; i < C * CH / 128; ++i)
+                o[i] = *reinterpret_cast<const uint4 *>(src + swz128_chunk(first + 128 / CH * i, ch & 7));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((tid >> 4) + 8 * i < L) *reinterpret_cast<uint4 *>(dst + (int64_t)i * 8 * p.H * TP) = o[i];
+            for (int i = 0; i < C * CH / 128; ++i)
+                if (first + 128 / CH * i < L) *reinterpret_cast<uint4 *>(dst + (int64_t)i * (128 / CH) * p.H * P) = o[i];
             fence_async_smem();
-            if (c + 2 < J.nc) {
-                if (half_sync_or(2, bad)) return true;  // the queries' place is free
-                if (warp == 1) {
-                    arm(B_KQ + (c & 1), (c + 2) >> 1 & 1);
-                    if (elect_one()) J.load_stage(c + 2);
-                }
+        }
+        if (c + 2 < J.nc) {
+            if (c >= 0 && half_sync_or(2, bad)) return true;  // the queries' place is free
+            if (warp == 1) {
+                arm(B_Q, c & 1);
+                if (elect_one()) J.load_queries(c + 2);
             }
         }
     }
@@ -962,6 +990,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob &J, Armed &arm) {
 }
 
 // Block (sequence in the plan's order, head).
+template <int P>
 __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,
                                                                 const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char chain_smem[];
@@ -972,17 +1001,18 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, t0 = p.cu[s], len = p.cu[s + 1] - t0;
     const int32_t slot = p.slot[s];
     if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
-    const ChainJob J = {p, ws, vmap, sm, s, h, t0, len, meta_chunks(p)[s], (len + C - 1) / C};
+    const ChainJob<P> J = {p, ws, vmap, sm, s, h, t0, len, meta_chunks(p)[s], (len + C - 1) / C};
     const int warp = threadIdx.x >> 5;
     if (warp == 5 && elect_one()) {
         for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i >= B_READY ? 4 : 1);
         fence_mbar_init();
         tma_prefetch_desc(&vmap);
-        J.load_stage(0);
+        J.load_keys(0);
         J.load_values(0);
+        J.load_queries(0);
         J.load_tile(0, B_T, sm.T, 0);
         J.load_tile(0, B_A, sm.A, kBlk);
-        if (J.nc > 1) J.load_stage(1);
+        if (J.nc > 1) J.load_keys(1);
     }
     if (warp == 0) {
         tmem_alloc(&sm.tmem, 256);
@@ -1001,17 +1031,18 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     } else {
         fewer_registers<kSideRegs>();
         Armed arm;
-        arm(B_KQ, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
-        if (J.nc > 1) arm(B_KQ + 1, 0);
+        arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
+        if (J.nc > 1) arm(B_K + 1, 0);
         failed = side_warps(J, arm);
-        if (threadIdx.x == 160) sm.armed[1] = arm.bars, sm.parity[1] = arm.parity;
+        if (threadIdx.x == 128) sm.armed[1] = arm.bars, sm.parity[1] = arm.parity;  // the products of the side's first warp
+        if (threadIdx.x == 160) sm.armed[2] = arm.bars, sm.parity[2] = arm.parity;  // the loads of its second
     }
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
         // the same bounded time to finish before its memory is released
         if (warp == 4 && elect_one()) {
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
-            for (int w = 0; w < 2; ++w)
+            for (int w = 0; w < 3; ++w)
                 for (int i = 0; i < kBars; ++i)
                     if (sm.armed[w] >> i & 1) wait_for(&sm.bar[i], sm.parity[w] >> i & 1);
         }
@@ -1039,7 +1070,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Rows of tokens x (heads * 128) values, in swizzled boxes of 64 tokens x 64 values; rows past the end
+// Rows of tokens x (heads * head_dim) values, in swizzled boxes of 64 tokens x 64 values; rows past the end
 // read as zero.
 bool value_map(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows) {
     EncodeTiledFn enc = encode_fn();
@@ -1054,7 +1085,8 @@ bool value_map(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows) {
 }  // namespace
 
 bool chunked_eligible(const mamba_layer_desc *d) {
-    return d->act_dtype == MAMBA_BF16 && d->state_dtype == MAMBA_BF16 && d->head_dim == TP && d->d_state == TN;
+    return d->act_dtype == MAMBA_BF16 && d->state_dtype == MAMBA_BF16 && (d->head_dim == 64 || d->head_dim == 128) &&
+           d->d_state == TN;
 }
 
 size_t chunked_workspace_bytes(const mamba_layer_desc *d, int T, int nseq) {
@@ -1062,19 +1094,20 @@ size_t chunked_workspace_bytes(const mamba_layer_desc *d, int T, int nseq) {
     return (size_t)(scan_max_chunks(T, nseq) * ws.chunk_bytes());
 }
 
-int chunked_launch(const ScanParams &p, cudaStream_t st) {
+int chunked_launch(const ScanParams &p, int head_dim, cudaStream_t st) {
     const WsLayout ws = {p.ws, p.H, p.G};
     CUtensorMap vmap;
-    if (!value_map(&vmap, p.v, (uint64_t)p.H * TP, (uint64_t)p.T)) return MAMBA_ECUDA;
+    if (!value_map(&vmap, p.v, (uint64_t)p.H * head_dim, (uint64_t)p.T)) return MAMBA_ECUDA;
     const bool pairs = p.HG % 2 == 0;  // heads of a group share its products, two a block
     auto prep = pairs ? k_gdn_prep<2> : k_gdn_prep<1>;
-    const size_t prep_smem = (pairs ? sizeof(PrepSmem<2>) : sizeof(PrepSmem<1>)) + 1024, chain = sizeof(ChainSmem) + 1024;
+    auto chain = head_dim == 128 ? k_gdn_chain<128> : k_gdn_chain<64>;
+    const size_t prep_smem = (pairs ? sizeof(PrepSmem<2>) : sizeof(PrepSmem<1>)) + 1024, chain_smem = sizeof(ChainSmem) + 1024;
     if (cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep_smem) != cudaSuccess ||
-        cudaFuncSetAttribute(k_gdn_chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain) != cudaSuccess)
+        cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain_smem) != cudaSuccess)
         return MAMBA_ECUDA;
     const dim3 grid((unsigned)scan_max_chunks(p.T, p.nseq), (unsigned)(pairs ? p.H / 2 : p.H));
     if (launch_pdl(prep, grid, dim3(kPrepThreads), prep_smem, st, p, ws) != cudaSuccess) return MAMBA_ECUDA;
-    if (launch_pdl(k_gdn_chain, dim3((unsigned)((int64_t)p.nseq * p.H)), dim3(kChainThreads), chain, st, p, ws, vmap) != cudaSuccess)
+    if (launch_pdl(chain, dim3((unsigned)((int64_t)p.nseq * p.H)), dim3(kChainThreads), chain_smem, st, p, ws, vmap) != cudaSuccess)
         return MAMBA_ECUDA;
     return launch_status();
 }
