@@ -55,12 +55,12 @@ static_assert(kGateBytes % 16 == 0, "bulk copy size");
 
 struct WsLayout {
     unsigned char *base;
-    int H, G;
-    __host__ __device__ int64_t chunk_bytes() const { return (int64_t)G * kKqBytes + (int64_t)H * kHeadBytes; }
-    __device__ unsigned char *kq(int chunk, int g) const { return base + chunk * chunk_bytes() + (int64_t)g * kKqBytes; }
-    __device__ unsigned char *head(int chunk, int h) const {
-        return base + chunk * chunk_bytes() + (int64_t)G * kKqBytes + (int64_t)h * kHeadBytes;
-    }
+    int64_t heads, stride;  // of a chunk: offset of the heads' part, bytes
+    WsLayout(unsigned char *b, int H, int G)
+        : base(b), heads((int64_t)G * kKqBytes), stride((int64_t)G * kKqBytes + (int64_t)H * kHeadBytes) {}
+    __host__ __device__ int64_t chunk_bytes() const { return stride; }
+    __device__ unsigned char *kq(int chunk, int g) const { return base + chunk * stride + (int64_t)g * kKqBytes; }
+    __device__ unsigned char *head(int chunk, int h) const { return base + chunk * stride + heads + (int64_t)h * kHeadBytes; }
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -484,7 +484,7 @@ struct ChainSmem {
     float unscale[2][kRows];   // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
-    uint32_t armed[3], parity[3];  // what the issuing warps leave behind (Armed)
+    uint32_t armed[5], parity[5];  // what the issuing warps (the chain's first, the side's four) leave behind (Armed)
 };
 
 // The barriers ever armed with a copy or a product, and the last phase of each: what is waited for
@@ -563,6 +563,13 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t (&
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+// A tile to memory, tracked in the issuing thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_prefetch(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
@@ -572,12 +579,13 @@ template <int P>
 struct ChainJob {
     const ScanParams &p;
     const WsLayout &ws;
-    const CUtensorMap &vmap;
+    const CUtensorMap &vmap, &ymap;
     ChainSmem &sm;
-    int s, h, t0, len, first, nc;
+    int s, h, t0, len, nc;
+    const unsigned char *head0, *kq0;  // the first chunk's part of the workspace
 
-    __device__ __forceinline__ const unsigned char *head(int c) const { return ws.head(first + c, h); }
-    __device__ __forceinline__ const unsigned char *kq(int c) const { return ws.kq(first + c, h / p.HG); }
+    __device__ __forceinline__ const unsigned char *head(int c) const { return head0 + c * ws.chunk_bytes(); }
+    __device__ __forceinline__ const unsigned char *kq(int c) const { return kq0 + c * ws.chunk_bytes(); }
     __device__ __forceinline__ void load_keys(int c) const {
         uint64_t *bar = &sm.bar[B_K + (c & 1)];
         mbar_arrive_expect_tx(bar, 2 * kBlk + kGateBytes);
@@ -670,9 +678,11 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         const HeadGates &gt = sm.gates[c & 3];
         // 1. X = S K^T, its operand stored at the last chunk's end
         bool rescale = c % kRescale == 0;  // this chunk starts from a new power of two
-        if (!wait_for(&sm.bar[B_K + ph], (c >> 1) & 1)) bad = 1;
         if (!rescale) arm(B_X, x_phase);
-        if (!rescale && warp == 0 && elect_one()) issue_x(c);
+        if (!rescale && warp == 0) {
+            if (!wait_for(&sm.bar[B_K + ph], (c >> 1) & 1)) bad = 1;
+            if (elect_one() && !bad) issue_x(c);
+        }
         if (!wait_for(&sm.bar[B_READY], ph)) bad = 1;
         const float vmax = sm.vmax[row];
         if (warp == 0 && !wait_for(&sm.bar[B_T], ph)) bad = 1;
@@ -861,11 +871,9 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
         }
         if (warp == 1 && c1 < J.nc && !bad) {
             arm(B_V, c1 & 1);
-            if (elect_one()) {
-                if (c >= 0) J.load_values(c1);
-                if (c1 + 1 < J.nc) J.prefetch(c1 + 1);
-            }
+            if (c >= 0 && elect_one()) J.load_values(c1);
         }
+        if (warp == 2 && c + 2 < J.nc && elect_one()) J.prefetch(c + 2);
         if (c1 < J.nc) {
             // the next chunk's values, turned in place
             if (!wait_for(&sm.bar[B_V], c1 & 1)) bad = 1;
@@ -891,9 +899,8 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
                 uint32_t m2 = 0;
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                    const uint32_t a = v[n][i] & 0x7fff7fffu;
                     const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m2),
-                                                     *reinterpret_cast<const __nv_bfloat162 *>(&a));
+                                                     __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[n][i])));
                     m2 = *reinterpret_cast<const uint32_t *>(&m);
                 }
                 float top = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
@@ -902,11 +909,12 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
                 if ((lane & 3) == 0) sm.vmax[32 * warp + 8 * i + (lane >> 2)] = top;
             }
             fence_async_smem();
+            if (!wait_for(&sm.bar[B_K + (c1 & 1)], (c1 >> 1) & 1)) bad = 1;  // (the gates: the chain reads them after this)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.bar[B_READY]);
             // its queries times e^c, in place, 16 bytes of a token each: tokens 16 apart, in both blocks of 64
             // elements
-            if (!wait_for(&sm.bar[B_K + (c1 & 1)], (c1 >> 1) & 1) || !wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
+            if (!wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
             const __half *g = sm.gates[c1 & 3].g + (tid >> 3);
             uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1]) + tid;
             uint4 u[8];
@@ -926,9 +934,16 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
         }
         // this chunk's outputs, over its queries and from there to memory
         if (c >= 0) {
+            const float *oq = sm.gates[c & 3].oq + (lane & 3) * 2;
+            float2 w[8];
+            float un[4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const float2 *>(oq + 8 * n);
             if (!wait_for(&sm.bar[B_Y], c & 1)) bad = 1;
             tc_fence_after();
-            if (warp == 1 && !bad) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
+            if (warp == 2 && !bad) {
                 if (c1 < J.nc) arm(B_A, c1 & 1);
                 if (c + 2 < J.nc) arm(B_K + (c & 1), (c + 2) >> 1 & 1);
                 if (elect_one()) {
@@ -937,62 +952,60 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
                 }
             }
             if (live) {
-                const float *oq = sm.gates[c & 3].oq + (lane & 3) * 2;
-                float un[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
 #pragma unroll
                 for (int n = 0; n < 8; n += 2) {
-                    const float2 w0 = *reinterpret_cast<const float2 *>(oq + 8 * n);
-                    const float2 w1 = *reinterpret_cast<const float2 *>(oq + 8 * n + 8);
                     float y[2][8];
                     tmem_frag2(lanes + T_Y + 8 * n, y);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
+                        const uint64_t w2 = pair(w[n + m].x, w[n + m].y);
                         uint32_t pk[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 w = m ? w1 : w0;
                             const float *yi = &y[i >> 1][4 * m + 2 * (i & 1)];
-                            const __nv_bfloat162 o = __floats2bfloat162_rn(yi[0] * (w.x * un[i]), yi[1] * (w.y * un[i]));
+                            float lo, hi;
+                            unpair(mul2(pair(yi[0], yi[1]), mul2(w2, pair(un[i], un[i]))), lo, hi);
+                            const __nv_bfloat162 o = __floats2bfloat162_rn(lo, hi);
                             pk[i] = *reinterpret_cast<const uint32_t *>(&o);
                         }
                         stmatrix4_trans(token_row(sm.q[c & 1], n + m), pk);
                     }
                 }
             }
+            fence_async_smem();
             tc_fence_before();
         }
         if (half_sync_or(2, bad)) return true;  // Y is taken, the outputs are staged, the next queries scaled
-        if (c >= 0) {
+        const bool whole = c >= 0 && (c + 1) * C <= J.len;
+        if (c >= 0 && !whole) {  // the sequence's last tokens: the rows after them are another's
             constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
-            const int L = min(C, J.len - c * C), ch = tid % CH, first = tid / CH;
-            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C + first) * p.H + J.h) * P + ch * 8;
+            const int L = J.len - c * C, ch = tid % CH;
+            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C) * p.H + J.h) * P + ch * 8;
             const unsigned char *src = sm.q[c & 1] + (ch >> 3) * kBlk;
-            uint4 o[C * CH / 128];
-#pragma unroll
-            for (int i = 0; i < C * CH / 128; ++i)
-                o[i] = *reinterpret_cast<const uint4 *>(src + swz128_chunk(first + 128 / CH * i, ch & 7));
-#pragma unroll
-            for (int i = 0; i < C * CH / 128; ++i)
-                if (first + 128 / CH * i < L) *reinterpret_cast<uint4 *>(dst + (int64_t)i * (128 / CH) * p.H * P) = o[i];
-            fence_async_smem();
+            for (int t = tid / CH; t < L; t += 128 / CH)
+                *reinterpret_cast<uint4 *>(dst + (int64_t)t * p.H * P) = *reinterpret_cast<const uint4 *>(src + swz128_chunk(t, ch & 7));
         }
-        if (c + 2 < J.nc) {
-            if (c >= 0 && half_sync_or(2, bad)) return true;  // the queries' place is free
-            if (warp == 1) {
-                arm(B_Q, c & 1);
-                if (elect_one()) J.load_queries(c + 2);
+        if (warp == 3) {
+            if (c + 2 < J.nc) arm(B_Q, c & 1);
+            if (elect_one()) {
+                if (whole) {
+                    for (int i = 0; i < P / 64; ++i) tma_store_2d(&J.ymap, sm.q[c & 1] + i * kBlk, J.h * P + 64 * i, J.t0 + c * C);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                }
+                if (c + 2 < J.nc) J.load_queries(c + 2);  // (a chunk with two after it is whole, or there is none: the place is free)
             }
         }
     }
+    // the copies out of shared memory have read it (bulk_wait_read, above); their writes complete with the grid
     return half_sync_or(2, bad);
 }
 
 // Block (sequence in the plan's order, head).
 template <int P>
 __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,
-                                                                const __grid_constant__ CUtensorMap vmap) {
+                                                                const __grid_constant__ CUtensorMap vmap,
+                                                                const __grid_constant__ CUtensorMap ymap) {
     extern __shared__ __align__(1024) unsigned char chain_smem[];
     ChainSmem &sm = *align1024<ChainSmem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -1001,7 +1014,8 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, t0 = p.cu[s], len = p.cu[s + 1] - t0;
     const int32_t slot = p.slot[s];
     if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
-    const ChainJob<P> J = {p, ws, vmap, sm, s, h, t0, len, meta_chunks(p)[s], (len + C - 1) / C};
+    const int first = meta_chunks(p)[s];
+    const ChainJob<P> J = {p, ws, vmap, ymap, sm, s, h, t0, len, (len + C - 1) / C, ws.head(first, h), ws.kq(first, h / p.HG)};
     const int warp = threadIdx.x >> 5;
     if (warp == 5 && elect_one()) {
         for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i >= B_READY ? 4 : 1);
@@ -1034,15 +1048,14 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
         if (J.nc > 1) arm(B_K + 1, 0);
         failed = side_warps(J, arm);
-        if (threadIdx.x == 128) sm.armed[1] = arm.bars, sm.parity[1] = arm.parity;  // the products of the side's first warp
-        if (threadIdx.x == 160) sm.armed[2] = arm.bars, sm.parity[2] = arm.parity;  // the loads of its second
+        if ((threadIdx.x & 31) == 0) sm.armed[warp - 3] = arm.bars, sm.parity[warp - 3] = arm.parity;
     }
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
         // the same bounded time to finish before its memory is released
         if (warp == 4 && elect_one()) {
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
-            for (int w = 0; w < 3; ++w)
+            for (int w = 0; w < 5; ++w)
                 for (int i = 0; i < kBars; ++i)
                     if (sm.armed[w] >> i & 1) wait_for(&sm.bar[i], sm.parity[w] >> i & 1);
         }
@@ -1090,14 +1103,16 @@ bool chunked_eligible(const mamba_layer_desc *d) {
 }
 
 size_t chunked_workspace_bytes(const mamba_layer_desc *d, int T, int nseq) {
-    const WsLayout ws = {nullptr, d->nheads, d->n_groups};
+    const WsLayout ws(nullptr, d->nheads, d->n_groups);
     return (size_t)(scan_max_chunks(T, nseq) * ws.chunk_bytes());
 }
 
 int chunked_launch(const ScanParams &p, int head_dim, cudaStream_t st) {
-    const WsLayout ws = {p.ws, p.H, p.G};
-    CUtensorMap vmap;
-    if (!value_map(&vmap, p.v, (uint64_t)p.H * head_dim, (uint64_t)p.T)) return MAMBA_ECUDA;
+    const WsLayout ws(p.ws, p.H, p.G);
+    CUtensorMap vmap, ymap;
+    if (!value_map(&vmap, p.v, (uint64_t)p.H * head_dim, (uint64_t)p.T) ||
+        !value_map(&ymap, p.y, (uint64_t)p.H * head_dim, (uint64_t)p.T))
+        return MAMBA_ECUDA;
     const bool pairs = p.HG % 2 == 0;  // heads of a group share its products, two a block
     auto prep = pairs ? k_gdn_prep<2> : k_gdn_prep<1>;
     auto chain = head_dim == 128 ? k_gdn_chain<128> : k_gdn_chain<64>;
@@ -1107,7 +1122,8 @@ int chunked_launch(const ScanParams &p, int head_dim, cudaStream_t st) {
         return MAMBA_ECUDA;
     const dim3 grid((unsigned)scan_max_chunks(p.T, p.nseq), (unsigned)(pairs ? p.H / 2 : p.H));
     if (launch_pdl(prep, grid, dim3(kPrepThreads), prep_smem, st, p, ws) != cudaSuccess) return MAMBA_ECUDA;
-    if (launch_pdl(chain, dim3((unsigned)((int64_t)p.nseq * p.H)), dim3(kChainThreads), chain_smem, st, p, ws, vmap) != cudaSuccess)
+    if (launch_pdl(chain, dim3((unsigned)((int64_t)p.nseq * p.H)), dim3(kChainThreads), chain_smem, st, p, ws, vmap, ymap) !=
+        cudaSuccess)
         return MAMBA_ECUDA;
     return launch_status();
 }
