@@ -472,8 +472,8 @@ constexpr int kRows = 128;               // rows of tensor memory; with head_dim
 constexpr int kRescale = 16;             // chunks between two choices of the rows' powers of two
 
 // What the block waits for: keys and gates (two stages), queries, T, A and the values from memory; the
-// products X, U, Q S^T, the increment and Y; the values turned, and R formed of them.
-enum { B_K = 0, B_Q = 2, B_T, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, B_READY, B_TAKEN, kBars };
+// products X, U, Q S^T, the increment and Y; the values turned; the queries scaled and the last Y taken.
+enum { B_K = 0, B_Q = 2, B_T, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, B_READY, B_SCALED, kBars };
 
 struct ChainSmem {
     // q: a chunk's queries, and once they are used its outputs on their way to memory; v: its values, first
@@ -484,7 +484,7 @@ struct ChainSmem {
     float unscale[2][kRows];   // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
-    uint32_t armed[5], parity[5];  // what the issuing warps (the chain's first, the side's four) leave behind (Armed)
+    uint32_t armed[8], parity[8];  // what each warp leaves behind (Armed)
 };
 
 // The barriers ever armed with a copy or a product, and the last phase of each: what is waited for
@@ -750,8 +750,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             if (!again) break;
             rescale = true;
         }
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.bar[B_TAKEN]);  // (after the barrier: the warp has read its values)
-        // 3. U^T = R^T T^T (the side issues the state's part of Y)
+        // 3. U^T = R^T T^T, the next values, and the state's part of Y, each from a warp of its own
         if (warp == 0) {
             if (!bad) arm(B_U, ph);
             if (elect_one() && !bad) {
@@ -762,6 +761,22 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
                 mma_commit(&sm.bar[B_U]);
             }
             if (!wait_for(&sm.bar[B_A], ph)) bad = 1;
+        } else if (warp == 1) {
+            if (c + 1 < J.nc && !bad) {
+                arm(B_V, ph ^ 1);
+                if (elect_one()) J.load_values(c + 1);  // (every row's values are in R)
+            }
+        } else if (warp == 2) {
+            if (!wait_for(&sm.bar[B_SCALED], ph)) bad = 1;
+            if (!bad) arm(B_OI, ph);
+            tc_fence_after();
+            if (elect_one() && !bad) {
+                const uint32_t q = smem_u32(sm.q[ph]), tm = sm.tmem;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+                mma_commit(&sm.bar[B_OI]);
+            }
         }
         // 4. U^T rounded, as it is and times e^(c_64 - c) |k| (a product of rounded numbers: a conversion from fp32
         // takes four times as long)
@@ -793,7 +808,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         // 5. the state's increment, over the columns of its copy and of R (both are read), and A's part of Y
         if (warp == 0) {
             if (!wait_for(&sm.bar[B_OI], ph)) bad = 1;
-            if (!bad) arm(B_S, ph), arm(B_Y, ph), arm(B_T, ph ^ (c + 1 < J.nc));
+            if (!bad) arm(B_S, ph), arm(B_Y, ph);
             if (elect_one() && !bad) {
                 const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
 #pragma unroll
@@ -806,8 +821,10 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
                     mma_bf16_ts(lanes + T_Y, lanes + T_U + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(A, kBlk, kk),
                                 idesc_f16(128, C, false), 1);
                 mma_commit(&sm.bar[B_Y]);
-                if (c + 1 < J.nc) J.load_tile(c + 1, B_T, sm.T, 0);
             }
+        } else if (warp == 1 && c + 1 < J.nc && !bad) {
+            arm(B_T, ph ^ 1);
+            if (elect_one()) J.load_tile(c + 1, B_T, sm.T, 0);  // (U is formed)
         }
         // 6. the new state, and its copy over the increment (a row's columns are its thread's own)
         const float last = gt.last;
@@ -837,8 +854,8 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     return false;
 }
 
-// The four warps beside the chain: they turn the values of the next chunk, scale its queries, issue the
-// state's part of Y, take the outputs to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31,
+// The four warps beside the chain: they turn the values of the next chunk, scale its queries, take the
+// outputs to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31,
 // the fragments of 32 values by 8 tokens.  Returns whether a wait gave up.
 template <int P>
 __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
@@ -846,7 +863,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     ChainSmem &sm = J.sm;
     const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
     const bool live = 32 * warp < P;  // this warp's rows are values
-    const uint32_t tm = sm.tmem, lanes = tm + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);
     // this lane's 16 bytes (8 values of a token) of a tile by tokens, for 8 tokens from 8 n
     auto token_row = [&](const unsigned char *tile, int n) {
         return smem_u32(tile) + (warp >> 1) * kBlk + swz128_chunk(8 * n + (lane & 7), 4 * (warp & 1) + (lane >> 3));
@@ -854,25 +871,6 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     int bad = 0;
     for (int c = -1; c < J.nc; ++c) {
         const int c1 = c + 1;
-        // R of this chunk is formed: its values' place is free, and the state's part of Y can start
-        if (c >= 0 && warp < 2) {
-            if (!wait_for(&sm.bar[B_TAKEN], c & 1)) bad = 1;
-            if (warp == 0 && !bad) {
-                arm(B_OI, c & 1);
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t q = smem_u32(sm.q[c & 1]);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-                    mma_commit(&sm.bar[B_OI]);
-                }
-            }
-        }
-        if (warp == 1 && c1 < J.nc && !bad) {
-            arm(B_V, c1 & 1);
-            if (c >= 0 && elect_one()) J.load_values(c1);
-        }
         if (warp == 2 && c + 2 < J.nc && elect_one()) J.prefetch(c + 2);
         if (c1 < J.nc) {
             // the next chunk's values, turned in place
@@ -976,6 +974,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
             tc_fence_before();
         }
         if (half_sync_or(2, bad)) return true;  // Y is taken, the outputs are staged, the next queries scaled
+        if (lane == 0) mbar_arrive(&sm.bar[B_SCALED]);
         const bool whole = c >= 0 && (c + 1) * C <= J.len;
         if (c >= 0 && !whole) {  // the sequence's last tokens: the rows after them are another's
             constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
@@ -1041,21 +1040,21 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         more_registers<kChainRegs>();
         Armed arm;
         failed = chain_warps(J, arm);
-        if (threadIdx.x == 0) sm.armed[0] = arm.bars, sm.parity[0] = arm.parity;
+        if ((threadIdx.x & 31) == 0) sm.armed[warp] = arm.bars, sm.parity[warp] = arm.parity;
     } else {
         fewer_registers<kSideRegs>();
         Armed arm;
         arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
         if (J.nc > 1) arm(B_K + 1, 0);
         failed = side_warps(J, arm);
-        if ((threadIdx.x & 31) == 0) sm.armed[warp - 3] = arm.bars, sm.parity[warp - 3] = arm.parity;
+        if ((threadIdx.x & 31) == 0) sm.armed[warp] = arm.bars, sm.parity[warp] = arm.parity;
     }
     if (__syncthreads_or(failed)) {
         // an operation did not complete in time: report it, and give what this block still has in flight
         // the same bounded time to finish before its memory is released
         if (warp == 4 && elect_one()) {
             flag_error(p.err, MAMBA_ERR_TIMEOUT);
-            for (int w = 0; w < 5; ++w)
+            for (int w = 0; w < 8; ++w)
                 for (int i = 0; i < kBars; ++i)
                     if (sm.armed[w] >> i & 1) wait_for(&sm.bar[i], sm.parity[w] >> i & 1);
         }
