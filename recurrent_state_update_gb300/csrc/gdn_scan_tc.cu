@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
 // ---------------------------------------------------------------------------------------
 
 constexpr int kChainThreads = 256;       // four warps on the chain, four beside it
-constexpr int kChainRegs = 200, kSideRegs = 56;  // (200 + 56) * 128 registers: what the block is launched with
+constexpr int kChainRegs = 184, kSideRegs = 72;  // (184 + 72) * 128 registers: what the block is launched with
 constexpr int kRows = 128;               // rows of tensor memory; with head_dim 64 the upper half holds zeros
 constexpr int kRescale = 16;             // chunks between two choices of the rows' powers of two
 
@@ -484,6 +484,11 @@ struct ChainSmem {
     float unscale[2][kRows];   // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
+    // the block's sequence, head, first token, tokens and chunks, and the first chunk's part of the workspace:
+    // here and not in registers, of which the chain has none to spare (what is spilled comes back from L2:
+    // next to this much shared memory almost no L1 is left)
+    int s, h, t0, len, nc;
+    const unsigned char *head0, *kq0;
     uint32_t armed[8], parity[8];  // what each warp leaves behind (Armed)
 };
 
@@ -543,13 +548,40 @@ __device__ __forceinline__ void tmem_frag2(uint32_t a, float (&v)[2][8]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __uint_as_float(r[i]);
 }
-// 16 32-bit columns (two 16-bit values each) of this warp's lanes; tmem_put_wait waits for all before it.
-__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&v)[16]) {
+// 16 fp32 columns of this warp's lanes, on their way after the first call and there after the second: what
+// stands between them hides the latency, and the second's operands keep the uses after it.
+__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
         : "memory");
+}
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+// N pieces of 16 columns from a, each given to f(piece, values) with the next one on its way.
+template <int N, typename F>
+__device__ __forceinline__ void tmem_pieces(uint32_t a, F f) {
+    uint32_t r[2][16];
+    tmem_get(a, r[0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        tmem_got(r[i & 1]);
+        if (i + 1 < N) tmem_get(a + 16 * (i + 1), r[(i + 1) & 1]);
+        f(i, r[i & 1]);
+    }
+}
+// 8 32-bit columns (two 16-bit values each) of this warp's lanes; tmem_put_wait waits for all before it.
+__device__ __forceinline__ void tmem_put8(uint32_t a, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -581,11 +613,9 @@ struct ChainJob {
     const WsLayout &ws;
     const CUtensorMap &vmap, &ymap;
     ChainSmem &sm;
-    int s, h, t0, len, nc;
-    const unsigned char *head0, *kq0;  // the first chunk's part of the workspace
 
-    __device__ __forceinline__ const unsigned char *head(int c) const { return head0 + c * ws.chunk_bytes(); }
-    __device__ __forceinline__ const unsigned char *kq(int c) const { return kq0 + c * ws.chunk_bytes(); }
+    __device__ __forceinline__ const unsigned char *head(int c) const { return sm.head0 + c * ws.chunk_bytes(); }
+    __device__ __forceinline__ const unsigned char *kq(int c) const { return sm.kq0 + c * ws.chunk_bytes(); }
     __device__ __forceinline__ void load_keys(int c) const {
         uint64_t *bar = &sm.bar[B_K + (c & 1)];
         mbar_arrive_expect_tx(bar, 2 * kBlk + kGateBytes);
@@ -600,7 +630,7 @@ struct ChainJob {
     }
     __device__ __forceinline__ void load_values(int c) const {
         mbar_arrive_expect_tx(&sm.bar[B_V], P / 64 * kBlk);
-        for (int i = 0; i < P / 64; ++i) tma_load_2d(sm.v + i * kBlk, &vmap, h * P + 64 * i, t0 + c * C, &sm.bar[B_V]);
+        for (int i = 0; i < P / 64; ++i) tma_load_2d(sm.v + i * kBlk, &vmap, sm.h * P + 64 * i, sm.t0 + c * C, &sm.bar[B_V]);
     }
     __device__ __forceinline__ void load_tile(int c, int i, unsigned char *dst, uint32_t off) const {
         mbar_arrive_expect_tx(&sm.bar[i], kBlk);
@@ -612,7 +642,7 @@ struct ChainJob {
         bulk_prefetch(kq(c), kKqBytes);
         for (int i = 0; i < P / 64; ++i)
             asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&vmap)),
-                         "r"(h * P + 64 * i), "r"(t0 + c * C)
+                         "r"(sm.h * P + 64 * i), "r"(sm.t0 + c * C)
                          : "memory");
     }
 };
@@ -625,13 +655,13 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     ChainSmem &sm = J.sm;
     const int row = threadIdx.x, warp = threadIdx.x >> 5;
     const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);  // (of warp 0: tensor memory's first lane)
-    const int32_t slot = p.slot[J.s];
+    const int32_t slot = p.slot[sm.s];
     auto pool_row = [&](int32_t to) {
-        return static_cast<bf16 *>(p.pool) + to * p.stride + ((int64_t)J.h * P + row) * TN;
+        return static_cast<bf16 *>(p.pool) + to * p.stride + ((int64_t)sm.h * P + row) * TN;
     };
     float S[TN];  // times the row's power of two
     {
-        const bool seeded = row < P && slot >= 0 && p.has_init && p.has_init[J.s];
+        const bool seeded = row < P && slot >= 0 && p.has_init && p.has_init[sm.s];
         const bf16 *src = pool_row(seeded ? slot : 0);
 #pragma unroll
         for (int e = 0; e < TN; e += 8) {
@@ -648,11 +678,11 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     uint32_t x_phase = 0;
     int bad = 0;  // a wait gave up: all four warps leave at the next barrier
 
-    auto store_state16 = [&](int e) {  // 32 columns of the state's copy for the products
-        uint32_t pk[16];
+    auto store_state16 = [&](int e) {  // 16 columns of the state's copy for the products
+        uint32_t pk[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(S[e + 2 * i], S[e + 2 * i + 1]);
-        tmem_put(lanes + T_S + e / 2, pk);
+        for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(S[e + 2 * i], S[e + 2 * i + 1]);
+        tmem_put8(lanes + T_S + e / 2, pk);
     };
     auto issue_x = [&](int c) {  // X = S K^T
         const uint32_t k = smem_u32(sm.k[c & 1]);
@@ -673,7 +703,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         }
     };
 
-    for (int c = 0; c < J.nc; ++c) {
+    for (int c = 0; c < sm.nc; ++c) {
         const uint32_t ph = c & 1;
         const HeadGates &gt = sm.gates[c & 3];
         // 1. X = S K^T, its operand stored at the last chunk's end
@@ -705,7 +735,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
 #pragma unroll
                 for (int e = 0; e < TN; ++e) S[e] *= ratio;
 #pragma unroll
-                for (int e = 0; e < TN; e += 32) store_state16(e);
+                for (int e = 0; e < TN; e += 16) store_state16(e);
                 tmem_put_wait();
                 tc_fence_before();
                 if (half_sync_or(1, bad)) return true;
@@ -717,31 +747,27 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             if (!wait_for(&sm.bar[B_X], x_phase)) bad = 1;
             x_phase ^= 1;
             tc_fence_after();
+            const uint64_t sc = pair(scale, scale);
+            tmem_pieces<4>(lanes + T_X, [&](int n, const uint32_t (&x)[16]) {  // 16 tokens, over their own columns
+                uint32_t pk[8];
 #pragma unroll
-            for (int n = 0; n < 8; n += 4) {
-                uint4 v8[4];  // 8 tokens' values each
-#pragma unroll
-                for (int m = 0; m < 4; ++m) v8[m] = *reinterpret_cast<const uint4 *>(sm.v + swz128_chunk(row, n + m));
-                float x[32];
-                tmem_ld32(lanes + T_X + 8 * n, x);
-                uint32_t pk[16];
-                const uint64_t sc = pair(scale, scale);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const uint32_t w[4] = {v8[m].x, v8[m].y, v8[m].z, v8[m].w};
-                    const float4 r0 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m));
-                    const float4 r1 = *reinterpret_cast<const float4 *>(gt.rk + 8 * (n + m) + 4);
+                for (int m = 0; m < 2; ++m) {
+                    const uint4 v8 = *reinterpret_cast<const uint4 *>(sm.v + swz128_chunk(row, 2 * n + m));
+                    const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
+                    const float4 r0 = *reinterpret_cast<const float4 *>(gt.rk + 16 * n + 8 * m);
+                    const float4 r1 = *reinterpret_cast<const float4 *>(gt.rk + 16 * n + 8 * m + 4);
                     const uint64_t rk[4] = {pair(-r0.x, -r0.y), pair(-r0.z, -r0.w), pair(-r1.x, -r1.y), pair(-r1.z, -r1.w)};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint64_t v2 = mul2(pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), sc);
+                        const int e = 8 * m + 2 * i;
                         float lo, hi;
-                        unpair(fma2(rk[i], pair(x[8 * m + 2 * i], x[8 * m + 2 * i + 1]), v2), lo, hi);
+                        unpair(fma2(rk[i], pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), v2), lo, hi);
                         pk[4 * m + i] = pack_f16x2(lo, hi);
                     }
                 }
-                tmem_put(lanes + T_X + 4 * n, pk);
-            }
+                tmem_put8(lanes + T_X + 8 * n, pk);  // (packed to the left: over what has been read)
+            });
             tmem_put_wait();
             sm.unscale[ph][row] = unscale;
             tc_fence_before();
@@ -762,7 +788,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             }
             if (!wait_for(&sm.bar[B_A], ph)) bad = 1;
         } else if (warp == 1) {
-            if (c + 1 < J.nc && !bad) {
+            if (c + 1 < sm.nc && !bad) {
                 arm(B_V, ph ^ 1);
                 if (elect_one()) J.load_values(c + 1);  // (every row's values are in R)
             }
@@ -782,25 +808,20 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         // takes four times as long)
         if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
         tc_fence_after();
+        tmem_pieces<4>(lanes + T_U, [&](int n, const uint32_t (&u)[16]) {  // 16 tokens: both forms over their own columns
+            const uint4 w0 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n), w1 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n + 8);
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            uint32_t pk[8];
 #pragma unroll
-        for (int n = 0; n < C; n += 32) {  // 32 tokens: both forms over their own columns
-            uint4 w[4];  // 8 tokens' factors each
+            for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+            tmem_put8(lanes + T_U + 16 * n, pk);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(gt.ek + n + 8 * i);
-            float u[32];
-            tmem_ld32(lanes + T_U + n, u);
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(u[2 * i], u[2 * i + 1]);
-            tmem_put(lanes + T_U + n, pk);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t f = (&w[i / 4].x)[i & 3];
-                const __half2 e = __hmul2(*reinterpret_cast<const __half2 *>(&pk[i]), *reinterpret_cast<const __half2 *>(&f));
+            for (int i = 0; i < 8; ++i) {
+                const __half2 e = __hmul2(*reinterpret_cast<const __half2 *>(&pk[i]), *reinterpret_cast<const __half2 *>(&w[i]));
                 pk[i] = *reinterpret_cast<const uint32_t *>(&e);
             }
-            tmem_put(lanes + T_U + n + 16, pk);
-        }
+            tmem_put8(lanes + T_U + 16 * n + 8, pk);
+        });
         tmem_put_wait();
         tc_fence_before();
         if (half_sync_or(1, bad)) return true;
@@ -813,16 +834,14 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
                 const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(lanes + T_D, lanes + T_U + (kk >> 1) * 32 + 16 + (kk & 1) * 8, desc_mnmajor(k, kBlk, kk),
-                                idesc_f16(128, TN, true), kk > 0);
+                    mma_bf16_ts(lanes + T_D, lanes + T_U + kk * 16 + 8, desc_mnmajor(k, kBlk, kk), idesc_f16(128, TN, true), kk > 0);
                 mma_commit(&sm.bar[B_S]);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(lanes + T_Y, lanes + T_U + (kk >> 1) * 32 + (kk & 1) * 8, desc_kmajor(A, kBlk, kk),
-                                idesc_f16(128, C, false), 1);
+                    mma_bf16_ts(lanes + T_Y, lanes + T_U + kk * 16, desc_kmajor(A, kBlk, kk), idesc_f16(128, C, false), 1);
                 mma_commit(&sm.bar[B_Y]);
             }
-        } else if (warp == 1 && c + 1 < J.nc && !bad) {
+        } else if (warp == 1 && c + 1 < sm.nc && !bad) {
             arm(B_T, ph ^ 1);
             if (elect_one()) J.load_tile(c + 1, B_T, sm.T, 0);  // (U is formed)
         }
@@ -830,20 +849,17 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         const float last = gt.last;
         if (!wait_for(&sm.bar[B_S], ph)) bad = 1;
         tc_fence_after();
+        tmem_pieces<8>(lanes + T_D, [&](int n, const uint32_t (&d)[16]) {
 #pragma unroll
-        for (int e = 0; e < TN; e += 32) {
-            float d[32];
-            tmem_ld32(lanes + T_D + e, d);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) S[e + i] = fmaf(last, S[e + i], d[i]);
-        }
+            for (int i = 0; i < 16; ++i) S[16 * n + i] = fmaf(last, S[16 * n + i], __uint_as_float(d[i]));
+        });
         if (p.ckpt_slots) {
-            const int32_t cs = ckpt_slot(p, J.s, min(J.len, (c + 1) * C), threadIdx.x == 0 && J.h == 0);
+            const int32_t cs = ckpt_slot(p, sm.s, min(sm.len, (c + 1) * C), threadIdx.x == 0 && sm.h == 0);
             if (cs >= 0) write_state(cs);
         }
-        if (c + 1 < J.nc && (c + 1) % kRescale != 0) {
+        if (c + 1 < sm.nc && (c + 1) % kRescale != 0) {
 #pragma unroll
-            for (int e = 0; e < TN; e += 32) store_state16(e);
+            for (int e = 0; e < TN; e += 16) store_state16(e);
             tmem_put_wait();
         }
         tc_fence_before();
@@ -869,10 +885,10 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
         return smem_u32(tile) + (warp >> 1) * kBlk + swz128_chunk(8 * n + (lane & 7), 4 * (warp & 1) + (lane >> 3));
     };
     int bad = 0;
-    for (int c = -1; c < J.nc; ++c) {
+    for (int c = -1; c < sm.nc; ++c) {
         const int c1 = c + 1;
-        if (warp == 2 && c + 2 < J.nc && elect_one()) J.prefetch(c + 2);
-        if (c1 < J.nc) {
+        if (warp == 2 && c + 2 < sm.nc && elect_one()) J.prefetch(c + 2);
+        if (c1 < sm.nc) {
             // the next chunk's values, turned in place
             if (!wait_for(&sm.bar[B_V], c1 & 1)) bad = 1;
             uint32_t v[8][4] = {};  // [n][i]: rows 8 i + T / 4, tokens 8 n + 2 (T % 4) and the next
@@ -880,7 +896,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
 #pragma unroll
                 for (int n = 0; n < 8; ++n) ldmatrix4_trans(v[n], token_row(sm.v, n));
             }
-            const int L = J.len - c1 * C;
+            const int L = sm.len - c1 * C;
             if (L < C) {  // rows past the sequence's end hold another sequence's values
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
@@ -942,11 +958,11 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
             if (warp == 2 && !bad) {
-                if (c1 < J.nc) arm(B_A, c1 & 1);
-                if (c + 2 < J.nc) arm(B_K + (c & 1), (c + 2) >> 1 & 1);
+                if (c1 < sm.nc) arm(B_A, c1 & 1);
+                if (c + 2 < sm.nc) arm(B_K + (c & 1), (c + 2) >> 1 & 1);
                 if (elect_one()) {
-                    if (c1 < J.nc) J.load_tile(c1, B_A, sm.A, kBlk);
-                    if (c + 2 < J.nc) J.load_keys(c + 2);
+                    if (c1 < sm.nc) J.load_tile(c1, B_A, sm.A, kBlk);
+                    if (c + 2 < sm.nc) J.load_keys(c + 2);
                 }
             }
             if (live) {
@@ -975,24 +991,24 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
         }
         if (half_sync_or(2, bad)) return true;  // Y is taken, the outputs are staged, the next queries scaled
         if (lane == 0) mbar_arrive(&sm.bar[B_SCALED]);
-        const bool whole = c >= 0 && (c + 1) * C <= J.len;
+        const bool whole = c >= 0 && (c + 1) * C <= sm.len;
         if (c >= 0 && !whole) {  // the sequence's last tokens: the rows after them are another's
             constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
-            const int L = J.len - c * C, ch = tid % CH;
-            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(J.t0 + c * C) * p.H + J.h) * P + ch * 8;
+            const int L = sm.len - c * C, ch = tid % CH;
+            bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(sm.t0 + c * C) * p.H + sm.h) * P + ch * 8;
             const unsigned char *src = sm.q[c & 1] + (ch >> 3) * kBlk;
             for (int t = tid / CH; t < L; t += 128 / CH)
                 *reinterpret_cast<uint4 *>(dst + (int64_t)t * p.H * P) = *reinterpret_cast<const uint4 *>(src + swz128_chunk(t, ch & 7));
         }
         if (warp == 3) {
-            if (c + 2 < J.nc) arm(B_Q, c & 1);
+            if (c + 2 < sm.nc) arm(B_Q, c & 1);
             if (elect_one()) {
                 if (whole) {
-                    for (int i = 0; i < P / 64; ++i) tma_store_2d(&J.ymap, sm.q[c & 1] + i * kBlk, J.h * P + 64 * i, J.t0 + c * C);
+                    for (int i = 0; i < P / 64; ++i) tma_store_2d(&J.ymap, sm.q[c & 1] + i * kBlk, sm.h * P + 64 * i, sm.t0 + c * C);
                     bulk_commit();
                     bulk_wait_read<0>();
                 }
-                if (c + 2 < J.nc) J.load_queries(c + 2);  // (a chunk with two after it is whole, or there is none: the place is free)
+                if (c + 2 < sm.nc) J.load_queries(c + 2);  // (a chunk with two after it is whole, or there is none: the place is free)
             }
         }
     }
@@ -1006,16 +1022,24 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
                                                                 const __grid_constant__ CUtensorMap vmap,
                                                                 const __grid_constant__ CUtensorMap ymap) {
     extern __shared__ __align__(1024) unsigned char chain_smem[];
-    ChainSmem &sm = *align1024<ChainSmem>(chain_smem);
+    ChainSmem &sm = *reinterpret_cast<ChainSmem *>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     if (p.meta[0] == 0) return;  // bad cu_seqlens (flagged): nothing is done
-    const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, t0 = p.cu[s], len = p.cu[s + 1] - t0;
-    const int32_t slot = p.slot[s];
-    if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
-    const int first = meta_chunks(p)[s];
-    const ChainJob<P> J = {p, ws, vmap, ymap, sm, s, h, t0, len, (len + C - 1) / C, ws.head(first, h), ws.kq(first, h / p.HG)};
+    {
+        const int s = meta_order(p)[blockIdx.x / p.H], h = blockIdx.x % p.H, len = p.cu[s + 1] - p.cu[s];
+        const int32_t slot = p.slot[s];
+        if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
+        if (threadIdx.x == 160) {
+            sm.s = s, sm.h = h, sm.t0 = p.cu[s], sm.len = len, sm.nc = (len + C - 1) / C;
+            const int first = meta_chunks(p)[s];
+            sm.head0 = ws.head(first, h);
+            sm.kq0 = ws.kq(first, h / p.HG);
+        }
+    }
+    const ChainJob<P> J = {p, ws, vmap, ymap, sm};
     const int warp = threadIdx.x >> 5;
+    __syncwarp();
     if (warp == 5 && elect_one()) {
         for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i >= B_READY ? 4 : 1);
         fence_mbar_init();
@@ -1025,7 +1049,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         J.load_queries(0);
         J.load_tile(0, B_T, sm.T, 0);
         J.load_tile(0, B_A, sm.A, kBlk);
-        if (J.nc > 1) J.load_keys(1);
+        if (sm.nc > 1) J.load_keys(1);
     }
     if (warp == 0) {
         tmem_alloc(&sm.tmem, 256);
@@ -1045,7 +1069,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
         fewer_registers<kSideRegs>();
         Armed arm;
         arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
-        if (J.nc > 1) arm(B_K + 1, 0);
+        if (sm.nc > 1) arm(B_K + 1, 0);
         failed = side_warps(J, arm);
         if ((threadIdx.x & 31) == 0) sm.armed[warp] = arm.bars, sm.parity[warp] = arm.parity;
     }
