@@ -467,20 +467,18 @@ __global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p
 // ---------------------------------------------------------------------------------------
 
 constexpr int kChainThreads = 256;       // four warps on the chain, four beside it
-constexpr int kChainRegs = 184, kSideRegs = 72;  // (184 + 72) * 128 registers: what the block is launched with
+constexpr int kChainRegs = 208, kSideRegs = 48;  // (208 + 48) * 128 registers: what the block is launched with
 constexpr int kRows = 128;               // rows of tensor memory; with head_dim 64 the upper half holds zeros
 constexpr int kRescale = 16;             // chunks between two choices of the rows' powers of two
 
-// What the block waits for: keys and gates (two stages), queries, T, A and the values from memory; the
-// products X, U, Q S^T, the increment and Y; the values turned; the queries scaled and the last Y taken.
-enum { B_K = 0, B_Q = 2, B_T, B_A, B_V, B_X, B_U, B_OI, B_S, B_Y, B_READY, B_SCALED, kBars };
+// What the block waits for: keys, gates and values (two stages), queries, T and A from memory; the products X, U,
+// Q S^T, the increment and Y; the values in registers.
+enum { B_IN = 0, B_Q = 2, B_T, B_A, B_X, B_U, B_OI, B_S, B_Y, B_TAKEN, kBars };
 
 struct ChainSmem {
-    // q: a chunk's queries, and once they are used its outputs on their way to memory; v: its values, first
-    // by token (64 values in a swizzled block of 64 tokens, twice), then by value (kRows rows of 64 tokens)
+    // q: a chunk's queries, and once they are used its outputs on their way to memory; v: its values, by token
     unsigned char k[2][2 * kBlk], q[2][2 * kBlk], T[kBlk], A[kBlk], v[2 * kBlk];
     HeadGates gates[4];
-    float vmax[kRows];        // largest magnitude among a chunk's values, by row
     float unscale[2][kRows];   // a chunk's inverse powers of two, by row
     uint64_t bar[kBars];
     uint32_t tmem;
@@ -585,11 +583,6 @@ __device__ __forceinline__ void tmem_put8(uint32_t a, const uint32_t (&v)[8]) {
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3])
-                 : "memory");
-}
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3])
@@ -617,7 +610,7 @@ struct ChainJob {
     __device__ __forceinline__ const unsigned char *head(int c) const { return sm.head0 + c * ws.chunk_bytes(); }
     __device__ __forceinline__ const unsigned char *kq(int c) const { return sm.kq0 + c * ws.chunk_bytes(); }
     __device__ __forceinline__ void load_keys(int c) const {
-        uint64_t *bar = &sm.bar[B_K + (c & 1)];
+        uint64_t *bar = &sm.bar[B_IN + (c & 1)];
         mbar_arrive_expect_tx(bar, 2 * kBlk + kGateBytes);
         bulk_g2s(sm.k[c & 1], kq(c), kBlk, bar);
         bulk_g2s(sm.k[c & 1] + kBlk, kq(c) + 2 * kBlk, kBlk, bar);
@@ -629,8 +622,9 @@ struct ChainJob {
         bulk_g2s(sm.q[c & 1] + kBlk, kq(c) + 3 * kBlk, kBlk, &sm.bar[B_Q]);
     }
     __device__ __forceinline__ void load_values(int c) const {
-        mbar_arrive_expect_tx(&sm.bar[B_V], P / 64 * kBlk);
-        for (int i = 0; i < P / 64; ++i) tma_load_2d(sm.v + i * kBlk, &vmap, sm.h * P + 64 * i, sm.t0 + c * C, &sm.bar[B_V]);
+        uint64_t *bar = &sm.bar[B_IN + (c & 1)];
+        mbar_arrive_expect_tx(bar, C * P * 2);
+        tma_load_2d(sm.v, &vmap, sm.h * P, sm.t0 + c * C, bar);
     }
     __device__ __forceinline__ void load_tile(int c, int i, unsigned char *dst, uint32_t off) const {
         mbar_arrive_expect_tx(&sm.bar[i], kBlk);
@@ -640,10 +634,9 @@ struct ChainJob {
     __device__ __forceinline__ void prefetch(int c) const {
         bulk_prefetch(head(c), kHeadBytes);
         bulk_prefetch(kq(c), kKqBytes);
-        for (int i = 0; i < P / 64; ++i)
-            asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&vmap)),
-                         "r"(sm.h * P + 64 * i), "r"(sm.t0 + c * C)
-                         : "memory");
+        asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&vmap)),
+                     "r"(sm.h * P), "r"(sm.t0 + c * C)
+                     : "memory");
     }
 };
 
@@ -674,8 +667,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             for (int i = 0; i < 8; ++i) S[e + i] = f[i];
         }
     }
-    float scale = 1.0f, unscale = 1.0f, limit = 0.0f;  // the power of two, its inverse, the largest value it takes
-    uint32_t x_phase = 0;
+    float scale = 1.0f, unscale = 1.0f, limit = -1.0f;  // the power of two, its inverse, the largest value it takes
     int bad = 0;  // a wait gave up: all four warps leave at the next barrier
 
     auto store_state16 = [&](int e) {  // 16 columns of the state's copy for the products
@@ -703,165 +695,162 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         }
     };
 
-    for (int c = 0; c < sm.nc; ++c) {
+    // The row's values of chunk c, two tokens' each (with head_dim 64 the upper rows hold zeros), and the row's
+    // power of two for it: one that brings the largest of state and values to [2, 4) is chosen every kRescale
+    // chunks and where a value outgrows 16 units.  Rows are their threads' own, so no other thread needs to know.
+    uint32_t vals[C / 2];
+    auto take_values = [&](int c) {
+        if (!wait_for(&sm.bar[B_IN + (c & 1)], c >> 1 & 1)) bad = 1;
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(sm.v) + (row & (P - 1));
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            vals[i] = v[2 * i * P] | (uint32_t)v[(2 * i + 1) * P] << 16;
+            if (row >= P) vals[i] = 0;
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.bar[B_TAKEN]);
+        const int L = sm.len - c * C;
+        if (__builtin_expect(L < C, 0)) {  // past the sequence's end the tile holds another's values
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) vals[i] = 2 * i + 1 < L ? vals[i] : (2 * i < L ? vals[i] & 0xffffu : 0u);
+        }
+    };
+    auto choose_power = [&](int c) {
+        __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[0]));
+#pragma unroll
+        for (int i = 1; i < C / 2; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[i])));
+        const float vmax = fmaxf(__low2float(m), __high2float(m));
+        if (__builtin_expect(c % kRescale == 0 || vmax > limit, 0)) {
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < TN; ++e) top = fmaxf(top, fabsf(S[e]));
+            top = fmaxf(top * unscale, vmax);
+            uint32_t E = __float_as_uint(top) >> 23;
+            E = top < INFINITY ? max(7u, min(247u, E)) : 127u;
+            scale = __uint_as_float((255u - E) << 23);
+            const float ratio = scale * unscale;
+            unscale = __uint_as_float((E - 1u) << 23);
+            limit = __uint_as_float((E + 3u) << 23);
+#pragma unroll
+            for (int e = 0; e < TN; ++e) S[e] *= ratio;
+        }
+        sm.unscale[c & 1][row] = unscale;
+#pragma unroll
+        for (int e = 0; e < TN; e += 16) store_state16(e);
+        tmem_put_wait();
+    };
+
+    for (int c = -1; c < sm.nc; ++c) {  // (from -1: only what readies the first chunk)
         const uint32_t ph = c & 1;
         const HeadGates &gt = sm.gates[c & 3];
-        // 1. X = S K^T, its operand stored at the last chunk's end
-        bool rescale = c % kRescale == 0;  // this chunk starts from a new power of two
-        if (!rescale) arm(B_X, x_phase);
-        if (!rescale && warp == 0) {
-            if (!wait_for(&sm.bar[B_K + ph], (c >> 1) & 1)) bad = 1;
-            if (elect_one() && !bad) issue_x(c);
-        }
-        if (!wait_for(&sm.bar[B_READY], ph)) bad = 1;
-        const float vmax = sm.vmax[row];
-        if (warp == 0 && !wait_for(&sm.bar[B_T], ph)) bad = 1;
-        int over = vmax > limit;  // a value outgrew 2^4 units of its row
-        // 2. R = V - e^c |k| X, rounded, over X (past the sequence's end the values, the keys and so X are
-        // zero); if a power of two has to change, X and R again from the rescaled state
-        for (;;) {
-            if (rescale) {
-                float top = 0.0f;
-#pragma unroll
-                for (int e = 0; e < TN; ++e) top = fmaxf(top, fabsf(S[e]));
-                top = fmaxf(top * unscale, vmax);
-                // the power that brings the largest to [2, 4); values may grow to 16 before the next choice
-                uint32_t E = __float_as_uint(top) >> 23;
-                E = top < INFINITY ? max(7u, min(247u, E)) : 127u;
-                scale = __uint_as_float((255u - E) << 23);
-                const float ratio = scale * unscale;
-                unscale = __uint_as_float((E - 1u) << 23);
-                limit = __uint_as_float((E + 3u) << 23);
-#pragma unroll
-                for (int e = 0; e < TN; ++e) S[e] *= ratio;
-#pragma unroll
-                for (int e = 0; e < TN; e += 16) store_state16(e);
-                tmem_put_wait();
-                tc_fence_before();
-                if (half_sync_or(1, bad)) return true;
-                tc_fence_after();
-                arm(B_X, x_phase);
-                if (warp == 0 && elect_one()) issue_x(c);
-                over = 0;
+        if (c >= 0) {
+            // 1. X = S K^T
+            if (warp == 0) {
+                arm(B_X, ph);
+                if (elect_one()) issue_x(c);
+                if (!wait_for(&sm.bar[B_T], ph)) bad = 1;
             }
-            if (!wait_for(&sm.bar[B_X], x_phase)) bad = 1;
-            x_phase ^= 1;
+            // 2. R = V - e^c |k| X, rounded, over X (past the sequence's end the values, the keys and so X are zero)
+            if (!wait_for(&sm.bar[B_X], ph)) bad = 1;
             tc_fence_after();
-            const uint64_t sc = pair(scale, scale);
-            tmem_pieces<4>(lanes + T_X, [&](int n, const uint32_t (&x)[16]) {  // 16 tokens, over their own columns
+            {
+                const uint64_t sc = pair(scale, scale);
+#pragma unroll
+                for (int n = 0; n < C / 16; ++n) {  // 16 tokens
+                    uint32_t x[16], pk[8];
+                    tmem_get(lanes + T_X + 16 * n, x);
+                    tmem_got(x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t w = vals[8 * n + i];
+                        const uint64_t v2 = mul2(pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), sc);
+                        const float2 r = *reinterpret_cast<const float2 *>(gt.rk + 16 * n + 2 * i);
+                        float lo, hi;
+                        unpair(fma2(pair(-r.x, -r.y), pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), v2), lo, hi);
+                        pk[i] = pack_f16x2(lo, hi);
+                    }
+                    tmem_put8(lanes + T_X + 8 * n, pk);  // (packed to the left: over what has been read)
+                }
+                tmem_put_wait();
+            }
+            tc_fence_before();
+            if (half_sync_or(1, bad)) return true;
+            tc_fence_after();
+            // 3. U^T = R^T T^T (the side, which has time for it, issues the state's part of Y and the loads: code that
+            // one warp runs once a chunk comes from far in the instruction cache, some 400 cycles a visit)
+            if (warp == 0) {
+                arm(B_U, ph);
+                if (elect_one()) {
+                    const uint32_t T = smem_u32(sm.T);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ts(lanes + T_U, lanes + T_X + kk * 8, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+                    mma_commit(&sm.bar[B_U]);
+                }
+            } else if (warp == 2) {
+                if (!wait_for(&sm.bar[B_A], ph)) bad = 1;
+            } else if (warp == 3) {
+                if (!wait_for(&sm.bar[B_OI], ph)) bad = 1;  // the state's copy is read: the increment may take its columns
+            }
+            // 4. U^T rounded, as it is and times e^(c_64 - c) |k| (a product of rounded numbers: a conversion from fp32
+            // takes four times as long)
+            if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
+            tc_fence_after();
+            tmem_pieces<4>(lanes + T_U, [&](int n, const uint32_t (&u)[16]) {  // 16 tokens: both forms over their own columns
+                const uint4 w0 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n), w1 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n + 8);
+                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                 uint32_t pk[8];
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint4 v8 = *reinterpret_cast<const uint4 *>(sm.v + swz128_chunk(row, 2 * n + m));
-                    const uint32_t w[4] = {v8.x, v8.y, v8.z, v8.w};
-                    const float4 r0 = *reinterpret_cast<const float4 *>(gt.rk + 16 * n + 8 * m);
-                    const float4 r1 = *reinterpret_cast<const float4 *>(gt.rk + 16 * n + 8 * m + 4);
-                    const uint64_t rk[4] = {pair(-r0.x, -r0.y), pair(-r0.z, -r0.w), pair(-r1.x, -r1.y), pair(-r1.z, -r1.w)};
+                for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+                tmem_put8(lanes + T_U + 16 * n, pk);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint64_t v2 = mul2(pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), sc);
-                        const int e = 8 * m + 2 * i;
-                        float lo, hi;
-                        unpair(fma2(rk[i], pair(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), v2), lo, hi);
-                        pk[4 * m + i] = pack_f16x2(lo, hi);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 e = __hmul2(*reinterpret_cast<const __half2 *>(&pk[i]), *reinterpret_cast<const __half2 *>(&w[i]));
+                    pk[i] = *reinterpret_cast<const uint32_t *>(&e);
                 }
-                tmem_put8(lanes + T_X + 8 * n, pk);  // (packed to the left: over what has been read)
+                tmem_put8(lanes + T_U + 16 * n + 8, pk);
             });
             tmem_put_wait();
-            sm.unscale[ph][row] = unscale;
             tc_fence_before();
-            const bool again = half_sync_or(1, bad || over);
+            if (half_sync_or(1, bad)) return true;
             tc_fence_after();
-            if (!again) break;
-            rescale = true;
-        }
-        // 3. U^T = R^T T^T, the next values, and the state's part of Y, each from a warp of its own
-        if (warp == 0) {
-            if (!bad) arm(B_U, ph);
-            if (elect_one() && !bad) {
-                const uint32_t T = smem_u32(sm.T);
+            // 5. the state's increment, over the columns of its copy and of R (both are read), and A's part of Y; meanwhile
+            // the next values
+            if (warp == 0) {
+                arm(B_S, ph), arm(B_Y, ph);
+                if (elect_one()) {
+                    const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(lanes + T_U, lanes + T_X + kk * 8, desc_kmajor(T, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-                mma_commit(&sm.bar[B_U]);
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ts(lanes + T_D, lanes + T_U + kk * 16 + 8, desc_mnmajor(k, kBlk, kk), idesc_f16(128, TN, true), kk > 0);
+                    mma_commit(&sm.bar[B_S]);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ts(lanes + T_Y, lanes + T_U + kk * 16, desc_kmajor(A, kBlk, kk), idesc_f16(128, C, false), 1);
+                    mma_commit(&sm.bar[B_Y]);
+                }
             }
-            if (!wait_for(&sm.bar[B_A], ph)) bad = 1;
-        } else if (warp == 1) {
-            if (c + 1 < sm.nc && !bad) {
-                arm(B_V, ph ^ 1);
-                if (elect_one()) J.load_values(c + 1);  // (every row's values are in R)
-            }
-        } else if (warp == 2) {
-            if (!wait_for(&sm.bar[B_SCALED], ph)) bad = 1;
-            if (!bad) arm(B_OI, ph);
+        }
+        if (c + 1 < sm.nc) take_values(c + 1);
+        if (c >= 0) {
+            // 6. the new state, and its copy over the increment (a row's columns are its thread's own)
+            const float last = gt.last;
+            if (!wait_for(&sm.bar[B_S], ph)) bad = 1;
             tc_fence_after();
-            if (elect_one() && !bad) {
-                const uint32_t q = smem_u32(sm.q[ph]), tm = sm.tmem;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
-                mma_commit(&sm.bar[B_OI]);
+            for (int n = 0; n < TN / 16; ++n) {
+                uint32_t d[16];
+                tmem_get(lanes + T_D + 16 * n, d);
+                tmem_got(d);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[16 * n + i] = fmaf(last, S[16 * n + i], __uint_as_float(d[i]));
+            }
+            if (p.ckpt_slots) {
+                const int32_t cs = ckpt_slot(p, sm.s, min(sm.len, (c + 1) * C), threadIdx.x == 0 && sm.h == 0);
+                if (__builtin_expect(cs >= 0, 0)) write_state(cs);
             }
         }
-        // 4. U^T rounded, as it is and times e^(c_64 - c) |k| (a product of rounded numbers: a conversion from fp32
-        // takes four times as long)
-        if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
-        tc_fence_after();
-        tmem_pieces<4>(lanes + T_U, [&](int n, const uint32_t (&u)[16]) {  // 16 tokens: both forms over their own columns
-            const uint4 w0 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n), w1 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n + 8);
-            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            uint32_t pk[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-            tmem_put8(lanes + T_U + 16 * n, pk);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const __half2 e = __hmul2(*reinterpret_cast<const __half2 *>(&pk[i]), *reinterpret_cast<const __half2 *>(&w[i]));
-                pk[i] = *reinterpret_cast<const uint32_t *>(&e);
-            }
-            tmem_put8(lanes + T_U + 16 * n + 8, pk);
-        });
-        tmem_put_wait();
-        tc_fence_before();
-        if (half_sync_or(1, bad)) return true;
-        tc_fence_after();
-        // 5. the state's increment, over the columns of its copy and of R (both are read), and A's part of Y
-        if (warp == 0) {
-            if (!wait_for(&sm.bar[B_OI], ph)) bad = 1;
-            if (!bad) arm(B_S, ph), arm(B_Y, ph);
-            if (elect_one() && !bad) {
-                const uint32_t A = smem_u32(sm.A), k = smem_u32(sm.k[ph]);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(lanes + T_D, lanes + T_U + kk * 16 + 8, desc_mnmajor(k, kBlk, kk), idesc_f16(128, TN, true), kk > 0);
-                mma_commit(&sm.bar[B_S]);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_ts(lanes + T_Y, lanes + T_U + kk * 16, desc_kmajor(A, kBlk, kk), idesc_f16(128, C, false), 1);
-                mma_commit(&sm.bar[B_Y]);
-            }
-        } else if (warp == 1 && c + 1 < sm.nc && !bad) {
-            arm(B_T, ph ^ 1);
-            if (elect_one()) J.load_tile(c + 1, B_T, sm.T, 0);  // (U is formed)
-        }
-        // 6. the new state, and its copy over the increment (a row's columns are its thread's own)
-        const float last = gt.last;
-        if (!wait_for(&sm.bar[B_S], ph)) bad = 1;
-        tc_fence_after();
-        tmem_pieces<8>(lanes + T_D, [&](int n, const uint32_t (&d)[16]) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) S[16 * n + i] = fmaf(last, S[16 * n + i], __uint_as_float(d[i]));
-        });
-        if (p.ckpt_slots) {
-            const int32_t cs = ckpt_slot(p, sm.s, min(sm.len, (c + 1) * C), threadIdx.x == 0 && sm.h == 0);
-            if (cs >= 0) write_state(cs);
-        }
-        if (c + 1 < sm.nc && (c + 1) % kRescale != 0) {
-#pragma unroll
-            for (int e = 0; e < TN; e += 16) store_state16(e);
-            tmem_put_wait();
-        }
+        if (c + 1 < sm.nc) choose_power(c + 1);
         tc_fence_before();
         if (half_sync_or(1, bad)) return true;
         tc_fence_after();
@@ -870,9 +859,9 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     return false;
 }
 
-// The four warps beside the chain: they turn the values of the next chunk, scale its queries, take the
-// outputs to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31,
-// the fragments of 32 values by 8 tokens.  Returns whether a wait gave up.
+// The four warps beside the chain: they scale the next chunk's queries, issue the state's part of Y, take the
+// outputs to memory, and load.  Warp w works on tensor-memory lanes 32 w .. + 31, as fragments of 32 values
+// by 8 tokens.  Returns whether a wait gave up.
 template <int P>
 __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     const ScanParams &p = J.p;
@@ -880,55 +869,40 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
     const bool live = 32 * warp < P;  // this warp's rows are values
     const uint32_t lanes = sm.tmem + ((uint32_t)(warp * 32) << 16);
-    // this lane's 16 bytes (8 values of a token) of a tile by tokens, for 8 tokens from 8 n
+    // this lane's 16 bytes (8 values of a token) of the outputs' tile, for 8 tokens from 8 n
     auto token_row = [&](const unsigned char *tile, int n) {
         return smem_u32(tile) + (warp >> 1) * kBlk + swz128_chunk(8 * n + (lane & 7), 4 * (warp & 1) + (lane >> 3));
     };
     int bad = 0;
     for (int c = -1; c < sm.nc; ++c) {
         const int c1 = c + 1;
-        if (warp == 2 && c + 2 < sm.nc && elect_one()) J.prefetch(c + 2);
+        if (c >= 0 && warp == 0) {
+            // the state's part of Y, once the state's copy is there (X is formed of it)
+            if (!wait_for(&sm.bar[B_X], c & 1)) bad = 1;
+            tc_fence_after();
+            if (!bad) {
+                arm(B_OI, c & 1);
+                if (elect_one()) {
+                    const uint32_t q = smem_u32(sm.q[c & 1]), tm = sm.tmem;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_ts(tm + T_Y, tm + T_S + 8 * kk, desc_kmajor(q, kBlk, kk), idesc_f16(128, C, false), kk > 0);
+                    mma_commit(&sm.bar[B_OI]);
+                }
+            }
+        } else if (c >= 0 && warp == 3 && c1 < sm.nc) {
+            if (!wait_for(&sm.bar[B_U], c & 1)) bad = 1;  // T is used
+            if (!bad) {
+                arm(B_T, c1 & 1);
+                if (elect_one()) J.load_tile(c1, B_T, sm.T, 0);
+            }
+        } else if (warp == 2 && c + 2 < sm.nc) {
+            if (elect_one()) J.prefetch(c + 2);
+        }
         if (c1 < sm.nc) {
-            // the next chunk's values, turned in place
-            if (!wait_for(&sm.bar[B_V], c1 & 1)) bad = 1;
-            uint32_t v[8][4] = {};  // [n][i]: rows 8 i + T / 4, tokens 8 n + 2 (T % 4) and the next
-            if (live) {
-#pragma unroll
-                for (int n = 0; n < 8; ++n) ldmatrix4_trans(v[n], token_row(sm.v, n));
-            }
-            const int L = sm.len - c1 * C;
-            if (L < C) {  // rows past the sequence's end hold another sequence's values
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const int t = 8 * n + (lane & 3) * 2;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[n][i] = t + 1 < L ? v[n][i] : (t < L ? v[n][i] & 0xffffu : 0u);
-                }
-            }
-            if (half_sync_or(2, bad)) return true;  // all values are in registers
-#pragma unroll
-            for (int n = 0; n < 8; ++n) stmatrix4(smem_u32(sm.v) + swz128_chunk(32 * warp + lane, n), v[n]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t m2 = 0;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m2),
-                                                     __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[n][i])));
-                    m2 = *reinterpret_cast<const uint32_t *>(&m);
-                }
-                float top = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if ((lane & 3) == 0) sm.vmax[32 * warp + 8 * i + (lane >> 2)] = top;
-            }
-            fence_async_smem();
-            if (!wait_for(&sm.bar[B_K + (c1 & 1)], (c1 >> 1) & 1)) bad = 1;  // (the gates: the chain reads them after this)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.bar[B_READY]);
-            // its queries times e^c, in place, 16 bytes of a token each: tokens 16 apart, in both blocks of 64
-            // elements
-            if (!wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
+            // the next chunk's queries times e^c, in place, 16 bytes of a token each: tokens 16 apart, in both blocks
+            // of 64 elements
+            if (!wait_for(&sm.bar[B_IN + (c1 & 1)], (c1 >> 1) & 1) || !wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
             const __half *g = sm.gates[c1 & 3].g + (tid >> 3);
             uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1]) + tid;
             uint4 u[8];
@@ -945,6 +919,13 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
                 ptr[128 * i] = u[i];
             }
             fence_async_smem();
+            if (warp == 1 && c + 2 < sm.nc) {
+                if (!wait_for(&sm.bar[B_TAKEN], c1 & 1)) bad = 1;  // the next values are in registers
+                if (!bad) {
+                    arm(B_IN + (c & 1), (c + 2) >> 1 & 1);
+                    if (elect_one()) J.load_values(c + 2);
+                }
+            }
         }
         // this chunk's outputs, over its queries and from there to memory
         if (c >= 0) {
@@ -959,7 +940,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
             for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
             if (warp == 2 && !bad) {
                 if (c1 < sm.nc) arm(B_A, c1 & 1);
-                if (c + 2 < sm.nc) arm(B_K + (c & 1), (c + 2) >> 1 & 1);
+                if (c + 2 < sm.nc) arm(B_IN + (c & 1), (c + 2) >> 1 & 1);
                 if (elect_one()) {
                     if (c1 < sm.nc) J.load_tile(c1, B_A, sm.A, kBlk);
                     if (c + 2 < sm.nc) J.load_keys(c + 2);
@@ -990,7 +971,6 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
             tc_fence_before();
         }
         if (half_sync_or(2, bad)) return true;  // Y is taken, the outputs are staged, the next queries scaled
-        if (lane == 0) mbar_arrive(&sm.bar[B_SCALED]);
         const bool whole = c >= 0 && (c + 1) * C <= sm.len;
         if (c >= 0 && !whole) {  // the sequence's last tokens: the rows after them are another's
             constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
@@ -1041,7 +1021,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     const int warp = threadIdx.x >> 5;
     __syncwarp();
     if (warp == 5 && elect_one()) {
-        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i >= B_READY ? 4 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i == B_TAKEN ? 4 : i < B_Q ? 2 : 1);
         fence_mbar_init();
         tma_prefetch_desc(&vmap);
         J.load_keys(0);
@@ -1068,8 +1048,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     } else {
         fewer_registers<kSideRegs>();
         Armed arm;
-        arm(B_K, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0), arm(B_V, 0);
-        if (sm.nc > 1) arm(B_K + 1, 0);
+        arm(B_IN, 0), arm(B_Q, 0), arm(B_T, 0), arm(B_A, 0);
         failed = side_warps(J, arm);
         if ((threadIdx.x & 31) == 0) sm.armed[warp] = arm.bars, sm.parity[warp] = arm.parity;
     }
@@ -1106,16 +1085,16 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Rows of tokens x (heads * head_dim) values, in swizzled boxes of 64 tokens x 64 values; rows past the end
-// read as zero.
-bool value_map(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows) {
+// Rows of tokens x (heads * head_dim) values, in boxes of 64 tokens: of a head's values each token after the
+// other to load, of 64 values swizzled to store.  Rows past the end read as zero.
+bool value_map(CUtensorMap *m, const void *ptr, uint64_t cols, uint64_t rows, int head_dim, bool store) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
-    cuuint32_t box[2] = {64, C}, es[2] = {1, 1};
+    cuuint32_t box[2] = {store ? 64u : (cuuint32_t)head_dim, C}, es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_INTERLEAVE_NONE, store ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -1133,8 +1112,8 @@ size_t chunked_workspace_bytes(const mamba_layer_desc *d, int T, int nseq) {
 int chunked_launch(const ScanParams &p, int head_dim, cudaStream_t st) {
     const WsLayout ws(p.ws, p.H, p.G);
     CUtensorMap vmap, ymap;
-    if (!value_map(&vmap, p.v, (uint64_t)p.H * head_dim, (uint64_t)p.T) ||
-        !value_map(&ymap, p.y, (uint64_t)p.H * head_dim, (uint64_t)p.T))
+    if (!value_map(&vmap, p.v, (uint64_t)p.H * head_dim, (uint64_t)p.T, head_dim, false) ||
+        !value_map(&ymap, p.y, (uint64_t)p.H * head_dim, (uint64_t)p.T, head_dim, true))
         return MAMBA_ECUDA;
     const bool pairs = p.HG % 2 == 0;  // heads of a group share its products, two a block
     auto prep = pairs ? k_gdn_prep<2> : k_gdn_prep<1>;
