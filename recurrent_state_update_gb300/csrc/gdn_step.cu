@@ -176,34 +176,6 @@ __device__ __forceinline__ void codes_to_f32(uint2 w, uint64_t (&v)[4]) {
         asm("add.rn.f32x2 %0, %0, %1;" : "+l"(v[e]) : "l"(bias));
     }
 }
-// The step on codes: S holds them as fp32, sc their columns' scales, which go into the keys and queries of
-// the sums and into the decay.  (Reading sc and k twice leaves the registers to the sums.)
-template <typename Map, typename ActT>
-__device__ __forceinline__ float token_codes(uint64_t (&S)[Map::RT][4], const float *scales, const ActT *ksrc, const ActT *qsrc,
-                                             float rk, float rq, float ukq, float a, float b, float v, int lane) {
-    uint64_t x[4], sc[4];
-    float f[8];
-    auto scaled = [&](const ActT *src) {  // keys or queries times the columns' scales
-        load8(src, f);
-        load_row_shared(scales, sc);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(pair(f[2 * e], f[2 * e + 1]), sc[e]);
-    };
-    scaled(qsrc);
-    const float sq = row_sum<Map>(S, x, lane);
-    scaled(ksrc);
-    const float u = b * (v - a * rk * row_sum<Map>(S, x, lane));
-    load8(ksrc, f);
-    load_row_shared(scales, sc);
-    const uint64_t a2 = pair(a, a);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[e] = pair(f[2 * e], f[2 * e + 1]);
-        sc[e] = mul2(sc[e], a2);
-    }
-    write_rows<Map>(S, sc, x, u, rk, lane);
-    return fmaf(a * rq, sq, u * ukq);
-}
 __device__ __forceinline__ uint2 f32_to_codes(const uint64_t (&v)[4], const uint64_t (&inv)[4]) {
     const uint64_t round = pair(12582912.0f, 12582912.0f);
     uint32_t half[4];
@@ -217,55 +189,19 @@ __device__ __forceinline__ uint2 f32_to_codes(const uint64_t (&v)[4], const uint
     return make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
 }
 
-// The largest magnitude in each of this lane's columns over its warp's rows.
-template <typename Map>
-__device__ __forceinline__ void column_maxima(const uint64_t (&S)[Map::RT][4], float *top, int sub) {
-    float m[8] = {};
-#pragma unroll
-    for (int r = 0; r < Map::RT; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float lo, hi;
-            unpair(S[r][c], lo, hi);
-            m[2 * c] = fmaxf(m[2 * c], fabsf(lo));
-            m[2 * c + 1] = fmaxf(m[2 * c + 1], fabsf(hi));
-        }
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int o = Map::LPR; o < 32; o *= 2) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
-    if (sub == 0) {
-        reinterpret_cast<float4 *>(top)[0] = make_float4(m[0], m[1], m[2], m[3]);
-        reinterpret_cast<float4 *>(top)[1] = make_float4(m[4], m[5], m[6], m[7]);
-    }
-}
-// From the warps' column maxima the new scales, a column a thread, and what codes are formed with.
-template <int WARPS, int N>
-__device__ __forceinline__ void new_scales(const float (*top)[N], float *inv, float *scales) {
-    for (int c = threadIdx.x; c < N; c += 32 * WARPS) {
-        float t = top[0][c];
-#pragma unroll
-        for (int w = 1; w < WARPS; ++w) t = fmaxf(t, top[w][c]);
-        inv[c] = t > kLeast ? 127.0f / t : 0.0f;
-        scales[c] = t / 127.0f;
-    }
-}
-template <typename Map, int N>
-__device__ __forceinline__ void store_codes(unsigned char *codes, const uint64_t (&S)[Map::RT][4], const float *inv) {
-    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(inv)[0], b = reinterpret_cast<const ulonglong2 *>(inv)[1];
-    const uint64_t inv2[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-    for (int r = 0; r < Map::RT; ++r) __stcs(reinterpret_cast<uint2 *>(codes + r * Map::RPW * N), f32_to_codes(S[r], inv2));
-}
-
-// Block (head, batch row): all rows of the head, because a scale covers a column of it.  Codes
-// become fp32 on load; the new state is scaled by the new column maxima (a maximum over the warps
-// through shared memory) and rounded to the grid of step max/127, as the int8 store does.
+// Block (head, batch row): all rows of the head, because a scale covers a column of it.  Codes become fp32
+// on load; what belongs to a column (its scale, key and query) is made once for the block; the new state is
+// scaled by the new column maxima (over the warps through shared memory) and rounded to the grid of
+// step max/127, as the int8 store does.  At 192 rows of 32 heads of 128 x 128 a step moves 213 MB in
+// 54.4 us, 0.57 of what a copy moves: some 9 instructions a value (two products, the update, the maximum, and
+// bytes to fp32 and back) and three barriers a block keep the SM from asking for more.
 template <typename ActT, int P, int N, int RT>
 __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(const Int8Args p) {
     using Map = RowMap<N, RT>;
     constexpr int WARPS = P / Map::ROWS;
-    __shared__ __align__(16) float top[WARPS][N], inv_s[N];  // inv_s: first the scales
+    // by column: largest magnitudes by warp; keys and queries times the scales; scales; keys; what codes are
+    // formed with
+    __shared__ __align__(16) float top[WARPS][N], ks[N], qs[N], sa[N], kf[N], inv[N];
     __shared__ float scalars[5];
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
@@ -280,18 +216,24 @@ __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(
     const int col = (lane & (Map::LPR - 1)) * 8, sub = lane / Map::LPR, row0 = warp * Map::ROWS;
     const int idx = (lane & (Map::LPR - 1)) / Map::SHARE, vrow = row0 + idx * Map::RPW + sub;
     unsigned char *codes = ent + ((int64_t)h * P + row0 + sub) * N + col;
-    float *scales = reinterpret_cast<float *>(ent + p.scale_off) + (int64_t)h * N + col;
+    float *scales = reinterpret_cast<float *>(ent + p.scale_off) + (int64_t)h * N;
     uint2 raw[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) raw[r] = __ldcs(reinterpret_cast<const uint2 *>(codes + r * Map::RPW * N));
     const int64_t th = (int64_t)i * p.H + h;
     const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.Cd;
-    const ActT *ksrc = xbc + p.H * P + (h / p.HG) * N + col, *qsrc = ksrc + p.G * N;
+    const ActT *ksrc = xbc + p.H * P + (h / p.HG) * N, *qsrc = ksrc + p.G * N;
     const float v = to_f32(xbc[h * P + vrow]);
-    for (int c = threadIdx.x; c < N; c += 32 * WARPS) inv_s[c] = scales[c - col];
-    if (warp == 0) {  // the token's scalars, once for the block
+    for (int c = threadIdx.x; c < N; c += 32 * WARPS) {
+        const float sc = scales[c], k = to_f32(ksrc[c]);
+        ks[c] = k * sc;
+        qs[c] = to_f32(qsrc[c]) * sc;
+        sa[c] = sc;
+        kf[c] = k;
+    }
+    if (warp == WARPS - 1) {  // the token's scalars, once for the block
         TokenIn<Map, ActT> in;
-        in.unpack(ksrc, qsrc);
+        in.unpack(ksrc + col, qsrc + col);
         in.load_scalars(p.gates, h, p.dt, p.beta, th);
         if (lane == 0) scalars[0] = in.rk, scalars[1] = in.rq, scalars[2] = in.ukq, scalars[3] = in.a, scalars[4] = in.b;
     }
@@ -299,14 +241,53 @@ __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(
 #pragma unroll
     for (int r = 0; r < RT; ++r) codes_to_f32(raw[r], S[r]);
     __syncthreads();
-    const float out = token_codes<Map>(S, &inv_s[col], ksrc, qsrc, scalars[0], scalars[1], scalars[2], scalars[3], scalars[4], v,
-                                       lane);
+    const float a = scalars[3], rk = scalars[0];
+    uint64_t k[4], x[4];
+    load_row_shared(qs + col, x);
+    const float sq = row_sum<Map>(S, x, lane);
+    load_row_shared(ks + col, x);
+    const float u = scalars[4] * (v - a * rk * row_sum<Map>(S, x, lane));
+    const float out = fmaf(a * scalars[1], sq, u * scalars[2]);
     if ((lane & (Map::SHARE - 1)) == 0) static_cast<ActT *>(p.y)[th * P + vrow] = from_f32<ActT>(out);
-    column_maxima<Map>(S, &top[warp][col], sub);
-    __syncthreads();  // (every thread has its scales, too)
-    new_scales<WARPS, N>(top, inv_s, scales - col);
+    load_row_shared(kf + col, k);
+    load_row_shared(sa + col, x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = mul2(x[c], pair(a, a));
+    write_rows<Map>(S, x, k, u, rk, lane);
+    {
+        float m[8] = {};
+#pragma unroll
+        for (int r = 0; r < RT; r += 2)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // (of two rows at a time: the maximum takes three numbers)
+                float lo, hi, lo2 = 0.0f, hi2 = 0.0f;
+                unpair(S[r][c], lo, hi);
+                if (r + 1 < RT) unpair(S[r + 1][c], lo2, hi2);
+                asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m[2 * c]) : "f"(lo), "f"(lo2));
+                asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m[2 * c + 1]) : "f"(hi), "f"(hi2));
+            }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int o = Map::LPR; o < 32; o *= 2) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+        if (sub == 0) {
+            reinterpret_cast<float4 *>(&top[warp][col])[0] = make_float4(m[0], m[1], m[2], m[3]);
+            reinterpret_cast<float4 *>(&top[warp][col])[1] = make_float4(m[4], m[5], m[6], m[7]);
+        }
+    }
     __syncthreads();
-    store_codes<Map, N>(codes, S, &inv_s[col]);
+    for (int c = threadIdx.x; c < N; c += 32 * WARPS) {
+        float t = top[0][c];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) t = fmaxf(t, top[w][c]);
+        inv[c] = t > kLeast ? 127.0f / t : 0.0f;
+        scales[c] = t / 127.0f;
+    }
+    __syncthreads();
+    uint64_t to[4];
+    load_row_shared(inv + col, to);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) __stcs(reinterpret_cast<uint2 *>(codes + r * Map::RPW * N), f32_to_codes(S[r], to));
 }
 
 // Blocks of two warps (P = 16: one) with as many rows a lane as have sums for its 16 lanes: measured at
@@ -332,6 +313,12 @@ int dispatch_step(StepArgs &a, int batch, int P, int N, cudaStream_t st) {
     return MAMBA_EUNSUPPORTED;
 }
 
+// Many rows a lane, whose products and maxima then cost a warp less for each: at 192 rows of 32 heads of
+// 128 x 128, 16 rows a lane (4 warps a block, three blocks an SM) took 54.3 us, 8 rows 69.8, 4 rows 74.7;
+// at 600 rows of 8 heads of 64 x 64, 8 rows 13.5 us, 4 rows 14.5; at 800 rows of 12 heads of 32 x 64, 15.4 and
+// 16.2.  Heads of 64 x 128 fill a block of 4 warps with 8 rows a lane: 56.0 us at 100 rows of 128 heads,
+// against 59.9 with 16.  Keeping only the codes and forming the new state twice, for twice the warps an SM,
+// took 70.8 us at the first of these sizes: half as many instructions again.
 template <typename ActT, int P, int N, int RT>
 int launch_int8(const Int8Args &a, int batch, cudaStream_t st) {
     const dim3 grid((unsigned)a.H, (unsigned)batch), block(P / RowMap<N, RT>::ROWS * 32);
@@ -341,10 +328,10 @@ int launch_int8(const Int8Args &a, int batch, cudaStream_t st) {
 
 template <typename ActT>
 int dispatch_int8(const Int8Args &a, int batch, int P, int N, cudaStream_t st) {
-    if (P == 128 && N == 128) return launch_int8<ActT, 128, 128, 8>(a, batch, st);
+    if (P == 128 && N == 128) return launch_int8<ActT, 128, 128, 16>(a, batch, st);
     if (P == 64 && N == 128) return launch_int8<ActT, 64, 128, 8>(a, batch, st);
-    if (P == 64 && N == 64) return launch_int8<ActT, 64, 64, 4>(a, batch, st);
-    if (P == 32 && N == 64) return launch_int8<ActT, 32, 64, 4>(a, batch, st);
+    if (P == 64 && N == 64) return launch_int8<ActT, 64, 64, 8>(a, batch, st);
+    if (P == 32 && N == 64) return launch_int8<ActT, 32, 64, 8>(a, batch, st);
     if (P == 16 && N == 16) return launch_int8<ActT, 16, 16, 1>(a, batch, st);
     return MAMBA_EUNSUPPORTED;
 }
