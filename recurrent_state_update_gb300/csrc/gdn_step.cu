@@ -115,35 +115,66 @@ __global__ void __launch_bounds__(64) k_gdn_step(const StepArgs p) {
 }
 
 // Several tokens in order, the state after each into its scratch slot when there are some, else the last
-// one's into the row's own.  Block (head and share of its rows, batch row).
+// one's into the row's own.  Block (head and share of its rows, batch row).  While the state is on its way the
+// tokens' keys, queries, values and scalars are brought to shared memory, a token to each LPR lanes, so that
+// the tokens follow one another without a wait on memory: 4 tokens into scratch slots for 48 rows of 32 heads of
+// 128 x 128 take 43.0 us, 0.88 of what a copy of those bytes takes (48.5 with each token's loads where it is used),
+// for 61 rows of 128 heads of 64 x 128 99.6 us, 0.96 (111.8).
 template <typename StateT, typename ActT, int P, int N, int RT>
 __global__ void __launch_bounds__(64) k_gdn_tokens_step(const StepArgs p) {
     using Map = RowMap<N, RT>;
+    using Raw = typename RawOf<StateT>::type;
+    __shared__ __align__(16) float ks[kMaxTok][N], qs[kMaxTok][N];
+    __shared__ float vs[kMaxTok][2 * Map::ROWS], scalars[kMaxTok][5];
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     const int i = blockIdx.y, h = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int32_t s = step_slot(p, i);
     if (s < 0) return;
-    const int row0 = (split * (blockDim.x >> 5) + warp) * Map::ROWS;
-    const int sub = lane / Map::LPR, idx = (lane & (Map::LPR - 1)) / Map::SHARE;
+    const int row0 = split * warps * Map::ROWS;  // the block's
+    const int sub = lane / Map::LPR, idx = (lane & (Map::LPR - 1)) / Map::SHARE, col = (lane & (Map::LPR - 1)) * 8;
+    const int lrow = warp * Map::ROWS + idx * Map::RPW + sub;
     StateT *pool = static_cast<StateT *>(p.pool);
-    const int64_t off = ((int64_t)h * P + row0 + sub) * N + (lane & (Map::LPR - 1)) * 8;
+    const int64_t off = ((int64_t)h * P + row0 + warp * Map::ROWS + sub) * N + col;
+    Raw raw[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) raw[r].load(pool + s * p.stride + off + (int64_t)r * Map::RPW * N);
+    const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.ntok * p.Cd;
+    for (int base = 0; base < p.ntok; base += warps * Map::RPW) {
+        const int own = base + warp * Map::RPW + sub, j = min(own, p.ntok - 1);
+        TokenIn<Map, ActT> in;
+        in.load_vectors(xbc + (int64_t)j * p.Cd, p.H * P, p.G * N, h / p.HG, N, lane);
+        in.load_scalars(p.gates, h, p.dt, p.beta, ((int64_t)i * p.ntok + j) * p.H + h);
+        if (own == j) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                *reinterpret_cast<ulonglong2 *>(&ks[j][col + 2 * e]) = make_ulonglong2(in.k[e], in.k[e + 1]);
+                *reinterpret_cast<ulonglong2 *>(&qs[j][col + 2 * e]) = make_ulonglong2(in.q[e], in.q[e + 1]);
+            }
+            if (col == 0) {
+                float *to = scalars[j];
+                to[0] = in.rk, to[1] = in.rq, to[2] = in.ukq, to[3] = in.a, to[4] = in.b;
+            }
+        }
+    }
+    for (int e = threadIdx.x; e < p.ntok * warps * Map::ROWS; e += blockDim.x) {
+        const int j = e / (warps * Map::ROWS), r = e % (warps * Map::ROWS);
+        vs[j][r] = to_f32(xbc[(int64_t)j * p.Cd + h * P + row0 + r]);
+    }
     uint64_t S[RT][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) load_row(pool + s * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
-    const int vrow = row0 + idx * Map::RPW + sub;
-    const ActT *xbc = static_cast<const ActT *>(p.xbc);
-    ActT *y = static_cast<ActT *>(p.y);
-    for (int j = 0; j < p.ntok; ++j) {
-        const int64_t t = (int64_t)i * p.ntok + j;
-        TokenIn<Map, ActT> in;
-        in.load_vectors(xbc + t * p.Cd, p.H * P, p.G * N, h / p.HG, N, lane);
-        in.load_scalars(p.gates, h, p.dt, p.beta, t * p.H + h);
-        const float v = to_f32(xbc[t * p.Cd + h * P + vrow]);
-        const float out = token_rows<Map>(S, in.k, in.q, in.rk, in.rq, in.ukq, in.a, in.b, v, lane);
-        if ((lane & (Map::SHARE - 1)) == 0) y[(t * p.H + h) * P + vrow] = from_f32<ActT>(out);
-        const int32_t d = p.scratch ? p.scratch[t] : (j == p.ntok - 1 ? s : -1);
+    for (int r = 0; r < RT; ++r) raw[r].unpack(S[r]);
+    __syncthreads();
+    ActT *y = static_cast<ActT *>(p.y) + ((int64_t)i * p.ntok * p.H + h) * P + row0 + lrow;
+    for (int j = 0; j < p.ntok; ++j, y += (int64_t)p.H * P) {
+        uint64_t k[4], q[4];
+        load_row_shared(&ks[j][col], k);
+        load_row_shared(&qs[j][col], q);
+        const float *in = scalars[j];
+        const float out = token_rows<Map>(S, k, q, in[0], in[1], in[2], in[3], in[4], vs[j][lrow], lane);
+        if ((lane & (Map::SHARE - 1)) == 0) *y = from_f32<ActT>(out);
+        const int32_t d = p.scratch ? p.scratch[(int64_t)i * p.ntok + j] : (j == p.ntok - 1 ? s : -1);
         if (d >= 0) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) store_row(pool + d * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
@@ -290,9 +321,11 @@ __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(
     for (int r = 0; r < RT; ++r) __stcs(reinterpret_cast<uint2 *>(codes + r * Map::RPW * N), f32_to_codes(S[r], to));
 }
 
-// Blocks of two warps (P = 16: one) with as many rows a lane as have sums for its 16 lanes: measured at
-// 256 rows of 32 heads of 128 x 128 in bf16, eight warps a block took 104 us, four 98, two 97, and 4 or 2
-// rows a lane 103 and 150 (the token's own scalars cost a warp as much as a few rows).
+// Blocks of two warps (one, where a head has no more rows) with 8 rows a lane: 256 rows of 32 heads of 128 x 128
+// in bf16 take 83.8 us, 0.95 of what a copy of those bytes takes; 89.8 with 16 rows a lane.  Measured with an
+// earlier form of the arithmetic, eight warps a block took 104 us, four 98, two 97, and 4 or 2 rows a lane 103
+// and 150 (the token's own scalars cost a warp as much as a few rows).  Of narrower heads 8 rows a lane are as
+// many as there are sums for its lanes: 6.8 us for 300 rows of 8 heads of 64 x 64, and 7.6 with 4.
 template <typename StateT, typename ActT, int P, int N, int RT>
 int launch_step(StepArgs &a, int batch, cudaStream_t st) {
     constexpr int rows = RowMap<N, RT>::ROWS, warps = P / rows < 2 ? P / rows : 2;
@@ -307,8 +340,8 @@ template <typename StateT, typename ActT>
 int dispatch_step(StepArgs &a, int batch, int P, int N, cudaStream_t st) {
     if (P == 128 && N == 128) return launch_step<StateT, ActT, 128, 128, 8>(a, batch, st);
     if (P == 64 && N == 128) return launch_step<StateT, ActT, 64, 128, 8>(a, batch, st);
-    if (P == 64 && N == 64) return launch_step<StateT, ActT, 64, 64, 4>(a, batch, st);
-    if (P == 32 && N == 64) return launch_step<StateT, ActT, 32, 64, 4>(a, batch, st);
+    if (P == 64 && N == 64) return launch_step<StateT, ActT, 64, 64, 8>(a, batch, st);
+    if (P == 32 && N == 64) return launch_step<StateT, ActT, 32, 64, 8>(a, batch, st);
     if (P == 16 && N == 16) return launch_step<StateT, ActT, 16, 16, 1>(a, batch, st);
     return MAMBA_EUNSUPPORTED;
 }
