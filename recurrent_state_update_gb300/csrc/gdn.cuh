@@ -131,11 +131,11 @@ __device__ __forceinline__ void store_row(T *p, const uint64_t (&v)[4]) {
     store8_stream(p, f);
 }
 
-// How a warp holds rows of S: LPR lanes a row with 8 consecutive values each, RPW rows side by
-// side, RT rows a lane (row r * RPW + lane / LPR of the warp's RPW * RT).
-template <int N, int RT_>
+// How a warp holds rows of S: LPR lanes a row with PIECES times 8 consecutive values each (a piece of all lanes
+// after the other), RPW rows side by side, RT rows a lane (row r * RPW + lane / LPR of the warp's RPW * RT).
+template <int N, int RT_, int PIECES = 1>
 struct RowMap {
-    static constexpr int LPR = N / 8, RPW = 32 / LPR, RT = RT_, ROWS = RPW * RT;
+    static constexpr int LPR = N / (8 * PIECES), RPW = 32 / LPR, RT = RT_, ROWS = RPW * RT, PAIRS = 4 * PIECES;
     static constexpr int SHARE = LPR / RT;   // lanes of a row's that end up with the same row's sum
     static_assert(LPR >= RT, "more sums than lanes of a row");
 };
@@ -174,13 +174,13 @@ __device__ __forceinline__ float sum_lanes(float v) {
 // S x of the rows a warp holds, that of row r in the lanes of index r, where a lane's index is (its place in
 // the row) / SHARE.
 template <typename Map>
-__device__ __forceinline__ float row_sum(const uint64_t (&S)[Map::RT][4], const uint64_t (&x)[4], int lane) {
+__device__ __forceinline__ float row_sum(const uint64_t (&S)[Map::RT][Map::PAIRS], const uint64_t (&x)[Map::PAIRS], int lane) {
     float val[Map::RT];
 #pragma unroll
     for (int r = 0; r < Map::RT; ++r) {
         uint64_t p = mul2(S[r][0], x[0]);
 #pragma unroll
-        for (int e = 1; e < 4; ++e) p = fma2(S[r][e], x[e], p);
+        for (int e = 1; e < Map::PAIRS; ++e) p = fma2(S[r][e], x[e], p);
         float lo, hi;
         unpair(p, lo, hi);
         val[r] = lo + hi;
@@ -190,26 +190,29 @@ __device__ __forceinline__ float row_sum(const uint64_t (&S)[Map::RT][4], const 
 // S <- a S + u (rk k)^T, u of row r from the lanes of index r; a may differ by column (int8 codes carry their
 // scale in it).
 template <typename Map>
-__device__ __forceinline__ void write_rows(uint64_t (&S)[Map::RT][4], const uint64_t (&a)[4], const uint64_t (&k)[4], float u,
-                                           float rk, int lane) {
+__device__ __forceinline__ void write_rows(uint64_t (&S)[Map::RT][Map::PAIRS], const uint64_t (&a)[Map::PAIRS],
+                                           const uint64_t (&k)[Map::PAIRS], float u, float rk, int lane) {
     const float own = u * rk;
 #pragma unroll
     for (int r = 0; r < Map::RT; ++r) {
         const float uk = __shfl_sync(0xffffffffu, own, (lane & ~(Map::LPR - 1)) + r * Map::SHARE);
         const uint64_t uk2 = pair(uk, uk);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[r][e] = fma2(a[e], S[r][e], mul2(uk2, k[e]));
+        for (int e = 0; e < Map::PAIRS; ++e) S[r][e] = fma2(a[e], S[r][e], mul2(uk2, k[e]));
     }
 }
 // One token on the rows a warp holds: the new states, and scale * S q of the row of this lane's index.  k, q:
 // this lane's 8 values, unscaled; rk, rq: their factors (rq with the output scale); ukq: their scaled
 // product k . q with the output scale (S q of the new state is a * (S q) + u * (k . q)); v: the row's value.
 template <typename Map>
-__device__ __forceinline__ float token_rows(uint64_t (&S)[Map::RT][4], const uint64_t (&k)[4], const uint64_t (&q)[4],
-                                            float rk, float rq, float ukq, float a, float b, float v, int lane) {
+__device__ __forceinline__ float token_rows(uint64_t (&S)[Map::RT][Map::PAIRS], const uint64_t (&k)[Map::PAIRS],
+                                            const uint64_t (&q)[Map::PAIRS], float rk, float rq, float ukq, float a,
+                                            float b, float v, int lane) {
     const float sq = row_sum<Map>(S, q, lane);
     const float u = b * (v - a * rk * row_sum<Map>(S, k, lane));
-    const uint64_t a2 = pair(a, a), as[4] = {a2, a2, a2, a2};
+    uint64_t as[Map::PAIRS];
+#pragma unroll
+    for (int e = 0; e < Map::PAIRS; ++e) as[e] = pair(a, a);
     write_rows<Map>(S, as, k, u, rk, lane);
     return fmaf(a * rq, sq, u * ukq);
 }

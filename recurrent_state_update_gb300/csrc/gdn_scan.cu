@@ -2,9 +2,9 @@
 // the token-by-token form in fp32 for fp32 states or activations and for the small state shapes.
 //
 // The token-by-token form keeps its rows of the state in registers and walks the sequence; the
-// rows of a head are independent (gdn.cuh), so a block takes a few rows of one head, 2 a lane:
-// a token is then a chain of about 200 cycles (two dot products, five shuffles, one update) that
-// bounds the call while there are fewer warps than the SMs hold.  Keys and queries of 16 tokens are
+// rows of a head are independent (gdn.cuh), so a block takes a few rows of one head: a token is
+// then a chain (two dot products, five shuffles, one update; 0.28 us measured for heads of 128 x 128)
+// that bounds the call while there are fewer warps than the SMs hold.  Keys and queries of 16 tokens are
 // scaled once and staged in shared memory in fp32 for all warps of the block, the next 16 tokens'
 // loads being in flight meanwhile.
 #include "gdn_scan_tc.h"
@@ -98,10 +98,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const ScanParams p) {
 }
 
 // Block (head and share of its rows, sequence in the plan's order).
-template <typename StateT, typename ActT, int P, int N, int RT, int WARPS>
+template <typename StateT, typename ActT, int P, int N, int RT, int PIECES, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
-    using Map = RowMap<N, RT>;
-    constexpr int ROWS = Map::ROWS * WARPS, SPLITS = P / ROWS, GROUPS = WARPS * Map::RPW;  // staging: a token a group of lanes
+    using Map = RowMap<N, RT, PIECES>;
+    constexpr int ROWS = Map::ROWS * WARPS, SPLITS = P / ROWS;
+    constexpr int SL = N / 8, GROUPS = 32 * WARPS / SL;  // staging: a token SL lanes
     constexpr int PASS = (kStage + GROUPS - 1) / GROUPS, VPASS = (kStage * ROWS + 32 * WARPS - 1) / (32 * WARPS);
     __shared__ __align__(16) float ks[kStage][N], qs[kStage][N];
     __shared__ float vs[kStage][ROWS];
@@ -115,20 +116,36 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
     const int32_t slot = p.slot[s];
     if (len <= 0 || slot < -1 || slot >= p.num_slots) return;  // empty, or bad slot (flagged)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int sub = lane / Map::LPR, col = (lane & (Map::LPR - 1)) * 8, idx = (lane & (Map::LPR - 1)) / Map::SHARE;
+    const int sub = lane / Map::LPR, idx = (lane & (Map::LPR - 1)) / Map::SHARE;
+    const int col = (lane & (SL - 1)) * 8, own = (lane & (Map::LPR - 1)) * 8;  // of staging, of the state
     const int brow = warp * Map::ROWS, row0 = split * ROWS + brow;
     const int lrow = brow + idx * Map::RPW + sub;  // the block's row whose sum this lane gets
     StateT *pool = static_cast<StateT *>(p.pool);
-    const int64_t off = ((int64_t)h * P + row0 + sub) * N + col;
-    uint64_t S[RT][4] = {};  // (pairs of zeros)
+    const int64_t off = ((int64_t)h * P + row0 + sub) * N + own;
+    uint64_t S[RT][Map::PAIRS] = {};  // (pairs of zeros)
+    auto piece = [](uint64_t *v, int i) -> uint64_t(&)[4] { return *reinterpret_cast<uint64_t(*)[4]>(v + 4 * i); };
+    auto columns = [&](const float *row, uint64_t (&x)[Map::PAIRS]) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) load_row_shared(row + own + i * Map::LPR * 8, piece(x, i));
+    };
+    auto write_state = [&](int32_t to) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+                store_row(pool + to * p.stride + off + r * Map::RPW * N + i * Map::LPR * 8, piece(S[r], i));
+    };
     if (slot >= 0 && p.has_init && p.has_init[s]) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) load_row(pool + slot * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+                load_row(pool + slot * p.stride + off + r * Map::RPW * N + i * Map::LPR * 8, piece(S[r], i));
     }
     const ActT *v = static_cast<const ActT *>(p.v), *k = static_cast<const ActT *>(p.k), *q = static_cast<const ActT *>(p.q);
     ActT *y = static_cast<ActT *>(p.y);
     const int64_t rowk = (int64_t)p.G * N, rowv = (int64_t)p.H * P;
-    const int group = tid / Map::LPR;
+    const int group = tid / SL;
     float kr[PASS][8], qr[PASS][8], dtr[PASS], br[PASS];
     ActT vr[VPASS];
     auto fetch = [&](int base) {
@@ -166,9 +183,9 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
                 qq = fmaf(qr[i][e], qr[i][e], qq);
                 kq = fmaf(kr[i][e], qr[i][e], kq);
             }
-            kk = sum_lanes<Map::LPR>(kk);
-            qq = sum_lanes<Map::LPR>(qq);
-            kq = sum_lanes<Map::LPR>(kq);
+            kk = sum_lanes<SL>(kk);
+            qq = sum_lanes<SL>(qq);
+            kq = sum_lanes<SL>(kq);
             const float rk = unit_factor(p.gates, kk), rq = unit_factor(p.gates, qq) * p.gates.scale;
             const int j = i * GROUPS + group;
             if (j < kStage) {
@@ -192,77 +209,74 @@ __global__ void __launch_bounds__(32 * WARPS) k_gdn_tokens(const ScanParams p) {
         __syncthreads();
         fetch(base + kStage);
         ActT *yt = y + (int64_t)(t0 + base) * rowv + (int64_t)h * P + split * ROWS + lrow;
-        // with few rows a lane the next token's operands wait in registers; with many, other warps hide them
-        constexpr bool AHEAD = RT <= 2;
-        uint64_t kc[4], qc[4];
+        // with few values a lane the next token's operands wait in registers; with many, other warps hide them
+        constexpr bool AHEAD = RT * PIECES <= 4;
+        uint64_t kc[Map::PAIRS], qc[Map::PAIRS];
         float ac = as[0], bc = bs[0], kqc = kqs[0], vc = vs[0][lrow];
-        load_row_shared(&ks[0][col], kc);
-        load_row_shared(&qs[0][col], qc);
+        columns(ks[0], kc);
+        columns(qs[0], qc);
 #pragma unroll 1
         for (int j = 0; j < L; ++j, yt += rowv) {
-            uint64_t kn[4], qn[4];
+            uint64_t kn[Map::PAIRS], qn[Map::PAIRS];
             const int jn = min(j + 1, kStage - 1);
             float an, bn, kqn, vn;
             auto next = [&] {
                 an = as[jn], bn = bs[jn], kqn = kqs[jn], vn = vs[jn][lrow];
-                load_row_shared(&ks[jn][col], kn);
-                load_row_shared(&qs[jn][col], qn);
+                columns(ks[jn], kn);
+                columns(qs[jn], qn);
             };
             if (AHEAD) next();
             const float out = token_rows<Map>(S, kc, qc, 1.0f, 1.0f, kqc, ac, bc, vc, lane);
             if (!AHEAD) next();
             if ((lane & (Map::SHARE - 1)) == 0) *yt = from_f32<ActT>(out);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) kc[e] = kn[e], qc[e] = qn[e];
+            for (int e = 0; e < Map::PAIRS; ++e) kc[e] = kn[e], qc[e] = qn[e];
             ac = an, bc = bn, kqc = kqn, vc = vn;
             if (p.ckpt_slots) {
                 const int32_t cs = ckpt_slot(p, s, base + j + 1, tid == 0 && blockIdx.x == 0);
-                if (cs >= 0) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) store_row(pool + cs * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
-                }
+                if (cs >= 0) write_state(cs);
             }
         }
     }
-    if (slot >= 0) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) store_row(pool + slot * p.stride + off + (int64_t)r * Map::RPW * N, S[r]);
-    }
+    if (slot >= 0) write_state(slot);
 }
 
-template <typename StateT, typename ActT, int P, int N, int RT, int WARPS>
+template <typename StateT, typename ActT, int P, int N, int RT, int PIECES, int WARPS>
 int launch_tokens(const ScanParams &p, cudaStream_t st) {
-    const dim3 grid((unsigned)(p.H * (P / (RowMap<N, RT>::ROWS * WARPS))), (unsigned)p.nseq);
-    if (launch_pdl(k_gdn_tokens<StateT, ActT, P, N, RT, WARPS>, grid, dim3(32 * WARPS), 0, st, p) != cudaSuccess)
+    const dim3 grid((unsigned)(p.H * (P / (RowMap<N, RT, PIECES>::ROWS * WARPS))), (unsigned)p.nseq);
+    if (launch_pdl(k_gdn_tokens<StateT, ActT, P, N, RT, PIECES, WARPS>, grid, dim3(32 * WARPS), 0, st, p) != cudaSuccess)
         return MAMBA_ECUDA;
     return launch_status();
 }
 
-// Rows a lane: a token costs a warp about 90 instructions and 25 a row, so many rows keep the SMs' issue
-// slots for the rows and few make many warps.  Measured on 32 heads of 128 x 128 with fp32 states: 16
-// sequences of 500 tokens 1.02 ms with 8 rows, 1.23 with 4, 1.68 with 2; one of 1000 tokens 0.50, 0.43, 0.40.
+// Rows a lane, and pieces of 8 columns: a token costs a warp of one piece about 90 instructions and 25 a row, so
+// many rows keep the SMs' issue slots for the rows and few make many warps.  Measured on 32 heads of 128 x 128
+// with fp32 states: 16 sequences of 500 tokens 0.95 ms with 8 rows, 1.18 with 4, 1.50 with 2; one of 1000
+// tokens 0.45, 0.31, 0.29.  Two pieces spare an exchange but read twice the columns: 1.09 ms (4 rows) and 0.30 (2)
+// there, yet for d_state 64, bf16 states: 64 sequences of 500 tokens of 8 heads of 64 x 64 0.39 ms with two
+// pieces of 2 rows, 0.45 with one of 4; four of 500 tokens 0.19 (two pieces, a row) and 0.23 (one, 2 rows).
 template <typename StateT, typename ActT>
 int dispatch_tokens(const ScanParams &p, int P, int N, cudaStream_t st) {
     const int64_t rows = (int64_t)p.nseq * p.H * P;
     if (P == 128 && N == 128) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 128, 128, 8, 4>(p, st);
-        if (rows >= kManyRows / 4) return launch_tokens<StateT, ActT, 128, 128, 4, 4>(p, st);
-        return launch_tokens<StateT, ActT, 128, 128, 2, 8>(p, st);
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 128, 128, 8, 1, 4>(p, st);
+        if (rows >= kManyRows / 4) return launch_tokens<StateT, ActT, 128, 128, 4, 1, 4>(p, st);
+        return launch_tokens<StateT, ActT, 128, 128, 2, 1, 8>(p, st);
     }
     if (P == 64 && N == 128) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 128, 8, 4>(p, st);
-        if (rows >= kManyRows / 4) return launch_tokens<StateT, ActT, 64, 128, 4, 4>(p, st);
-        return launch_tokens<StateT, ActT, 64, 128, 2, 8>(p, st);
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 128, 8, 1, 4>(p, st);
+        if (rows >= kManyRows / 4) return launch_tokens<StateT, ActT, 64, 128, 4, 1, 4>(p, st);
+        return launch_tokens<StateT, ActT, 64, 128, 2, 1, 8>(p, st);
     }
     if (P == 64 && N == 64) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 64, 4, 4>(p, st);
-        return launch_tokens<StateT, ActT, 64, 64, 2, 4>(p, st);
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 64, 2, 2, 4>(p, st);
+        return launch_tokens<StateT, ActT, 64, 64, 1, 2, 4>(p, st);
     }
     if (P == 32 && N == 64) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 32, 64, 4, 2>(p, st);
-        return launch_tokens<StateT, ActT, 32, 64, 2, 4>(p, st);
+        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 32, 64, 2, 2, 2>(p, st);
+        return launch_tokens<StateT, ActT, 32, 64, 1, 2, 4>(p, st);
     }
-    if (P == 16 && N == 16) return launch_tokens<StateT, ActT, 16, 16, 1, 1>(p, st);
+    if (P == 16 && N == 16) return launch_tokens<StateT, ActT, 16, 16, 1, 1, 1>(p, st);
     return MAMBA_EUNSUPPORTED;
 }
 

@@ -95,11 +95,11 @@ constexpr int kPrepThreads = 256;
 constexpr float kSpan = 96.0f;  // largest base-2 exponent span of a block whose decays are factored
 
 // T of one head on the way: L's diagonal 16 x 16 blocks in fp32 (two blocks start 16 banks apart), the
-// rest of L and (I + L)^-1 in fp16, rows 144 bytes apart so that eight rows' 16 bytes miss one another's
-// banks.
+// rest of L in fp16, rows 144 bytes apart so that eight rows' 16 bytes miss one another's banks.  The blocks
+// of (I + L)^-1 take the places of L's that are used.
 struct Inverse {
     float diag[4][16 * 20 + 16];
-    __half L[C][72], t[C][72];
+    __half L[C][72];
 };
 // Decays within a 32-token half of the chunk and from the first half to the second, as a factor of the
 // row times one of the column (with the key's length); see decay_factors.
@@ -163,7 +163,7 @@ template <int K>
 __device__ __forceinline__ void lower_left(const Inverse &v, int row, int mid, int left, float (&out)[2 * K][4], int lane) {
     uint32_t a[K][4], b[4];
 #pragma unroll
-    for (int k = 0; k < K; ++k) ldmatrix4(a[k], block16(v.t, row, mid + 16 * k, lane));
+    for (int k = 0; k < K; ++k) ldmatrix4(a[k], block16(v.L, row, mid + 16 * k, lane));
     float x[2 * K][4] = {};
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -184,7 +184,7 @@ __device__ __forceinline__ void lower_left(const Inverse &v, int row, int mid, i
                                 pack_f16x2(-x[2 * k + 1][2], -x[2 * k + 1][3])};
 #pragma unroll
         for (int n = 0; n < K; ++n) {
-            ldmatrix4_trans(b, block16(v.t, left + 16 * k, left + 16 * n, lane));
+            ldmatrix4_trans(b, block16(v.L, left + 16 * k, left + 16 * n, lane));
             mma16(out[2 * n], xa, b[0], b[1]);
             mma16(out[2 * n + 1], xa, b[2], b[3]);
         }
@@ -211,11 +211,11 @@ __device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float
             }
             x[r] = acc[0] + acc[1];
             const int row = 16 * d + r, col = 16 * d + c;
-            v.t[row][col] = __float2half_rn(x[r]);
+            v.L[row][col] = __float2half_rn(x[r]);
             *reinterpret_cast<__half *>(T + swz128_offset(row, col)) = __float2half_rn(x[r] * bc);
         }
         // the block right of the first of the pair's two diagonal blocks
-        *reinterpret_cast<uint4 *>(&v.t[32 * w + c][32 * w + 16 + (lane >> 4) * 8]) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(&v.L[32 * w + c][32 * w + 16 + (lane >> 4) * 8]) = make_uint4(0, 0, 0, 0);
     }
     __syncwarp();
     const int fr = lane >> 2, fc = (lane & 3) * 2;
@@ -227,12 +227,13 @@ __device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float
         float o[2][4];
         const int left = 32 * w, mid = left + 16;
         lower_left<1>(v, mid, mid, left, o, lane);
+        __syncwarp();
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = mid + fr + 8 * e, col = left + 8 * n + fc;
-                *reinterpret_cast<uint32_t *>(&v.t[row][col]) = pack_f16x2(o[n][2 * e], o[n][2 * e + 1]);
+                *reinterpret_cast<uint32_t *>(&v.L[row][col]) = pack_f16x2(o[n][2 * e], o[n][2 * e + 1]);
                 put(row, col, o[n][2 * e], o[n][2 * e + 1]);
             }
     }
@@ -247,9 +248,12 @@ __device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float
     }
 }
 
-// Block (chunk, group and share of its heads).
+// Block (chunk, group and share of its heads): two heads of a group share its keys' and queries' one product,
+// K K^T over Q K^T.  0.5 MB of a 64-token chunk of 32 heads and 16 groups are read and 1.1 MB written; 8192 tokens
+// take 53 us (3 TB/s).  Neither memory nor the issue slots (a third used) bound it but a block's own row of steps
+// (loads, product, decays, the inverse); three blocks an SM run side by side, 68 KB of shared memory each.
 template <int HEADS>
-__global__ void __launch_bounds__(kPrepThreads, 2) k_gdn_prep(const ScanParams p, const WsLayout ws) {
+__global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p, const WsLayout ws) {
     extern __shared__ __align__(1024) unsigned char prep_smem[];
     PrepSmem<HEADS> &sm = *align1024<PrepSmem<HEADS>>(prep_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -797,7 +801,8 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
             tc_fence_after();
             tmem_pieces<4>(lanes + T_U, [&](int n, const uint32_t (&u)[16]) {  // 16 tokens: both forms over their own columns
-                const uint4 w0 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n), w1 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n + 8);
+                const uint4 w0 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n);
+                const uint4 w1 = *reinterpret_cast<const uint4 *>(gt.ek + 16 * n + 8);
                 const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                 uint32_t pk[8];
 #pragma unroll
@@ -996,7 +1001,12 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     return half_sync_or(2, bad);
 }
 
-// Block (sequence in the plan's order, head).
+// Block (sequence in the plan's order, head).  What bounds it is the chain itself, some 5100 cycles for 64 tokens
+// (one prompt of 8192 tokens, 32 blocks: 316 us): three products that wait for one another, 370 to 510 cycles each from
+// issue to completion, and between them the 128 rows' R, U and state read, rounded and written back by the four
+// warps that may reach their tensor-memory lanes.  Two blocks share an SM at little cost: 8 ragged prompts of
+// 32768 tokens in all, 256 blocks, take 324 us for the longest.  Heads of 64 values leave half of the rows idle:
+// tcgen05's 64-row form puts its accumulator's rows elsewhere, and the chain's length would be the same.
 template <int P>
 __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,
                                                                 const __grid_constant__ CUtensorMap vmap,

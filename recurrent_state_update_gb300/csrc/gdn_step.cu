@@ -4,8 +4,8 @@
 // Mathematics and row layout: gdn.cuh.  Both are streaming passes: an element of the state is read
 // once and written once (once a draft) for about 8 floating operations, so device memory bounds
 // them, and a call of few rows is bound by the latency of one load, two short chains of shuffles
-// and one store.  Rows of a head are independent, so a block takes as many of them as keep the
-// GPU busy: 16 a warp in long launches, 4 a warp over more blocks in short ones.
+// and one store.  Rows of a head are independent but for the int8 scales' maxima, so a block takes a few
+// of them, or there all of a head's.
 #include "gdn.cuh"
 #include "int8_entry.h"
 
