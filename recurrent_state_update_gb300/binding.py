@@ -522,15 +522,18 @@ def gdn_chunk_scan(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, v, k, q, dt,
     H, P, N = desc.nheads, desc.head_dim, desc.d_state
     act, dtt, f32 = code[desc.act_dtype], code[desc.dt_dtype], code[MAMBA_F32]
     nseq, total, GN = cu_seqlens.shape[0] - 1, v.shape[0], desc.n_groups * N
+    if ckpt_slots is not None and ckpt_slots.dim() != 2:
+        raise ValueError("gdn_chunk_scan: ckpt_slots: expected (sequences, checkpoints)")
+    max_ckpt = 0 if ckpt_slots is None else ckpt_slots.shape[1]
     pool, cu, ids, init, ckpt, vp, kp, qp, dp, bp, ap, bias, yp, wp, err = _gdn_pointers("gdn_chunk_scan", (
         ("ssm_pool", ssm_pool, code[desc.state_dtype], -1, False), ("cu_seqlens", cu_seqlens, i32, -1, True),
         ("slot_ids", slot_ids, i32, nseq, True), ("has_initial_state", has_initial_state, u8, nseq, True),
-        ("ckpt_slots", ckpt_slots, i32, -1, True), ("v", v, act, total * H * P, True), ("k", k, act, total * GN, True),
+        ("ckpt_slots", ckpt_slots, i32, nseq * max_ckpt, True), ("v", v, act, total * H * P, True), ("k", k, act, total * GN, True),
         ("q", q, act, total * GN, True), ("dt", dt, dtt, total * H, True), ("beta", beta, dtt, total * H, True),
         ("A", A, f32, H, True), ("dt_bias", dt_bias, f32, H, True), ("y", y, act, total * H * P, True),
         ("workspace", workspace, workspace.dtype, -1, True), ("err_word", err_word, i32, 1, False)))
     rc = (_lib or lib()).gdn_chunk_scan(ctypes.byref(desc), pool, ssm_pool.stride(0), ssm_pool.shape[0], cu, nseq, total, ids,
-                                        init, ckpt, 0 if ckpt_slots is None else ckpt_slots.shape[1], ckpt_interval, vp, kp,
+                                        init, ckpt, max_ckpt, ckpt_interval, vp, kp,
                                         qp, dp, bp, ap, bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
                                         1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, wp,
                                         workspace.numel() * workspace.element_size(), err,
