@@ -464,6 +464,19 @@ def _gdn_pointers(what, tensors):
     return out
 
 
+def _gdn_slots(what, pool, H, P, N):
+    """(elements from slot to slot, slots) of a pool whose slots each hold a dense (H, P, N) state, in that shape
+    or flat."""
+    shape, strides = pool.shape, pool.stride()
+    if shape[1:] != (H, P, N) or strides[1:] != (P * N, N, 1):
+        one = pool.select(0, 0) if len(shape) > 1 and shape[0] else pool
+        if len(shape) < 2 or not one.is_contiguous() or (shape[0] and one.numel() < H * P * N) or (
+                len(shape) == 4 and shape[1:] != (H, P, N)):
+            raise ValueError(f"{what}: ssm_pool: expected slots of dense ({H}, {P}, {N}) states, got shape {tuple(shape)} "
+                             f"with strides {tuple(strides)}")
+    return strides[0], shape[0]
+
+
 def gdn_state_update(desc: LayerDesc, ssm_pool, slot_ids, xbc, dt, beta, A, y, *, scratch_slots=None, dt_bias=None,
                      dt_softplus=True, beta_sigmoid=True, qk_l2norm=True, scale=None, err_word=None, stream=None):
     """The gated delta rule's step over (batch, ntok, conv_dim) convolved channels v | k | q, in
@@ -478,8 +491,9 @@ def gdn_state_update(desc: LayerDesc, ssm_pool, slot_ids, xbc, dt, beta, A, y, *
         ("scratch_slots", scratch_slots, i32, rows, True), ("xbc", xbc, act, rows * (H * P + 2 * desc.n_groups * N), True),
         ("dt", dt, dtt, rows * H, True), ("beta", beta, dtt, rows * H, True), ("A", A, f32, H, True),
         ("dt_bias", dt_bias, f32, H, True), ("y", y, act, rows * H * P, True), ("err_word", err_word, i32, 1, False)))
-    rc = (_lib or lib()).gdn_state_update(ctypes.byref(desc), pool, ssm_pool.stride(0), ssm_pool.shape[0], ids, scr, batch,
-                                          ntok, xp, dp, bp, ap, bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
+    stride, slots = _gdn_slots("gdn_state_update", ssm_pool, H, P, N)
+    rc = (_lib or lib()).gdn_state_update(ctypes.byref(desc), pool, stride, slots, ids, scr, batch, ntok, xp, dp, bp, ap,
+                                          bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
                                           1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, err,
                                           now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
     if rc:
@@ -532,10 +546,10 @@ def gdn_chunk_scan(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, v, k, q, dt,
         ("q", q, act, total * GN, True), ("dt", dt, dtt, total * H, True), ("beta", beta, dtt, total * H, True),
         ("A", A, f32, H, True), ("dt_bias", dt_bias, f32, H, True), ("y", y, act, total * H * P, True),
         ("workspace", workspace, workspace.dtype, -1, True), ("err_word", err_word, i32, 1, False)))
-    rc = (_lib or lib()).gdn_chunk_scan(ctypes.byref(desc), pool, ssm_pool.stride(0), ssm_pool.shape[0], cu, nseq, total, ids,
-                                        init, ckpt, max_ckpt, ckpt_interval, vp, kp,
-                                        qp, dp, bp, ap, bias, 1 if dt_softplus else 0, 1 if beta_sigmoid else 0,
-                                        1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, wp,
+    stride, slots = _gdn_slots("gdn_chunk_scan", ssm_pool, H, P, N)
+    rc = (_lib or lib()).gdn_chunk_scan(ctypes.byref(desc), pool, stride, slots, cu, nseq, total, ids, init, ckpt, max_ckpt,
+                                        ckpt_interval, vp, kp, qp, dp, bp, ap, bias, 1 if dt_softplus else 0,
+                                        1 if beta_sigmoid else 0, 1 if qk_l2norm else 0, N ** -0.5 if scale is None else scale, yp, wp,
                                         workspace.numel() * workspace.element_size(), err,
                                         now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
     if rc:

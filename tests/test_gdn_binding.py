@@ -67,3 +67,39 @@ def test_a_checkpoint_table_that_is_not_a_row_a_sequence_is_refused(library, row
 def test_a_checkpoint_table_of_enough_rows_is_taken(library, rows):
     scan(pool(), ckpt_slots=dev(rows, 4, dtype=torch.int32), ckpt_interval=64)
     assert library.calls == ["gdn_chunk_scan"]
+
+
+def step(ssm, **kw):
+    f32, i32 = torch.float32, torch.int32
+    bd.gdn_state_update(bd.layer_desc(SHAPE), ssm, dev(2, dtype=i32), dev(2, 1, SHAPE.conv_dim), dev(2, 1, H, dtype=f32),
+                        dev(2, 1, H, dtype=f32), dev(H, dtype=f32), dev(2, 1, H * P), stream=Stream, **kw)
+
+
+POOL = torch.zeros(4, H, P, N, dtype=torch.bfloat16)
+WIDE = torch.zeros(4, 2, H, P, N, dtype=torch.bfloat16)
+WRONG = {
+    "keys before values": POOL.transpose(2, 3),
+    "its memory transposed": torch.zeros(4, H, N, P, dtype=torch.bfloat16).transpose(2, 3),
+    "every second key": torch.zeros(4, H, P, 2 * N, dtype=torch.bfloat16)[..., ::2],
+    "a head too few": torch.zeros(4, H + 1, P, N, dtype=torch.bfloat16)[:, 1:, :, :64],
+    "a slot too small": torch.zeros(4, H * P * N - 8, dtype=torch.bfloat16),
+    "one number": torch.zeros(4 * H * P * N, dtype=torch.bfloat16),
+}
+RIGHT = {"dense": POOL, "slots apart": WIDE[:, 0], "flat": POOL.view(4, -1), "one slot": POOL[:1], "room behind": WIDE.view(4, -1),
+         "empty": POOL[:0]}
+
+
+@pytest.mark.parametrize("call", [step, scan])
+@pytest.mark.parametrize("layout", WRONG)
+def test_a_pool_whose_slots_are_not_dense_states_is_refused(library, call, layout):
+    """The device reads a slot as (nheads, head_dim, d_state) without gaps."""
+    with pytest.raises(ValueError, match="ssm_pool"):
+        call(pool(WRONG[layout]))
+    assert not library.calls
+
+
+@pytest.mark.parametrize("call", [step, scan])
+@pytest.mark.parametrize("layout", RIGHT)
+def test_a_pool_of_dense_slots_is_taken(library, call, layout):
+    call(pool(RIGHT[layout]))
+    assert len(library.calls) == 1
