@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_gdn_plan(const ScanParams p) {
     const int run = (p.nseq + kPlanThreads - 1) / kPlanThreads, lo = min(p.nseq, tid * run), hi = min(p.nseq, lo + run);
     int n = 0;
     for (int s = lo; s < hi; ++s) {
-        const int len = p.cu[s + 1] - p.cu[s];
-        if (len < 0) ok = 0;
+        const int a = p.cu[s], b = p.cu[s + 1], len = b - a;
+        if (b < a) ok = 0;  // (compared, not subtracted: a difference past 2^31 wraps; in order from 0 to T none does)
         const int32_t sl = p.slot[s];
         if (sl < -1 || sl >= p.num_slots) flag_error(p.err, MAMBA_ERR_SLOT_RANGE);
         n += (len + kChunk - 1) / kChunk;
