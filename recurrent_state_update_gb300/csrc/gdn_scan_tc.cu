@@ -81,6 +81,12 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
     return false;
 }
 
+// The same with one outcome for the whole warp, which has to arrive together: a wait gives up lane by lane, and
+// lanes that disagree whether to go on would leave an election (elect_one) waiting for the others.
+__device__ __forceinline__ bool warp_wait_for(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_for(bar, parity));
+}
+
 // The swizzled tiles want 1024-byte boundaries; the launches ask for that much more.
 template <typename T>
 __device__ __forceinline__ T *align1024(unsigned char *p) {
@@ -878,12 +884,12 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     auto token_row = [&](const unsigned char *tile, int n) {
         return smem_u32(tile) + (warp >> 1) * kBlk + swz128_chunk(8 * n + (lane & 7), 4 * (warp & 1) + (lane >> 3));
     };
-    int bad = 0;
+    int bad = 0;  // the same in all lanes of a warp
     for (int c = -1; c < sm.nc; ++c) {
         const int c1 = c + 1;
         if (c >= 0 && warp == 0) {
             // the state's part of Y, once the state's copy is there (X is formed of it)
-            if (!wait_for(&sm.bar[B_X], c & 1)) bad = 1;
+            if (!warp_wait_for(&sm.bar[B_X], c & 1)) bad = 1;
             tc_fence_after();
             if (!bad) {
                 arm(B_OI, c & 1);
@@ -896,7 +902,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
                 }
             }
         } else if (c >= 0 && warp == 3 && c1 < sm.nc) {
-            if (!wait_for(&sm.bar[B_U], c & 1)) bad = 1;  // T is used
+            if (!warp_wait_for(&sm.bar[B_U], c & 1)) bad = 1;  // T is used
             if (!bad) {
                 arm(B_T, c1 & 1);
                 if (elect_one()) J.load_tile(c1, B_T, sm.T, 0);
@@ -907,7 +913,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
         if (c1 < sm.nc) {
             // the next chunk's queries times e^c, in place, 16 bytes of a token each: tokens 16 apart, in both blocks
             // of 64 elements
-            if (!wait_for(&sm.bar[B_IN + (c1 & 1)], (c1 >> 1) & 1) || !wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
+            if (!warp_wait_for(&sm.bar[B_IN + (c1 & 1)], (c1 >> 1) & 1) || !warp_wait_for(&sm.bar[B_Q], c1 & 1)) bad = 1;
             const __half *g = sm.gates[c1 & 3].g + (tid >> 3);
             uint4 *ptr = reinterpret_cast<uint4 *>(sm.q[c1 & 1]) + tid;
             uint4 u[8];
@@ -925,7 +931,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
             }
             fence_async_smem();
             if (warp == 1 && c + 2 < sm.nc) {
-                if (!wait_for(&sm.bar[B_TAKEN], c1 & 1)) bad = 1;  // the next values are in registers
+                if (!warp_wait_for(&sm.bar[B_TAKEN], c1 & 1)) bad = 1;  // the next values are in registers
                 if (!bad) {
                     arm(B_IN + (c & 1), (c + 2) >> 1 & 1);
                     if (elect_one()) J.load_values(c + 2);
@@ -939,7 +945,7 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
             float un[4];
 #pragma unroll
             for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const float2 *>(oq + 8 * n);
-            if (!wait_for(&sm.bar[B_Y], c & 1)) bad = 1;
+            if (!warp_wait_for(&sm.bar[B_Y], c & 1)) bad = 1;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 4; ++i) un[i] = sm.unscale[c & 1][32 * warp + 8 * i + (lane >> 2)];
