@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
                                                                 const __grid_constant__ CUtensorMap vmap,
                                                                 const __grid_constant__ CUtensorMap ymap) {
     extern __shared__ __align__(1024) unsigned char chain_smem[];
-    ChainSmem &sm = *reinterpret_cast<ChainSmem *>(chain_smem);
+    ChainSmem &sm = *align1024<ChainSmem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     if (p.meta[0] == 0) return;  // bad cu_seqlens (flagged): nothing is done

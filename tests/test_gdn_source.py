@@ -25,3 +25,12 @@ def test_the_sides_warps_agree_whether_a_wait_gave_up():
     assert len(re.findall(r"\bwarp_wait_for\(", side)) >= 6
     shared = function(text, "warp_wait_for")
     assert "__all_sync(0xffffffffu, wait_for(bar, parity))" in shared
+
+
+def test_both_kernels_put_their_swizzled_tiles_on_1024_byte_boundaries():
+    """A swizzled operand is read right only from such a boundary; the language promises 16 bytes of the base."""
+    text = open(os.path.join(CSRC, "gdn_scan_tc.cu")).read()
+    for kernel, base in (("k_gdn_prep", "prep_smem"), ("k_gdn_chain", "chain_smem")):
+        body = function(text, kernel)
+        assert len(re.findall(r"= \*?align1024<\w+(<HEADS>)?>\(%s\)" % base, body)) == 1, kernel
+        assert body.count(base) == 2  # its declaration and that
