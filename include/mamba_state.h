@@ -514,6 +514,8 @@ int gdn_state_update(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_s
  * the entry's size as slot stride.
  *   entries (batch) int32, -1 = padding; out of range: MAMBA_ERR_SLOT_RANGE, row left untouched.
  *   Entries must be distinct.  xbc (batch, conv_dim), y (batch, nheads*head_dim).
+ * A column (head, d_state channel) whose new state holds a NaN or an infinity gets a NaN as its
+ * scale, and so reads as NaN in every row.
  * Every step rounds the state to half a grid step (max over head_dim / 254) at most; where the
  * decay alone acts it only scales, so codes do not drift under it.
  * Limits: batch <= 65535.

@@ -220,10 +220,18 @@ __device__ __forceinline__ uint2 f32_to_codes(const uint64_t (&v)[4], const uint
     return make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
 }
 
+// The larger of two magnitudes, or NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Block (head, batch row): all rows of the head, because a scale covers a column of it.  Codes become fp32
 // on load; what belongs to a column (its scale, key and query) is made once for the block; the new state is
 // scaled by the new column maxima (over the warps through shared memory) and rounded to the grid of
-// step max/127, as the int8 store does.  At 192 rows of 32 heads of 128 x 128 a step moves 213 MB in
+// step max/127, as the int8 store does; a column that holds a NaN or an infinity has no such grid and gets a NaN as
+// its scale, so that it reads as NaN from then on.  At 192 rows of 32 heads of 128 x 128 a step moves 213 MB in
 // 54.4 us, 0.57 of what a copy moves: some 9 instructions a value (two products, the update, the maximum, and
 // bytes to fp32 and back) and three barriers a block keep the SM from asking for more.
 template <typename ActT, int P, int N, int RT>
@@ -294,13 +302,13 @@ __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(
                 float lo, hi, lo2 = 0.0f, hi2 = 0.0f;
                 unpair(S[r][c], lo, hi);
                 if (r + 1 < RT) unpair(S[r + 1][c], lo2, hi2);
-                asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m[2 * c]) : "f"(lo), "f"(lo2));
-                asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m[2 * c + 1]) : "f"(hi), "f"(hi2));
+                asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m[2 * c]) : "f"(lo), "f"(lo2));
+                asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m[2 * c + 1]) : "f"(hi), "f"(hi2));
             }
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
-            for (int o = Map::LPR; o < 32; o *= 2) m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
+            for (int o = Map::LPR; o < 32; o *= 2) m[c] = max_nan(m[c], __shfl_xor_sync(0xffffffffu, m[c], o));
         if (sub == 0) {
             reinterpret_cast<float4 *>(&top[warp][col])[0] = make_float4(m[0], m[1], m[2], m[3]);
             reinterpret_cast<float4 *>(&top[warp][col])[1] = make_float4(m[4], m[5], m[6], m[7]);
@@ -310,9 +318,9 @@ __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(
     for (int c = threadIdx.x; c < N; c += 32 * WARPS) {
         float t = top[0][c];
 #pragma unroll
-        for (int w = 1; w < WARPS; ++w) t = fmaxf(t, top[w][c]);
+        for (int w = 1; w < WARPS; ++w) t = max_nan(t, top[w][c]);
         inv[c] = t > kLeast ? 127.0f / t : 0.0f;
-        scales[c] = t / 127.0f;
+        scales[c] = t < INFINITY ? t / 127.0f : NAN;  // what a column no longer holds stays visible in its scale
     }
     __syncthreads();
     uint64_t to[4];
