@@ -737,12 +737,17 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             top = fmaxf(top * unscale, vmax);
             uint32_t E = __float_as_uint(top) >> 23;
             E = top < INFINITY ? max(7u, min(247u, E)) : 127u;
+            int shift = (int)(__float_as_uint(unscale) >> 23) + 1 - (int)E;  // from the old power to the new one
             scale = __uint_as_float((255u - E) << 23);
-            const float ratio = scale * unscale;
             unscale = __uint_as_float((E - 1u) << 23);
             limit = __uint_as_float((E + 3u) << 23);
+            while (shift != 0) {  // (in two steps where no float holds their ratio)
+                const int by = max(-126, min(126, shift));
+                const float ratio = __uint_as_float((uint32_t)(127 + by) << 23);
+                shift -= by;
 #pragma unroll
-            for (int e = 0; e < TN; ++e) S[e] *= ratio;
+                for (int e = 0; e < TN; ++e) S[e] *= ratio;
+            }
         }
         sm.unscale[c & 1][row] = unscale;
 #pragma unroll

@@ -11,7 +11,7 @@ from recurrent_state_update_gb300 import build as bld
 from recurrent_state_update_gb300 import workloads as wl
 
 from gpu_util import f64, to_dev, to_i32
-from test_gdn_gpu import FULL, _vkq, _work, states
+from test_gdn_gpu import DTYPES, FULL, _vkq, _work, states, tol
 
 pytestmark = pytest.mark.gpu
 
@@ -22,6 +22,70 @@ def _lib():
     bld.build()
     bd.lib()
     torch.cuda.set_device(0)
+
+
+PAIR = wl.LayerShape(nheads=2, head_dim=128, d_state=128, n_groups=1)
+NARROW = wl.LayerShape(nheads=2, head_dim=64, d_state=128, n_groups=1)
+BOTH = [DTYPES[0], DTYPES[1]]  # bf16 states (in chunks) and fp32 states (token by token), bf16 activations
+SMALLEST = 2.0 ** -100  # a tile below it holds what fp32 need not keep apart from zero
+
+
+def tile_err(got, want):
+    """Largest error of a head's tile over the tile's largest value: (heads, ..) arrays."""
+    axes = tuple(range(1, want.ndim))
+    return float((np.abs(got - want).max(axis=axes) / np.maximum(np.abs(want).max(axis=axes), SMALLEST)).max())
+
+
+def follow(seed, shape, st, lens, edit=None, init=None, interval=0, act=wl.BF16, flags={}, skip=(), y_tol=None, s_tol=None):
+    """One call on sequences of these lengths, each 64-token tile of the outputs, each final state and each checkpoint
+    (one every `interval` tokens) against the 64-bit form.  edit(xbc, dt, beta, states) changes the inputs, as float64,
+    before they are stored; tiles whose number is in skip are only asked to be finite."""
+    import torch
+    T, n = int(sum(lens)), len(lens)
+    H, HP = shape.nheads, shape.nheads * shape.head_dim
+    A, bias = ref.layer(seed, shape)
+    xbc, raw, beta = (np.array(wl.upcast(a, d)) for a, d in zip(ref.inputs(seed, shape, (T,), act), (act, wl.F32, wl.F32)))
+    kept = [L // interval if interval else 0 for L in lens]
+    before = np.array(wl.upcast(states(seed, shape, n + sum(kept), st), st))
+    if edit:
+        edit(xbc, raw, beta, before)
+    stored = [wl.store(a, d) for a, d in ((xbc, act), (raw, wl.F32), (beta, wl.F32), (before, st))]
+    ckpt = np.full((n, max(1, max(kept))), -1)
+    for i, k in enumerate(kept):
+        ckpt[i, :k] = n + sum(kept[:i]) + np.arange(k)
+    dx, dr, db, pool = (to_dev(a, d) for a, d in zip(stored, (act, wl.F32, wl.F32, st)))
+    y = torch.zeros(T, H, shape.head_dim, dtype=dx.dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = wl.cu_seqlens(lens)
+    bd.gdn_chunk_scan(bd.layer_desc(shape, state=st, act=act), pool, to_i32(cu), to_i32(np.arange(n)),
+                      *[t.contiguous() for t in _vkq(shape, dx)], dr, db, to_dev(A, wl.F32), y, _work(shape, T, n, st, act),
+                      dt_bias=to_dev(bias, wl.F32), has_initial_state=None if init is None else to_dev(np.array(init), wl.F32).byte(),
+                      ckpt_slots=to_i32(ckpt) if interval else None, ckpt_interval=interval, err_word=err,
+                      **{{"softplus": "dt_softplus", "sigmoid": "beta_sigmoid", "l2norm": "qk_l2norm"}.get(k, k): w
+                         for k, w in flags.items()})
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    xbc, raw, beta, before = (wl.upcast(a, d) for a, d in zip(stored, (act, wl.F32, wl.F32, st)))
+    got, after = f64(y), f64(pool)
+    assert np.isfinite(got).all() and np.isfinite(after).all()
+    y_tol, s_tol = y_tol or tol(act, True), s_tol or tol(st, True)
+    v, k, q = ref.split(shape, xbc)
+    rep = H // shape.n_groups
+    k, q = (np.repeat(ref.unit(x, flags.get("l2norm", True)), rep, axis=1) for x in (k, q))
+    a, b = ref.gates(raw, beta, A.astype(float), bias.astype(float), flags.get("softplus", True), flags.get("sigmoid", True))
+    scale = flags.get("scale", shape.d_state ** -0.5)
+    for i, L in enumerate(lens):
+        S = before[i] if init is not None and init[i] else np.zeros(before.shape[1:])
+        want = np.zeros((L, H, shape.head_dim))
+        for t in range(L):
+            S, want[t] = ref.step(S, v[cu[i] + t], k[cu[i] + t], q[cu[i] + t], a[cu[i] + t], b[cu[i] + t], scale)
+            if interval and (t + 1) % interval == 0 and t // 64 not in skip:
+                assert tile_err(after[ckpt[i, t // interval]], S) <= s_tol, f"checkpoint after {t + 1}"
+        for c in range((L + 63) // 64):
+            rows = slice(64 * c, min(L, 64 * c + 64))
+            if c not in skip:
+                assert tile_err(got[cu[i]:cu[i + 1]][rows].transpose(1, 0, 2), want[rows].transpose(1, 0, 2)) <= y_tol, f"tile {c}"
+        assert tile_err(after[i], S) <= s_tol, "final state"
 
 
 @pytest.mark.parametrize("st", [wl.BF16, wl.F32])
@@ -41,3 +105,23 @@ def test_boundaries_whose_differences_wrap_are_refused(st, inner):
     torch.cuda.synchronize()
     assert int(err.item()) == bd.MAMBA_ERR_SEQLENS
     assert torch.equal(pool, before) and (y == 7.0).all()
+
+
+# ---- numbers whose size changes along a sequence ----
+
+@pytest.mark.parametrize("shape", [PAIR, NARROW], ids=["128", "64"])
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("loud", [512.0, 1e36])
+def test_values_after_a_state_that_vanished(shape, st, act, loud):
+    """Loud values, a stretch whose steps wipe the state out while nothing is written, and ordinary values: more than
+    2^126 lies between the largest numbers of chunk 0 and of chunk 16."""
+    HP = shape.nheads * shape.head_dim
+
+    def edit(xbc, raw, beta, before):
+        xbc[:64, :HP] = np.sign(xbc[:64, :HP]) * loud
+        xbc[14 * 64:18 * 64, :HP] = 0
+        raw[14 * 64:18 * 64] = 300
+        if loud > 512:  # what the loud values left has to be gone before the tiles that are compared
+            raw[64:14 * 64], xbc[64:14 * 64, :HP] = 300, 0
+
+    follow(51, shape, st, [20 * 64 + 5], edit, skip=range(18))
