@@ -1,12 +1,15 @@
 // gdn_scan_tc.cu -- the chunked gated delta rule on the tcgen05 tensor cores.
 //
 // For a chunk of 64 tokens and a head with the state S (P x N) before it, with c_i the running sum
-// of the log decays, unit keys and queries k_i, q_i of lengths |k_i|, |q_i| (after any scaling):
-//   (I + L) U = diag(b) R,   L_ij = b_i |k_i||k_j| (k_i . k_j) e^(c_i - c_j), j < i
-//   R = V - diag(e^c |k|) K S^T            the values, less what the decayed state already returns
-//   U = T R,  T = (I + L)^-1 diag(b)       what is written
-//   Y = |q| (diag(e^c) Q S^T + A U),       A_ij = |k_j| (q_i . k_j) e^(c_i - c_j), j <= i
-//   S <- e^(c_64) S + (diag(e^(c_64 - c) |k|) U)^T K
+// of the log decays, unit keys and queries k_i, q_i of lengths |k_i|, |q_i| (after any scaling), and
+// w_i = b_i |k_i|^2, what a token's write takes of what the state holds along its key:
+//   (I + L) U = R,   L_ij = w_i (k_i . k_j) e^(c_i - c_j), j < i
+//   R = diag(b |k|) V - diag(w e^c) K S^T  the values, less what the decayed state already returns
+//   U = T R,  T = (I + L)^-1               what is written, along unit keys
+//   Y = |q| (diag(e^c) Q S^T + A U),       A_ij = (q_i . k_j) e^(c_i - c_j), j <= i
+//   S <- e^(c_64) S + (diag(e^(c_64 - c)) U)^T K
+// So the gates and the keys' lengths, which may have any size, meet the values and the state in fp32; L, T and A
+// hold nothing past 2, the most that w may be.
 // T and A need no state, so k_gdn_prep forms them for all chunks of the batch at once; the chain
 // from chunk to chunk, k_gdn_chain, has four products left, all of them transposed so that the
 // value index is the row: its left operands S, R^T, U^T are the accumulators of the product
@@ -16,9 +19,8 @@
 // Number formats: the products run on fp16 operands (11 bits; bf16's 8 would put four times the
 // output's own rounding into y), sums in fp32, and the state itself stays in fp32 in registers.
 // Keys and queries are of unit length before they are rounded.  Values have bf16's range, so every
-// row of the state (one value index) has a power of two that brings its values and state to a few
-// units, taken anew every 16 chunks and whenever a value outgrows it; the rule cannot grow the state
-// past sqrt(tokens) times the largest value, far inside the 2^12 left.
+// row of the state (one value index) has a power of two that brings what is written to it (b |k| v) and its
+// state to a few units, taken anew every 16 chunks and whenever a write outgrows it.
 #include <mutex>
 
 #include <cuda_fp16.h>
@@ -43,10 +45,12 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint32_t kBlk = 64 * 128;          // one swizzled block of 64 rows
 constexpr uint32_t kKqBytes = 4 * kBlk;
 struct HeadGates {
-    float rk[C];   // e^c |k|
+    float f[C];    // b |k|
+    float rk[C];   // w e^c
     float oq[C];   // |q| * scale
-    __half ek[C];  // e^(c_64 - c) |k|, for operands of 11 bits
+    __half ek[C];  // e^(c_64 - c), for operands of 11 bits
     __half g[C];   // e^c, as well
+    bf16 near_f[C];  // b |k| to 8 bits, for the choice of a row's power of two
     float last, pad[3];  // e^(c_64)
 };
 constexpr uint32_t kGateBytes = sizeof(HeadGates);
@@ -108,9 +112,9 @@ struct Inverse {
     __half L[C][72];
 };
 // Decays within a 32-token half of the chunk and from the first half to the second, as a factor of the
-// row times one of the column (with the key's length); see decay_factors.
+// row times one of the column; w: see above.
 struct Decays {
-    float cum[C], b[C], near[C], far[32];
+    float cum[C], w[C], near[C], far[32];
 };
 
 template <int HEADS>
@@ -123,7 +127,6 @@ struct PrepSmem {
     HeadGates gates[HEADS];
     Decays dec[HEADS];
     float ss[2 * C];  // squared lengths of keys and queries
-    float nk[C];
     uint64_t bar;
     uint32_t tmem;
     float half_sum[HEADS];
@@ -197,13 +200,12 @@ __device__ __forceinline__ void lower_left(const Inverse &v, int row, int mid, i
     }
 }
 
-// T = (I + L)^-1 diag(b) of one head by a pair of warps (w = 0, 1 of the pair).  The diagonal blocks of
+// T = (I + L)^-1 of one head by a pair of warps (w = 0, 1 of the pair).  The diagonal blocks of
 // 16 by forward substitution in fp32, a column a thread; the blocks below them by products.
-__device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float *b, int w, int lane, int pair) {
+__device__ __forceinline__ void invert(Inverse &v, unsigned char *T, int w, int lane, int pair) {
     const int d = 2 * w + (lane >> 4), c = lane & 15;  // diagonal block and its column
     {
         float x[16];
-        const float bc = b[16 * d + c];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             float acc[2] = {r == c ? 1.0f : 0.0f, 0.0f};
@@ -218,7 +220,7 @@ __device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float
             x[r] = acc[0] + acc[1];
             const int row = 16 * d + r, col = 16 * d + c;
             v.L[row][col] = __float2half_rn(x[r]);
-            *reinterpret_cast<__half *>(T + swz128_offset(row, col)) = __float2half_rn(x[r] * bc);
+            *reinterpret_cast<__half *>(T + swz128_offset(row, col)) = v.L[row][col];
         }
         // the block right of the first of the pair's two diagonal blocks
         *reinterpret_cast<uint4 *>(&v.L[32 * w + c][32 * w + 16 + (lane >> 4) * 8]) = make_uint4(0, 0, 0, 0);
@@ -226,8 +228,7 @@ __device__ __forceinline__ void invert(Inverse &v, unsigned char *T, const float
     __syncwarp();
     const int fr = lane >> 2, fc = (lane & 3) * 2;
     auto put = [&](int row, int col, float v0, float v1) {
-        const float2 w2 = *reinterpret_cast<const float2 *>(b + col);
-        *reinterpret_cast<uint32_t *>(T + swz128_offset(row, col)) = pack_f16x2(v0 * w2.x, v1 * w2.y);
+        *reinterpret_cast<uint32_t *>(T + swz128_offset(row, col)) = pack_f16x2(v0, v1);
     };
     {
         float o[2][4];
@@ -333,7 +334,6 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
             if (lane >= o) run += v;
         }
         if (tok == 31) sm.half_sum[hh] = run;
-        sm.dec[hh].b[tok] = b;
     }
     fence_async_smem();
     tc_fence_before();
@@ -362,16 +362,18 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
         dec.cum[tok] = run;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + hh) : "memory");
         const float kk = sm.ss[tok], qq = sm.ss[C + tok], last = dec.cum[C - 1], e = exp2f(run);
-        const float nk = sqrtf(kk) * unit_factor(p.gates, kk);
+        const float nk = sqrtf(kk) * unit_factor(p.gates, kk), f = b * nk, w = f * nk;
         HeadGates &gt = sm.gates[hh];
-        gt.rk[tok] = e * nk;
-        gt.ek[tok] = __float2half_rn(exp2f(last - run) * nk);
+        gt.f[tok] = f;
+        gt.near_f[tok] = __float2bfloat16(f);
+        gt.rk[tok] = w * e;
+        dec.w[tok] = w;
+        gt.ek[tok] = __float2half_rn(exp2f(last - run));
         gt.g[tok] = __float2half_rn(e);
         gt.oq[tok] = sqrtf(qq) * unit_factor(p.gates, qq) * p.gates.scale;
         if (tok == 0) gt.last = exp2f(last);
-        dec.near[tok] = exp2f(fminf(dec.cum[tok & 32] - run, kSpan)) * nk;
-        if (tok < 32) dec.far[tok] = exp2f(dec.cum[31] - run) * nk;
-        if (hh == 0) sm.nk[tok] = nk;
+        dec.near[tok] = exp2f(fminf(dec.cum[tok & 32] - run, kSpan));
+        if (tok < 32) dec.far[tok] = exp2f(dec.cum[31] - run);
     }
     const int bad = wait_for(&sm.bar, 0) ? 0 : 1;
     tc_fence_after();
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
 #pragma unroll 1
         for (int x = 0; x < HEADS; ++x) {
             const Decays &dec = sm.dec[x];
-            const float ci = dec.cum[i], wi = q < 2 ? dec.b[i] * sm.nk[i] : 1.0f;
+            const float ci = dec.cum[i], wi = q < 2 ? dec.w[i] : 1.0f;
             float w[32];
             if (hf < (q & 1)) {  // from the first half to the second
                 const float f = exp2f(ci - dec.cum[31]) * wi;
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float v = dots[j] * wi * sm.nk[hf * 32 + j] * exp2_approx(ci - dec.cum[hf * 32 + j]);
+                        const float v = dots[j] * wi * exp2_approx(ci - dec.cum[hf * 32 + j]);
                         w[j] = j < lim ? v : 0.0f;
                     }
                 }
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
         __syncthreads();
         if (warp < 2 * HEADS) {
             const int x = warp >> 1;
-            invert(sm.inv[x], sm.out[x], sm.dec[x].b, warp & 1, lane, x);
+            invert(sm.inv[x], sm.out[x], warp & 1, lane, x);
         }
         fence_async_smem();
         __syncthreads();
@@ -706,8 +708,8 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     };
 
     // The row's values of chunk c, two tokens' each (with head_dim 64 the upper rows hold zeros), and the row's
-    // power of two for it: one that brings the largest of state and values to [2, 4) is chosen every kRescale
-    // chunks and where a value outgrows 16 units.  Rows are their threads' own, so no other thread needs to know.
+    // power of two for it: one that brings the largest of state and writes b |k| v to [2, 4) is chosen every kRescale
+    // chunks and where a write outgrows 16 units.  Rows are their threads' own, so no other thread needs to know.
     uint32_t vals[C / 2];
     auto take_values = [&](int c) {
         if (!wait_for(&sm.bar[B_IN + (c & 1)], c >> 1 & 1)) bad = 1;
@@ -726,9 +728,12 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         }
     };
     auto choose_power = [&](int c) {
-        __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[0]));
+        __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
 #pragma unroll
-        for (int i = 1; i < C / 2; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[i])));
+        for (int i = 0; i < C / 2; ++i) {
+            const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(sm.gates[c & 3].near_f + 2 * i);
+            m = __hmax2(m, __habs2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[i]), f)));
+        }
         const float vmax = fmaxf(__low2float(m), __high2float(m));
         if (__builtin_expect(c % kRescale == 0 || vmax > limit, 0)) {
             float top = 0.0f;
@@ -765,7 +770,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
                 if (elect_one()) issue_x(c);
                 if (!wait_for(&sm.bar[B_T], ph)) bad = 1;
             }
-            // 2. R = V - e^c |k| X, rounded, over X (past the sequence's end the values, the keys and so X are zero)
+            // 2. R = b |k| V - w e^c X, rounded, over X (past the sequence's end the values, the keys and so X are zero)
             if (!wait_for(&sm.bar[B_X], ph)) bad = 1;
             tc_fence_after();
             {
@@ -778,7 +783,9 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t w = vals[8 * n + i];
-                        const uint64_t v2 = mul2(pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), sc);
+                        const float2 f = *reinterpret_cast<const float2 *>(gt.f + 16 * n + 2 * i);
+                        const uint64_t v2 =
+                            mul2(mul2(pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), pair(f.x, f.y)), sc);
                         const float2 r = *reinterpret_cast<const float2 *>(gt.rk + 16 * n + 2 * i);
                         float lo, hi;
                         unpair(fma2(pair(-r.x, -r.y), pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), v2), lo, hi);
@@ -807,7 +814,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             } else if (warp == 3) {
                 if (!wait_for(&sm.bar[B_OI], ph)) bad = 1;  // the state's copy is read: the increment may take its columns
             }
-            // 4. U^T rounded, as it is and times e^(c_64 - c) |k| (a product of rounded numbers: a conversion from fp32
+            // 4. U^T rounded, as it is and times e^(c_64 - c) (a product of rounded numbers: a conversion from fp32
             // takes four times as long)
             if (!wait_for(&sm.bar[B_U], ph)) bad = 1;
             tc_fence_after();

@@ -125,3 +125,76 @@ def test_values_after_a_state_that_vanished(shape, st, act, loud):
             raw[64:14 * 64], xbc[64:14 * 64, :HP] = 300, 0
 
     follow(51, shape, st, [20 * 64 + 5], edit, skip=range(18))
+
+
+# ---- write gates and keys over the rule's whole domain, 0 <= b |k|^2 <= 2 ----
+
+HP, GN = 256, 128  # of PAIR
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("logit", [-12, -14, -16, -18, -30])
+@pytest.mark.parametrize("shape", [PAIR, NARROW], ids=["128", "64"])
+def test_gates_nearly_closed(shape, st, act, logit):
+    """Little is written and nothing was there: outputs and state are as small as the gates."""
+    def edit(xbc, raw, beta, before):
+        beta += logit
+
+    follow(52, shape, st, [200, 64, 3], edit)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+def test_gates_that_open_and_close(st, act):
+    def edit(xbc, raw, beta, before):
+        beta[:100] -= 18
+        beta[160:230:3] -= 40
+        beta[260:] -= 12
+
+    follow(53, PAIR, st, [300], edit, init=[1])
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("length,gate", [(1000.0, 1e-6), (3000.0, 1e-7), (1e8, 1e-16), (0.004, 6e4), (1e-8, 1e16), (None, 1.0)])
+def test_keys_of_any_length(st, act, length, gate):
+    """Keys and gates as they are: the product b |k|^2 is the rule's, whatever each of them is (None: lengths from
+    1/1000 to 1000 side by side, their gates to match)."""
+    def edit(xbc, raw, beta, before):
+        k = xbc[:, HP:HP + GN]
+        k /= np.sqrt((k * k).sum(1, keepdims=True))
+        lengths = length or np.exp(wl.rng(54, 3).uniform(-7, 7, (len(k), 1)))
+        k *= lengths
+        beta[...] = wl.rng(54, 4).uniform(0.3, 1.0, beta.shape) * (gate if length else 1 / lengths ** 2)
+        before *= gate * (length or 1)  # what such writes leave
+
+    follow(54, PAIR, st, [200, 70], edit, init=[1, 0], flags=dict(sigmoid=False, l2norm=False))
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+def test_full_reflections(st, act):
+    """b |k|^2 = 2 and no decay: no write is forgotten, and no rounding either.  Five chunks' errors of 8e-4 rms, one
+    sequence's tile being off by the root of their sum, stay within the scan's tolerance."""
+    bias = ref.layer(55, PAIR)[1]
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = -bias
+        beta[...] = 2.0
+
+    follow(55, PAIR, st, [300], edit, init=[1], flags=dict(softplus=False, sigmoid=False))
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+def test_one_key_reflected_with_values_of_either_sign(st, act):
+    """s <- -s + 2 v along one key: the state grows by 2 |v| a token, and a token's rounding stays in it.  In chunks
+    64 roundings of twice 2^-12 / sqrt(3) of the state rms add up to 2.3e-3, over four chunks to 4.5e-3 and at the
+    outside (4.5 deviations) to 2e-2; token by token in fp32 to 2^12 times less."""
+    bias = ref.layer(56, PAIR)[1]
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = -bias
+        beta[...] = 2.0
+        xbc[:, HP:HP + GN] = xbc[0, HP:HP + GN]
+        xbc[:, :HP] = np.abs(xbc[:, :HP]) * np.where(np.arange(len(xbc)) % 2, 1, -1)[:, None]
+
+    chunks = st == wl.BF16
+    follow(56, PAIR, st, [200], edit, flags=dict(softplus=False, sigmoid=False), y_tol=2 ** -8 + 2e-2 if chunks else None,
+           s_tol=2 ** -8 + 2e-2 if chunks else None)
