@@ -44,6 +44,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 // and queries stacked are one operand of 128 rows; per head T, A (64 x 64, swizzled) and the gates.
 constexpr uint32_t kBlk = 64 * 128;          // one swizzled block of 64 rows
 constexpr uint32_t kKqBytes = 4 * kBlk;
+// |k| is the length that gives the rounded unit key the token's w exactly: its factor 1 - w on what the state holds
+// along its key multiplies up over the tokens, and nothing dampens that where w comes near 2.
 struct HeadGates {
     float f[C];    // b |k|
     float rk[C];   // w e^c
@@ -127,6 +129,7 @@ struct PrepSmem {
     HeadGates gates[HEADS];
     Decays dec[HEADS];
     float ss[2 * C];  // squared lengths of keys and queries
+    float inv_unit[C];  // 1 over the lengths of the keys rounded
     uint64_t bar;
     uint32_t tmem;
     float half_sum[HEADS];
@@ -319,6 +322,17 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
             u.z = pack_f16x2(f[4] * inv, f[5] * inv);
             u.w = pack_f16x2(f[6] * inv, f[7] * inv);
             *reinterpret_cast<uint4 *>(sm.kq + (col >> 6) * 2 * kBlk + swz128_chunk(row, (col & 63) >> 3)) = u;
+            if (i < 4) {  // what rounding made of the key's unit length goes into its length (see HeadGates)
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                float rr = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                    rr = fmaf(r.x, r.x, fmaf(r.y, r.y, rr));
+                }
+                rr = sum_lanes<16>(rr);
+                if (col == 0) sm.inv_unit[row] = rr > 0.0f ? rsqrtf(rr) : 0.0f;
+            }
             if (col == 0) sm.ss[row] = ss;
         }
     }
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
         dec.cum[tok] = run;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + hh) : "memory");
         const float kk = sm.ss[tok], qq = sm.ss[C + tok], last = dec.cum[C - 1], e = exp2f(run);
-        const float nk = sqrtf(kk) * unit_factor(p.gates, kk), f = b * nk, w = f * nk;
+        const float nk = sqrtf(kk) * unit_factor(p.gates, kk) * sm.inv_unit[tok], f = b * nk, w = f * nk;
         HeadGates &gt = sm.gates[hh];
         gt.f[tok] = f;
         gt.near_f[tok] = __float2bfloat16(f);
