@@ -480,8 +480,9 @@ int mamba1_state_update(const mamba1_layer_desc *desc, void *ssm_pool, int64_t s
  *     b = sigmoid(beta)                                           (beta itself if !beta_sigmoid)
  *     k, q divided by sqrt(|.|^2 + 1e-6) if qk_l2norm
  *     u = b * (v - a * S k),   S <- a * S + u k^T,   y = scale * S q      (S k sums over d_state)
- * The method's domain is A <= 0, Delta >= 0 and b * |k|^2 <= 2, where the state cannot grow by its
- * own (qk_l2norm gives |k| <= 1, and the sigmoid b < 1).
+ * The method's domain is A <= 0, Delta >= 0 and 0 <= b * |k|^2 <= 2, where the state cannot grow by
+ * its own (qk_l2norm gives |k| <= 1, and the sigmoid b < 1), with |k|^2 and |q|^2 numbers that fp32
+ * holds.  Up to b * |k|^2 = 1 a write also makes room for itself, and roundings fade with it.
  *
  * Arguments common to the three calls:
  *   dt, beta         (batch, ntok, nheads) or (total_tokens, nheads), both dt_dtype.
@@ -537,6 +538,10 @@ size_t gdn_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t tota
  *   k, q             (total_tokens, n_groups, d_state) act_dtype.
  *   y                (total_tokens, nheads, head_dim) act_dtype.
  *   workspace        at least gdn_chunk_scan_workspace_bytes(...) bytes (MAMBA_ENOSPACE otherwise).
+ * Layers of bf16 state and activations, head_dim 64 or 128 and d_state 128 run in chunks of 64 tokens
+ * from each sequence's start, on operands of 11 bits: of a state's row (one value index) and its
+ * outputs, errors are about 2^-11 of the largest numbers that the row and its writes b * |k| * v take
+ * within the chunk, and what lies below 2^-24 of these is lost.  Other layers run token by token in fp32.
  * Limits: nseq <= 65535.
  */
 int gdn_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,

@@ -19,8 +19,13 @@
 // Number formats: the products run on fp16 operands (11 bits; bf16's 8 would put four times the
 // output's own rounding into y), sums in fp32, and the state itself stays in fp32 in registers.
 // Keys and queries are of unit length before they are rounded.  Values have bf16's range, so every
-// row of the state (one value index) has a power of two that brings what is written to it (b |k| v) and its
-// state to a few units, taken anew every 16 chunks and whenever a write outgrows it.
+// row of the state (one value index) has a power of two, chosen anew for every chunk, that brings the largest
+// of its state and of what is written to it (b |k| v) to [2^7, 2^8).  The chunk takes that no further than 151 times:
+// a write moves a row's length (sqrt(128) times its largest value, at most) by |b k v| and nothing else makes it
+// grow, so it stays below sqrt(128) + 64 = 75.3 times the largest, and |U| below twice that and one; 151 * 2^8 is
+// inside fp16's 65504.  The row's power stands that high because fp16 rounds below 2^-14 to multiples of 2^-24: a
+// row's small numbers (values that fall silent, what a decay over a chunk leaves) are held to 2^-12 of themselves or
+// 2^-24 of the largest in the chunk.
 #include <mutex>
 
 #include <cuda_fp16.h>
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
 constexpr int kChainThreads = 256;       // four warps on the chain, four beside it
 constexpr int kChainRegs = 208, kSideRegs = 48;  // (208 + 48) * 128 registers: what the block is launched with
 constexpr int kRows = 128;               // rows of tensor memory; with head_dim 64 the upper half holds zeros
-constexpr int kRescale = 16;             // chunks between two choices of the rows' powers of two
+constexpr int kTop = 7;                  // a row's power of two brings its largest value to [2^kTop, 2^(kTop + 1))
 
 // What the block waits for: keys, gates and values (two stages), queries, T and A from memory; the products X, U,
 // Q S^T, the increment and Y; the values in registers.
@@ -552,6 +557,9 @@ __device__ __forceinline__ bool half_sync_or(int half, int v) {
         : "r"(v), "r"(half)
         : "memory");
     return any != 0;
+}
+__device__ __forceinline__ void max_abs(float &m, float a, float b) {
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(a), "f"(b));
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -679,6 +687,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         return static_cast<bf16 *>(p.pool) + to * p.stride + ((int64_t)sm.h * P + row) * TN;
     };
     float S[TN];  // times the row's power of two
+    float top = 0.0f;  // the row's largest magnitude, as S holds it
     {
         const bool seeded = row < P && slot >= 0 && p.has_init && p.has_init[sm.s];
         const bf16 *src = pool_row(seeded ? slot : 0);
@@ -690,10 +699,10 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
             float f[8];
             unpack16(w, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) S[e + i] = f[i];
+            for (int i = 0; i < 8; ++i) S[e + i] = f[i], top = fmaxf(top, fabsf(f[i]));
         }
     }
-    float scale = 1.0f, unscale = 1.0f, limit = -1.0f;  // the power of two, its inverse, the largest value it takes
+    float scale = 1.0f, unscale = 1.0f;  // the power of two and its inverse
     int bad = 0;  // a wait gave up: all four warps leave at the next barrier
 
     auto store_state16 = [&](int e) {  // 16 columns of the state's copy for the products
@@ -722,8 +731,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
     };
 
     // The row's values of chunk c, two tokens' each (with head_dim 64 the upper rows hold zeros), and the row's
-    // power of two for it: one that brings the largest of state and writes b |k| v to [2, 4) is chosen every kRescale
-    // chunks and where a write outgrows 16 units.  Rows are their threads' own, so no other thread needs to know.
+    // power of two for it, by the largest of state and writes b |k| v.  Rows are their threads' own, so no other thread needs to know.
     uint32_t vals[C / 2];
     auto take_values = [&](int c) {
         if (!wait_for(&sm.bar[B_IN + (c & 1)], c >> 1 & 1)) bad = 1;
@@ -742,24 +750,28 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         }
     };
     auto choose_power = [&](int c) {
-        __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+        __nv_bfloat162 m[4];  // (four chains of maxima: one would be the latency of 32)
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-            const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(sm.gates[c & 3].near_f + 2 * i);
-            m = __hmax2(m, __habs2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[i]), f)));
+        for (int n = 0; n < C / 8; ++n) {
+            const uint4 fw = *reinterpret_cast<const uint4 *>(sm.gates[c & 3].near_f + 8 * n);
+            const uint32_t f[4] = {fw.x, fw.y, fw.z, fw.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 w = __habs2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&vals[4 * n + i]),
+                                                         *reinterpret_cast<const __nv_bfloat162 *>(&f[i])));
+                m[i] = n ? __hmax2(m[i], w) : w;
+            }
         }
-        const float vmax = fmaxf(__low2float(m), __high2float(m));
-        if (__builtin_expect(c % kRescale == 0 || vmax > limit, 0)) {
-            float top = 0.0f;
-#pragma unroll
-            for (int e = 0; e < TN; ++e) top = fmaxf(top, fabsf(S[e]));
-            top = fmaxf(top * unscale, vmax);
-            uint32_t E = __float_as_uint(top) >> 23;
-            E = top < INFINITY ? max(7u, min(247u, E)) : 127u;
-            int shift = (int)(__float_as_uint(unscale) >> 23) + 1 - (int)E;  // from the old power to the new one
-            scale = __uint_as_float((255u - E) << 23);
-            unscale = __uint_as_float((E - 1u) << 23);
-            limit = __uint_as_float((E + 3u) << 23);
+        m[0] = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+        const float vmax = fmaxf(__low2float(m[0]), __high2float(m[0]));
+        // biased exponents: E of the largest, old of the one that the present power brings to 2^kTop
+        const float most = fmaxf(top * unscale, vmax);
+        const uint32_t old = (__float_as_uint(unscale) >> 23) + kTop;
+        const uint32_t E = most < INFINITY ? max(1u + kTop, __float_as_uint(most) >> 23) : old;
+        if (E != old) {
+            scale = __uint_as_float((254u + kTop - E) << 23);
+            unscale = __uint_as_float((E - kTop) << 23);
+            int shift = (int)old - (int)E;
             while (shift != 0) {  // (in two steps where no float holds their ratio)
                 const int by = max(-126, min(126, shift));
                 const float ratio = __uint_as_float((uint32_t)(127 + by) << 23);
@@ -795,15 +807,17 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
                     tmem_get(lanes + T_X + 16 * n, x);
                     tmem_got(x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w = vals[8 * n + i];
-                        const float2 f = *reinterpret_cast<const float2 *>(gt.f + 16 * n + 2 * i);
-                        const uint64_t v2 =
-                            mul2(mul2(pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), pair(f.x, f.y)), sc);
-                        const float2 r = *reinterpret_cast<const float2 *>(gt.rk + 16 * n + 2 * i);
-                        float lo, hi;
-                        unpair(fma2(pair(-r.x, -r.y), pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), v2), lo, hi);
-                        pk[i] = pack_f16x2(lo, hi);
+                    for (int i = 0; i < 8; i += 2) {  // two tokens, twice
+                        const float4 f = *reinterpret_cast<const float4 *>(gt.f + 16 * n + 2 * i);
+                        const float4 r = *reinterpret_cast<const float4 *>(gt.rk + 16 * n + 2 * i);
+                        auto two = [&](int j, float f0, float f1, float r0, float r1) {
+                            const uint32_t w = vals[8 * n + j];
+                            const uint64_t v2 = mul2(mul2(pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), pair(f0, f1)), sc);
+                            float lo, hi;
+                            unpair(fma2(pair(-r0, -r1), pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), v2), lo, hi);
+                            pk[j] = pack_f16x2(lo, hi);
+                        };
+                        two(i, f.x, f.y, r.x, r.y), two(i + 1, f.z, f.w, r.z, r.w);
                     }
                     tmem_put8(lanes + T_X + 8 * n, pk);  // (packed to the left: over what has been read)
                 }
@@ -872,6 +886,7 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
         if (c >= 0) {
             // 6. the new state, and its copy over the increment (a row's columns are its thread's own)
             const float last = gt.last;
+            float tops[4] = {};
             if (!wait_for(&sm.bar[B_S], ph)) bad = 1;
             tc_fence_after();
 #pragma unroll
@@ -881,7 +896,10 @@ __device__ __forceinline__ bool chain_warps(const ChainJob<P> &J, Armed &arm) {
                 tmem_got(d);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[16 * n + i] = fmaf(last, S[16 * n + i], __uint_as_float(d[i]));
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) max_abs(tops[i / 2 & 3], S[16 * n + i], S[16 * n + i + 1]);
             }
+            top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             if (p.ckpt_slots) {
                 const int32_t cs = ckpt_slot(p, sm.s, min(sm.len, (c + 1) * C), threadIdx.x == 0 && sm.h == 0);
                 if (__builtin_expect(cs >= 0, 0)) write_state(cs);

@@ -218,3 +218,83 @@ def test_reflections_keep_their_length(st, act):
     chunks = st == wl.BF16
     follow(57, shape, st, [300], edit, flags=dict(softplus=False, sigmoid=False), y_tol=2 ** -8 + 2.3e-2 if chunks else None,
            s_tol=2 ** -8 + 2.3e-2 if chunks else None)
+
+
+# ---- values that grow and shrink along a sequence ----
+
+def decay_of(seed, shape, a):
+    """(dt without softplus, flags) for a decay of a in every token and head."""
+    A, bias = ref.layer(seed, shape)
+    return np.log(a) / A - bias, dict(softplus=False)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("shape", [PAIR, NARROW], ids=["128", "64"])
+@pytest.mark.parametrize("exponent", [-17, -20, -23])
+def test_values_and_state_that_fall(shape, st, act, exponent):
+    """Values fall after 64 tokens and the state with them, by 0.74 a token."""
+    dt, flags = decay_of(58, shape, 0.74)
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = dt
+        xbc[64:, :shape.nheads * shape.head_dim] *= 2.0 ** exponent
+
+    follow(58, shape, st, [300], edit, init=[1], flags=flags)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("a,power,chunks", [(0.98, 2, 20), (0.9, 10, 7), (0.9, -2, 20), (0.8, -3, 36), (0.5, -12, 6)])
+def test_values_that_grow_and_shrink_by_the_chunk(st, act, a, power, chunks):
+    dt, flags = decay_of(59, PAIR, a)
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = dt
+        xbc[:, :HP] *= 2.0 ** (power * (np.arange(len(xbc)) // 64))[:, None]
+
+    follow(59, PAIR, st, [64 * chunks - 7], edit, flags=flags, interval=128)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+def test_a_loud_token_and_a_loud_seed(st, act):
+    """One token, and one state from the pool, 2^15 times the rest."""
+    dt, flags = decay_of(60, PAIR, 0.8)
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = dt
+        xbc[333, :HP] *= 2.0 ** 15
+        before[1] *= 2.0 ** 15
+
+    follow(60, PAIR, st, [700, 500], edit, init=[0, 1], flags=flags, interval=64)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+def test_nothing_written_for_twenty_chunks(st, act):
+    """The state only decays, and what is written afterwards stands beside what is left of it."""
+    dt, flags = decay_of(61, PAIR, 0.995)
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = dt
+        xbc[70:1300, :HP] = 0
+        xbc[1300:, :HP] *= 2.0 ** -10
+
+    follow(61, PAIR, st, [1400], edit, init=[1], flags=flags, interval=256)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("shape", [PAIR, NARROW], ids=["128", "64"])
+def test_many_chunks(shape, st, act):
+    follow(62, shape, st, [2111, 1024, 1089], init=[1, 0, 1], interval=512)
+
+
+@pytest.mark.parametrize("st,act", BOTH)
+def test_what_lies_far_below_the_loudest_of_its_tokens(st, act):
+    """Values that fall by 2^-40 while the state is halved with every token.  In chunks a row's numbers are held to
+    2^-24 of the largest of the same 64 tokens: the chunk of the fall loses the quiet values, and the one after it starts
+    from that loss.  From then on they are as exact as any."""
+    dt, flags = decay_of(63, PAIR, 0.5)
+
+    def edit(xbc, raw, beta, before):
+        raw[...] = dt
+        xbc[64:, :HP] *= 2.0 ** -40
+
+    follow(63, PAIR, st, [320], edit, init=[1], flags=flags, skip=(1, 2) if st == wl.BF16 else ())
