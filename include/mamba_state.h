@@ -541,7 +541,8 @@ size_t gdn_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t tota
  * Layers of bf16 state and activations, head_dim 64 or 128 and d_state 128 run in chunks of 64 tokens
  * from each sequence's start, on operands of 11 bits: of a state's row (one value index) and its
  * outputs, errors are about 2^-11 of the largest numbers that the row and its writes b * |k| * v take
- * within the chunk, and what lies below 2^-24 of these is lost.  Other layers run token by token in fp32.
+ * within the chunk, and what lies below 2^-24 of these is lost; a NaN or an infinity also reaches the
+ * outputs of earlier tokens of its chunk.  Other layers run token by token in fp32.
  * Limits: nseq <= 65535.
  */
 int gdn_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,

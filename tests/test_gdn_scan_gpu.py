@@ -298,3 +298,45 @@ def test_what_lies_far_below_the_loudest_of_its_tokens(st, act):
         xbc[64:, :HP] *= 2.0 ** -40
 
     follow(63, PAIR, st, [320], edit, init=[1], flags=flags, skip=(1, 2) if st == wl.BF16 else ())
+
+
+# ---- what is not a number ----
+
+@pytest.mark.parametrize("what", ["value", "key", "query", "step", "gate"])
+@pytest.mark.parametrize("st,act", BOTH)
+def test_how_far_a_nan_reaches(st, act, what):
+    """Later tokens of its sequence, and in chunks the other tokens of its own 64 too; never an earlier chunk, a
+    checkpoint before it, another head (a value, a step or a gate) or another row of the state (a value)."""
+    import torch
+    T, bad = 200, 100
+    A, bias = (to_dev(a, wl.F32) for a in ref.layer(65, PAIR))
+    xbc, raw, beta = ref.inputs(65, PAIR, (T,), act)
+    outs = []
+    for poison in (False, True):
+        x, r, b = to_dev(xbc, act), to_dev(raw, wl.F32), to_dev(beta, wl.F32)
+        if poison:
+            at = {"value": (x, 5), "key": (x, HP + 3), "query": (x, HP + GN + 3), "step": (r, 0), "gate": (b, 0)}[what]
+            at[0][bad, at[1]] = float("nan")
+        pool = to_dev(states(65, PAIR, 4, st), st)
+        y = torch.zeros(T, 2, 128, dtype=x.dtype, device="cuda")
+        bd.gdn_chunk_scan(bd.layer_desc(PAIR, state=st, act=act), pool, to_i32([0, T]), to_i32([0]),
+                          *[t.contiguous() for t in _vkq(PAIR, x)], r, b, A, y, _work(PAIR, T, 1, st, act), dt_bias=bias,
+                          ckpt_slots=to_i32([[1, 2, 3]]), ckpt_interval=64)
+        outs.append((f64(y), f64(pool)))
+    (good, good_pool), (got, pool) = outs
+    clean = 64 if st == wl.BF16 else bad
+    np.testing.assert_array_equal(got[:clean], good[:clean])
+    np.testing.assert_array_equal(pool[1], good_pool[1])
+    assert np.isnan(got[bad, 0]).any()
+    if what == "query":  # it is only read with
+        np.testing.assert_array_equal(got[128:], good[128:])
+        np.testing.assert_array_equal(pool, good_pool)
+    else:
+        assert np.isnan(got[bad + 1:, 0]).any(axis=1).all() and all(np.isnan(pool[i, 0]).any() for i in (0, 2, 3))
+    if what in ("value", "step", "gate"):
+        np.testing.assert_array_equal(got[:, 1], good[:, 1])
+        np.testing.assert_array_equal(pool[:, 1], good_pool[:, 1])
+    if what == "value":
+        rows = [i for i in range(128) if i != 5]
+        np.testing.assert_array_equal(got[:, 0, rows], good[:, 0, rows])
+        np.testing.assert_array_equal(pool[:, 0, rows], good_pool[:, 0, rows])
