@@ -340,3 +340,50 @@ def test_how_far_a_nan_reaches(st, act, what):
         rows = [i for i in range(128) if i != 5]
         np.testing.assert_array_equal(got[:, 0, rows], good[:, 0, rows])
         np.testing.assert_array_equal(pool[:, 0, rows], good_pool[:, 0, rows])
+
+
+# ---- heads that share keys in odd numbers ----
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("heads,head_dim,groups", [(3, 128, 3), (3, 128, 1), (5, 64, 5), (6, 64, 2), (1, 128, 1)])
+def test_odd_numbers_of_heads_a_group(heads, head_dim, groups, st, act):
+    shape = wl.LayerShape(nheads=heads, head_dim=head_dim, d_state=128, n_groups=groups)
+    follow(66, shape, st, [200, 1, 64, 129], init=[1, 0, 1, 1], interval=64)
+
+
+# ---- plans of many sequences ----
+
+@pytest.mark.parametrize("st", [wl.BF16, wl.F32])
+@pytest.mark.parametrize("nseq", [1030, 2500, 5000])
+def test_many_sequences(nseq, st):
+    """The same bytes as in calls of 200 sequences: over 1024 a thread of the plan numbers several, over 4096 they run
+    in the order given."""
+    import torch
+    shape = wl.LayerShape(nheads=1, head_dim=64, d_state=128, n_groups=1)
+    g = np.random.default_rng(nseq)
+    lens = g.integers(0, 20, nseq)
+    lens[g.permutation(nseq)[:40]] = g.integers(60, 200, 40)
+    T, cu = int(lens.sum()), wl.cu_seqlens(lens)
+    A, bias = (to_dev(a, wl.F32) for a in ref.layer(67, shape))
+    xbc, raw, beta = ref.inputs(67, shape, (T,), wl.BF16)
+    vkq = [t.contiguous() for t in _vkq(shape, to_dev(xbc, wl.BF16))]
+    r, b = to_dev(raw, wl.F32), to_dev(beta, wl.F32)
+    slots = g.permutation(nseq + 7)[:nseq].astype(np.int32)
+    slots[g.permutation(nseq)[:20]] = -1
+    init = torch.from_numpy(g.integers(0, 2, nseq).astype(np.uint8)).cuda()
+    start = to_dev(states(67, shape, nseq + 7, st), st)
+    outs = []
+    for step in (nseq, 200):
+        pool, y = start.clone(), torch.zeros(T, 1, 64, dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(0, nseq, step):
+            j = min(nseq, i + step)
+            lo, hi = int(cu[i]), int(cu[j])
+            bd.gdn_chunk_scan(bd.layer_desc(shape, state=st), pool, to_i32(cu[i:j + 1] - lo), to_i32(slots[i:j]),
+                              *[t[lo:hi] for t in vkq], r[lo:hi], b[lo:hi], A, y[lo:hi], _work(shape, hi - lo, j - i, st, wl.BF16),
+                              dt_bias=bias, has_initial_state=init[i:j], err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        outs.append((y, pool))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert (outs[0][0] != 0).any(dim=2).all() and not torch.equal(outs[0][1], start)
