@@ -109,6 +109,9 @@ __device__ __forceinline__ T *align1024(unsigned char *p) {
 // ---------------------------------------------------------------------------------------
 
 constexpr int kPrepThreads = 256;
+// A decay below 2^-150 is zero in fp32; with no logs lower than that the running sum of 64 of them is rounded to 2^-11
+// at most, so that what decays little after a token that forgets all is still told apart.
+constexpr float kNothing = -150.0f;
 constexpr float kSpan = 96.0f;  // largest base-2 exponent span of a block whose decays are factored
 
 // T of one head on the way: L's diagonal 16 x 16 blocks in fp32 (two blocks start 16 banks apart), the
@@ -345,6 +348,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p
     if (hh < HEADS) {
         if (tok < L) {
             run = log_decay(p.gates, run, h0 + hh) * LOG2E;
+            if (run < kNothing) run = kNothing;  // (a NaN stays)
             b = write_gate(p.gates, b);
         }
 #pragma unroll

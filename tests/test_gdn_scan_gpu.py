@@ -387,3 +387,20 @@ def test_many_sequences(nseq, st):
         outs.append((y, pool))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
     assert (outs[0][0] != 0).any(dim=2).all() and not torch.equal(outs[0][1], start)
+
+
+# ---- steps of any size ----
+
+@pytest.mark.parametrize("st,act", BOTH)
+@pytest.mark.parametrize("step", [30.0, 1e3, 1e6, 3e38, float("inf")])
+def test_steps_that_wipe_the_state_out(st, act, step):
+    """Tokens whose decay is zero in any arithmetic among tokens of ordinary steps, in one chunk and at its ends: what
+    comes after them decays as exactly as if they had not been that large."""
+    def edit(xbc, raw, beta, before):
+        raw[10:40] = step
+        raw[63] = step
+        raw[64] = step
+        raw[100:190:9] = step
+        raw[192:256] = step
+
+    follow(68, PAIR, st, [300], edit, init=[1], interval=64)
