@@ -468,7 +468,7 @@ def _gdn_slots(what, pool, H, P, N):
     """(elements from slot to slot, slots) of a pool whose slots each hold a dense (H, P, N) state, in that shape
     or flat."""
     shape, strides = pool.shape, pool.stride()
-    if shape[1:] != (H, P, N) or strides[1:] != (P * N, N, 1):
+    if shape != (shape[0], H, P, N) or strides != (strides[0], P * N, N, 1):
         one = pool.select(0, 0) if len(shape) > 1 and shape[0] else pool
         if len(shape) < 2 or not one.is_contiguous() or (shape[0] and one.numel() < H * P * N) or (
                 len(shape) == 4 and shape[1:] != (H, P, N)):
