@@ -268,8 +268,8 @@ __device__ __forceinline__ void invert(Inverse &v, unsigned char *T, int w, int 
 
 // Block (chunk, group and share of its heads): two heads of a group share its keys' and queries' one product,
 // K K^T over Q K^T.  0.5 MB of a 64-token chunk of 32 heads and 16 groups are read and 1.1 MB written; 8192 tokens
-// take 53 us (3 TB/s).  Neither memory nor the issue slots (a third used) bound it but a block's own row of steps
-// (loads, product, decays, the inverse); three blocks an SM run side by side, 68 KB of shared memory each.
+// take 57 us (3.6 TB/s).  Neither memory nor the issue slots (a third used) bound it but a block's own row of steps
+// (loads, product, decays, the inverse); three blocks an SM run side by side, 70 KB of shared memory each.
 template <int HEADS>
 __global__ void __launch_bounds__(kPrepThreads, 3) k_gdn_prep(const ScanParams p, const WsLayout ws) {
     extern __shared__ __align__(1024) unsigned char prep_smem[];
@@ -1055,11 +1055,13 @@ __device__ __forceinline__ bool side_warps(const ChainJob<P> &J, Armed &arm) {
     return half_sync_or(2, bad);
 }
 
-// Block (sequence in the plan's order, head).  What bounds it is the chain itself, some 5100 cycles for 64 tokens
-// (one prompt of 8192 tokens, 32 blocks: 316 us): three products that wait for one another, 370 to 510 cycles each from
-// issue to completion, and between them the 128 rows' R, U and state read, rounded and written back by the four
-// warps that may reach their tensor-memory lanes.  Two blocks share an SM at little cost: 8 ragged prompts of
-// 32768 tokens in all, 256 blocks, take 324 us for the longest.  Heads of 64 values leave half of the rows idle:
+// Block (sequence in the plan's order, head).  What bounds it is the chain itself, 2.8 us for 64 tokens (one prompt of
+// 8192 tokens, 32 blocks: 358 us).  Three products that wait for one another take 370 to 510 cycles each from issue
+// to completion, together a quarter of that; the rest are the four warps that may reach their tensor-memory lanes,
+// which scale, round and write back the 128 rows' R, U and state, a row a thread, one warp on each of the SM's
+// schedulers.  The writes' scaling in fp32, the row's largest value and its power of two in every chunk are an eighth
+// of the time.  Two blocks share an SM: 8 ragged prompts of 32768 tokens in all, 256 blocks, take 355 us for the 104
+// chunks of the longest, 3.4 us each, a fifth more than alone.  Heads of 64 values leave half of the rows idle:
 // tcgen05's 64-row form puts its accumulator's rows elsewhere, and the chain's length would be the same.
 template <int P>
 __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams p, const WsLayout ws,

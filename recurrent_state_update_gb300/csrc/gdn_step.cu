@@ -232,8 +232,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // scaled by the new column maxima (over the warps through shared memory) and rounded to the grid of
 // step max/127, as the int8 store does; a column that holds a NaN or an infinity has no such grid and gets a NaN as
 // its scale, so that it reads as NaN from then on.  At 192 rows of 32 heads of 128 x 128 a step moves 213 MB in
-// 54.4 us, 0.57 of what a copy moves: some 9 instructions a value (two products, the update, the maximum, and
-// bytes to fp32 and back) and three barriers a block keep the SM from asking for more.
+// 54.4 us, 0.57 of what a copy moves.  That is latency: 30 million warp instructions (9 a value: two products, the
+// update, the maximum, and bytes to fp32 and back) fill 45 % of the issue slots and 33 % of the memory's time, because
+// 168 registers a thread leave 11 warps an SM, whose blocks each load once, meet at three barriers and store, with
+// nothing of another head on its way meanwhile.
 template <typename ActT, int P, int N, int RT>
 __global__ void __launch_bounds__(P / RowMap<N, RT>::ROWS * 32) k_gdn_step_int8(const Int8Args p) {
     using Map = RowMap<N, RT>;
