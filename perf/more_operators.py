@@ -203,7 +203,7 @@ def prepare_plan(case, seed):
     new, past = [0] * rows, [0] * rows
     for i, n, c in zip(order, lens, computed):
         new[i], past[i] = n, c
-    cols = 1 + max((c + n) // block for c, n in zip(past, new)) if block else 1
+    cols = 1 + (8 * block + max(lens)) // block if block else 1
     slots = rows * cols + 1
     ids = list(range(slots))
     r.shuffle(ids)
