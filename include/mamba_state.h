@@ -554,6 +554,137 @@ int gdn_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slo
                    int32_t qk_l2norm, float scale, void *y, void *workspace, size_t workspace_bytes,
                    int32_t *err_word, void *stream);
 
+/* ---------------------------------------------------------------------------------------- */
+/* linear attention layers                                                                   */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * A linear attention layer with a fixed decay for each head keeps one (head_dim, d_state) state a head
+ * in a slot of the same pool and is described by the same mamba_layer_desc, read as for a gated delta
+ * rule layer: values of head_dim, keys and queries of d_state in n_groups groups, channels [v | k | q].
+ * It has no convolution and no steps (conv_kernel, conv_dtype and dt_dtype are not used);
+ * mamba_spec_commit, mamba_slot_copy and the int8 store serve it as they are, with conv_pool NULL.
+ * Per head h (group g = h / (H / G)) and token:
+ *     S <- exp(log_decay[h]) * S + v k^T,   y = scale * S q            (S q sums over d_state)
+ * The method's domain is log_decay <= 0.
+ *
+ * Norm and rotation of keys and queries, in this order, each on request, in fp32 with one rounding:
+ *     x <- x / sqrt(mean(x^2) + eps) * weight            over the d_state values of a head   (qk_norm)
+ *     the pair (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) if interleaved, for i < rot_dim/2, is turned by
+ *     the angle position * inv_freq[i]: (a, b) -> (a cos - b sin, b cos + a sin)          (rot_dim > 0)
+ *   k_weight, q_weight  (d_state) fp32 or NULL (ones).
+ *   positions           int32, one a token, required when rot_dim > 0.
+ *   inv_freq            (rot_dim / 2) fp32, 0 <= inv_freq <= 1, required when rot_dim > 0.  Angles are
+ *                       formed in 64 bits modulo a whole turn, so far positions lose nothing.
+ *   rot_dim             0 (none) or a multiple of 16, at most d_state.
+ */
+
+/*
+ * la_state_update -- the recurrent step of ntok tokens a request, in order, in place on the pool, with
+ * the norm and rotation of its keys and queries in the same launch.  Slot ids, scratch_slots, batch, ntok
+ * and y as in mamba_state_update; a row one of whose slot ids is out of range is left untouched.
+ *   xbc              (batch, ntok, conv_dim) act_dtype, channels [v | k | q], 16-byte aligned.
+ *   log_decay        (nheads) fp32, required.
+ *   positions        (batch, ntok).
+ *   scale            factor of the output (d_state^-1/2 in the method).
+ * Compiled shapes: those of mamba_decode_supported.  Limits: 1 <= ntok <= 8, batch <= 65535.
+ * Alignment: the pool 16 bytes, its slot stride in bytes a multiple of 16, y its element size.
+ */
+int la_state_update(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,
+                    int64_t num_slots, const int32_t *slot_ids, const int32_t *scratch_slots,
+                    int32_t batch, int32_t ntok, const void *xbc, const float *log_decay,
+                    int32_t qk_norm, const float *k_weight, const float *q_weight, float eps,
+                    const int32_t *positions, const float *inv_freq, int32_t rot_dim,
+                    int32_t interleaved, float scale, void *y, int32_t *err_word, void *stream);
+
+/*
+ * la_qk_norm_rope -- norm and rotation of the keys and queries of `tokens` tokens in one pass, for the
+ * prefill.
+ *   k, q             (tokens, n_groups, d_state) act_dtype, a token's heads dense, tokens k_stride and
+ *                    q_stride elements apart (at least n_groups*d_state).
+ *   k_out, q_out     the same with k_out_stride and q_out_stride; k_out may be k and q_out q (with equal
+ *                    strides), else they may not overlap with k or q.
+ *   positions        (tokens); a negative position marks a padding row, whose outputs are not written.
+ *                    May be NULL when rot_dim is 0: then every row is done.
+ * Requires d_state 16, 32, 64, 128 or 256.  Alignment: k, q, k_out, q_out and their strides in bytes
+ * multiples of 16.
+ */
+int la_qk_norm_rope(const mamba_layer_desc *desc, const void *k, int64_t k_stride, const void *q,
+                    int64_t q_stride, int32_t tokens, int32_t qk_norm, const float *k_weight,
+                    const float *q_weight, float eps, const int32_t *positions, const float *inv_freq,
+                    int32_t rot_dim, int32_t interleaved, void *k_out, int64_t k_out_stride, void *q_out,
+                    int64_t q_out_stride, void *stream);
+
+/* Bytes of device workspace la_chunk_scan needs for these sizes (0 on a bad argument). */
+size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total_tokens, int32_t nseq);
+
+/*
+ * la_chunk_scan -- linear attention over a varlen prefill batch.  Sequences, slot ids, initial states,
+ * final states and checkpoints as in mamba_chunk_scan, with two differences: cu_seqlens[nseq] may be
+ * less than total_tokens (the rows behind it are neither used nor written, so that a captured graph of one
+ * size serves smaller batches), and ckpt_interval is a positive multiple of 128 when ckpt_slots is given.
+ *   v                (total_tokens, nheads, head_dim) act_dtype, a token's heads dense, tokens v_stride
+ *                    elements apart.
+ *   k, q             (total_tokens, n_groups, d_state) act_dtype, likewise with k_stride and q_stride; after
+ *                    any norm and rotation.
+ *   log_decay        (nheads) fp32, required.
+ *   y                (total_tokens, nheads, head_dim) act_dtype, dense.
+ *   workspace        at least la_chunk_scan_workspace_bytes(...) bytes (MAMBA_ENOSPACE otherwise); two calls
+ *                    that may run at the same time need one each.
+ * Layers of bf16 activations with head_dim and d_state each 64 or 128 run on the tensor cores in chunks
+ * of 128 tokens from each sequence's start: products of bf16 operands (the scores and the state read by the
+ * queries are rounded to bf16, 2^-9 of each), sums and the state itself in fp32; with an fp32 pool the decayed
+ * keys that enter the state are held to 16 bits.  A NaN or an infinity of one token also reaches the outputs
+ * of earlier tokens of its chunk there.  Other layers run token by token in fp32.
+ * Limits: nseq <= 65535.  Alignment: the pool, workspace, v, k, q and y 16 bytes; the slot stride and the
+ * token strides in bytes multiples of 16.
+ */
+int la_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,
+                  int64_t num_slots, const int32_t *cu_seqlens, int32_t nseq, int32_t total_tokens,
+                  const int32_t *slot_ids, const uint8_t *has_initial_state, const int32_t *ckpt_slots,
+                  int32_t max_ckpt, int32_t ckpt_interval, const void *v, int64_t v_stride, const void *k,
+                  int64_t k_stride, const void *q, int64_t q_stride, const float *log_decay, float scale,
+                  void *y, void *workspace, size_t workspace_bytes, int32_t *err_word, void *stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* the plan of a batch                                                                       */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * mamba_batch_plan -- what the varlen and step calls take of a batch, built on the device from the
+ * requests' lengths and block table, so that a captured graph serves whatever batch its buffers describe
+ * [P1 block-table modes "none" and "align": a request's state pages; varlen chunk metadata].  Request i has
+ * computed[i] = c tokens in its state and brings new_tokens[i] = n; n == 0 marks a padding row.  A state
+ * after t tokens lives in column (t - 1) / block of the request's row of the table ("align"), or in column 0
+ * always when block == 0 ("none").
+ *   new_tokens, computed  (rows) int32, >= 0.
+ *   block_table      (rows, table_cols) int32 slot ids, rows table_stride elements apart.
+ *   block            tokens of a block, or 0.
+ * Outputs (each may be NULL except cu_seqlens and slot_ids):
+ *   cu_seqlens       (rows + 1): running sums of new_tokens.
+ *   slot_ids         (rows): the page of the state after the new tokens; -1 for padding rows.
+ *   has_initial_state (rows) uint8: c > 0 (0 for padding rows).
+ *   copy_src, copy_dst (rows), both or neither: the page of the state after c tokens and the page of slot_ids
+ *                    where they differ and c > 0, else -1: what mamba_slot_copy has to copy before the batch runs.
+ *   ckpt_slots       (rows, max_ckpt): for k = 1..max_ckpt the page of the state after c + k*block tokens, where c
+ *                    is a multiple of block and k*block < n; else -1.  (Checkpoints of the scans count from a
+ *                    sequence's first new token: cut a prompt's chunks at multiples of block to have them.)
+ *                    A table entry of -1 skips its checkpoint.
+ *   positions, token_rows (max_tokens): position (c + its place) and row of each token; -1 behind the last one.
+ * Errors: lengths that are negative, sum to more than max_tokens, or positions of 2^31 and more:
+ * MAMBA_ERR_SEQLENS, and the outputs are those of a batch of padding rows.  A page that is needed but not
+ * in the table or not in [0, num_slots), or a needed checkpoint page below -1 or >= num_slots:
+ * MAMBA_ERR_SLOT_RANGE; the request's slot id is then -2, which every call refuses and leaves untouched,
+ * and its copy and checkpoints are -1.
+ * Limits: rows <= 65535.
+ */
+int mamba_batch_plan(const int32_t *new_tokens, const int32_t *computed, int32_t rows,
+                     const int32_t *block_table, int64_t table_stride, int32_t table_cols, int32_t block,
+                     int64_t num_slots, int32_t max_tokens, int32_t max_ckpt, int32_t *cu_seqlens,
+                     int32_t *slot_ids, uint8_t *has_initial_state, int32_t *copy_src, int32_t *copy_dst,
+                     int32_t *ckpt_slots, int32_t *positions, int32_t *token_rows, int32_t *err_word,
+                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

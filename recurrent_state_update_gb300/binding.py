@@ -100,6 +100,15 @@ SIGNATURES = {
     "gdn_chunk_scan_workspace_bytes": (_sz, [_dp, _i32, _i32]),
     "gdn_chunk_scan": (ctypes.c_int, [_dp, _vp, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp,
                                       _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp, _vp, _sz, _vp, _vp]),
+    "la_state_update": (ctypes.c_int, [_dp, _vp, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _f32, _vp, _vp,
+                                       _i32, _i32, _f32, _vp, _vp, _vp]),
+    "la_qk_norm_rope": (ctypes.c_int, [_dp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _f32, _vp, _vp, _i32, _i32, _vp,
+                                       _i64, _vp, _i64, _vp]),
+    "la_chunk_scan_workspace_bytes": (_sz, [_dp, _i32, _i32]),
+    "la_chunk_scan": (ctypes.c_int, [_dp, _vp, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _i64,
+                                     _vp, _i64, _vp, _f32, _vp, _vp, _sz, _vp, _vp]),
+    "mamba_batch_plan": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i64, _i32, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _vp]),
     "mamba_check_slot_ids": (ctypes.c_int, [_vp, _i32, _vp, _i32, _i64, ctypes.POINTER(_i64)]),
     "mamba_selftest_wait_timeout": (ctypes.c_int, [_vp, _vp, _vp]),
 }
@@ -554,3 +563,140 @@ def gdn_chunk_scan(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, v, k, q, dt,
                                         now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "gdn_chunk_scan")
+
+
+# ------------------------------------------------------------------------------------------
+# linear attention layers
+# ------------------------------------------------------------------------------------------
+
+def _la_rows(what, name, t, tokens, heads, dim):
+    """Elements from token to token of a (tokens, heads, dim) tensor whose tokens are each dense, in that shape or flat."""
+    shape, strides = t.shape, t.stride()
+    if shape == (tokens, heads, dim):
+        dense = strides[2] == 1 and (strides[1] == dim or heads == 1)
+    else:
+        dense = shape == (tokens, heads * dim) and strides[1] == 1
+    if not dense or (tokens > 1 and strides[0] < heads * dim):
+        raise ValueError(f"{what}: {name}: expected ({tokens}, {heads}, {dim}) with dense tokens, got shape {tuple(shape)} "
+                         f"with strides {tuple(strides)}")
+    return strides[0] if tokens > 1 else heads * dim
+
+
+def la_state_update(desc: LayerDesc, ssm_pool, slot_ids, xbc, log_decay, y, *, scratch_slots=None, qk_norm=False, k_weight=None,
+                    q_weight=None, eps=1e-6, positions=None, inv_freq=None, interleaved=False, scale=None, err_word=None,
+                    stream=None):
+    """Linear attention's step over (batch, ntok, conv_dim) channels v | k | q, in place on the pool (or into
+    ``scratch_slots``), with the norm (``qk_norm``) and the rotation (``inv_freq``, ``positions``) of its keys and
+    queries.  ``scale`` defaults to d_state ** -0.5."""
+    code, i32, _, now = _gdn_types or _gdn_setup()
+    H, P, N = desc.nheads, desc.head_dim, desc.d_state
+    act, f32 = code[desc.act_dtype], code[MAMBA_F32]
+    batch, ntok = slot_ids.shape[0], xbc.shape[1]
+    rows = batch * ntok
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    pool, ids, scr, xp, dp, kw, qw, pos, fp, yp, err = _gdn_pointers("la_state_update", (
+        ("ssm_pool", ssm_pool, code[desc.state_dtype], -1, False), ("slot_ids", slot_ids, i32, -1, True),
+        ("scratch_slots", scratch_slots, i32, rows, True), ("xbc", xbc, act, rows * (H * P + 2 * desc.n_groups * N), True),
+        ("log_decay", log_decay, f32, H, True), ("k_weight", k_weight, f32, N, True), ("q_weight", q_weight, f32, N, True),
+        ("positions", positions, i32, rows, True), ("inv_freq", inv_freq, f32, -1, True), ("y", y, act, rows * H * P, True),
+        ("err_word", err_word, i32, 1, False)))
+    stride, slots = _gdn_slots("la_state_update", ssm_pool, H, P, N)
+    rc = (_lib or lib()).la_state_update(ctypes.byref(desc), pool, stride, slots, ids, scr, batch, ntok, xp, dp,
+                                         1 if qk_norm else 0, kw, qw, eps, pos, fp, rot, 1 if interleaved else 0,
+                                         N ** -0.5 if scale is None else scale, yp, err,
+                                         now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "la_state_update")
+
+
+def la_qk_norm_rope(desc: LayerDesc, k, q, k_out, q_out, *, qk_norm=True, k_weight=None, q_weight=None, eps=1e-6,
+                    positions=None, inv_freq=None, interleaved=False, stream=None):
+    """Norm and rotation of (tokens, n_groups, d_state) keys and queries, whose tokens may lie apart (views of a
+    projection's rows); in place when ``k_out`` is ``k`` and ``q_out`` is ``q``.  Rows of a negative position are
+    not written."""
+    code, i32, _, now = _gdn_types or _gdn_setup()
+    G, N = desc.n_groups, desc.d_state
+    act, f32 = code[desc.act_dtype], code[MAMBA_F32]
+    T = k.shape[0]
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    kp, qp, ko, qo, kw, qw, pos, fp = _gdn_pointers("la_qk_norm_rope", (
+        ("k", k, act, -1, False), ("q", q, act, -1, False), ("k_out", k_out, act, -1, False), ("q_out", q_out, act, -1, False),
+        ("k_weight", k_weight, f32, N, True), ("q_weight", q_weight, f32, N, True), ("positions", positions, i32, T, True),
+        ("inv_freq", inv_freq, f32, -1, True)))
+    ks, qs, kos, qos = [_la_rows("la_qk_norm_rope", n, t, T, G, N)
+                        for n, t in (("k", k), ("q", q), ("k_out", k_out), ("q_out", q_out))]
+    rc = (_lib or lib()).la_qk_norm_rope(ctypes.byref(desc), kp, ks, qp, qs, T, 1 if qk_norm else 0, kw, qw, eps, pos, fp, rot,
+                                         1 if interleaved else 0, ko, kos, qo, qos,
+                                         now(k.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "la_qk_norm_rope")
+
+
+def la_chunk_scan_workspace_bytes(desc: LayerDesc, total_tokens: int, nseq: int) -> int:
+    return lib().la_chunk_scan_workspace_bytes(ctypes.byref(desc), total_tokens, nseq)
+
+
+def la_chunk_scan(desc: LayerDesc, ssm_pool, cu_seqlens, slot_ids, v, k, q, log_decay, y, workspace, *, has_initial_state=None,
+                  ckpt_slots=None, ckpt_interval=0, scale=None, err_word=None, stream=None):
+    """Linear attention over a varlen prefill batch; final states and checkpoints written into the pool.  The
+    tokens of ``v``, ``k`` and ``q`` may lie apart (views of a projection's rows), and ``cu_seqlens`` may end before
+    the last of them.  ``scale`` defaults to d_state ** -0.5."""
+    code, i32, u8, now = _gdn_types or _gdn_setup()
+    H, P, N, G = desc.nheads, desc.head_dim, desc.d_state, desc.n_groups
+    act, f32 = code[desc.act_dtype], code[MAMBA_F32]
+    nseq, total = cu_seqlens.shape[0] - 1, v.shape[0]
+    if ckpt_slots is not None and ckpt_slots.dim() != 2:
+        raise ValueError("la_chunk_scan: ckpt_slots: expected (sequences, checkpoints)")
+    max_ckpt = 0 if ckpt_slots is None else ckpt_slots.shape[1]
+    pool, cu, ids, init, ckpt, vp, kp, qp, dp, yp, wp, err = _gdn_pointers("la_chunk_scan", (
+        ("ssm_pool", ssm_pool, code[desc.state_dtype], -1, False), ("cu_seqlens", cu_seqlens, i32, -1, True),
+        ("slot_ids", slot_ids, i32, nseq, True), ("has_initial_state", has_initial_state, u8, nseq, True),
+        ("ckpt_slots", ckpt_slots, i32, nseq * max_ckpt, True), ("v", v, act, -1, False), ("k", k, act, -1, False),
+        ("q", q, act, -1, False), ("log_decay", log_decay, f32, H, True), ("y", y, act, total * H * P, True),
+        ("workspace", workspace, workspace.dtype, -1, True), ("err_word", err_word, i32, 1, False)))
+    stride, slots = _gdn_slots("la_chunk_scan", ssm_pool, H, P, N)
+    vs = _la_rows("la_chunk_scan", "v", v, total, H, P)
+    ks, qs = (_la_rows("la_chunk_scan", n, t, total, G, N) for n, t in (("k", k), ("q", q)))
+    rc = (_lib or lib()).la_chunk_scan(ctypes.byref(desc), pool, stride, slots, cu, nseq, total, ids, init, ckpt, max_ckpt,
+                                       ckpt_interval, vp, vs, kp, ks, qp, qs, dp, N ** -0.5 if scale is None else scale, yp, wp,
+                                       workspace.numel() * workspace.element_size(), err,
+                                       now(ssm_pool.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "la_chunk_scan")
+
+
+# ------------------------------------------------------------------------------------------
+# the plan of a batch
+# ------------------------------------------------------------------------------------------
+
+def mamba_batch_plan(new_tokens, computed, block_table, block: int, num_slots: int, *, cu_seqlens, slot_ids,
+                     has_initial_state=None, copy_src=None, copy_dst=None, ckpt_slots=None, positions=None, token_rows=None,
+                     err_word=None, stream=None):
+    """The arguments of a batch's calls from its requests' lengths and block table, on the device, into the tensors
+    given by keyword (each as long as the header says; ``positions`` and ``token_rows`` are as long as the most
+    tokens of a batch)."""
+    _, i32, u8, now = _gdn_types or _gdn_setup()
+    rows = new_tokens.shape[0]
+    for name, t, dims in (("block_table", block_table, 2), ("ckpt_slots", ckpt_slots, 2), ("positions", positions, 1),
+                          ("token_rows", token_rows, 1)):
+        if t is not None and t.dim() != dims:
+            raise ValueError(f"mamba_batch_plan: {name}: expected {dims} dimension{'s' if dims > 1 else ''}")
+    if block_table.shape[0] < rows or (rows and block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("mamba_batch_plan: block_table: expected a row of dense pages for each request")
+    per_token = [t.shape[0] for t in (positions, token_rows) if t is not None]
+    max_tokens = min(per_token) if per_token else 2 ** 31 - 1
+    if per_token and max(per_token) != max_tokens:
+        raise ValueError("mamba_batch_plan: positions and token_rows: expected the same length")
+    max_ckpt = 0 if ckpt_slots is None else ckpt_slots.shape[1]
+    new, past, table, cu, ids, init, src, dst, ckpt, pos, tok, err = _gdn_pointers("mamba_batch_plan", (
+        ("new_tokens", new_tokens, i32, -1, True), ("computed", computed, i32, rows, True), ("block_table", block_table, i32, -1, False),
+        ("cu_seqlens", cu_seqlens, i32, rows + 1, True), ("slot_ids", slot_ids, i32, rows, True),
+        ("has_initial_state", has_initial_state, u8, rows, True), ("copy_src", copy_src, i32, rows, True),
+        ("copy_dst", copy_dst, i32, rows, True), ("ckpt_slots", ckpt_slots, i32, rows * max_ckpt, True),
+        ("positions", positions, i32, -1, True), ("token_rows", token_rows, i32, -1, True), ("err_word", err_word, i32, 1, False)))
+    cols = block_table.shape[1]
+    rc = (_lib or lib()).mamba_batch_plan(new, past, rows, table, block_table.stride(0) if rows > 1 else cols, cols, block, num_slots,
+                                          max_tokens, max_ckpt, cu, ids, init, src, dst, ckpt, pos, tok, err,
+                                          now(new_tokens.device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mamba_batch_plan")
