@@ -21,10 +21,9 @@
 // the result is the same up to rounding.  Shared memory ~98 KB and 256 TMEM columns per CTA,
 // so two CTAs share an SM and cover each other's waits; each CTA's eight warps split every
 // row's work in two.  All waits are bounded.
-#include <mutex>
-
 #include "common.cuh"
 #include "scan_tc.h"
+#include "tensor_map.h"
 #include "umma.cuh"
 
 namespace ms {
@@ -520,24 +519,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) k_ssd_tc(const ScanTcParams p, 
 // ---------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
-    });
-    return fn;
-}
 
 // 2-D bf16 map over rows x cols (row pitch cols elements), 64 x 128 boxes, 128-byte swizzle,
 // rows past the end read as zero.

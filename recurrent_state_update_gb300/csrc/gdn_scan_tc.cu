@@ -26,11 +26,10 @@
 // inside fp16's 65504.  The row's power stands that high because fp16 rounds below 2^-14 to multiples of 2^-24: a
 // row's small numbers (values that fall silent, what a decay over a chunk leaves) are held to 2^-12 of themselves or
 // 2^-24 of the largest in the chunk.
-#include <mutex>
-
 #include <cuda_fp16.h>
 
 #include "gdn_scan_tc.h"
+#include "tensor_map.h"
 #include "umma.cuh"
 
 namespace ms {
@@ -584,43 +583,6 @@ __device__ __forceinline__ void tmem_frag2(uint32_t a, float (&v)[2][8]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __uint_as_float(r[i]);
 }
-// 16 fp32 columns of this warp's lanes, on their way after the first call and there after the second: what
-// stands between them hides the latency, and the second's operands keep the uses after it.
-__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(a)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_got(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-// N pieces of 16 columns from a, each given to f(piece, values) with the next one on its way.
-template <int N, typename F>
-__device__ __forceinline__ void tmem_pieces(uint32_t a, F f) {
-    uint32_t r[2][16];
-    tmem_get(a, r[0]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        tmem_got(r[i & 1]);
-        if (i + 1 < N) tmem_get(a + 16 * (i + 1), r[(i + 1) & 1]);
-        f(i, r[i & 1]);
-    }
-}
-// 8 32-bit columns (two 16-bit values each) of this warp's lanes; tmem_put_wait waits for all before it.
-__device__ __forceinline__ void tmem_put8(uint32_t a, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3])
@@ -1132,23 +1094,6 @@ __global__ void __launch_bounds__(kChainThreads, 2) k_gdn_chain(const ScanParams
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tm, 256);
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
-    });
-    return fn;
 }
 
 // Rows of tokens x (heads * head_dim) values, in boxes of 64 tokens: of a head's values each token after the

@@ -247,8 +247,9 @@ using namespace ms;
 
 extern "C" size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *d, int32_t total_tokens, int32_t nseq) {
     if (check_layer(d) != MAMBA_OK || total_tokens < 0 || nseq < 0) return 0;
-    const int64_t segs = scan_max_segments(total_tokens, nseq, segment_tokens(d, total_tokens, nseq));
-    return scan_meta_bytes(segs) + (chunked_eligible(d) ? chunked_workspace_bytes(d, segs, nseq) : 0);
+    const int tokens = segment_tokens(d, total_tokens, nseq);
+    const int64_t segs = scan_max_segments(total_tokens, nseq, tokens);
+    return scan_meta_bytes(segs) + (chunked_eligible(d) ? chunked_workspace_bytes(d, segs, nseq, tokens) : 0);
 }
 
 extern "C" int la_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t ssm_slot_stride, int64_t num_slots,

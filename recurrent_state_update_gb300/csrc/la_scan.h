@@ -59,7 +59,7 @@ bool chunked_eligible(const mamba_layer_desc *d);
 // Tokens of a segment of the chunked form for a batch of these sizes.
 int chunked_segment_tokens(int H, int T, int nseq);
 // Workspace past the plan.
-size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq);
+size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq, int seg_tokens);
 // Launches the chunked form after the plan; MAMBA_OK or a negative status.
 int chunked_launch(const ScanParams &p, const mamba_layer_desc *d, cudaStream_t stream);
 

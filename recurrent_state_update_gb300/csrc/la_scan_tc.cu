@@ -1,9 +1,682 @@
+// la_scan_tc.cu -- the chunked form of linear attention on the tcgen05 tensor cores.
+//
+// For a chunk of L <= 128 tokens i = 0..L-1 and a head with the decay d = e^log_decay and the state S (P x N)
+// before it:
+//   A = (Q K^T) . D,  D_ij = d^(i-j) for j <= i, else 0
+//   Y = A V + diag(d^(i+1)) Q S^T
+//   S <- d^L S + V^T K',  K'_j = d^(L-1-j) k_j
+// Four products of 128 x 128 x 128, none of which waits for another one's result but A V for A, and Q S^T for
+// the state before: only the state's own update, elementwise, follows from chunk to chunk.  Everything else of the next
+// chunk is under way meanwhile, in warps of its own: loads, products, A's decays, the keys' decays, the state, and the outputs.
+// The state's transpose stands in tensor memory in fp32 (a key index a lane), where the product adds to it; its
+// copy for the queries, A and K' are rounded to bf16, the type of V, K and Q that they meet.  K' in one bf16 number is as exact as a
+// bf16 pool; under an fp32 pool it is held as the sum of two (16 bits), in twice the product.
+//
+// A sequence's state is linear in what came before, so a long sequence of few heads is cut into segments that are
+// worked on side by side: k_la_segment forms what each but the last adds to the state, and a segment's block
+// starts from the decayed sum of those before it.
 #include "la_scan.h"
+#include "tensor_map.h"
+#include "umma.cuh"
+
 namespace ms {
 namespace la {
-bool chunked_eligible(const mamba_layer_desc *d) { return false; }
-int chunked_segment_tokens(int H, int T, int nseq) { return 1 << 30; }
-size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq) { return 0; }
-int chunked_launch(const ScanParams &p, const mamba_layer_desc *d, cudaStream_t stream) { return MAMBA_EUNSUPPORTED; }
+
+using namespace umma;
+
+namespace {
+
+constexpr int C = kChunk;
+constexpr int kWhole = 1 << 30;               // tokens of a segment where sequences are not cut
+constexpr uint32_t kPolls = umma::kWaitPolls;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr uint32_t kBlk = 128 * 128;          // bytes of a swizzled block: 128 tokens, 64 values each
+constexpr uint32_t kTile = 2 * kBlk;          // of a tile of 128 tokens x 128 (or 64, in its first block)
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// d^m from log2(d) <= 0, also where that is minus infinity.
+__device__ __forceinline__ float power(float l2, int m) { return m == 0 ? 1.0f : exp2f(l2 * (float)m); }
+
+// Waits with one outcome for the whole warp, which takes part in collective instructions afterwards; gives up
+// after the poll limit, or once another warp has.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *failed) {
+    bool ok = false;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPolls; ++i) {
+        if (mbar_try_wait(bar, parity)) {
+            ok = true;
+            break;
+        }
+        if (*failed) break;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *failed = 1;
+    return ok;
+}
+// The same bounded wait for what is still in flight after a failure.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPolls; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+}
+
+template <typename T>
+__device__ __forceinline__ T *align1024(unsigned char *p) {
+    return reinterpret_cast<T *>(p + (-smem_u32(p) & 1023u));  // (an offset, so that accesses stay shared-memory ones)
+}
+
+// What a block works on.
+struct Job {
+    int seq, index, last, t0, len, nc, entry;  // entry: of the sequence's first in the workspace, if it has several segments
+    int32_t slot;
+    bool ok;
+};
+__device__ __forceinline__ Job find_job(const ScanParams &p, int b) {
+    Job j;
+    j.ok = b < p.meta[0];
+    if (!j.ok) return j;
+    const Segment g = meta_segments(p)[b];
+    const int a = p.cu[g.seq], len = p.cu[g.seq + 1] - a;
+    j.seq = g.seq, j.index = g.index, j.slot = p.slot[g.seq];
+    j.last = (len - 1) / p.seg_tokens;
+    j.t0 = a + g.index * p.seg_tokens;
+    j.len = min(p.seg_tokens, len - g.index * p.seg_tokens);
+    j.nc = (j.len + C - 1) / C;
+    j.entry = g.first + g.seq;
+    j.ok = j.slot >= -1 && j.slot < p.num_slots;  // (else flagged by the plan)
+    return j;
+}
+// Entries of the workspace: of each sequence, its initial state and what each segment but the last adds; a head's
+// state each, transposed like tensor memory's lanes: value p of key n at p * 128 + n.
+__device__ __forceinline__ float *entry_at(const ScanParams &p, int e, int h, int P) {
+    return p.ws + ((int64_t)e * p.H + h) * (128 * P);
+}
+
+template <typename StateT>
+__device__ __forceinline__ float load_state(const ScanParams &p, int32_t slot, int h, int P, int N, int v, int n) {
+    return to_f32(static_cast<const StateT *>(p.pool)[slot * p.stride + ((int64_t)h * P + v) * N + n]);
+}
+
+// A row of 64 * BLOCKS bf16 values of a swizzled tile, times f: back in place, and what rounding took to lo.
+template <int BLOCKS, bool LO>
+__device__ __forceinline__ void scale_row(unsigned char *tile, unsigned char *lo, int row, float f) {
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint32_t at = b * kBlk + swz128_chunk(row, c);
+            uint4 w = *reinterpret_cast<const uint4 *>(tile + at);
+            uint32_t *u = reinterpret_cast<uint32_t *>(&w), r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = __uint_as_float(u[e] << 16) * f, y = __uint_as_float(u[e] & 0xffff0000u) * f;
+                u[e] = pack2(x, y);
+                if (LO) r[e] = pack2(x - __uint_as_float(u[e] << 16), y - __uint_as_float(u[e] & 0xffff0000u));
+            }
+            *reinterpret_cast<uint4 *>(tile + at) = w;
+            if (LO) *reinterpret_cast<uint4 *>(lo + at) = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+}
+template <int BLOCKS>
+__device__ __forceinline__ void clear_row(unsigned char *tile, int row) {
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tile + b * kBlk + swz128_chunk(row, c)) = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------------------
+// the chain: a segment of a sequence, one head
+// ---------------------------------------------------------------------------------------
+
+// Each barrier's phase c is chunk c's (of a stage: the c-th use of the stage).
+enum {
+    B_QF = 0, B_KF = 2, B_VF = 4,   // loaded, by stage
+    B_QE = 6, B_KE = 8, B_VE = 10,  // the products have read it
+    B_P = 12,  // Q K^T is there
+    B_A,       // A is in tensor memory
+    B_K2,      // K' is in place of K
+    B_Y,       // A V and Q S^T are there
+    B_YE,      // ... and read
+    B_S,       // the state is updated
+    B_SB,      // its copy is written, and the state is decayed for the next update (phase 0: before the first chunk)
+    B_END,     // every product has finished
+    kBars
+};
+constexpr int kWarps = 18, kThreads = 32 * kWarps;  // 4 for A, 4 for outputs, 4 for the state, 4 for the keys' decays, loads, products
+
+template <int P, bool F32S>
+struct ChainSmem {
+    static constexpr int NQ = F32S ? 1 : 2;  // (with the second halves of K' there is room for one tile of queries)
+    unsigned char q[NQ][kTile], k[2][kTile], v[2][P * 256], sb[P * 256], rest[F32S ? kTile : 1024];  // rest: K's second halves
+    float diag[32], col[32];  // d^m; d^(31-m)
+    uint64_t bar[kBars];
+    uint32_t tmem;
+    int failed;
+};
+
+constexpr uint32_t T_P = 0, T_Y = 128, T_Y2 = 256, T_S = 384;  // tensor memory columns; A takes the first half of Q K^T's
+
+template <int P, int N, bool F32S>
+__global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, const __grid_constant__ CUtensorMap qmap,
+                                                          const __grid_constant__ CUtensorMap kmap,
+                                                          const __grid_constant__ CUtensorMap vmap) {
+    using Smem = ChainSmem<P, F32S>;
+    using StateT = typename std::conditional<F32S, float, bf16>::type;
+    constexpr int NQ = Smem::NQ, NB = N / 64, PB = P / 64;
+    extern __shared__ __align__(1024) unsigned char chain_smem[];
+    Smem &sm = *align1024<Smem>(chain_smem);
+    pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
+    pdl_launch_dependents();
+    const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Job job = find_job(p, blockIdx.x / p.H);
+    if (!job.ok) return;
+    const float l2 = p.log_decay[h] * LOG2E;
+    if (tid < 32) sm.diag[tid] = power(l2, tid);
+    else if (tid < 64) sm.col[tid - 32] = power(l2, 63 - tid);
+    if (N == 64)  // the keys' lanes without keys: products read them
+        for (int i = tid; i < (int)kBlk / 16; i += kThreads) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) reinterpret_cast<uint4 *>(sm.k[s] + kBlk)[i] = make_uint4(0, 0, 0, 0);
+            if (F32S) reinterpret_cast<uint4 *>(sm.rest + (F32S ? kBlk : 0))[i] = make_uint4(0, 0, 0, 0);
+        }
+    if (warp == 16 && elect_one()) {
+        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i == B_A || i == B_K2 || i == B_YE || i == B_SB ? 4 : 1);
+        fence_mbar_init();
+        sm.failed = 0;
+    }
+    if (warp == 17) {
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;
+    volatile int *failed = &sm.failed;
+    unsigned char *second = F32S ? sm.rest : nullptr;
+    const int nc = job.nc;
+    auto wait = [&](int b, uint32_t use) { return warp_wait(&sm.bar[b], use & 1, failed); };
+    const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const int row = tid & 127;
+    int loaded = 0;
+
+    if (warp < 4) {
+        // A: row i a thread, in pieces of 32 columns j.  Left of the diagonal's piece d^(i-j) is
+        // d^(i-j0-31) * d^(31-(j-j0)), neither of which can overflow.
+        float rf[3];
+#pragma unroll
+        for (int b = 0; b < 3; ++b) rf[b] = row >= 32 * b + 32 ? power(l2, row - 32 * b - 31) : 0.0f;
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(B_P, c)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t pk[16];
+                if (b < warp) {
+                    float x[32];
+                    tmem_ld32(lanes + T_P + 32 * b, x);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&sm.col[e]);
+                        pk[e / 2] = pack2(x[e] * (f.x * rf[b < 3 ? b : 0]), x[e + 1] * (f.y * rf[b < 3 ? b : 0]));
+                        pk[e / 2 + 1] = pack2(x[e + 2] * (f.z * rf[b < 3 ? b : 0]), x[e + 3] * (f.w * rf[b < 3 ? b : 0]));
+                    }
+                } else if (b == warp) {
+                    float x[32];
+                    tmem_ld32(lanes + T_P + 32 * b, x);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        pk[e / 2] = pack2(e <= lane ? x[e] * sm.diag[max(lane - e, 0)] : 0.0f,
+                                          e + 1 <= lane ? x[e + 1] * sm.diag[max(lane - e - 1, 0)] : 0.0f);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                }
+                tmem_st16(lanes + T_P + 16 * b, pk);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&sm.bar[B_A]);
+        }
+    } else if (warp < 8) {
+        // the outputs: row i a thread
+        const float f2 = p.scale * power(l2, row + 1);
+        bf16 *y = static_cast<bf16 *>(p.y) + ((int64_t)(job.t0 + row) * p.H + h) * P;
+        for (int c = 0; c < nc; ++c, y += (int64_t)C * p.H * P) {
+            if (!wait(B_Y, c)) break;
+            tc_fence_after();
+            const bool live = c * C + row < job.len;
+#pragma unroll
+            for (int b = 0; b < P / 32; ++b) {
+                float a[32], s[32];
+                tmem_ld32(lanes + T_Y + 32 * b, a);
+                tmem_ld32(lanes + T_Y2 + 32 * b, s);
+                if (b == P / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&sm.bar[B_YE]);
+                }
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = fmaf(f2, s[e + i], p.scale * a[e + i]);
+                        *reinterpret_cast<uint4 *>(y + 32 * b + e) = pack16(o);
+                    }
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // the state: key index n a thread (with N 64 the upper half hold zeros)
+        const int n = row;
+        StateT *pool = static_cast<StateT *>(p.pool) + (int64_t)h * P * N + n;
+        const bool seeded = job.slot >= 0 && p.has_init && p.has_init[job.seq];
+        auto ready = [&](int b, const float (&s)[32], float decay) {  // 32 values: the copy, and the state for the next update
+            float d[32];
+            if (n < N) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    const float f[8] = {s[e], s[e + 1], s[e + 2], s[e + 3], s[e + 4], s[e + 5], s[e + 6], s[e + 7]};
+                    *reinterpret_cast<uint4 *>(sm.sb + (b >> 1) * (N * 128) + swz128_chunk(n, (b & 1) * 4 + e / 8)) = pack16(f);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) d[e] = s[e] * decay;
+            tmem_st32(lanes + T_S + 32 * b, d);
+        };
+        auto done = [&] {
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&sm.bar[B_SB]);
+        };
+        const float whole = power(l2, C), part = power(l2, job.len - (nc - 1) * C);  // over a chunk, and the last one
+        {
+            const float over = power(l2, job.last ? p.seg_tokens : 0);
+            const float *from = entry_at(p, job.entry, h, P) + n;
+#pragma unroll 1
+            for (int b = 0; b < P / 32; ++b) {
+                float s[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] = 0.0f;
+                if (n < N && seeded) {
+                    if (job.last) {  // several segments: from the copy, since the last one's block writes the slot
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = from[(32 * b + e) * 128];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = load_state<StateT>(p, job.slot, h, P, N, 32 * b + e, n);
+                    }
+                }
+                if (n < N)
+                    for (int r = 1; r <= job.index; ++r) {
+                        const float *add = from + (int64_t)r * p.H * (128 * P);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = fmaf(over, s[e], add[(32 * b + e) * 128]);
+                    }
+                ready(b, s, nc == 1 ? part : whole);
+            }
+            done();
+        }
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(B_S, c)) break;
+            tc_fence_after();
+            const bool end = c + 1 == nc;
+            const int at = job.index * p.seg_tokens + min(job.len, (c + 1) * C);  // tokens of the sequence in this state
+            const int32_t keep = end && job.index < job.last ? -1 : end ? job.slot : -1;
+            const int32_t ckpt = ckpt_slot(p, job.seq, at, row == 0 && h == 0);
+#pragma unroll 1
+            for (int b = 0; b < P / 32; ++b) {
+                float s[32];
+                tmem_ld32(lanes + T_S + 32 * b, s);
+                if (n < N) {
+                    if (ckpt >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pool[ckpt * p.stride + (int64_t)(32 * b + e) * N] = from_f32<StateT>(s[e]);
+                    }
+                    if (keep >= 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pool[keep * p.stride + (int64_t)(32 * b + e) * N] = from_f32<StateT>(s[e]);
+                    }
+                }
+                if (!end) ready(b, s, c + 2 == nc ? part : whole);
+            }
+            if (!end) done();
+        }
+    } else if (warp < 16) {
+        // K' in place of K, token j a thread; past the segment's end zeros, in V as well: the tiles hold another's tokens there
+        const float f = power(l2, C - 1 - row);
+        for (int c = 0; c < nc; ++c) {
+            if (!wait(B_P, c)) break;  // the scores have read K
+            const int L = min(C, job.len - c * C);
+            if (L == C) {
+                scale_row<NB, F32S>(sm.k[c & 1], second, row, f);
+            } else {
+                if (!wait(B_VF + (c & 1), c >> 1)) break;
+                if (row < L) {
+                    scale_row<NB, F32S>(sm.k[c & 1], second, row, power(l2, L - 1 - row));
+                } else {
+                    clear_row<NB>(sm.k[c & 1], row);
+                    if (F32S) clear_row<NB>(second, row);
+                    clear_row<PB>(sm.v[c & 1], row);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&sm.bar[B_K2]);
+        }
+    } else if (warp == 16) {
+        const int g = h / p.HG;
+        int c = 0;
+        for (; c < nc; ++c) {
+            const int st = c & 1, use = c >> 1, qs = c % NQ, quse = c / NQ, t = job.t0 + c * C;
+            if (use && !wait(B_KE + st, use - 1)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sm.bar[B_KF + st], NB * kBlk);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) tma_load_2d(sm.k[st] + b * kBlk, &kmap, g * N + 64 * b, t, &sm.bar[B_KF + st]);
+            }
+            __syncwarp();
+            if (quse && !wait(B_QE + qs, quse - 1)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sm.bar[B_QF + qs], NB * kBlk);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) tma_load_2d(sm.q[qs] + b * kBlk, &qmap, g * N + 64 * b, t, &sm.bar[B_QF + qs]);
+            }
+            __syncwarp();
+            if (use && !wait(B_VE + st, use - 1)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sm.bar[B_VF + st], PB * kBlk);
+#pragma unroll
+                for (int b = 0; b < PB; ++b) tma_load_2d(sm.v[st] + b * kBlk, &vmap, h * P + 64 * b, t, &sm.bar[B_VF + st]);
+            }
+            __syncwarp();
+        }
+        loaded = c;
+    } else {
+        constexpr uint32_t ID_P = idesc_bf16(128, 128, false, false), ID_S = idesc_bf16(128, P, true, true),
+                           ID_Y = idesc_bf16(128, P, false, true);
+        for (int c = 0; c < nc; ++c) {
+            const int st = c & 1, use = c >> 1, qs = c % NQ;
+            const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), v = smem_u32(sm.v[st]), sb = smem_u32(sm.sb),
+                           lo = smem_u32(sm.rest);
+            if (!wait(B_KF + st, use) || !wait(B_QF + qs, c / NQ)) break;
+            if (c && !wait(B_Y, c - 1)) break;  // A, which lies where the scores go, is read
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk) mma_bf16(tm + T_P, desc_kmajor(q, kBlk, kk), desc_kmajor(k, kBlk, kk), ID_P, kk > 0);
+                mma_commit(&sm.bar[B_P]);
+            }
+            __syncwarp();
+            if (!wait(B_SB, c) || (c && !wait(B_YE, c - 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk)
+                    mma_bf16(tm + T_Y2, desc_kmajor(q, kBlk, kk), desc_mnmajor(sb, N * 128, kk), ID_Y, kk > 0);
+                mma_commit(&sm.bar[B_QE + qs]);
+            }
+            __syncwarp();
+            if (!wait(B_K2, c) || !wait(B_VF + st, use)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16(tm + T_S, desc_mnmajor(k, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, 1);
+                if (F32S) {
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk)
+                        mma_bf16(tm + T_S, desc_mnmajor(lo, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, 1);
+                }
+                mma_commit(&sm.bar[B_S]);
+                mma_commit(&sm.bar[B_KE + st]);
+            }
+            __syncwarp();
+            if (!wait(B_A, c)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16_ts(tm + T_Y, tm + T_P + 8 * kk, desc_mnmajor(v, kBlk, kk), ID_Y, kk > 0);
+                mma_commit(&sm.bar[B_Y]);
+                mma_commit(&sm.bar[B_VE + st]);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(&sm.bar[B_END]);
+        __syncwarp();
+        drain(&sm.bar[B_END], 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (sm.failed) {  // loads that nothing has waited for end before the block does: those of the last chunks
+        if (warp == 16)
+            for (int i = max(0, loaded - 2); i <= min(loaded, nc - 1); ++i) {
+                drain(&sm.bar[B_KF + (i & 1)], (i >> 1) & 1);
+                drain(&sm.bar[B_QF + i % NQ], (i / NQ) & 1);
+                drain(&sm.bar[B_VF + (i & 1)], (i >> 1) & 1);
+            }
+        if (tid == 0) flag_error(p.err, MAMBA_ERR_TIMEOUT);
+        __syncthreads();
+    }
+    if (warp == 17) tmem_dealloc(tm, 512);
+}
+
+// ---------------------------------------------------------------------------------------
+// what a segment adds to the state
+// ---------------------------------------------------------------------------------------
+
+enum { G_F = 0, G_E = 3, G_K2 = 6, G_END = 9, kSegBars };  // loaded, read, scaled (by stage); every product has finished
+constexpr int kSegThreads = 32 * 10;                       // two groups of 4 warps for the keys' decays, loads, products
+
+template <int P, bool F32S>
+struct SegSmem {
+    static constexpr int NS = F32S ? 2 : 3;
+    unsigned char k[NS][kTile], v[NS][P * 256], rest[2][F32S ? kTile : 1024];
+    uint64_t bar[kSegBars];
+    uint32_t tmem;
+    int failed;
+};
+
+// One segment but a sequence's last, one head: sum of d^(tokens behind it in the segment) k_j v_j^T, as one long product.  The
+// first one's block also keeps the sequence's initial state.
+template <int P, int N, bool F32S>
+__global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams p, const __grid_constant__ CUtensorMap kmap,
+                                                               const __grid_constant__ CUtensorMap vmap) {
+    using Smem = SegSmem<P, F32S>;
+    using StateT = typename std::conditional<F32S, float, bf16>::type;
+    constexpr int NS = Smem::NS, NB = N / 64, PB = P / 64;
+    extern __shared__ __align__(1024) unsigned char seg_smem[];
+    Smem &sm = *align1024<Smem>(seg_smem);
+    pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
+    pdl_launch_dependents();
+    const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & 127;
+    const Job job = find_job(p, blockIdx.x / p.H);
+    if (!job.ok || job.index == job.last) return;
+    const float l2 = p.log_decay[h] * LOG2E;
+    if (N == 64)
+        for (int i = tid; i < (int)kBlk / 16; i += kSegThreads) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) reinterpret_cast<uint4 *>(sm.k[s] + kBlk)[i] = make_uint4(0, 0, 0, 0);
+            if (F32S) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) reinterpret_cast<uint4 *>(sm.rest[s] + (F32S ? kBlk : 0))[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    if (warp == 8 && elect_one()) {
+        for (int i = 0; i < kSegBars; ++i) mbar_init(&sm.bar[i], i >= G_K2 && i < G_END ? 4 : 1);
+        fence_mbar_init();
+        sm.failed = 0;
+    }
+    if (warp == 9) {
+        tmem_alloc(&sm.tmem, 128);
+        tmem_relinquish();
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sm.tmem;
+    volatile int *failed = &sm.failed;
+    const int nc = job.nc;  // (whole chunks: the segment is not the sequence's last)
+    int loaded = 0;
+    auto wait = [&](int b, uint32_t use) { return warp_wait(&sm.bar[b], use & 1, failed); };
+    if (warp < 8) {
+        const int group = warp >> 2;
+        if (group == 1 && job.index == 0 && row < N && job.slot >= 0 && p.has_init && p.has_init[job.seq]) {
+            float *to = entry_at(p, job.entry, h, P) + row;
+#pragma unroll 16
+            for (int e = 0; e < P; ++e) to[e * 128] = load_state<StateT>(p, job.slot, h, P, N, e, row);
+        }
+        for (int c = group; c < nc; c += 2) {
+            const int st = c % NS;
+            const float f = power(l2, job.len - 1 - (c * C + row));
+            if (!wait(G_F + st, c / NS)) break;
+            // (the second halves' place is the group's: free once the product of its last chunk is done, which the load
+            // of this chunk has waited for, two stages being two chunks)
+            scale_row<NB, F32S>(sm.k[st], F32S ? sm.rest[group] : nullptr, row, f);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&sm.bar[G_K2 + st]);
+        }
+        if (group == 0 && warp_wait(&sm.bar[G_END], 0, failed) && !*failed) {
+            tc_fence_after();
+            float *to = entry_at(p, job.entry + 1 + job.index, h, P) + row;
+            const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
+            for (int b = 0; b < P / 32; ++b) {
+                float s[32];
+                tmem_ld32(lanes + 32 * b, s);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) to[(32 * b + e) * 128] = s[e];
+            }
+        }
+    } else if (warp == 8) {
+        const int g = h / p.HG;
+        int c = 0;
+        for (; c < nc; ++c) {
+            const int st = c % NS, use = c / NS, t = job.t0 + c * C;
+            if (use && !wait(G_E + st, use - 1)) break;
+            if (elect_one()) {
+                uint64_t *bar = &sm.bar[G_F + st];
+                mbar_arrive_expect_tx(bar, (NB + PB) * kBlk);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) tma_load_2d(sm.k[st] + b * kBlk, &kmap, g * N + 64 * b, t, bar);
+#pragma unroll
+                for (int b = 0; b < PB; ++b) tma_load_2d(sm.v[st] + b * kBlk, &vmap, h * P + 64 * b, t, bar);
+            }
+            __syncwarp();
+        }
+        loaded = c;
+    } else {
+        constexpr uint32_t ID_S = idesc_bf16(128, P, true, true);
+        for (int c = 0; c < nc; ++c) {
+            const int st = c % NS;
+            const uint32_t k = smem_u32(sm.k[st]), v = smem_u32(sm.v[st]), lo = smem_u32(sm.rest[c & 1]);
+            if (!wait(G_K2 + st, c / NS) || !wait(G_F + st, c / NS)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16(tm, desc_mnmajor(k, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, c > 0 || kk > 0);
+                if (F32S) {
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk) mma_bf16(tm, desc_mnmajor(lo, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, 1);
+                }
+                mma_commit(&sm.bar[G_E + st]);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(&sm.bar[G_END]);
+        __syncwarp();
+        drain(&sm.bar[G_END], 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (sm.failed) {
+        if (warp == 8)
+            for (int i = max(0, loaded - NS); i < loaded; ++i) drain(&sm.bar[G_F + i % NS], (i / NS) & 1);
+        if (tid == 0) flag_error(p.err, MAMBA_ERR_TIMEOUT);
+        __syncthreads();
+    }
+    if (warp == 9) tmem_dealloc(tm, 128);
+}
+
+// Rows of tokens, `stride` elements apart, of `cols` values, in boxes of 128 tokens x 64 values, 128-byte swizzle.  Rows
+// past the end read as zero.
+bool tile_map(CUtensorMap *m, const void *ptr, int64_t cols, int64_t rows, int64_t stride) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    cuuint32_t box[2] = {64, C}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int P, int N, bool F32S>
+int launch(const ScanParams &p, cudaStream_t st) {
+    CUtensorMap qmap, kmap, vmap;
+    if (!tile_map(&qmap, p.q, (int64_t)p.G * N, p.T, p.qs) || !tile_map(&kmap, p.k, (int64_t)p.G * N, p.T, p.ks) ||
+        !tile_map(&vmap, p.v, (int64_t)p.H * P, p.T, p.vs))
+        return MAMBA_ECUDA;
+    const dim3 grid((unsigned)((int64_t)p.max_segs * p.H));
+    if (p.seg_tokens < kWhole) {
+        auto kern = k_la_segment<P, N, F32S>;
+        constexpr size_t smem = sizeof(SegSmem<P, F32S>) + 1024;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return MAMBA_ECUDA;
+        if (launch_pdl(kern, grid, dim3(kSegThreads), smem, st, p, kmap, vmap) != cudaSuccess) return MAMBA_ECUDA;
+    }
+    auto kern = k_la_chain<P, N, F32S>;
+    constexpr size_t smem = sizeof(ChainSmem<P, F32S>) + 1024;
+    static_assert(smem <= 232448, "shared memory of a block");
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return MAMBA_ECUDA;
+    if (launch_pdl(kern, grid, dim3(kThreads), smem, st, p, qmap, kmap, vmap) != cudaSuccess) return MAMBA_ECUDA;
+    return launch_status();
+}
+
+template <bool F32S>
+int dispatch(const ScanParams &p, int P, int N, cudaStream_t st) {
+    if (P == 128) return N == 128 ? launch<128, 128, F32S>(p, st) : launch<128, 64, F32S>(p, st);
+    return N == 128 ? launch<64, 128, F32S>(p, st) : launch<64, 64, F32S>(p, st);
+}
+
+}  // namespace
+
+bool chunked_eligible(const mamba_layer_desc *d) {
+    return d->act_dtype == MAMBA_BF16 && (d->head_dim == 64 || d->head_dim == 128) && (d->d_state == 64 || d->d_state == 128);
+}
+
+// Sequences are cut where their heads alone are fewer than the SMs: into as many segments as make one block an SM, at
+// least 4 chunks each (what a segment adds to the state costs about half of its pass).
+int chunked_segment_tokens(int H, int T, int nseq) {
+    const int64_t blocks = 152 / H;
+    if (blocks < 2 * (int64_t)nseq) return kWhole;
+    const int64_t chunks = ((int64_t)T + C - 1) / C, spare = blocks - nseq / 2;
+    const int64_t per = (chunks + spare - 1) / spare;
+    return (int)((per < 4 ? 4 : per) * C);
+}
+
+size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq, int seg_tokens) {
+    return seg_tokens == kWhole ? 0 : (size_t)(max_segs + nseq) * d->nheads * 128 * d->head_dim * sizeof(float);
+}
+
+int chunked_launch(const ScanParams &p, const mamba_layer_desc *d, cudaStream_t st) {
+    return d->state_dtype == MAMBA_F32 ? dispatch<true>(p, d->head_dim, d->d_state, st)
+                                       : dispatch<false>(p, d->head_dim, d->d_state, st);
+}
+
 }  // namespace la
 }  // namespace ms

@@ -195,6 +195,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
+// 16 fp32 columns of this warp's lanes, on their way after the first call and there after the second: what
+// stands between them hides the latency, and the second's operands keep the uses after it.
+__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+// N pieces of 16 columns from a, each given to f(piece, values) with the next one on its way.
+template <int N, typename F>
+__device__ __forceinline__ void tmem_pieces(uint32_t a, F f) {
+    uint32_t r[2][16];
+    tmem_get(a, r[0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        tmem_got(r[i & 1]);
+        if (i + 1 < N) tmem_get(a + 16 * (i + 1), r[(i + 1) & 1]);
+        f(i, r[i & 1]);
+    }
+}
+// 8 32-bit columns (two 16-bit values each) of this warp's lanes; tmem_put_wait waits for all before it.
+__device__ __forceinline__ void tmem_put8(uint32_t a, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ------------------------------------------------------------------------------------------
 // tcgen05.mma (kind::f16, bf16 inputs, fp32 accumulator in TMEM, one CTA)
 // ------------------------------------------------------------------------------------------
