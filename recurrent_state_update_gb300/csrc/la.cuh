@@ -26,6 +26,17 @@ struct QkPrep {
     int norm, half, inter;  // half: pairs turned, rot_dim / 2
 };
 
+// e^l as the sum of two fp32 numbers: a head that remembers 1 / |l| tokens multiplies what rounding a single one to 24 bits
+// takes by that many.  The logarithm's own error is relative to l, so that it is no larger than one such rounding over that time.
+__device__ __forceinline__ float2 decay_of(float l) {
+    const float hi = expf(l);
+    return make_float2(hi, hi > 1e-30f && hi < 1.0f ? hi * (l - logf(hi)) : 0.0f);
+}
+// S <- d S + v k on two of a row's values at a time.
+__device__ __forceinline__ uint64_t decayed_add(uint64_t hi, uint64_t lo, uint64_t S, uint64_t v, uint64_t k) {
+    return fma2(hi, S, fma2(lo, S, mul2(v, k)));
+}
+
 // Turns a position, as a fraction of 2^64 (0 <= f; exact to 2^-62 of itself or 2^-64).
 __device__ __forceinline__ uint64_t turns(float f) {
     const uint32_t bits = __float_as_uint(f), e = (bits >> 23) & 255u;

@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(32 * WARPS) k_la_tokens(const ScanParams p) {
     const int col = (lane & (SL - 1)) * 8, own = (lane & (Map::LPR - 1)) * 8;  // of staging, of the state
     const int brow = warp * Map::ROWS, row0 = split * ROWS + brow;
     const int lrow = brow + idx * Map::RPW + sub;  // the block's row whose sum this lane gets
-    const float decay = expf(p.log_decay[h]);
-    const uint64_t d2 = pair(decay, decay);
+    const float2 decay = decay_of(p.log_decay[h]);
+    const uint64_t dh = pair(decay.x, decay.x), dl = pair(decay.y, decay.y);
     StateT *pool = static_cast<StateT *>(p.pool);
     const int64_t off = ((int64_t)h * P + row0 + sub) * N + own;
     uint64_t S[RT][Map::PAIRS] = {};  // (pairs of zeros)
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_la_tokens(const ScanParams p) {
                 const float x = vs[j][brow + r * Map::RPW + sub];
                 const uint64_t v2 = pair(x, x);
 #pragma unroll
-                for (int e = 0; e < Map::PAIRS; ++e) S[r][e] = fma2(d2, S[r][e], mul2(v2, kc[e]));
+                for (int e = 0; e < Map::PAIRS; ++e) S[r][e] = decayed_add(dh, dl, S[r][e], v2, kc[e]);
             }
             const float out = row_sum<Map>(S, qc, lane);
             if ((lane & (Map::SHARE - 1)) == 0) *yt = from_f32<ActT>(out);

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
     for (int r = 0; r < RT; ++r) raw[r].load(pool + s * p.stride + off + (int64_t)r * Map::RPW * N);
     const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.ntok * p.Cd;
     const ActT *keys = xbc + p.H * P + (h / p.HG) * N, *queries = keys + p.G * N;
-    const float decay = expf(p.log_decay[h]);
+    const float2 decay = decay_of(p.log_decay[h]);
     for (int e = tid; e < p.ntok * p.prep.half; e += blockDim.x) {
         const int j = e / p.prep.half, a = e % p.prep.half;
         table[j][a] = turned(turns(p.prep.inv_freq[a]), p.prep.pos[(int64_t)i * p.ntok + j]);
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
     uint64_t S[RT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r) raw[r].unpack(S[r]);
-    const uint64_t d2 = pair(decay, decay);
+    const uint64_t dh = pair(decay.x, decay.x), dl = pair(decay.y, decay.y);
     __syncthreads();
     ActT *y = static_cast<ActT *>(p.y) + ((int64_t)i * p.ntok * p.H + h) * P + row0 + warp * Map::ROWS + idx * Map::RPW + sub;
     for (int j = 0; j < p.ntok; ++j, y += (int64_t)p.H * P) {
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
             const float v = vs[j][warp * Map::ROWS + r * Map::RPW + sub];
             const uint64_t v2 = pair(v, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[r][e] = fma2(d2, S[r][e], mul2(v2, k[e]));
+            for (int e = 0; e < 4; ++e) S[r][e] = decayed_add(dh, dl, S[r][e], v2, k[e]);
         }
         const float out = row_sum<Map>(S, q, lane);
         if ((lane & (Map::SHARE - 1)) == 0) *y = from_f32<ActT>(out);
