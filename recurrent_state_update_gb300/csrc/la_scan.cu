@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_la_plan(const ScanParams p) {
         const int m = segments(s);
         for (int i = 0; i < m; ++i) {  // (the order among equals is not fixed, and no result depends on it)
             const int to = atomicAdd(&place[rank(tokens_of(s, i))], 1);
-            out[to] = {s, i, at, 0};
+            const int32_t sl = p.slot[s];
+            const bool in = sl >= -1 && sl < p.num_slots;
+            out[to] = {s, i, m - 1, at + s, p.cu[s] + i * p.seg_tokens, tokens_of(s, i), in ? sl : -2, in && sl >= 0 && p.has_init && p.has_init[s]};
         }
         at += m;
     }
@@ -99,11 +101,11 @@ __global__ void __launch_bounds__(32 * WARPS) k_la_tokens(const ScanParams p) {
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     if ((int)blockIdx.y >= p.meta[0]) return;  // no such sequence: empty ones, or cu_seqlens refused (flagged)
-    const int s = meta_segments(p)[blockIdx.y].seq;
+    const Segment job = meta_segments(p)[blockIdx.y];  // (the whole sequence)
     const int h = blockIdx.x / SPLITS, split = blockIdx.x % SPLITS, grp = h / p.HG;
-    const int t0 = p.cu[s], len = p.cu[s + 1] - t0;
-    const int32_t slot = p.slot[s];
-    if (slot < -1 || slot >= p.num_slots) return;  // bad slot (flagged)
+    const int s = job.seq, t0 = job.t0, len = job.len;
+    const int32_t slot = job.slot;
+    if (slot < -1) return;  // bad slot (flagged)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane / Map::LPR, idx = (lane & (Map::LPR - 1)) / Map::SHARE;
     const int col = (lane & (SL - 1)) * 8, own = (lane & (Map::LPR - 1)) * 8;  // of staging, of the state
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_la_tokens(const ScanParams p) {
             for (int i = 0; i < PIECES; ++i)
                 store_row(pool + to * p.stride + off + r * Map::RPW * N + i * Map::LPR * 8, piece(S[r], i));
     };
-    if (slot >= 0 && p.has_init && p.has_init[s]) {
+    if (job.seeded) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll

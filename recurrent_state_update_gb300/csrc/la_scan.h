@@ -8,10 +8,14 @@ namespace la {
 
 constexpr int kChunk = 128;  // tokens of one chunk of the chunked form
 
-// A run of whole chunks of a sequence (the sequence's last one ends with it), worked on from start to end by one block a head.
-struct Segment {
-    int32_t seq, index, first;  // of which sequence, which one of it, the sequence's first segment in order of sequences
-    int32_t pad;
+// A run of whole chunks of a sequence (the sequence's last one ends with it), worked on from start to end by one block a head: all
+// that its block has to know, in one load.
+struct __align__(16) Segment {
+    int32_t seq, index, last;  // of which sequence, which one of it, and the sequence's last one's index
+    int32_t entry;             // the sequence's first entry in the workspace
+    int32_t t0, len;           // first token, tokens
+    int32_t slot;              // the sequence's, -2 where it is outside the pool
+    int32_t seeded;            // whether the sequence starts from its slot's state
 };
 
 struct ScanParams {

@@ -41,6 +41,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // d^m from log2(d) <= 0, also where that is minus infinity.
 __device__ __forceinline__ float power(float l2, int m) { return m == 0 ? 1.0f : exp2f(l2 * (float)m); }
 
@@ -81,67 +86,82 @@ __device__ __forceinline__ T *align1024(unsigned char *p) {
     return reinterpret_cast<T *>(p + (-smem_u32(p) & 1023u));  // (an offset, so that accesses stay shared-memory ones)
 }
 
-// What a block works on.
-struct Job {
-    int seq, index, last, t0, len, nc, entry;  // entry: of the sequence's first in the workspace, if it has several segments
-    int32_t slot;
-    bool ok;
-};
-__device__ __forceinline__ Job find_job(const ScanParams &p, int b) {
-    Job j;
-    j.ok = b < p.meta[0];
-    if (!j.ok) return j;
-    const Segment g = meta_segments(p)[b];
-    const int a = p.cu[g.seq], len = p.cu[g.seq + 1] - a;
-    j.seq = g.seq, j.index = g.index, j.slot = p.slot[g.seq];
-    j.last = (len - 1) / p.seg_tokens;
-    j.t0 = a + g.index * p.seg_tokens;
-    j.len = min(p.seg_tokens, len - g.index * p.seg_tokens);
-    j.nc = (j.len + C - 1) / C;
-    j.entry = g.first + g.seq;
-    j.ok = j.slot >= -1 && j.slot < p.num_slots;  // (else flagged by the plan)
-    return j;
-}
 // Entries of the workspace: of each sequence, its initial state and what each segment but the last adds; a head's
 // state each, transposed like tensor memory's lanes: value p of key n at p * 128 + n.
 __device__ __forceinline__ float *entry_at(const ScanParams &p, int e, int h, int P) {
     return p.ws + ((int64_t)e * p.H + h) * (128 * P);
 }
 
-// A row of 64 * BLOCKS bf16 values of a swizzled tile, times f, as a sum of 1 + MORE bf16 numbers: the first back in
-// place, the others into the tiles at rest.
-template <int BLOCKS, int MORE>
-__device__ __forceinline__ void scale_row(unsigned char *tile, unsigned char *rest, int row, float f) {
-#pragma unroll
-    for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint32_t at = b * kBlk + swz128_chunk(row, c);
-            const uint4 w = *reinterpret_cast<const uint4 *>(tile + at);
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t out[1 + MORE][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = __uint_as_float(in[e] << 16) * f, y = __uint_as_float(in[e] & 0xffff0000u) * f;
-#pragma unroll
-                for (int m = 0; m < MORE; ++m) {  // (cut off, not rounded: what is left is exact, and goes to the next)
-                    out[m][e] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-                    x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-                    y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-                }
-                out[MORE][e] = MORE == 2 ? __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632) : pack2(x, y);  // (8 bits are left)
-            }
-            *reinterpret_cast<uint4 *>(tile + at) = make_uint4(out[0][0], out[0][1], out[0][2], out[0][3]);
-#pragma unroll
-            for (int m = 0; m < MORE; ++m)
-                *reinterpret_cast<uint4 *>(rest + m * kTile + at) = make_uint4(out[m + 1][0], out[m + 1][1], out[m + 1][2], out[m + 1][3]);
-        }
+// A token's weight in the state: w, and as bf16 numbers, twice each, w1 of it and w2 of what is left.
+struct Weight {
+    float w;
+    __nv_bfloat162 w1, w2;
+    __device__ __forceinline__ explicit Weight(float f) : w(f) {
+        w1 = __float2bfloat162_rn(f);
+        w2 = __float2bfloat162_rn(f - __low2float(w1));
+    }
+};
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
+// Offset of the 16-byte piece i (8 a block) of a row of a swizzled tile.
+__device__ __forceinline__ uint32_t piece_at(int row, int i) { return (i >> 3) * kBlk + swz128_chunk(row, i & 7); }
+// K' = w k of 8 values as a sum of 1 + MORE bf16 numbers.  The first is k w1, rounded, two values an instruction.
+__device__ __forceinline__ uint4 first_part(const uint4 &k, const Weight &w) {
+    auto one = [&](uint32_t x) { return as_u32(__hmul2(as_bf16x2(x), w.w1)); };
+    return make_uint4(one(k.x), one(k.y), one(k.z), one(k.w));
 }
-template <int BLOCKS>
-__device__ __forceinline__ void clear_row(unsigned char *tile, int row) {
+// The others.  What rounding took from k w1 is a bf16 number itself, which a fused multiply-add gives; with k w2 it makes
+// 16 bits.  Three parts take the product in fp32, and the second cuts off, so that 8 bits are left.
+template <int MORE>
+__device__ __forceinline__ void other_parts(const uint4 &k, const uint4 &first, const Weight &w, uint4 (&out)[MORE]) {
+    const uint32_t in[4] = {k.x, k.y, k.z, k.w}, hi[4] = {first.x, first.y, first.z, first.w};
+    uint32_t o[2][4];
 #pragma unroll
-    for (int b = 0; b < BLOCKS; ++b)
+    for (int e = 0; e < 4; ++e) {
+        if (MORE == 1) {
+            const __nv_bfloat162 x = as_bf16x2(in[e]);
+            o[0][e] = as_u32(__hfma2(x, w.w2, __hfma2(x, w.w1, __hneg2(as_bf16x2(hi[e])))));
+        } else {
+            const uint64_t less = pair(-__uint_as_float(hi[e] << 16), -__uint_as_float(hi[e] & 0xffff0000u));
+            float lo, up;
+            unpair(fma2(pair(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), pair(w.w, w.w), less), lo, up);
+            o[0][e] = __byte_perm(__float_as_uint(lo), __float_as_uint(up), 0x7632);
+            lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+            up -= __uint_as_float(__float_as_uint(up) & 0xffff0000u);
+            o[1][e] = pack2(lo, up);
+        }
+    }
 #pragma unroll
+    for (int m = 0; m < MORE; ++m) out[m] = make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
+}
+// The other parts of blocks B0 .. B1 - 1 of a row of K into the tiles at rest, and the first parts to registers (to tile, if
+// it is given).  Four pieces are read before the first is worked on.
+template <int MORE, int B0, int B1>
+__device__ __forceinline__ void other_parts(const unsigned char *k, unsigned char *rest, int row, const Weight &w, uint4 *first,
+                                            unsigned char *tile) {
+#pragma unroll
+    for (int i = 8 * B0; i < 8 * B1; i += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4 *>(k + piece_at(row, i + c));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t at = piece_at(row, i + c);
+            const uint4 hi = first_part(x[c], w);
+            uint4 out[MORE];
+            other_parts<MORE>(x[c], hi, w, out);
+            if (first) first[i - 8 * B0 + c] = hi;
+            if (tile) *reinterpret_cast<uint4 *>(tile + at) = hi;
+#pragma unroll
+            for (int m = 0; m < MORE; ++m) *reinterpret_cast<uint4 *>(rest + m * kTile + at) = out[m];
+        }
+    }
+}
+__device__ __forceinline__ void clear_row(unsigned char *tile, int row, int b0, int b1) {
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b)
+#pragma unroll 1
         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(tile + b * kBlk + swz128_chunk(row, c)) = make_uint4(0, 0, 0, 0);
 }
 
@@ -153,11 +173,12 @@ __device__ __forceinline__ void clear_row(unsigned char *tile, int row) {
 enum {
     B_QF = 0, B_KF = 2, B_VF = 4,   // loaded, by stage
     B_QE = 6, B_KE = 8, B_VE = 10,  // the products have read it
-    B_P = 12,  // Q K^T is there
-    B_A,       // A is in tensor memory
+    B_P = 12,  // Q K^T is there, by place
+    B_A = 14,       // A is in tensor memory
     B_K2,      // K' is in place of K
-    B_Y,       // A V and Q S^T are there
-    B_YE,      // ... and read
+    B_Y2,      // Q S^T is there
+    B_M,       // ... scaled, and in the place where A V adds to it
+    B_Y,       // the outputs are there
     B_S,       // V^T K' is there
     B_SB,      // ... and added, and the state's copy is written (phase 0: before the first chunk)
     B_END,     // every product has finished
@@ -166,40 +187,73 @@ enum {
 // Groups of 4 warps: for A, for outputs, for the state, for the keys' decays, and one of which a warp loads and another issues the
 // products.  The state's group takes registers from the others, within what the launch gave the block: 5 warps a scheduler
 // leave 96 a thread (launch() checks that the compiler made it so).
-constexpr int kThreads = 5 * 128, kRegs = 96, kStateRegs = 176, kOtherRegs = 88, kIssueRegs = 40;
-static_assert(kStateRegs + 3 * kOtherRegs + kIssueRegs <= 5 * kRegs, "registers of the launch");
+constexpr int kThreads = 5 * 128, kRegs = 96, kScoreRegs = 88, kOutRegs = 88, kStateRegs = 168, kKeyRegs = 104,
+              kIssueRegs = 32;
+static_assert(kScoreRegs + kOutRegs + kStateRegs + kKeyRegs + kIssueRegs <= 5 * kRegs, "registers of the launch");
 
-template <int P, bool F32S>
+// Barrier of the outputs' group; whether any of its threads passed true.
+__device__ __forceinline__ bool outputs_sync_or(bool v) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(any)
+        : "r"((uint32_t)v)
+        : "memory");
+    return any != 0;
+}
+// A tile to memory, tracked in the issuing thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
+
+template <int P, int N, bool F32S>
 struct ChainSmem {
     // Parts of K' past the first, and stages of queries and values: what the parts leave room for.  Keys are needed first and
     // read last, so that they always have two.
     static constexpr int MORE = F32S ? 2 : 1, NQ = P == 64 && !F32S ? 2 : 1, NV = P == 128 && F32S ? 1 : 2;
-    unsigned char q[NQ][kTile], k[2][kTile], v[NV][P * 256], sb[P * 256], rest[MORE][kTile];
-    float diag[32], col[32];  // d^m; d^(31-m)
+    // Where the outputs stand on their way to memory: in a place of their own, where there is room for one, or over the chunk's
+    // values, which are used by then, or its K' where values have one stage.  (Over K' the next keys come late: a ragged batch
+    // took 209 us so.)
+    static constexpr bool OWN_OUT = P == 64 || N == 64, OUT_ON_V = !OWN_OUT && NV == 2, OUT_ON_K = !OWN_OUT && !OUT_ON_V;
+    static constexpr uint32_t kQ = N * 256, kSb = P * N * 2, kOut = OWN_OUT ? P * 256 : 1024;
+    unsigned char q[NQ][kQ], k[2][kTile], v[NV][P * 256], sb[kSb], rest[MORE][kTile], out[kOut];
+    float diag[32];  // d^m
     uint64_t bar[kBars];
     uint32_t tmem;
     int failed;
 };
 
-constexpr uint32_t T_P = 0, T_Y = 128, T_Y2 = 256, T_D = 384;  // tensor memory columns; A takes the first half of Q K^T's
 
 template <int P, int N, bool F32S>
 __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, const __grid_constant__ CUtensorMap qmap,
                                                           const __grid_constant__ CUtensorMap kmap,
-                                                          const __grid_constant__ CUtensorMap vmap) {
-    using Smem = ChainSmem<P, F32S>;
+                                                          const __grid_constant__ CUtensorMap vmap,
+                                                          const __grid_constant__ CUtensorMap ymap) {
+    using Smem = ChainSmem<P, N, F32S>;
     using StateT = typename std::conditional<F32S, float, bf16>::type;
     constexpr int NQ = Smem::NQ, NV = Smem::NV, MORE = Smem::MORE, NB = N / 64, PB = P / 64;
+    // Tensor memory columns: scores (of two chunks, where there is room), the state's part of the outputs, the outputs, the
+    // state's update.  A takes the second half of its scores' columns.
+    constexpr int NP = P == 64 && NQ == 2 ? 2 : 1;
+    constexpr uint32_t T_P = 0, T_Y2 = NP * 128, T_Y = T_Y2 + P, T_D = T_Y + P;
+    static_assert(T_D + P <= 512, "tensor memory");
+    constexpr bool HELP = MORE == 2 && NB == 2;  // whether the scores' group takes half of the other parts
     extern __shared__ __align__(1024) unsigned char chain_smem[];
     Smem &sm = *align1024<Smem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Job job = find_job(p, blockIdx.x / p.H);
-    if (!job.ok) return;
+    const int which = blockIdx.x / p.H;
+    const Segment job = meta_segments(p)[min(which, p.max_segs - 1)];
+    if (which >= p.meta[0] || job.slot < -1) return;  // no such segment, or its slot is bad (flagged)
     const float l2 = p.log_decay[h] * LOG2E;
     if (tid < 32) sm.diag[tid] = power(l2, tid);
-    else if (tid < 64) sm.col[tid - 32] = power(l2, 63 - tid);
     if (N == 64)  // the keys' lanes without keys: products read them
         for (int i = tid; i < (int)kBlk / 16; i += kThreads) {
 #pragma unroll
@@ -208,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
             for (int m = 0; m < MORE; ++m) reinterpret_cast<uint4 *>(sm.rest[m] + kBlk)[i] = make_uint4(0, 0, 0, 0);
         }
     if (warp == 16 && elect_one()) {
-        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i == B_A || i == B_K2 || i == B_YE || i == B_SB ? 4 : 1);
+        tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap), tma_prefetch_desc(&ymap);
+        for (int i = 0; i < kBars; ++i) mbar_init(&sm.bar[i], i == B_K2 && HELP ? 8 : i == B_A || i == B_K2 || i == B_M || i == B_SB ? 4 : 1);
         fence_mbar_init();
         sm.failed = 0;
     }
@@ -222,107 +277,197 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     tc_fence_after();
     const uint32_t tm = sm.tmem;
     volatile int *failed = &sm.failed;
-    const int nc = job.nc;
+    const int nc = (job.len + C - 1) / C;
     auto wait = [&](int b, uint32_t use) { return warp_wait(&sm.bar[b], use & 1, failed); };
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const int row = tid & 127;
-    int loaded = 0;
+    int loaded = 0, in_flight = -1, of = 1;  // what this warp has loaded, and the first barrier of its stages
 
     if (warp < 4) {
-        fewer_registers<kOtherRegs>();
-        // A: row i a thread, in pieces of 32 columns j.  Left of the diagonal's piece d^(i-j) is
-        // d^(i-j0-31) * d^(31-(j-j0)), neither of which can overflow.
-        float rf[3];
+        fewer_registers<kScoreRegs>();
+        // A: row i a thread, in pieces of 16 columns j, from the diagonal's two to the left.  There d^(i-j) is
+        // d^(i-j0-15) * d^(15-(j-j0)), neither of which can overflow.  A lies from column 64 on, where scores stood that have
+        // been read by the time.
+        uint64_t col[8];
 #pragma unroll
-        for (int b = 0; b < 3; ++b) rf[b] = row >= 32 * b + 32 ? power(l2, row - 32 * b - 31) : 0.0f;
+        for (int e = 0; e < 8; ++e) col[e] = pair(power(l2, 15 - 2 * e), power(l2, 14 - 2 * e));
+        const float step = power(l2, 16), first = power(l2, lane + 1);
         for (int c = 0; c < nc; ++c) {
-            if (!wait(B_P, c)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t pk[16];
-                if (b < warp) {
-                    float x[32];
-                    tmem_ld32(lanes + T_P + 32 * b, x);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&sm.col[e]);
-                        pk[e / 2] = pack2(x[e] * (f.x * rf[b < 3 ? b : 0]), x[e + 1] * (f.y * rf[b < 3 ? b : 0]));
-                        pk[e / 2 + 1] = pack2(x[e + 2] * (f.z * rf[b < 3 ? b : 0]), x[e + 3] * (f.w * rf[b < 3 ? b : 0]));
-                    }
-                } else if (b == warp) {
-                    float x[32];
-                    tmem_ld32(lanes + T_P + 32 * b, x);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        pk[e / 2] = pack2(e <= lane ? x[e] * sm.diag[max(lane - e, 0)] : 0.0f,
-                                          e + 1 <= lane ? x[e + 1] * sm.diag[max(lane - e - 1, 0)] : 0.0f);
+            if (HELP) {  // three parts of K' take the keys' group longer than the scores take to come: the second block is done here
+                if (!wait(B_KF + (c & 1), c >> 1) || (c && !wait(B_S, c - 1))) break;
+                const int L = min(C, job.len - c * C);
+                uint4 part[8];
+                if (row < L) {
+                    other_parts<MORE, NB / 2, NB>(sm.k[c & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part, nullptr);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                    for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, NB / 2, NB);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) part[i] = make_uint4(0, 0, 0, 0);
                 }
-                tmem_st16(lanes + T_P + 16 * b, pk);
+                __syncwarp();
+                if (!wait(B_P + c % NP, c / NP)) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(sm.k[c & 1] + piece_at(row, 8 * (NB / 2) + i)) = part[i];
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&sm.bar[B_K2]);
+            } else if (!wait(B_P + c % NP, c / NP)) {
+                break;
             }
+            tc_fence_after();
+            const uint32_t T_c = lanes + T_P + (NP == 2 ? (c & 1) * 128 : 0), T_A = T_c + 64;
+            uint32_t x[2][16], pk[8];
+            tmem_get(T_c + 32 * warp + 16, x[0]);
+            if (warp < 3) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pk[e] = 0u;
+#pragma unroll 1
+                for (int i = 2 * warp + 2; i < 8; ++i) tmem_put8(T_A + 8 * i, pk);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // columns 16 .. 31 of the diagonal's 32, then 0 .. 15
+                tmem_got(x[u]);
+                if (u == 0) tmem_get(T_c + 32 * warp, x[1]);
+                else if (warp) tmem_get(T_c + 32 * warp - 16, x[0]);
+                const int at = lane - (u ? 0 : 16);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2)
+                    pk[e / 2] = pack2(e <= at ? __uint_as_float(x[u][e]) * sm.diag[max(at - e, 0)] : 0.0f,
+                                      e + 1 <= at ? __uint_as_float(x[u][e + 1]) * sm.diag[max(at - e - 1, 0)] : 0.0f);
+                tmem_put8(T_A + 8 * (2 * warp + 1 - u), pk);
+            }
+            float rf = first;
+#pragma unroll 1
+            for (int i = 2 * warp - 1; i > 0; i -= 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    tmem_got(x[u]);
+                    if (u == 0 || i > 1) tmem_get(T_c + 16 * (i - u - 1), x[u ^ 1]);
+                    const uint64_t r2 = pair(rf, rf);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float lo, hi;
+                        unpair(mul2(pair(__uint_as_float(x[u][2 * e]), __uint_as_float(x[u][2 * e + 1])), mul2(col[e], r2)), lo, hi);
+                        pk[e] = pack2(lo, hi);
+                    }
+                    tmem_put8(T_A + 8 * (i - u), pk);
+                    rf *= step;
+                }
+            }
+            tmem_put_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(&sm.bar[B_A]);
         }
     } else if (warp < 8) {
-        fewer_registers<kOtherRegs>();
-        // the outputs: row i a thread
-        const float f2 = p.scale * power(l2, row + 1);
-        bf16 *y = static_cast<bf16 *>(p.y) + ((int64_t)(job.t0 + row) * p.H + h) * P;
-        for (int c = 0; c < nc; ++c, y += (int64_t)C * p.H * P) {
-            if (!wait(B_Y, c)) break;
+        fewer_registers<kOutRegs>();
+        // The outputs, row i a thread: the state's part, decayed, to where A V adds to it (so that it leaves its place for the next
+        // chunk's long before the outputs are done, and the queries theirs), and the sum through shared memory, whence whole chunks go as tiles.  (Stored from here, 32 rows apart in
+        // every instruction, they took 2000 cycles of the load and store unit a chunk.)
+        const float f = power(l2, row + 1);
+        const uint64_t f2 = pair(f, f), scale = pair(p.scale, p.scale);
+        for (int c = 0; c < nc; ++c) {
+            unsigned char *out = Smem::OWN_OUT ? sm.out : Smem::OUT_ON_V ? sm.v[c % NV] : sm.k[c & 1];
+            if (!wait(B_Y2, c)) break;
             tc_fence_after();
-            const bool live = c * C + row < job.len;
+            uint32_t a[2][16];
+            tmem_get(lanes + T_Y2, a[0]);
+#pragma unroll 1
+            for (int b = 0; b < P / 16; b += 2) {
 #pragma unroll
-            for (int b = 0; b < P / 32; ++b) {
-                float a[32], s[32];
-                tmem_ld32(lanes + T_Y + 32 * b, a);
-                tmem_ld32(lanes + T_Y2 + 32 * b, s);
-                if (b == P / 32 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(&sm.bar[B_YE]);
-                }
-                if (live) {
+                for (int u = 0; u < 2; ++u) {
+                    tmem_got(a[u]);
+                    if (u == 0 || b + 2 < P / 16) tmem_get(lanes + T_Y2 + 16 * (b + u + 1), a[u ^ 1]);
+                    uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = fmaf(f2, s[e + i], p.scale * a[e + i]);
-                        *reinterpret_cast<uint4 *>(y + 32 * b + e) = pack16(o);
+                    for (int e = 0; e < 16; e += 2) {
+                        float lo, hi;
+                        unpair(mul2(f2, pair(__uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]))), lo, hi);
+                        o[e] = __float_as_uint(lo), o[e + 1] = __float_as_uint(hi);
                     }
+                    tmem_put16(lanes + T_Y + 16 * (b + u), o);
                 }
             }
+            tmem_put_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(&sm.bar[B_M]);
+            if (Smem::OWN_OUT && warp == 4) bulk_wait_read<0>();  // (by the thread that issued the last tile)
+            if (outputs_sync_or(!wait(B_Y, c))) break;
+            tc_fence_after();
+            tmem_get(lanes + T_Y, a[0]);
+#pragma unroll 1
+            for (int b = 0; b < P / 16; b += 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    tmem_got(a[u]);
+                    if (u == 0 || b + 2 < P / 16) tmem_get(lanes + T_Y + 16 * (b + u + 1), a[u ^ 1]);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float lo, hi;
+                        unpair(mul2(scale, pair(__uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]))), lo, hi);
+                        o[e / 2] = pack2(lo, hi);
+                    }
+                    unsigned char *to = out + ((b + u) >> 2) * kBlk;
+                    *reinterpret_cast<uint4 *>(to + swz128_chunk(row, ((b + u) & 3) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(to + swz128_chunk(row, ((b + u) & 3) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            }
+            tc_fence_before();
+            fence_async_smem();
+            const int L = job.len - c * C;
+            if (outputs_sync_or(false)) break;
+            if (L >= C) {
+                if (warp == 4 && elect_one()) {
+#pragma unroll
+                    for (int b = 0; b < PB; ++b) tma_store_2d(&ymap, out + b * kBlk, h * P + 64 * b, job.t0 + c * C);
+                    bulk_commit();
+                    if (!Smem::OWN_OUT) {
+                        bulk_wait_read<0>();
+                        arrive(&sm.bar[Smem::OUT_ON_V ? B_VE + c % NV : B_KE + (c & 1)]);
+                    }
+                }
+                __syncwarp();
+            } else {  // the sequence's last tokens: the rows after them are another's
+                constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
+                const int ch = row % CH;
+                bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(job.t0 + c * C) * p.H + h) * P + ch * 8;
+                for (int t = row / CH; t < L; t += 128 / CH)
+                    *reinterpret_cast<uint4 *>(dst + (int64_t)t * p.H * P) =
+                        *reinterpret_cast<const uint4 *>(out + (ch >> 3) * kBlk + swz128_chunk(t, ch & 7));
+            }
         }
+        if (Smem::OWN_OUT && warp == 4) bulk_wait_read<0>();
     } else if (warp < 12) {
         // the state: key index n a thread (with N 64 the upper half hold zeros)
         more_registers<kStateRegs>();
         const int n = row;
         StateT *pool = static_cast<StateT *>(p.pool) + (int64_t)h * P * N + n;
-        const bool seeded = n < N && job.slot >= 0 && p.has_init && p.has_init[job.seq];
-        float S[P];
+        const bool seeded = n < N && job.seeded;
+        uint64_t S[P / 2];  // values 2 e and 2 e + 1
         {
             const float *from = entry_at(p, job.entry, h, P) + n;
             if (!seeded) {
 #pragma unroll
-                for (int e = 0; e < P; ++e) S[e] = 0.0f;
+                for (int e = 0; e < P / 2; ++e) S[e] = 0;
             } else if (job.last) {  // several segments: from the copy, since the last one's block writes the slot
 #pragma unroll
-                for (int e = 0; e < P; ++e) S[e] = from[e * 128];
+                for (int e = 0; e < P / 2; ++e) S[e] = pair(from[2 * e * 128], from[(2 * e + 1) * 128]);
             } else {
 #pragma unroll
-                for (int e = 0; e < P; ++e) S[e] = to_f32(pool[job.slot * p.stride + e * N]);
+                for (int e = 0; e < P / 2; ++e)
+                    S[e] = pair(to_f32(pool[job.slot * p.stride + 2 * e * N]), to_f32(pool[job.slot * p.stride + (2 * e + 1) * N]));
             }
             if (n < N && job.index) {
                 const float over = power(l2, p.seg_tokens);
+                const uint64_t over2 = pair(over, over);
 #pragma unroll 1
                 for (int r = 1; r <= job.index; ++r) {
                     from += (int64_t)p.H * (128 * P);
 #pragma unroll
-                    for (int e = 0; e < P; ++e) S[e] = fmaf(over, S[e], from[e * 128]);
+                    for (int e = 0; e < P / 2; ++e) S[e] = fma2(over2, S[e], pair(from[2 * e * 128], from[(2 * e + 1) * 128]));
                 }
             }
         }
@@ -332,20 +477,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 if (!wait(B_S, c)) break;
                 tc_fence_after();
                 const float over = c + 1 == nc ? part : whole;
+                const uint64_t over2 = pair(over, over);
+                tmem_pieces<P / 16>(lanes + T_D, [&](int i, const uint32_t (&d)[16]) {
 #pragma unroll
-                for (int b = 0; b < P / 32; ++b) {
-                    float d[32];
-                    tmem_ld32(lanes + T_D + 32 * b, d);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) S[32 * b + e] = fmaf(over, S[32 * b + e], d[e]);
-                }
+                    for (int e = 0; e < 8; ++e)
+                        S[8 * i + e] = fma2(over2, S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+                });
             }
             if (c + 1 < nc) {
                 if (n < N) {
 #pragma unroll
-                    for (int e = 0; e < P; e += 8) {
-                        const float f[8] = {S[e], S[e + 1], S[e + 2], S[e + 3], S[e + 4], S[e + 5], S[e + 6], S[e + 7]};
-                        *reinterpret_cast<uint4 *>(sm.sb + (e >> 6) * (N * 128) + swz128_chunk(n, (e >> 3) & 7)) = pack16(f);
+                    for (int e = 0; e < P / 2; e += 4) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float lo, hi;
+                            unpair(S[e + i], lo, hi);
+                            o[i] = pack2(lo, hi);
+                        }
+                        *reinterpret_cast<uint4 *>(sm.sb + (e >> 5) * (N * 128) + swz128_chunk(n, (e >> 2) & 7)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
                 fence_async_smem();
@@ -360,131 +511,140 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                     if (slot < 0 || n >= N) return;
                     StateT *to = pool + slot * p.stride;
 #pragma unroll
-                    for (int e = 0; e < P; ++e) to[e * N] = from_f32<StateT>(S[e]);
+                    for (int e = 0; e < P / 2; ++e) {
+                        float lo, hi;
+                        unpair(S[e], lo, hi);
+                        to[2 * e * N] = from_f32<StateT>(lo);
+                        to[(2 * e + 1) * N] = from_f32<StateT>(hi);
+                    }
                 };
                 if (ckpt >= 0) write(ckpt);
                 if (end) write(job.slot);
             }
         }
     } else if (warp < 16) {
-        fewer_registers<kOtherRegs>();
-        // K' in place of K, token j a thread; past the segment's end zeros, in V as well: the tiles hold another's tokens there
-        const float f = power(l2, C - 1 - row);
+        more_registers<kKeyRegs>();
+        // K', token j a thread: its other parts (with the scores' group, see there) once the chunk before is through with theirs,
+        // while the scores are formed, and the first in place of K when these have read it.  Past the segment's end zeros, in V as
+        // well: the tiles hold another's tokens there.
         for (int c = 0; c < nc; ++c) {
-            if (!wait(B_P, c)) break;  // the scores have read K
             const int L = min(C, job.len - c * C);
-            if (L == C) {
-                scale_row<NB, MORE>(sm.k[c & 1], sm.rest[0], row, f);
+            unsigned char *tile = sm.k[c & 1];
+            const Weight w(power(l2, max(L - 1 - row, 0)));
+            if (!wait(B_KF + (c & 1), c >> 1) || (c && !wait(B_S, c - 1))) break;
+            constexpr int OWN = HELP ? NB / 2 : NB;
+            uint4 first[8 * OWN];
+            if (row < L) {
+                other_parts<MORE, 0, OWN>(tile, sm.rest[0], row, w, first, nullptr);
             } else {
-                if (!wait(B_VF + c % NV, c / NV)) break;
-                if (row < L) {
-                    scale_row<NB, MORE>(sm.k[c & 1], sm.rest[0], row, power(l2, L - 1 - row));
-                } else {
-                    clear_row<NB>(sm.k[c & 1], row);
 #pragma unroll
-                    for (int m = 0; m < MORE; ++m) clear_row<NB>(sm.rest[m], row);
-                    clear_row<PB>(sm.v[c % NV], row);
-                }
+                for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, 0, OWN);
+#pragma unroll
+                for (int i = 0; i < 8 * OWN; ++i) first[i] = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+            if (!wait(B_P + c % NP, c / NP)) break;
+#pragma unroll
+            for (int i = 0; i < 8 * OWN; ++i) *reinterpret_cast<uint4 *>(tile + piece_at(row, i)) = first[i];
+            if (L < C) {
+                if (!wait(B_VF + c % NV, c / NV)) break;
+                if (row >= L) clear_row(sm.v[c % NV], row, 0, PB);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&sm.bar[B_K2]);
         }
-    } else if (warp == 16) {
+    } else if (warp != 17) {
         fewer_registers<kIssueRegs>();
-        const int g = h / p.HG;
-        int c = 0;
-        for (; c < nc; ++c) {
-            const int st = c & 1, use = c >> 1, qs = c % NQ, quse = c / NQ, vs = c % NV, vuse = c / NV, t = job.t0 + c * C;
-            if (use && !wait(B_KE + st, use - 1)) break;
+        // loads: of queries, keys and values, a warp each
+        const int stages = warp == 16 ? NQ : warp == 18 ? 2 : NV, full = warp == 16 ? B_QF : warp == 18 ? B_KF : B_VF,
+                  empty = warp == 16 ? B_QE : warp == 18 ? B_KE : B_VE, blocks = warp == 19 ? PB : NB,
+                  x = warp == 19 ? h * P : h / p.HG * N;
+        unsigned char *tiles = warp == 16 ? sm.q[0] : warp == 18 ? sm.k[0] : sm.v[0];
+        const uint32_t size = warp == 16 ? Smem::kQ : warp == 18 ? kTile : P * 256;
+        const CUtensorMap *map = warp == 16 ? &qmap : warp == 18 ? &kmap : &vmap;
+        int st = 0, use = 0;
+        for (; loaded < nc; ++loaded) {
+            if (use && !wait(empty + st, use - 1)) break;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&sm.bar[B_KF + st], NB * kBlk);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) tma_load_2d(sm.k[st] + b * kBlk, &kmap, g * N + 64 * b, t, &sm.bar[B_KF + st]);
+                mbar_arrive_expect_tx(&sm.bar[full + st], blocks * kBlk);
+                for (int b = 0; b < blocks; ++b)
+                    tma_load_2d(tiles + st * size + b * kBlk, map, x + 64 * b, job.t0 + loaded * C, &sm.bar[full + st]);
             }
             __syncwarp();
-            if (quse && !wait(B_QE + qs, quse - 1)) break;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&sm.bar[B_QF + qs], NB * kBlk);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) tma_load_2d(sm.q[qs] + b * kBlk, &qmap, g * N + 64 * b, t, &sm.bar[B_QF + qs]);
-            }
-            __syncwarp();
-            if (vuse && !wait(B_VE + vs, vuse - 1)) break;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&sm.bar[B_VF + vs], PB * kBlk);
-#pragma unroll
-                for (int b = 0; b < PB; ++b) tma_load_2d(sm.v[vs] + b * kBlk, &vmap, h * P + 64 * b, t, &sm.bar[B_VF + vs]);
-            }
-            __syncwarp();
+            if (++st == stages) st = 0, ++use;
         }
-        loaded = c;
-    } else if (warp == 17) {
+        in_flight = full, of = stages;
+    } else {
         fewer_registers<kIssueRegs>();
         constexpr uint32_t ID_P = idesc_bf16(128, 128, false, false), ID_S = idesc_bf16(128, P, true, true),
                            ID_Y = idesc_bf16(128, P, false, true);
-        for (int c = 0; c < nc; ++c) {
-            const int st = c & 1, use = c >> 1, qs = c % NQ, vs = c % NV;
-            const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), v = smem_u32(sm.v[vs]), sb = smem_u32(sm.sb);
-            if (!wait(B_KF + st, use) || !wait(B_QF + qs, c / NQ)) break;
-            if (c && !wait(B_Y, c - 1)) break;  // A, which lies where the scores go, is read
+        constexpr bool AHEAD = NP == 2;  // whether the next chunk's scores go before this one's outputs
+        auto scores = [&](int c) {
+            const int st = c & 1, qs = c % NQ;
+            if (!wait(B_KF + st, c >> 1) || !wait(B_QF + qs, c / NQ)) return false;
+            if (c >= NP && !wait(B_Y, c - NP)) return false;  // A, which lies where the scores go, is read
             tc_fence_after();
             if (elect_one()) {
+                const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), to = tm + T_P + (NP == 2 ? (c & 1) * 128 : 0);
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) mma_bf16(tm + T_P, desc_kmajor(q, kBlk, kk), desc_kmajor(k, kBlk, kk), ID_P, kk > 0);
-                mma_commit(&sm.bar[B_P]);
+                for (int kk = 0; kk < N / 16; ++kk) mma_bf16(to, desc_kmajor(q, kBlk, kk), desc_kmajor(k, kBlk, kk), ID_P, kk > 0);
+                mma_commit(&sm.bar[B_P + c % NP]);
             }
             __syncwarp();
-            if (!wait(B_SB, c) || (c && !wait(B_YE, c - 1))) break;
-            tc_fence_after();
-            if (elect_one()) {
+            return true;
+        };
+        if (scores(0))
+            for (int c = 0; c < nc; ++c) {
+                const int st = c & 1, qs = c % NQ, vs = c % NV;
+                const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), v = smem_u32(sm.v[vs]), sb = smem_u32(sm.sb);
+                if (!wait(B_SB, c) || (c && !wait(B_M, c - 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk)
-                    mma_bf16(tm + T_Y2, desc_kmajor(q, kBlk, kk), desc_mnmajor(sb, N * 128, kk), ID_Y, kk > 0);
-                mma_commit(&sm.bar[B_QE + qs]);
-            }
-            __syncwarp();
-            if (!wait(B_K2, c) || !wait(B_VF + vs, c / NV)) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int m = MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
-                    const uint32_t part = m ? smem_u32(sm.rest[m - 1]) : k;
-#pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_bf16(tm + T_D, desc_mnmajor(part, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, m < MORE || kk > 0);
+                    for (int kk = 0; kk < N / 16; ++kk)
+                        mma_bf16(tm + T_Y2, desc_kmajor(q, kBlk, kk), desc_mnmajor(sb, N * 128, kk), ID_Y, kk > 0);
+                    mma_commit(&sm.bar[B_QE + qs]);
+                    mma_commit(&sm.bar[B_Y2]);
                 }
-                mma_commit(&sm.bar[B_S]);
-                mma_commit(&sm.bar[B_KE + st]);
-            }
-            __syncwarp();
-            if (!wait(B_A, c)) break;
-            tc_fence_after();
-            if (elect_one()) {
+                __syncwarp();
+                if (!wait(B_K2, c) || !wait(B_VF + vs, c / NV)) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    mma_bf16_ts(tm + T_Y, tm + T_P + 8 * kk, desc_mnmajor(v, kBlk, kk), ID_Y, kk > 0);
-                mma_commit(&sm.bar[B_Y]);
-                mma_commit(&sm.bar[B_VE + vs]);
+                    for (int m = MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
+                        const uint32_t part = m ? smem_u32(sm.rest[m - 1]) : k;
+#pragma unroll
+                        for (int kk = 0; kk < C / 16; ++kk)
+                            mma_bf16(tm + T_D, desc_mnmajor(part, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, m < MORE || kk > 0);
+                    }
+                    mma_commit(&sm.bar[B_S]);
+                    if (!Smem::OUT_ON_K) mma_commit(&sm.bar[B_KE + st]);  // (else the outputs go there first)
+                }
+                __syncwarp();
+                if (AHEAD && c + 1 < nc && !scores(c + 1)) break;
+                if (!wait(B_A, c) || !wait(B_M, c)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t a = tm + T_P + (NP == 2 ? (c & 1) * 128 : 0) + 64;
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ts(tm + T_Y, a + 8 * kk, desc_mnmajor(v, kBlk, kk), ID_Y, 1);
+                    mma_commit(&sm.bar[B_Y]);
+                    if (!Smem::OUT_ON_V) mma_commit(&sm.bar[B_VE + vs]);
+                }
+                __syncwarp();
+                if (!AHEAD && c + 1 < nc && !scores(c + 1)) break;
             }
-            __syncwarp();
-        }
         if (elect_one()) mma_commit(&sm.bar[B_END]);
         __syncwarp();
         drain(&sm.bar[B_END], 0);
-    } else {
-        fewer_registers<kIssueRegs>();  // (a group's registers go together)
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (sm.failed) {  // loads that nothing has waited for end before the block does: those of the last chunks
-        if (warp == 16)
-            for (int i = max(0, loaded - 2); i <= min(loaded, nc - 1); ++i) {
-                drain(&sm.bar[B_KF + (i & 1)], (i >> 1) & 1);
-                drain(&sm.bar[B_QF + i % NQ], (i / NQ) & 1);
-                drain(&sm.bar[B_VF + i % NV], (i / NV) & 1);
-            }
+    if (sm.failed) {  // loads that nothing has waited for end before the block does
+        if (in_flight >= 0)
+            for (int i = max(0, loaded - of); i < loaded; ++i) drain(&sm.bar[in_flight + i % of], (i / of) & 1);
         if (tid == 0) flag_error(p.err, MAMBA_ERR_TIMEOUT);
         __syncthreads();
     }
@@ -502,7 +662,7 @@ static_assert(kSumRegs + 2 * kScaleRegs + kSegIssueRegs <= 4 * kSegRegs, "regist
 
 template <int P, bool F32S>
 struct SegSmem {
-    static constexpr int MORE = F32S ? 2 : 1, GROUPS = P == 128 && F32S ? 1 : 2;  // groups: of warps for the keys' decays
+    static constexpr int MORE = F32S ? 2 : 1, GROUPS = P == 128 && F32S ? 1 : 2;  // places for a chunk's other parts
     unsigned char k[2][kTile], v[2][P * 256], rest[GROUPS][MORE][kTile];
     uint64_t bar[kSegBars];
     uint32_t tmem;
@@ -522,8 +682,9 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & 127;
-    const Job job = find_job(p, blockIdx.x / p.H);
-    if (!job.ok || job.index == job.last) return;
+    const int which = blockIdx.x / p.H;
+    const Segment job = meta_segments(p)[min(which, p.max_segs - 1)];
+    if (which >= p.meta[0] || job.slot < -1 || job.index == job.last) return;
     const float l2 = p.log_decay[h] * LOG2E;
     if (N == 64)
         for (int i = tid; i < (int)kBlk / 16; i += kSegThreads) {
@@ -533,7 +694,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
             for (int s = 0; s < GROUPS * MORE; ++s) reinterpret_cast<uint4 *>(sm.rest[s / MORE][s % MORE] + kBlk)[i] = make_uint4(0, 0, 0, 0);
         }
     if (warp == 12 && elect_one()) {
-        for (int i = 0; i < kSegBars; ++i) mbar_init(&sm.bar[i], (i >= G_K2 && i < G_D) || (i >= G_DE && i < G_END) ? 4 : 1);
+        for (int i = 0; i < kSegBars; ++i) mbar_init(&sm.bar[i], i >= G_K2 && i < G_D && GROUPS == 1 && NB == 2 ? 8 : (i >= G_K2 && i < G_D) || (i >= G_DE && i < G_END) ? 4 : 1);
         fence_mbar_init();
         sm.failed = 0;
     }
@@ -547,48 +708,49 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
     tc_fence_after();
     const uint32_t tm = sm.tmem;
     volatile int *failed = &sm.failed;
-    const int nc = job.nc;  // (whole chunks: the segment is not the sequence's last)
+    const int nc = job.len / C;  // (whole chunks: the segment is not the sequence's last)
     int loaded = 0;
     auto wait = [&](int b, uint32_t use) { return warp_wait(&sm.bar[b], use & 1, failed); };
     if (warp < 8) {
         fewer_registers<kScaleRegs>();
+        // Where there is room for two chunks' other parts the groups take chunks in turn, else half of each chunk's keys.  A place
+        // is free once the product of its last chunk is done: two chunks ago, for which the load of this one has waited, or one.
+        constexpr bool TURNS = GROUPS == 2 || NB == 1;
         const int group = warp >> 2;
-        for (int c = group; c < nc && group < GROUPS; c += GROUPS) {
+        for (int c = TURNS ? group : 0; c < nc && group < (TURNS ? GROUPS : 2); c += TURNS ? GROUPS : 1) {
             const int st = c & 1;
-            const float f = power(l2, job.len - 1 - (c * C + row));
+            const Weight w(power(l2, job.len - 1 - (c * C + row)));
             if (!wait(G_F + st, c >> 1)) break;
-            // The other parts' place is the group's: free once the product of its last chunk is done.  Where groups take
-            // turns that was two chunks ago, and the load of this chunk has waited for it.
             if (GROUPS == 1 && c && !wait(G_E + (c - 1 & 1), (c - 1) >> 1)) break;
-            scale_row<NB, MORE>(sm.k[st], sm.rest[group % GROUPS][0], row, f);
+            unsigned char *k = sm.k[st], *rest = sm.rest[c % GROUPS][0];
+            if (TURNS) other_parts<MORE, 0, NB>(k, rest, row, w, nullptr, k);
+            else if (group == 0) other_parts<MORE, 0, NB / 2>(k, rest, row, w, nullptr, k);
+            else other_parts<MORE, NB / 2, NB>(k, rest, row, w, nullptr, k);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) arrive(&sm.bar[G_K2 + st]);
         }
     } else if (warp < 12) {
         more_registers<kSumRegs>();
-        if (job.index == 0 && row < N && job.slot >= 0 && p.has_init && p.has_init[job.seq]) {
+        if (job.index == 0 && row < N && job.seeded) {
             float *to = entry_at(p, job.entry, h, P) + row;
             const StateT *from = static_cast<const StateT *>(p.pool) + job.slot * p.stride + (int64_t)h * P * N + row;
 #pragma unroll 16
             for (int e = 0; e < P; ++e) to[e * 128] = to_f32(from[e * N]);
         }
-        float S[P];
+        uint64_t S[P / 2];  // values 2 e and 2 e + 1
 #pragma unroll
-        for (int e = 0; e < P; ++e) S[e] = 0.0f;
+        for (int e = 0; e < P / 2; ++e) S[e] = 0;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         int c = 0;
         for (; c < nc; ++c) {
             const int st = c & 1;
             if (!wait(G_D + st, c >> 1)) break;
             tc_fence_after();
+            tmem_pieces<P / 16>(lanes + 128 * st, [&](int i, const uint32_t (&d)[16]) {
 #pragma unroll
-            for (int b = 0; b < P / 32; ++b) {
-                float d[32];
-                tmem_ld32(lanes + 128 * st + 32 * b, d);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) S[32 * b + e] += d[e];
-            }
+                for (int e = 0; e < 8; ++e) S[8 * i + e] = add2(S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+            });
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(&sm.bar[G_DE + st]);
@@ -596,7 +758,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
         if (c == nc) {
             float *to = entry_at(p, job.entry + 1 + job.index, h, P) + row;
 #pragma unroll
-            for (int e = 0; e < P; ++e) to[e * 128] = S[e];
+            for (int e = 0; e < P / 2; ++e) unpair(S[e], to[2 * e * 128], to[(2 * e + 1) * 128]);
         }
     } else if (warp == 12) {
         fewer_registers<kSegIssueRegs>();
@@ -677,9 +839,9 @@ bool ready(const void *kern, size_t smem, int regs) {
 
 template <int P, int N, bool F32S>
 int launch(const ScanParams &p, cudaStream_t st) {
-    CUtensorMap qmap, kmap, vmap;
+    CUtensorMap qmap, kmap, vmap, ymap;
     if (!tile_map(&qmap, p.q, (int64_t)p.G * N, p.T, p.qs) || !tile_map(&kmap, p.k, (int64_t)p.G * N, p.T, p.ks) ||
-        !tile_map(&vmap, p.v, (int64_t)p.H * P, p.T, p.vs))
+        !tile_map(&vmap, p.v, (int64_t)p.H * P, p.T, p.vs) || !tile_map(&ymap, p.y, (int64_t)p.H * P, p.T, (int64_t)p.H * P))
         return MAMBA_ECUDA;
     const dim3 grid((unsigned)((int64_t)p.max_segs * p.H));
     if (p.seg_tokens < kWhole) {
@@ -690,10 +852,10 @@ int launch(const ScanParams &p, cudaStream_t st) {
         if (launch_pdl(kern, grid, dim3(kSegThreads), smem, st, p, kmap, vmap) != cudaSuccess) return MAMBA_ECUDA;
     }
     auto kern = k_la_chain<P, N, F32S>;
-    constexpr size_t smem = sizeof(ChainSmem<P, F32S>) + 1024;
+    constexpr size_t smem = sizeof(ChainSmem<P, N, F32S>) + 1024;
     static_assert(smem <= 232448, "shared memory of a block");
     if (!ready(reinterpret_cast<const void *>(kern), smem, kRegs)) return MAMBA_ECUDA;
-    if (launch_pdl(kern, grid, dim3(kThreads), smem, st, p, qmap, kmap, vmap) != cudaSuccess) return MAMBA_ECUDA;
+    if (launch_pdl(kern, grid, dim3(kThreads), smem, st, p, qmap, kmap, vmap, ymap) != cudaSuccess) return MAMBA_ECUDA;
     return launch_status();
 }
 
