@@ -56,50 +56,83 @@ __device__ __forceinline__ float2 turned(uint64_t t, int32_t pos) {
     return r;
 }
 
-// One row's norm and rotation in registers: a lane holds 8 consecutive values of N, LPR = N / 8 lanes a row.
-// w: the lane's 8 weights; table: cosine and sine of the row's `half` angles.  All 32 lanes take part.
-template <int N>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], const float (&w)[8], const QkPrep &p, const float2 *table, int lane) {
-    constexpr int LPR = N / 8;
+// One row's norm and rotation in registers, N / (2 V) lanes a row, 2 V values a lane: V from `a` and V from `b` of the row.
+// Where halves are rotated against each other these are the two halves of V pairs, so that no lane needs another's
+// values but for the sum of squares; elsewhere b is a + V.  Either way lane idx turns the angles V idx .. V idx + V - 1.
+template <int V>
+struct LaneRow {
+    int a, b, angle;
+    bool turns;  // whether this lane's values are among those rotated
+    __device__ __forceinline__ LaneRow(const QkPrep &p, int idx) : angle(V * idx), turns(V * idx < p.half) {
+        const bool halves = turns && !p.inter;
+        a = halves ? V * idx : 2 * V * idx;
+        b = halves ? p.half + V * idx : 2 * V * idx + V;
+    }
+};
+// w: the lane's weights; t: cosines and sines of its angles.  All lanes of the row take part.
+template <int N, int V>
+__device__ __forceinline__ void norm_rotate(float (&x)[2 * V], const float (&w)[2 * V], const QkPrep &p, const float2 (&t)[V],
+                                            const LaneRow<V> &l) {
     if (p.norm) {
         float ss = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(sum_lanes<LPR>(ss) * (1.0f / N) + p.eps);
+        for (int e = 0; e < 2 * V; ++e) ss = fmaf(x[e], x[e], ss);
+        const float r = rsqrtf(sum_lanes<N / (2 * V)>(ss) * (1.0f / N) + p.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
+        for (int e = 0; e < 2 * V; ++e) x[e] *= r * w[e];
     }
-    if (p.half) {
-        const int idx = lane & (LPR - 1);
-        if (p.inter) {
-            if (idx * 4 < p.half) {
+    auto turn = [](float &u, float &v, float2 t) {
+        const float a = u, b = v;
+        u = a * t.x - b * t.y;
+        v = b * t.x + a * t.y;
+    };
+    if (l.turns && p.inter) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 t = table[idx * 4 + e];
-                    const float a = x[2 * e], b = x[2 * e + 1];
-                    x[2 * e] = a * t.x - b * t.y;
-                    x[2 * e + 1] = b * t.x + a * t.y;
-                }
-            }
+        for (int e = 0; e < V; ++e) turn(x[2 * e], x[2 * e + 1], t[e]);
+    } else if (l.turns) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) turn(x[e], x[V + e], t[e]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void norm_weights(const float *w, const LaneRow<V> &l, float (&to)[2 * V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        to[e] = w ? __ldg(w + l.a + e) : 1.0f;
+        to[V + e] = w ? __ldg(w + l.b + e) : 1.0f;
+    }
+}
+// V values, as they are stored, and in fp32.
+template <typename T, int V> struct Some;
+template <int V> struct Some<bf16, V> {
+    uint2 v[V / 4];
+    __device__ __forceinline__ void load(const bf16 *p) {
+        if constexpr (V == 8) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+            v[0] = make_uint2(x.x, x.y), v[1] = make_uint2(x.z, x.w);
         } else {
-            const int far = p.half / 8;  // lanes between the halves of a pair
-            const bool first = idx < far, in = idx < 2 * far;
-            const int with = in ? (first ? lane + far : lane - far) : lane;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float o = __shfl_sync(0xffffffffu, x[e], with);
-                const float2 t = in ? table[(first ? idx : idx - far) * 8 + e] : make_float2(1.0f, 0.0f);
-                x[e] = first ? x[e] * t.x - o * t.y : (in ? x[e] * t.x + o * t.y : x[e]);
-            }
+            v[0] = *reinterpret_cast<const uint2 *>(p);
         }
     }
-}
-
-template <int N>
-__device__ __forceinline__ void norm_weights(const float *w, int lane, float (&to)[8]) {
+    __device__ __forceinline__ void get(float *f) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) to[e] = w ? __ldg(w + (lane & (N / 8 - 1)) * 8 + e) : 1.0f;
-}
+        for (int i = 0; i < V / 4; ++i) {
+            f[4 * i] = __uint_as_float(v[i].x << 16), f[4 * i + 1] = __uint_as_float(v[i].x & 0xffff0000u);
+            f[4 * i + 2] = __uint_as_float(v[i].y << 16), f[4 * i + 3] = __uint_as_float(v[i].y & 0xffff0000u);
+        }
+    }
+};
+template <int V> struct Some<float, V> {
+    float4 v[V / 4];
+    __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) v[i] = reinterpret_cast<const float4 *>(p)[i];
+    }
+    __device__ __forceinline__ void get(float *f) const {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) f[4 * i] = v[i].x, f[4 * i + 1] = v[i].y, f[4 * i + 2] = v[i].z, f[4 * i + 3] = v[i].w;
+    }
+};
 
 // The checks of a call's norm and rotation.
 inline int check_prep(int N, int32_t qk_norm, float eps, const int32_t *pos, const float *inv_freq, int32_t rot_dim) {

@@ -42,7 +42,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_la_plan(const ScanParams p) {
         }
         return;
     }
-    auto segments = [&](int s) { return (int)(((int64_t)p.cu[s + 1] - p.cu[s] + p.seg_tokens - 1) / p.seg_tokens); };
+    auto segments = [&](int s) {  // none of a sequence whose slot is bad: it is left untouched
+        const int32_t sl = p.slot[s];
+        return sl < -1 || sl >= p.num_slots ? 0 : (int)(((int64_t)p.cu[s + 1] - p.cu[s] + p.seg_tokens - 1) / p.seg_tokens);
+    };
     // longest first: place 0 is for the longest
     auto rank = [&](int tokens) { return kPlanThreads - 1 - min(kPlanThreads - 1, tokens / kChunk); };
     auto tokens_of = [&](int s, int i) { return min(p.seg_tokens, p.cu[s + 1] - p.cu[s] - i * p.seg_tokens); };
@@ -81,12 +84,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_la_plan(const ScanParams p) {
         for (int i = 0; i < m; ++i) {  // (the order among equals is not fixed, and no result depends on it)
             const int to = atomicAdd(&place[rank(tokens_of(s, i))], 1);
             const int32_t sl = p.slot[s];
-            const bool in = sl >= -1 && sl < p.num_slots;
-            out[to] = {s, i, m - 1, at + s, p.cu[s] + i * p.seg_tokens, tokens_of(s, i), in ? sl : -2, in && sl >= 0 && p.has_init && p.has_init[s]};
+            out[to] = {s, i, m - 1, at + s, p.cu[s] + i * p.seg_tokens, tokens_of(s, i), sl, sl >= 0 && p.has_init && p.has_init[s]};
         }
         at += m;
     }
-    if (tid == 0) p.meta[0] = total;
+    if (tid == 0) p.meta[0] = total, p.meta[1] = 0;
 }
 
 // Block (head and share of its rows, sequence in the plan's order).
@@ -100,12 +102,11 @@ __global__ void __launch_bounds__(32 * WARPS) k_la_tokens(const ScanParams p) {
     __shared__ float vs[kStage][ROWS];
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
-    if ((int)blockIdx.y >= p.meta[0]) return;  // no such sequence: empty ones, or cu_seqlens refused (flagged)
+    if ((int)blockIdx.y >= p.meta[0]) return;  // no such sequence: empty ones, bad slots, cu_seqlens refused (flagged)
     const Segment job = meta_segments(p)[blockIdx.y];  // (the whole sequence)
     const int h = blockIdx.x / SPLITS, split = blockIdx.x % SPLITS, grp = h / p.HG;
     const int s = job.seq, t0 = job.t0, len = job.len;
     const int32_t slot = job.slot;
-    if (slot < -1) return;  // bad slot (flagged)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sub = lane / Map::LPR, idx = (lane & (Map::LPR - 1)) / Map::SHARE;
     const int col = (lane & (SL - 1)) * 8, own = (lane & (Map::LPR - 1)) * 8;  // of staging, of the state

@@ -14,7 +14,7 @@ struct __align__(16) Segment {
     int32_t seq, index, last;  // of which sequence, which one of it, and the sequence's last one's index
     int32_t entry;             // the sequence's first entry in the workspace
     int32_t t0, len;           // first token, tokens
-    int32_t slot;              // the sequence's, -2 where it is outside the pool
+    int32_t slot;              // the sequence's
     int32_t seeded;            // whether the sequence starts from its slot's state
 };
 
@@ -34,7 +34,7 @@ struct ScanParams {
     int32_t *err;
     int seg_tokens;  // tokens of a whole segment, a multiple of kChunk
     int max_segs;    // segments of the batch, at most
-    int32_t *meta;   // workspace: [segments, pad x3, Segment[max_segs]]
+    int32_t *meta;   // workspace: [segments, units given out past the first of each block, pad x2, Segment[max_segs]]
     float *ws;       // workspace of the chunked form, past meta
 };
 

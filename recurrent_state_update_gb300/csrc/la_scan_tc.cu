@@ -28,6 +28,7 @@ using namespace umma;
 namespace {
 
 constexpr int C = kChunk;
+constexpr int kSMs = 152;
 constexpr int kWhole = 1 << 30;               // tokens of a segment where sequences are not cut
 constexpr uint32_t kPolls = umma::kWaitPolls;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -182,8 +183,10 @@ enum {
     B_S,       // V^T K' is there
     B_SB,      // ... and added, and the state's copy is written (phase 0: before the first chunk)
     B_END,     // every product has finished
-    kBars
+    B_U,       // a unit is given out, by turn
+    kBars = B_U + 8
 };
+constexpr int kRing = 8;
 // Groups of 4 warps: for A, for outputs, for the state, for the keys' decays, and one of which a warp loads and another issues the
 // products.  The state's group takes registers from the others, within what the launch gave the block: 5 warps a scheduler
 // leave 96 a thread (launch() checks that the compiler made it so).
@@ -223,12 +226,38 @@ struct ChainSmem {
     static constexpr bool OWN_OUT = P == 64 || N == 64, OUT_ON_V = !OWN_OUT && NV == 2, OUT_ON_K = !OWN_OUT && !OUT_ON_V;
     static constexpr uint32_t kQ = N * 256, kSb = P * N * 2, kOut = OWN_OUT ? P * 256 : 1024;
     unsigned char q[NQ][kQ], k[2][kTile], v[NV][P * 256], sb[kSb], rest[MORE][kTile], out[kOut];
-    float diag[32];  // d^m
+    float diag[4][32];  // d^m, for each of the scores' warps
+    int32_t ring[kRing];   // units given out, by turn
     uint64_t bar[kBars];
     uint32_t tmem;
     int failed;
 };
 
+
+// The segments and heads that a block works on, the longest first: the first by the block's index, each further one taken from
+// the grid's counter by the warp that loads keys with the last of its loads for the unit before, and passed on through shared
+// memory.  (Given out beforehand, in turn there and back, they took 512 sequences of narrow heads 148 us; taken a unit ahead,
+// 256 ragged ones 238 us instead of 190.)
+struct Units {
+    const ScanParams &p;
+    const int32_t *ring;
+    uint64_t *bar;
+    volatile int *failed;
+    int total, k, h;  // h: the head of the last one given
+    __device__ __forceinline__ Units(const ScanParams &q, const int32_t *ring, uint64_t *bar, volatile int *failed)
+        : p(q), ring(ring), bar(bar), failed(failed), total(q.meta[0] * q.H), k(0), h(0) {}
+    __device__ __forceinline__ bool at(int i, Segment &job) {
+        if ((uint32_t)i >= (uint32_t)total) return false;
+        job = meta_segments(p)[i / p.H];
+        h = i % p.H;
+        return true;
+    }
+    __device__ __forceinline__ bool next(Segment &job) {
+        const int at_ring = k % kRing, use = k / kRing;  // (the first is not passed on: the k-th after it is the ring's k - 1st)
+        ++k;
+        return warp_wait(&bar[at_ring], use & 1, failed) && at(ring[at_ring], job);
+    }
+};
 
 template <int P, int N, bool F32S>
 __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, const __grid_constant__ CUtensorMap qmap,
@@ -248,12 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     Smem &sm = *align1024<Smem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
-    const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int which = blockIdx.x / p.H;
-    const Segment job = meta_segments(p)[min(which, p.max_segs - 1)];
-    if (which >= p.meta[0] || job.slot < -1) return;  // no such segment, or its slot is bad (flagged)
-    const float l2 = p.log_decay[h] * LOG2E;
-    if (tid < 32) sm.diag[tid] = power(l2, tid);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *failed = &sm.failed;
+    Units units(p, sm.ring, &sm.bar[B_U], failed);
+    Segment job;
+    if (!units.at(blockIdx.x, job)) return;
     if (N == 64)  // the keys' lanes without keys: products read them
         for (int i = tid; i < (int)kBlk / 16; i += kThreads) {
 #pragma unroll
@@ -276,304 +304,341 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sm.tmem;
-    volatile int *failed = &sm.failed;
-    const int nc = (job.len + C - 1) / C;
     auto wait = [&](int b, uint32_t use) { return warp_wait(&sm.bar[b], use & 1, failed); };
     const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const int row = tid & 127;
     int loaded = 0, in_flight = -1, of = 1;  // what this warp has loaded, and the first barrier of its stages
+    int g = 0;                               // chunks before this one, of all the block's segments
+    bool ok = true;                          // no wait has given up
 
     if (warp < 4) {
         fewer_registers<kScoreRegs>();
         // A: row i a thread, in pieces of 16 columns j, from the diagonal's two to the left.  There d^(i-j) is
         // d^(i-j0-15) * d^(15-(j-j0)), neither of which can overflow.  A lies from column 64 on, where scores stood that have
         // been read by the time.
-        uint64_t col[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) col[e] = pair(power(l2, 15 - 2 * e), power(l2, 14 - 2 * e));
-        const float step = power(l2, 16), first = power(l2, lane + 1);
-        for (int c = 0; c < nc; ++c) {
-            if (HELP) {  // three parts of K' take the keys' group longer than the scores take to come: the second block is done here
-                if (!wait(B_KF + (c & 1), c >> 1) || (c && !wait(B_S, c - 1))) break;
-                const int L = min(C, job.len - c * C);
-                uint4 part[8];
-                if (row < L) {
-                    other_parts<MORE, NB / 2, NB>(sm.k[c & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part, nullptr);
-                } else {
-#pragma unroll
-                    for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, NB / 2, NB);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) part[i] = make_uint4(0, 0, 0, 0);
-                }
-                __syncwarp();
-                if (!wait(B_P + c % NP, c / NP)) break;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(sm.k[c & 1] + piece_at(row, 8 * (NB / 2) + i)) = part[i];
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive(&sm.bar[B_K2]);
-            } else if (!wait(B_P + c % NP, c / NP)) {
-                break;
-            }
-            tc_fence_after();
-            const uint32_t T_c = lanes + T_P + (NP == 2 ? (c & 1) * 128 : 0), T_A = T_c + 64;
-            uint32_t x[2][16], pk[8];
-            tmem_get(T_c + 32 * warp + 16, x[0]);
-            if (warp < 3) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pk[e] = 0u;
-#pragma unroll 1
-                for (int i = 2 * warp + 2; i < 8; ++i) tmem_put8(T_A + 8 * i, pk);
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {  // columns 16 .. 31 of the diagonal's 32, then 0 .. 15
-                tmem_got(x[u]);
-                if (u == 0) tmem_get(T_c + 32 * warp, x[1]);
-                else if (warp) tmem_get(T_c + 32 * warp - 16, x[0]);
-                const int at = lane - (u ? 0 : 16);
-#pragma unroll
-                for (int e = 0; e < 16; e += 2)
-                    pk[e / 2] = pack2(e <= at ? __uint_as_float(x[u][e]) * sm.diag[max(at - e, 0)] : 0.0f,
-                                      e + 1 <= at ? __uint_as_float(x[u][e + 1]) * sm.diag[max(at - e - 1, 0)] : 0.0f);
-                tmem_put8(T_A + 8 * (2 * warp + 1 - u), pk);
-            }
-            float rf = first;
-#pragma unroll 1
-            for (int i = 2 * warp - 1; i > 0; i -= 2) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    tmem_got(x[u]);
-                    if (u == 0 || i > 1) tmem_get(T_c + 16 * (i - u - 1), x[u ^ 1]);
-                    const uint64_t r2 = pair(rf, rf);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float lo, hi;
-                        unpair(mul2(pair(__uint_as_float(x[u][2 * e]), __uint_as_float(x[u][2 * e + 1])), mul2(col[e], r2)), lo, hi);
-                        pk[e] = pack2(lo, hi);
-                    }
-                    tmem_put8(T_A + 8 * (i - u), pk);
-                    rf *= step;
-                }
-            }
-            tmem_put_wait();
-            tc_fence_before();
+        do {
+            const float l2 = p.log_decay[units.h] * LOG2E;
+            sm.diag[warp][lane] = power(l2, lane);
             __syncwarp();
-            if (lane == 0) arrive(&sm.bar[B_A]);
-        }
+            const float *diag = sm.diag[warp];
+            uint64_t col[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) col[e] = pair(power(l2, 15 - 2 * e), power(l2, 14 - 2 * e));
+            const float step = power(l2, 16), first = power(l2, lane + 1);
+            for (int left = job.len; left > 0; left -= C, ++g) {
+                if (HELP) {  // three parts of K' take the keys' group longer than the scores take to come: the second block is done here
+                    if (!(ok = wait(B_KF + (g & 1), g >> 1) && (!g || wait(B_S, g - 1)))) break;
+                    const int L = min(C, left);
+                    uint4 part[8];
+                    if (row < L) {
+                        other_parts<MORE, NB / 2, NB>(sm.k[g & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part, nullptr);
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, NB / 2, NB);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) part[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                    if (!(ok = wait(B_P + g % NP, g / NP))) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(sm.k[g & 1] + piece_at(row, 8 * (NB / 2) + i)) = part[i];
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(&sm.bar[B_K2]);
+                } else if (!(ok = wait(B_P + g % NP, g / NP))) {
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t T_c = lanes + T_P + (NP == 2 ? (g & 1) * 128 : 0), T_A = T_c + 64;
+                uint32_t x[2][16], pk[8];
+                tmem_get(T_c + 32 * warp + 16, x[0]);
+                if (warp < 3) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pk[e] = 0u;
+#pragma unroll 1
+                    for (int i = 2 * warp + 2; i < 8; ++i) tmem_put8(T_A + 8 * i, pk);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {  // columns 16 .. 31 of the diagonal's 32, then 0 .. 15
+                    tmem_got(x[u]);
+                    if (u == 0) tmem_get(T_c + 32 * warp, x[1]);
+                    else if (warp) tmem_get(T_c + 32 * warp - 16, x[0]);
+                    const int at = lane - (u ? 0 : 16);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2)
+                        pk[e / 2] = pack2(e <= at ? __uint_as_float(x[u][e]) * diag[max(at - e, 0)] : 0.0f,
+                                          e + 1 <= at ? __uint_as_float(x[u][e + 1]) * diag[max(at - e - 1, 0)] : 0.0f);
+                    tmem_put8(T_A + 8 * (2 * warp + 1 - u), pk);
+                }
+                float rf = first;
+#pragma unroll 1
+                for (int i = 2 * warp - 1; i > 0; i -= 2) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        tmem_got(x[u]);
+                        if (u == 0 || i > 1) tmem_get(T_c + 16 * (i - u - 1), x[u ^ 1]);
+                        const uint64_t r2 = pair(rf, rf);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float lo, hi;
+                            unpair(mul2(pair(__uint_as_float(x[u][2 * e]), __uint_as_float(x[u][2 * e + 1])), mul2(col[e], r2)), lo, hi);
+                            pk[e] = pack2(lo, hi);
+                        }
+                        tmem_put8(T_A + 8 * (i - u), pk);
+                        rf *= step;
+                    }
+                }
+                tmem_put_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(&sm.bar[B_A]);
+            }
+        } while (ok && units.next(job));
     } else if (warp < 8) {
         fewer_registers<kOutRegs>();
         // The outputs, row i a thread: the state's part, decayed, to where A V adds to it (so that it leaves its place for the next
-        // chunk's long before the outputs are done, and the queries theirs), and the sum through shared memory, whence whole chunks go as tiles.  (Stored from here, 32 rows apart in
-        // every instruction, they took 2000 cycles of the load and store unit a chunk.)
-        const float f = power(l2, row + 1);
-        const uint64_t f2 = pair(f, f), scale = pair(p.scale, p.scale);
-        for (int c = 0; c < nc; ++c) {
-            unsigned char *out = Smem::OWN_OUT ? sm.out : Smem::OUT_ON_V ? sm.v[c % NV] : sm.k[c & 1];
-            if (!wait(B_Y2, c)) break;
-            tc_fence_after();
-            uint32_t a[2][16];
-            tmem_get(lanes + T_Y2, a[0]);
+        // chunk's long before the outputs are done, and the queries theirs), and the sum through shared memory, whence whole
+        // chunks go as tiles.  (Stored from here, 32 rows apart in every instruction, they took 2000 cycles of the load and store
+        // unit a chunk.)
+        const uint64_t scale = pair(p.scale, p.scale);
+        do {
+            const int h = units.h;
+            const float f = power(p.log_decay[h] * LOG2E, row + 1);
+            const uint64_t f2 = pair(f, f);
+            int t = job.t0;
+            for (int left = job.len; left > 0; left -= C, t += C, ++g) {
+                unsigned char *out = Smem::OWN_OUT ? sm.out : Smem::OUT_ON_V ? sm.v[g % NV] : sm.k[g & 1];
+                if (outputs_sync_or(!wait(B_Y2, g))) {  // (all four warps leave together: they meet below)
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t a[2][16];
+                tmem_get(lanes + T_Y2, a[0]);
 #pragma unroll 1
-            for (int b = 0; b < P / 16; b += 2) {
+                for (int b = 0; b < P / 16; b += 2) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    tmem_got(a[u]);
-                    if (u == 0 || b + 2 < P / 16) tmem_get(lanes + T_Y2 + 16 * (b + u + 1), a[u ^ 1]);
-                    uint32_t o[16];
+                    for (int u = 0; u < 2; ++u) {
+                        tmem_got(a[u]);
+                        if (u == 0 || b + 2 < P / 16) tmem_get(lanes + T_Y2 + 16 * (b + u + 1), a[u ^ 1]);
+                        uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float lo, hi;
-                        unpair(mul2(f2, pair(__uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]))), lo, hi);
-                        o[e] = __float_as_uint(lo), o[e + 1] = __float_as_uint(hi);
-                    }
-                    tmem_put16(lanes + T_Y + 16 * (b + u), o);
-                }
-            }
-            tmem_put_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(&sm.bar[B_M]);
-            if (Smem::OWN_OUT && warp == 4) bulk_wait_read<0>();  // (by the thread that issued the last tile)
-            if (outputs_sync_or(!wait(B_Y, c))) break;
-            tc_fence_after();
-            tmem_get(lanes + T_Y, a[0]);
-#pragma unroll 1
-            for (int b = 0; b < P / 16; b += 2) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    tmem_got(a[u]);
-                    if (u == 0 || b + 2 < P / 16) tmem_get(lanes + T_Y + 16 * (b + u + 1), a[u ^ 1]);
-                    uint32_t o[8];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float lo, hi;
-                        unpair(mul2(scale, pair(__uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]))), lo, hi);
-                        o[e / 2] = pack2(lo, hi);
-                    }
-                    unsigned char *to = out + ((b + u) >> 2) * kBlk;
-                    *reinterpret_cast<uint4 *>(to + swz128_chunk(row, ((b + u) & 3) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(to + swz128_chunk(row, ((b + u) & 3) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-            }
-            tc_fence_before();
-            fence_async_smem();
-            const int L = job.len - c * C;
-            if (outputs_sync_or(false)) break;
-            if (L >= C) {
-                if (warp == 4 && elect_one()) {
-#pragma unroll
-                    for (int b = 0; b < PB; ++b) tma_store_2d(&ymap, out + b * kBlk, h * P + 64 * b, job.t0 + c * C);
-                    bulk_commit();
-                    if (!Smem::OWN_OUT) {
-                        bulk_wait_read<0>();
-                        arrive(&sm.bar[Smem::OUT_ON_V ? B_VE + c % NV : B_KE + (c & 1)]);
+                        for (int e = 0; e < 16; e += 2) {
+                            float lo, hi;
+                            unpair(mul2(f2, pair(__uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]))), lo, hi);
+                            o[e] = __float_as_uint(lo), o[e + 1] = __float_as_uint(hi);
+                        }
+                        tmem_put16(lanes + T_Y + 16 * (b + u), o);
                     }
                 }
+                tmem_put_wait();
+                tc_fence_before();
                 __syncwarp();
-            } else {  // the sequence's last tokens: the rows after them are another's
-                constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
-                const int ch = row % CH;
-                bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)(job.t0 + c * C) * p.H + h) * P + ch * 8;
-                for (int t = row / CH; t < L; t += 128 / CH)
-                    *reinterpret_cast<uint4 *>(dst + (int64_t)t * p.H * P) =
-                        *reinterpret_cast<const uint4 *>(out + (ch >> 3) * kBlk + swz128_chunk(t, ch & 7));
+                if (lane == 0) arrive(&sm.bar[B_M]);
+                if (Smem::OWN_OUT && warp == 4) bulk_wait_read<0>();  // (by the thread that issued the last tile)
+                if (!(ok = !outputs_sync_or(!wait(B_Y, g)))) break;
+                tc_fence_after();
+                tmem_get(lanes + T_Y, a[0]);
+#pragma unroll 1
+                for (int b = 0; b < P / 16; b += 2) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        tmem_got(a[u]);
+                        if (u == 0 || b + 2 < P / 16) tmem_get(lanes + T_Y + 16 * (b + u + 1), a[u ^ 1]);
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            float lo, hi;
+                            unpair(mul2(scale, pair(__uint_as_float(a[u][e]), __uint_as_float(a[u][e + 1]))), lo, hi);
+                            o[e / 2] = pack2(lo, hi);
+                        }
+                        unsigned char *to = out + ((b + u) >> 2) * kBlk;
+                        *reinterpret_cast<uint4 *>(to + swz128_chunk(row, ((b + u) & 3) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(to + swz128_chunk(row, ((b + u) & 3) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+                tc_fence_before();
+                fence_async_smem();
+                outputs_sync_or(false);
+                if (left >= C) {
+                    if (warp == 4 && elect_one()) {
+#pragma unroll
+                        for (int b = 0; b < PB; ++b) tma_store_2d(&ymap, out + b * kBlk, h * P + 64 * b, t);
+                        bulk_commit();
+                        if (!Smem::OWN_OUT) {
+                            bulk_wait_read<0>();
+                            arrive(&sm.bar[Smem::OUT_ON_V ? B_VE + g % NV : B_KE + (g & 1)]);
+                        }
+                    }
+                    __syncwarp();
+                } else {  // the sequence's last tokens: the rows after them are another's
+                    constexpr int CH = P / 8;  // 16-byte pieces of a token's outputs; a thread takes every 128 / CH-th token
+                    const int ch = row % CH;
+                    bf16 *dst = static_cast<bf16 *>(p.y) + ((int64_t)t * p.H + h) * P + ch * 8;
+                    for (int i = row / CH; i < left; i += 128 / CH)
+                        *reinterpret_cast<uint4 *>(dst + (int64_t)i * p.H * P) =
+                            *reinterpret_cast<const uint4 *>(out + (ch >> 3) * kBlk + swz128_chunk(i, ch & 7));
+                    if (!Smem::OWN_OUT) {  // the place is the next segment's
+                        outputs_sync_or(false);
+                        if (row == 0) arrive(&sm.bar[Smem::OUT_ON_V ? B_VE + g % NV : B_KE + (g & 1)]);
+                        __syncwarp();
+                    }
+                }
             }
-        }
+        } while (ok && units.next(job));
         if (Smem::OWN_OUT && warp == 4) bulk_wait_read<0>();
     } else if (warp < 12) {
         // the state: key index n a thread (with N 64 the upper half hold zeros)
         more_registers<kStateRegs>();
         const int n = row;
-        StateT *pool = static_cast<StateT *>(p.pool) + (int64_t)h * P * N + n;
-        const bool seeded = n < N && job.seeded;
-        uint64_t S[P / 2];  // values 2 e and 2 e + 1
-        {
-            const float *from = entry_at(p, job.entry, h, P) + n;
-            if (!seeded) {
+        do {
+            const int h = units.h, nc = (job.len + C - 1) / C;
+            const float l2 = p.log_decay[h] * LOG2E;
+            StateT *pool = static_cast<StateT *>(p.pool) + (int64_t)h * P * N + n;
+            const bool seeded = n < N && job.seeded;
+            uint64_t S[P / 2];  // values 2 e and 2 e + 1
+            {
+                const float *from = entry_at(p, job.entry, h, P) + n;
+                if (!seeded) {
 #pragma unroll
-                for (int e = 0; e < P / 2; ++e) S[e] = 0;
-            } else if (job.last) {  // several segments: from the copy, since the last one's block writes the slot
+                    for (int e = 0; e < P / 2; ++e) S[e] = 0;
+                } else if (job.last) {  // several segments: from the copy, since the last one's block writes the slot
 #pragma unroll
-                for (int e = 0; e < P / 2; ++e) S[e] = pair(from[2 * e * 128], from[(2 * e + 1) * 128]);
-            } else {
+                    for (int e = 0; e < P / 2; ++e) S[e] = pair(from[2 * e * 128], from[(2 * e + 1) * 128]);
+                } else {
 #pragma unroll
-                for (int e = 0; e < P / 2; ++e)
-                    S[e] = pair(to_f32(pool[job.slot * p.stride + 2 * e * N]), to_f32(pool[job.slot * p.stride + (2 * e + 1) * N]));
-            }
-            if (n < N && job.index) {
-                const float over = power(l2, p.seg_tokens);
-                const uint64_t over2 = pair(over, over);
+                    for (int e = 0; e < P / 2; ++e)
+                        S[e] = pair(to_f32(pool[job.slot * p.stride + 2 * e * N]), to_f32(pool[job.slot * p.stride + (2 * e + 1) * N]));
+                }
+                if (n < N && job.index) {
+                    const float over = power(l2, p.seg_tokens);
+                    const uint64_t over2 = pair(over, over);
 #pragma unroll 1
-                for (int r = 1; r <= job.index; ++r) {
-                    from += (int64_t)p.H * (128 * P);
+                    for (int r = 1; r <= job.index; ++r) {
+                        from += (int64_t)p.H * (128 * P);
 #pragma unroll
-                    for (int e = 0; e < P / 2; ++e) S[e] = fma2(over2, S[e], pair(from[2 * e * 128], from[(2 * e + 1) * 128]));
+                        for (int e = 0; e < P / 2; ++e) S[e] = fma2(over2, S[e], pair(from[2 * e * 128], from[(2 * e + 1) * 128]));
+                    }
                 }
             }
-        }
-        const float whole = power(l2, C), part = power(l2, job.len - (nc - 1) * C);  // over a chunk, and the last one
-        for (int c = -1; c < nc; ++c) {  // (from -1: only the copy for the first chunk)
-            if (c >= 0) {
-                if (!wait(B_S, c)) break;
-                tc_fence_after();
-                const float over = c + 1 == nc ? part : whole;
-                const uint64_t over2 = pair(over, over);
-                tmem_pieces<P / 16>(lanes + T_D, [&](int i, const uint32_t (&d)[16]) {
+            const float whole = power(l2, C), part = power(l2, job.len - (nc - 1) * C);  // over a chunk, and the last one
+            for (int c = -1; c < nc; ++c) {  // (from -1: only the copy for the first chunk)
+                if (c >= 0) {
+                    if (!(ok = wait(B_S, g))) break;
+                    ++g;
+                    tc_fence_after();
+                    const float over = c + 1 == nc ? part : whole;
+                    const uint64_t over2 = pair(over, over);
+                    tmem_pieces<P / 16>(lanes + T_D, [&](int i, const uint32_t (&d)[16]) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        S[8 * i + e] = fma2(over2, S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-                });
-            }
-            if (c + 1 < nc) {
-                if (n < N) {
+                        for (int e = 0; e < 8; ++e)
+                            S[8 * i + e] = fma2(over2, S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+                    });
+                }
+                if (c + 1 < nc) {
+                    if (n < N) {
 #pragma unroll
-                    for (int e = 0; e < P / 2; e += 4) {
-                        uint32_t o[4];
+                        for (int e = 0; e < P / 2; e += 4) {
+                            uint32_t o[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float lo, hi;
-                            unpair(S[e + i], lo, hi);
-                            o[i] = pack2(lo, hi);
+                            for (int i = 0; i < 4; ++i) {
+                                float lo, hi;
+                                unpair(S[e + i], lo, hi);
+                                o[i] = pack2(lo, hi);
+                            }
+                            *reinterpret_cast<uint4 *>(sm.sb + (e >> 5) * (N * 128) + swz128_chunk(n, (e >> 2) & 7)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
                         }
-                        *reinterpret_cast<uint4 *>(sm.sb + (e >> 5) * (N * 128) + swz128_chunk(n, (e >> 2) & 7)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
                     }
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&sm.bar[B_SB]);
                 }
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(&sm.bar[B_SB]);
-            }
-            if (c >= 0) {
-                const bool end = c + 1 == nc && job.index == job.last;
-                const int32_t ckpt = ckpt_slot(p, job.seq, job.index * p.seg_tokens + min(job.len, (c + 1) * C), row == 0 && h == 0);
-                auto write = [&](int32_t slot) {
-                    if (slot < 0 || n >= N) return;
-                    StateT *to = pool + slot * p.stride;
+                if (c >= 0) {
+                    const bool end = c + 1 == nc && job.index == job.last;
+                    const int32_t ckpt = ckpt_slot(p, job.seq, job.index * p.seg_tokens + min(job.len, (c + 1) * C), row == 0 && h == 0);
+                    auto write = [&](int32_t slot) {
+                        if (slot < 0 || n >= N) return;
+                        StateT *to = pool + slot * p.stride;
 #pragma unroll
-                    for (int e = 0; e < P / 2; ++e) {
-                        float lo, hi;
-                        unpair(S[e], lo, hi);
-                        to[2 * e * N] = from_f32<StateT>(lo);
-                        to[(2 * e + 1) * N] = from_f32<StateT>(hi);
-                    }
-                };
-                if (ckpt >= 0) write(ckpt);
-                if (end) write(job.slot);
+                        for (int e = 0; e < P / 2; ++e) {
+                            float lo, hi;
+                            unpair(S[e], lo, hi);
+                            to[2 * e * N] = from_f32<StateT>(lo);
+                            to[(2 * e + 1) * N] = from_f32<StateT>(hi);
+                        }
+                    };
+                    if (ckpt >= 0) write(ckpt);
+                    if (end) write(job.slot);
+                }
             }
-        }
+        } while (ok && units.next(job));
     } else if (warp < 16) {
         more_registers<kKeyRegs>();
         // K', token j a thread: its other parts (with the scores' group, see there) once the chunk before is through with theirs,
         // while the scores are formed, and the first in place of K when these have read it.  Past the segment's end zeros, in V as
         // well: the tiles hold another's tokens there.
-        for (int c = 0; c < nc; ++c) {
-            const int L = min(C, job.len - c * C);
-            unsigned char *tile = sm.k[c & 1];
-            const Weight w(power(l2, max(L - 1 - row, 0)));
-            if (!wait(B_KF + (c & 1), c >> 1) || (c && !wait(B_S, c - 1))) break;
-            constexpr int OWN = HELP ? NB / 2 : NB;
-            uint4 first[8 * OWN];
-            if (row < L) {
-                other_parts<MORE, 0, OWN>(tile, sm.rest[0], row, w, first, nullptr);
-            } else {
+        do {
+            const float l2 = p.log_decay[units.h] * LOG2E;
+            for (int left = job.len; left > 0; left -= C, ++g) {
+                const int L = min(C, left);
+                unsigned char *tile = sm.k[g & 1];
+                const Weight w(power(l2, max(L - 1 - row, 0)));
+                if (!(ok = wait(B_KF + (g & 1), g >> 1) && (!g || wait(B_S, g - 1)))) break;
+                constexpr int OWN = HELP ? NB / 2 : NB;
+                uint4 first[8 * OWN];
+                if (row < L) {
+                    other_parts<MORE, 0, OWN>(tile, sm.rest[0], row, w, first, nullptr);
+                } else {
 #pragma unroll
-                for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, 0, OWN);
+                    for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, 0, OWN);
 #pragma unroll
-                for (int i = 0; i < 8 * OWN; ++i) first[i] = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 8 * OWN; ++i) first[i] = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+                if (!(ok = wait(B_P + g % NP, g / NP))) break;
+#pragma unroll
+                for (int i = 0; i < 8 * OWN; ++i) *reinterpret_cast<uint4 *>(tile + piece_at(row, i)) = first[i];
+                if (L < C) {
+                    if (!(ok = wait(B_VF + g % NV, g / NV))) break;
+                    if (row >= L) clear_row(sm.v[g % NV], row, 0, PB);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(&sm.bar[B_K2]);
             }
-            __syncwarp();
-            if (!wait(B_P + c % NP, c / NP)) break;
-#pragma unroll
-            for (int i = 0; i < 8 * OWN; ++i) *reinterpret_cast<uint4 *>(tile + piece_at(row, i)) = first[i];
-            if (L < C) {
-                if (!wait(B_VF + c % NV, c / NV)) break;
-                if (row >= L) clear_row(sm.v[c % NV], row, 0, PB);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive(&sm.bar[B_K2]);
-        }
+        } while (ok && units.next(job));
     } else if (warp != 17) {
         fewer_registers<kIssueRegs>();
         // loads: of queries, keys and values, a warp each
         const int stages = warp == 16 ? NQ : warp == 18 ? 2 : NV, full = warp == 16 ? B_QF : warp == 18 ? B_KF : B_VF,
-                  empty = warp == 16 ? B_QE : warp == 18 ? B_KE : B_VE, blocks = warp == 19 ? PB : NB,
-                  x = warp == 19 ? h * P : h / p.HG * N;
+                  empty = warp == 16 ? B_QE : warp == 18 ? B_KE : B_VE, blocks = warp == 19 ? PB : NB;
         unsigned char *tiles = warp == 16 ? sm.q[0] : warp == 18 ? sm.k[0] : sm.v[0];
         const uint32_t size = warp == 16 ? Smem::kQ : warp == 18 ? kTile : P * 256;
         const CUtensorMap *map = warp == 16 ? &qmap : warp == 18 ? &kmap : &vmap;
         int st = 0, use = 0;
-        for (; loaded < nc; ++loaded) {
-            if (use && !wait(empty + st, use - 1)) break;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&sm.bar[full + st], blocks * kBlk);
-                for (int b = 0; b < blocks; ++b)
-                    tma_load_2d(tiles + st * size + b * kBlk, map, x + 64 * b, job.t0 + loaded * C, &sm.bar[full + st]);
+        do {
+            const int x = warp == 19 ? units.h * P : units.h / p.HG * N;
+            for (int t = job.t0; t < job.t0 + job.len; t += C, ++loaded) {
+                if (use && !(ok = wait(empty + st, use - 1))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sm.bar[full + st], blocks * kBlk);
+                    for (int b = 0; b < blocks; ++b)
+                        tma_load_2d(tiles + st * size + b * kBlk, map, x + 64 * b, t, &sm.bar[full + st]);
+                }
+                __syncwarp();
+                if (++st == stages) st = 0, ++use;
+                if (warp == 18 && t + C >= job.t0 + job.len) {  // the next unit, for all warps.  (None is as many as kRing behind this one.)
+                    const int k = units.k % kRing;
+                    if (elect_one()) {
+                        sm.ring[k] = gridDim.x + atomicAdd(&p.meta[1], 1);
+                        arrive(&sm.bar[B_U + k]);
+                    }
+                    __syncwarp();
+                }
             }
-            __syncwarp();
-            if (++st == stages) st = 0, ++use;
-        }
+        } while (ok && units.next(job));
         in_flight = full, of = stages;
     } else {
         fewer_registers<kIssueRegs>();
@@ -594,11 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
             __syncwarp();
             return true;
         };
-        if (scores(0))
-            for (int c = 0; c < nc; ++c) {
-                const int st = c & 1, qs = c % NQ, vs = c % NV;
+        ok = scores(0);
+        for (bool more = true; ok && more;) {
+            for (int left = job.len; left > 0; left -= C, ++g) {
+                const int st = g & 1, qs = g % NQ, vs = g % NV;
                 const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), v = smem_u32(sm.v[vs]), sb = smem_u32(sm.sb);
-                if (!wait(B_SB, c) || (c && !wait(B_M, c - 1))) break;
+                if (!(ok = wait(B_SB, g) && (!g || wait(B_M, g - 1)))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -608,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                     mma_commit(&sm.bar[B_Y2]);
                 }
                 __syncwarp();
-                if (!wait(B_K2, c) || !wait(B_VF + vs, c / NV)) break;
+                if (!(ok = wait(B_K2, g) && wait(B_VF + vs, g / NV))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -622,19 +688,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                     if (!Smem::OUT_ON_K) mma_commit(&sm.bar[B_KE + st]);  // (else the outputs go there first)
                 }
                 __syncwarp();
-                if (AHEAD && c + 1 < nc && !scores(c + 1)) break;
-                if (!wait(B_A, c) || !wait(B_M, c)) break;
+                if (left <= C) more = units.next(job);  // (given out when the chunk's keys were loaded)
+                if (AHEAD && (left > C || more) && !(ok = scores(g + 1))) break;
+                if (!(ok = wait(B_A, g) && wait(B_M, g))) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t a = tm + T_P + (NP == 2 ? (c & 1) * 128 : 0) + 64;
+                    const uint32_t a = tm + T_P + (NP == 2 ? (g & 1) * 128 : 0) + 64;
 #pragma unroll
                     for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ts(tm + T_Y, a + 8 * kk, desc_mnmajor(v, kBlk, kk), ID_Y, 1);
                     mma_commit(&sm.bar[B_Y]);
                     if (!Smem::OUT_ON_V) mma_commit(&sm.bar[B_VE + vs]);
                 }
                 __syncwarp();
-                if (!AHEAD && c + 1 < nc && !scores(c + 1)) break;
+                if (!AHEAD && (left > C || more) && !(ok = scores(g + 1))) break;
             }
+        }
         if (elect_one()) mma_commit(&sm.bar[B_END]);
         __syncwarp();
         drain(&sm.bar[B_END], 0);
@@ -684,7 +752,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
     const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & 127;
     const int which = blockIdx.x / p.H;
     const Segment job = meta_segments(p)[min(which, p.max_segs - 1)];
-    if (which >= p.meta[0] || job.slot < -1 || job.index == job.last) return;
+    if (which >= p.meta[0] || job.index == job.last) return;
     const float l2 = p.log_decay[h] * LOG2E;
     if (N == 64)
         for (int i = tid; i < (int)kBlk / 16; i += kSegThreads) {
@@ -843,19 +911,19 @@ int launch(const ScanParams &p, cudaStream_t st) {
     if (!tile_map(&qmap, p.q, (int64_t)p.G * N, p.T, p.qs) || !tile_map(&kmap, p.k, (int64_t)p.G * N, p.T, p.ks) ||
         !tile_map(&vmap, p.v, (int64_t)p.H * P, p.T, p.vs) || !tile_map(&ymap, p.y, (int64_t)p.H * P, p.T, (int64_t)p.H * P))
         return MAMBA_ECUDA;
-    const dim3 grid((unsigned)((int64_t)p.max_segs * p.H));
+    const int64_t units = (int64_t)p.max_segs * p.H;
     if (p.seg_tokens < kWhole) {
         auto kern = k_la_segment<P, N, F32S>;
         constexpr size_t smem = sizeof(SegSmem<P, F32S>) + 1024;
         static_assert(smem <= 232448, "shared memory of a block");
         if (!ready(reinterpret_cast<const void *>(kern), smem, kSegRegs)) return MAMBA_ECUDA;
-        if (launch_pdl(kern, grid, dim3(kSegThreads), smem, st, p, kmap, vmap) != cudaSuccess) return MAMBA_ECUDA;
+        if (launch_pdl(kern, dim3((unsigned)units), dim3(kSegThreads), smem, st, p, kmap, vmap) != cudaSuccess) return MAMBA_ECUDA;
     }
     auto kern = k_la_chain<P, N, F32S>;
     constexpr size_t smem = sizeof(ChainSmem<P, N, F32S>) + 1024;
     static_assert(smem <= 232448, "shared memory of a block");
     if (!ready(reinterpret_cast<const void *>(kern), smem, kRegs)) return MAMBA_ECUDA;
-    if (launch_pdl(kern, grid, dim3(kThreads), smem, st, p, qmap, kmap, vmap, ymap) != cudaSuccess) return MAMBA_ECUDA;
+    if (launch_pdl(kern, dim3((unsigned)(units < kSMs ? units : kSMs)), dim3(kThreads), smem, st, p, qmap, kmap, vmap, ymap) != cudaSuccess) return MAMBA_ECUDA;
     return launch_status();
 }
 
@@ -874,7 +942,7 @@ bool chunked_eligible(const mamba_layer_desc *d) {
 // Sequences are cut where their heads alone are fewer than the SMs: into as many segments as make one block an SM, at
 // least 4 chunks each (what a segment adds to the state costs about half of its pass).
 int chunked_segment_tokens(int H, int T, int nseq) {
-    const int64_t blocks = 152 / H;
+    const int64_t blocks = kSMs / H;
     if (blocks < 2 * (int64_t)nseq) return kWhole;
     const int64_t chunks = ((int64_t)T + C - 1) / C, spare = blocks - nseq / 2;
     const int64_t per = (chunks + spare - 1) / spare;

@@ -29,17 +29,17 @@ struct StepArgs {
 // Block (head and share of its rows, batch row).  While the state is on its way the block forms its tokens' angles,
 // an angle a thread, and then their keys and queries, a row of either to each LPR lanes, in shared memory in
 // fp32, so that the tokens follow one another without a wait on memory.
-template <typename StateT, typename ActT, int P, int N, int RT>
-__global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
+template <typename StateT, typename ActT, int P, int N, int RT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) k_la_step(const StepArgs p) {
     using Map = RowMap<N, RT>;
     using Raw = typename RawOf<StateT>::type;
     __shared__ __align__(16) float kq[2 * kMaxTok][N];  // a token's key and query
-    __shared__ float2 table[kMaxTok][N / 2];
-    __shared__ float vs[kMaxTok][2 * Map::ROWS];
+    __shared__ __align__(16) float2 table[kMaxTok][N / 2];
+    __shared__ float vs[kMaxTok][WARPS * Map::ROWS];
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
     const int i = blockIdx.y, h = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t s = p.slot[i];
     if (s == -1) return;  // padding row
     bool bad = s < -1 || s >= p.num_slots;
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
         if (tid == 0) flag_error(p.err, MAMBA_ERR_SLOT_RANGE);
         return;
     }
-    const int row0 = split * warps * Map::ROWS;  // the block's
+    const int row0 = split * WARPS * Map::ROWS;  // the block's
     const int sub = lane / Map::LPR, idx = (lane & (Map::LPR - 1)) / Map::SHARE, col = (lane & (Map::LPR - 1)) * 8;
     StateT *pool = static_cast<StateT *>(p.pool);
     const int64_t off = ((int64_t)h * P + row0 + warp * Map::ROWS + sub) * N + col;
@@ -62,26 +62,34 @@ __global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
     const ActT *xbc = static_cast<const ActT *>(p.xbc) + (int64_t)i * p.ntok * p.Cd;
     const ActT *keys = xbc + p.H * P + (h / p.HG) * N, *queries = keys + p.G * N;
     const float2 decay = decay_of(p.log_decay[h]);
-    for (int e = tid; e < p.ntok * p.prep.half; e += blockDim.x) {
+    for (int e = tid; e < p.ntok * p.prep.half; e += 32 * WARPS) {
         const int j = e / p.prep.half, a = e % p.prep.half;
         table[j][a] = turned(turns(p.prep.inv_freq[a]), p.prep.pos[(int64_t)i * p.ntok + j]);
     }
-    for (int e = tid; e < p.ntok * warps * Map::ROWS; e += blockDim.x) {
-        const int j = e / (warps * Map::ROWS), r = e % (warps * Map::ROWS);
+    for (int e = tid; e < p.ntok * WARPS * Map::ROWS; e += 32 * WARPS) {
+        const int j = e / (WARPS * Map::ROWS), r = e % (WARPS * Map::ROWS);
         vs[j][r] = to_f32(xbc[(int64_t)j * p.Cd + h * P + row0 + r]);
     }
     __syncthreads();
-    for (int base = warp * Map::RPW; base < 2 * p.ntok; base += warps * Map::RPW) {  // (the same of all lanes of a warp)
-        const int own = base + sub, t = min(own, 2 * p.ntok - 1);
+    const LaneRow<4> own(p.prep, lane & (Map::LPR - 1));
+    for (int base = warp * Map::RPW; base < 2 * p.ntok; base += WARPS * Map::RPW) {  // (the same of all lanes of a warp)
+        const int mine = base + sub, t = min(mine, 2 * p.ntok - 1);
+        const ActT *from = ((t & 1) ? queries : keys) + (int64_t)(t >> 1) * p.Cd;
+        Some<ActT, 4> lo, hi;
+        lo.load(from + own.a);
+        hi.load(from + own.b);
         float x[8], w[8];
-        load8(((t & 1) ? queries : keys) + (int64_t)(t >> 1) * p.Cd + col, x);
-        norm_weights<N>((t & 1) ? p.prep.qw : p.prep.kw, lane, w);
-        norm_rotate<N>(x, w, p.prep, table[t >> 1], lane);
-        if (own == t) {
-            const float f = (t & 1) ? p.scale : 1.0f;
+        lo.get(x);
+        hi.get(x + 4);
+        norm_weights((t & 1) ? p.prep.qw : p.prep.kw, own, w);
+        float2 turn[4];
 #pragma unroll
-            for (int e = 0; e < 8; e += 4)
-                *reinterpret_cast<float4 *>(&kq[t][col + e]) = make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
+        for (int e = 0; e < 4; ++e) turn[e] = own.turns ? table[t >> 1][own.angle + e] : make_float2(1.0f, 0.0f);
+        norm_rotate<N, 4>(x, w, p.prep, turn, own);
+        if (mine == t) {
+            const float f = (t & 1) ? p.scale : 1.0f;
+            *reinterpret_cast<float4 *>(&kq[t][own.a]) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+            *reinterpret_cast<float4 *>(&kq[t][own.b]) = make_float4(x[4] * f, x[5] * f, x[6] * f, x[7] * f);
         }
     }
     uint64_t S[RT][4];
@@ -113,17 +121,22 @@ __global__ void __launch_bounds__(64) k_la_step(const StepArgs p) {
 
 template <typename StateT, typename ActT, int P, int N, int RT>
 int launch_step(StepArgs &a, int batch, cudaStream_t st) {
-    constexpr int rows = RowMap<N, RT>::ROWS, warps = P / rows < 2 ? P / rows : 2;
+    constexpr int rows = RowMap<N, RT>::ROWS, most = sizeof(StateT) == 2 ? 4 : 2, warps = P / rows < most ? P / rows : most;
     a.splits = P / (rows * warps);
     const dim3 grid((unsigned)(a.H * a.splits), (unsigned)batch);
-    if (launch_pdl(k_la_step<StateT, ActT, P, N, RT>, grid, dim3(32 * warps), 0, st, a) != cudaSuccess) return MAMBA_ECUDA;
+    if (launch_pdl(k_la_step<StateT, ActT, P, N, RT, warps>, grid, dim3(32 * warps), 0, st, a) != cudaSuccess) return MAMBA_ECUDA;
     return launch_status();
 }
 
+// Rows a lane and warps a block, in us at 256 rows of 32 heads of 128 x 128, 61 of 128 heads of 64 x 128, and 48 of the
+// former with four drafts: fp32 states 160, 79 and 88 with 8 rows and two warps, 167, 82 and 101 with 4 rows, 170, 83 and 89
+// with four warps; bf16 states, whose rows are half as many bytes for the same preparation, 90, 45 and 46 with 4 rows and four
+// warps, 92, 46 and 50 with 8 rows and two warps, 97, 48 and 47 with 8 rows and four.  One warp a block took 100 to 160.
 template <typename StateT, typename ActT>
 int dispatch_step(StepArgs &a, int batch, int P, int N, cudaStream_t st) {
-    if (P == 128 && N == 128) return launch_step<StateT, ActT, 128, 128, 8>(a, batch, st);
-    if (P == 64 && N == 128) return launch_step<StateT, ActT, 64, 128, 8>(a, batch, st);
+    constexpr int R = sizeof(StateT) == 2 ? 4 : 8;
+    if (P == 128 && N == 128) return launch_step<StateT, ActT, 128, 128, R>(a, batch, st);
+    if (P == 64 && N == 128) return launch_step<StateT, ActT, 64, 128, R>(a, batch, st);
     if (P == 64 && N == 64) return launch_step<StateT, ActT, 64, 64, 8>(a, batch, st);
     if (P == 32 && N == 64) return launch_step<StateT, ActT, 32, 64, 8>(a, batch, st);
     if (P == 16 && N == 16) return launch_step<StateT, ActT, 16, 16, 1>(a, batch, st);
@@ -132,73 +145,81 @@ int dispatch_step(StepArgs &a, int batch, int P, int N, cudaStream_t st) {
 
 // ---- norm and rotation on their own ----
 
-constexpr int kPrepThreads = 256, kPrepItems = 4;  // threads a block; pieces of 8 values a thread has on its way
+constexpr int kPrepThreads = 128, kPrepAhead = 2;  // threads a block; rows of a lane on their way at a time
 
 struct PrepArgs {
     const void *k, *q;
     void *k_out, *q_out;
     int64_t ks, qs, kos, qos;  // token strides, elements
-    int T, G, per;             // per: tokens of a pass of a block
+    int T, G, rows, parts;     // rows: of a token's 2 G heads' keys and queries that a warp takes; parts: warps a token
     QkPrep prep;
 };
 
-// Streaming: 2 G N values a token in and out.  A block takes `per` tokens at a time, as many as fill its
-// threads' pieces: their angles go to shared memory, an angle a thread and step (each shared by all heads of
-// the token), while the pieces are on their way.
+// Streaming: 2 G N values a token in and out.  A warp takes a token's rows, or a part of them: its lanes' angles are then
+// the same for all of them and stay in registers, and warps need nothing of one another.
 template <typename ActT, int N>
 __global__ void __launch_bounds__(kPrepThreads) k_la_qk_prep(const PrepArgs p) {
-    constexpr int LPR = N / 8;
-    extern __shared__ __align__(16) float2 angles[];  // [per][half]
+    constexpr int V = 8, LPR = N / (2 * V), RPW = 32 / LPR;
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, col = (tid & (LPR - 1)) * 8, half = p.prep.half;
-    float kw[8], qw[8];
-    norm_weights<N>(p.prep.kw, lane, kw);
-    norm_weights<N>(p.prep.qw, lane, qw);
-    const ActT *k = static_cast<const ActT *>(p.k), *q = static_cast<const ActT *>(p.q);
-    ActT *ko = static_cast<ActT *>(p.k_out), *qo = static_cast<ActT *>(p.q_out);
-    const int rows = p.per * 2 * p.G;  // rows (a head's key or query) of a pass
-    for (int64_t t0 = (int64_t)blockIdx.x * p.per; t0 < p.T; t0 += (int64_t)gridDim.x * p.per) {
-        const int n = (int)min((int64_t)p.per, p.T - t0);
-        for (int base = 0; base < rows; base += kPrepItems * kPrepThreads / LPR) {
-            float x[kPrepItems][8];
-            int at[kPrepItems];  // row of the pass, or -1
+    const int64_t id = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5), t = id / p.parts;
+    if (t >= p.T) return;
+    const int32_t pos = p.prep.pos ? p.prep.pos[t] : 0;
+    if (pos < 0) return;  // padding row
+    const int lane = threadIdx.x & 31, sub = lane / LPR;
+    const int begin = (int)(id % p.parts) * p.rows + sub, end = min(2 * p.G, (int)(id % p.parts + 1) * p.rows);
+    const LaneRow<V> own(p.prep, lane & (LPR - 1));
+    const ActT *k = static_cast<const ActT *>(p.k) + t * p.ks, *q = static_cast<const ActT *>(p.q) + t * p.qs;
+    ActT *ko = static_cast<ActT *>(p.k_out) + t * p.kos, *qo = static_cast<ActT *>(p.q_out) + t * p.qos;
+    Some<ActT, V> lo[kPrepAhead], hi[kPrepAhead];
+    auto fetch = [&](int i, int r) {
+        const ActT *from = r < p.G ? k + r * N : q + (r - p.G) * N;
+        if (r < end) lo[i].load(from + own.a), hi[i].load(from + own.b);
+    };
 #pragma unroll
-            for (int i = 0; i < kPrepItems; ++i) {
-                const int r = base + (i * kPrepThreads + tid) / LPR, j = r / (2 * p.G), g = r % (2 * p.G);
-                at[i] = j < n && (!p.prep.pos || p.prep.pos[t0 + j] >= 0) ? r : -1;
+    for (int i = 0; i < kPrepAhead; ++i) fetch(i, begin + i * RPW);
+    float2 turn[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
-                if (at[i] >= 0)
-                    load8(g < p.G ? k + (t0 + j) * p.ks + g * N + col : q + (t0 + j) * p.qs + (g - p.G) * N + col, x[i]);
+    for (int e = 0; e < V; ++e)
+        turn[e] = own.turns ? turned(turns(p.prep.inv_freq[own.angle + e]), pos) : make_float2(1.0f, 0.0f);
+    float w[2 * V];
+    int kind = -1;
+    for (int base = begin; base - sub < end; base += kPrepAhead * RPW) {  // (the same for all lanes of a warp)
+#pragma unroll
+        for (int i = 0; i < kPrepAhead; ++i) {
+            const int r = base + i * RPW;
+            float x[2 * V] = {};
+            if (r < end) lo[i].get(x), hi[i].get(x + V);
+            fetch(i, r + kPrepAhead * RPW);
+            if (kind != (r >= p.G)) {
+                kind = r >= p.G;
+                norm_weights(kind ? p.prep.qw : p.prep.kw, own, w);
             }
-            if (base == 0 && half) {
-                __syncthreads();  // the last pass has read its angles
-                for (int e = tid; e < n * half; e += kPrepThreads)
-                    angles[e] = turned(turns(p.prep.inv_freq[e % half]), p.prep.pos[t0 + e / half]);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int i = 0; i < kPrepItems; ++i) {
-                const int r = max(at[i], 0), j = r / (2 * p.G), g = r % (2 * p.G);
-                norm_rotate<N>(x[i], g < p.G ? kw : qw, p.prep, angles + j * half, lane);
-                if (at[i] < 0) continue;
-                ActT *to = g < p.G ? ko + (t0 + j) * p.kos + g * N + col : qo + (t0 + j) * p.qos + (g - p.G) * N + col;
-                store8_stream(to, x[i]);
+            norm_rotate<N, V>(x, w, p.prep, turn, own);
+            if (r < end) {
+                ActT *to = r < p.G ? ko + r * N : qo + (r - p.G) * N;
+                const float u[V] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]},
+                            v[V] = {x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]};
+                store8_stream(to + own.a, u);
+                store8_stream(to + own.b, v);
             }
         }
     }
 }
 
+// A warp's rows: all of a token's where tokens alone fill the SMs several times, else fewer.
 template <typename ActT, int N>
 int launch_prep(PrepArgs &a, cudaStream_t st) {
-    constexpr int rows = kPrepItems * kPrepThreads * 8 / N;
-    a.per = rows / (2 * a.G) < 1 ? 1 : rows / (2 * a.G);
-    const int64_t passes = ((int64_t)a.T + a.per - 1) / a.per;
-    const unsigned grid = (unsigned)(passes < 152 * 8 ? passes : 152 * 8);
-    if (launch_pdl(k_la_qk_prep<ActT, N>, dim3(grid), dim3(kPrepThreads), (size_t)a.per * a.prep.half * sizeof(float2), st, a) !=
-        cudaSuccess)
-        return MAMBA_ECUDA;
+    constexpr int RPW = 32 * 16 / N;
+    const int64_t passes = ((int64_t)2 * a.G + RPW - 1) / RPW, want = 152 * 64;  // passes of a warp over a token's rows; warps
+    int64_t parts = (want + a.T - 1) / a.T;
+    if (parts > passes) parts = passes;
+    const int64_t per = (passes + parts - 1) / parts;
+    a.rows = (int)per * RPW;
+    a.parts = (int)((passes + per - 1) / per);
+    const int64_t blocks = ((int64_t)a.T * a.parts + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+    if (blocks > INT32_MAX) return MAMBA_EINVAL;
+    if (launch_pdl(k_la_qk_prep<ActT, N>, dim3((unsigned)blocks), dim3(kPrepThreads), 0, st, a) != cudaSuccess) return MAMBA_ECUDA;
     return launch_status();
 }
 
