@@ -136,11 +136,10 @@ __device__ __forceinline__ void other_parts(const uint4 &k, const uint4 &first, 
 #pragma unroll
     for (int m = 0; m < MORE; ++m) out[m] = make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
 }
-// The other parts of blocks B0 .. B1 - 1 of a row of K into the tiles at rest, and the first parts to registers (to tile, if
-// it is given).  Four pieces are read before the first is worked on.
+// The other parts of blocks B0 .. B1 - 1 of a row of K into the tiles at rest, and the first parts to registers.  Four pieces are
+// read before the first is worked on.
 template <int MORE, int B0, int B1>
-__device__ __forceinline__ void other_parts(const unsigned char *k, unsigned char *rest, int row, const Weight &w, uint4 *first,
-                                            unsigned char *tile) {
+__device__ __forceinline__ void other_parts(const unsigned char *k, unsigned char *rest, int row, const Weight &w, uint4 *first) {
 #pragma unroll
     for (int i = 8 * B0; i < 8 * B1; i += 4) {
         uint4 x[4];
@@ -152,8 +151,7 @@ __device__ __forceinline__ void other_parts(const unsigned char *k, unsigned cha
             const uint4 hi = first_part(x[c], w);
             uint4 out[MORE];
             other_parts<MORE>(x[c], hi, w, out);
-            if (first) first[i - 8 * B0 + c] = hi;
-            if (tile) *reinterpret_cast<uint4 *>(tile + at) = hi;
+            first[i - 8 * B0 + c] = hi;
 #pragma unroll
             for (int m = 0; m < MORE; ++m) *reinterpret_cast<uint4 *>(rest + m * kTile + at) = out[m];
         }
@@ -331,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                     const int L = min(C, left);
                     uint4 part[8];
                     if (row < L) {
-                        other_parts<MORE, NB / 2, NB>(sm.k[g & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part, nullptr);
+                        other_parts<MORE, NB / 2, NB>(sm.k[g & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part);
                     } else {
 #pragma unroll
                         for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, NB / 2, NB);
@@ -589,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 constexpr int OWN = HELP ? NB / 2 : NB;
                 uint4 first[8 * OWN];
                 if (row < L) {
-                    other_parts<MORE, 0, OWN>(tile, sm.rest[0], row, w, first, nullptr);
+                    other_parts<MORE, 0, OWN>(tile, sm.rest[0], row, w, first);
                 } else {
 #pragma unroll
                     for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, 0, OWN);
@@ -723,28 +721,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
 // what a segment adds to the state
 // ---------------------------------------------------------------------------------------
 
-enum { G_F = 0, G_E = 2, G_K2 = 4, G_D = 6, G_DE = 8, G_END = 10, kSegBars };  // by stage: loaded, read, scaled, the product is there, added
+// By stage: loaded, read, the product is there, added; scaled, by group and stage; other parts read, by group.
+enum { G_F = 0, G_E = 2, G_D = 4, G_DE = 6, G_K2 = 8, G_R = 12, G_END = 14, kSegBars };
 // Two groups of 4 warps for the keys' decays, one for the sum, and one of which a warp loads and another issues the products.
 constexpr int kSegThreads = 4 * 128, kSegRegs = 128, kSumRegs = 192, kScaleRegs = 112, kSegIssueRegs = 40;
 static_assert(kSumRegs + 2 * kScaleRegs + kSegIssueRegs <= 4 * kSegRegs, "registers of the launch");
 
 template <int P, bool F32S>
 struct SegSmem {
-    static constexpr int MORE = F32S ? 2 : 1, GROUPS = P == 128 && F32S ? 1 : 2;  // places for a chunk's other parts
-    unsigned char k[2][kTile], v[2][P * 256], rest[GROUPS][MORE][kTile];
+    static constexpr int MORE = F32S ? 2 : 1;
+    unsigned char k[2][kTile], v[2][P * 256], rest[2][MORE][kTile / 2];  // rest: the other parts of half a chunk, by group
     uint64_t bar[kSegBars];
     uint32_t tmem;
     int failed;
 };
 
 // One segment but a sequence's last, one head: sum of d^(tokens behind it in the segment) k_j v_j^T.  The first one's block
-// also keeps the sequence's initial state.
+// also keeps the sequence's initial state.  Each group of warps readies half of every chunk's tokens, and one half's product
+// runs while the other half is readied.
 template <int P, int N, bool F32S>
 __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams p, const __grid_constant__ CUtensorMap kmap,
                                                                const __grid_constant__ CUtensorMap vmap) {
     using Smem = SegSmem<P, F32S>;
     using StateT = typename std::conditional<F32S, float, bf16>::type;
-    constexpr int MORE = Smem::MORE, GROUPS = Smem::GROUPS, NB = N / 64, PB = P / 64;
+    constexpr int MORE = Smem::MORE, NB = N / 64, PB = P / 64;
     extern __shared__ __align__(1024) unsigned char seg_smem[];
     Smem &sm = *align1024<Smem>(seg_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -759,10 +759,11 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
 #pragma unroll
             for (int s = 0; s < 2; ++s) reinterpret_cast<uint4 *>(sm.k[s] + kBlk)[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int s = 0; s < GROUPS * MORE; ++s) reinterpret_cast<uint4 *>(sm.rest[s / MORE][s % MORE] + kBlk)[i] = make_uint4(0, 0, 0, 0);
+            for (int s = 0; s < 2 * MORE; ++s)
+                if (i < (int)kBlk / 32) reinterpret_cast<uint4 *>(sm.rest[s / MORE][s % MORE] + kBlk / 2)[i] = make_uint4(0, 0, 0, 0);
         }
     if (warp == 12 && elect_one()) {
-        for (int i = 0; i < kSegBars; ++i) mbar_init(&sm.bar[i], i >= G_K2 && i < G_D && GROUPS == 1 && NB == 2 ? 8 : (i >= G_K2 && i < G_D) || (i >= G_DE && i < G_END) ? 4 : 1);
+        for (int i = 0; i < kSegBars; ++i) mbar_init(&sm.bar[i], (i >= G_DE && i < G_R) ? 4 : 1);
         fence_mbar_init();
         sm.failed = 0;
     }
@@ -781,22 +782,32 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
     auto wait = [&](int b, uint32_t use) { return warp_wait(&sm.bar[b], use & 1, failed); };
     if (warp < 8) {
         fewer_registers<kScaleRegs>();
-        // Where there is room for two chunks' other parts the groups take chunks in turn, else half of each chunk's keys.  A place
-        // is free once the product of its last chunk is done: two chunks ago, for which the load of this one has waited, or one.
-        constexpr bool TURNS = GROUPS == 2 || NB == 1;
-        const int group = warp >> 2;
-        for (int c = TURNS ? group : 0; c < nc && group < (TURNS ? GROUPS : 2); c += TURNS ? GROUPS : 1) {
+        constexpr int PC = 4 * NB;  // 16-byte pieces a thread: half of a token's
+        const int group = warp >> 2, j = group * 64 + (tid & 63), i0 = (row >> 6) * PC;
+        for (int c = 0; c < nc; ++c) {
             const int st = c & 1;
-            const Weight w(power(l2, job.len - 1 - (c * C + row)));
-            if (!wait(G_F + st, c >> 1)) break;
-            if (GROUPS == 1 && c && !wait(G_E + (c - 1 & 1), (c - 1) >> 1)) break;
-            unsigned char *k = sm.k[st], *rest = sm.rest[c % GROUPS][0];
-            if (TURNS) other_parts<MORE, 0, NB>(k, rest, row, w, nullptr, k);
-            else if (group == 0) other_parts<MORE, 0, NB / 2>(k, rest, row, w, nullptr, k);
-            else other_parts<MORE, NB / 2, NB>(k, rest, row, w, nullptr, k);
+            const Weight w(power(l2, job.len - 1 - (c * C + j)));
+            if (!wait(G_F + st, c >> 1) || (c && !wait(G_R + group, c - 1))) break;
+#pragma unroll
+            for (int i = 0; i < PC; i += 4) {
+                uint4 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const uint4 *>(sm.k[st] + piece_at(j, i0 + i + e));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = i0 + i + e;
+                    const uint4 hi = first_part(x[e], w);
+                    uint4 out[MORE];
+                    other_parts<MORE>(x[e], hi, w, out);
+                    *reinterpret_cast<uint4 *>(sm.k[st] + piece_at(j, at)) = hi;
+#pragma unroll
+                    for (int m = 0; m < MORE; ++m)  // (blocks of 64 tokens)
+                        *reinterpret_cast<uint4 *>(sm.rest[group][m] + (at >> 3) * (kBlk / 2) + swz128_chunk(j & 63, at & 7)) = out[m];
+                }
+            }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) arrive(&sm.bar[G_K2 + st]);
+            if (lane == 0) arrive(&sm.bar[G_K2 + 2 * group + st]);
         }
     } else if (warp < 12) {
         more_registers<kSumRegs>();
@@ -852,20 +863,29 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
         for (int c = 0; c < nc; ++c) {
             const int st = c & 1, use = c >> 1;
             const uint32_t k = smem_u32(sm.k[st]), v = smem_u32(sm.v[st]);
-            if (!wait(G_K2 + st, use) || !wait(G_F + st, use) || (use && !wait(G_DE + st, use - 1))) break;
-            tc_fence_after();
-            if (elect_one()) {
+            if (!wait(G_F + st, use) || (use && !wait(G_DE + st, use - 1))) break;
+            bool ok = true;
 #pragma unroll
-                for (int m = MORE; m >= 0; --m) {
-                    const uint32_t part = m ? smem_u32(sm.rest[c % GROUPS][m - 1]) : k;
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = wait(G_K2 + 2 * half + st, use))) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_bf16(tm + 128 * st, desc_mnmajor(part, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, m < MORE || kk > 0);
+                    for (int m = MORE; m >= 0; --m)  // (the smallest first: their sums cut off less)
+#pragma unroll
+                        for (int kk = 0; kk < C / 32; ++kk)
+                            mma_bf16(tm + 128 * st,
+                                     m ? desc_mnmajor(smem_u32(sm.rest[half][m - 1]), kBlk / 2, kk) : desc_mnmajor(k, kBlk, 4 * half + kk),
+                                     desc_mnmajor(v, kBlk, 4 * half + kk), ID_S, half > 0 || m < MORE || kk > 0);
+                    mma_commit(&sm.bar[G_R + half]);
+                    if (half == 1) {
+                        mma_commit(&sm.bar[G_E + st]);
+                        mma_commit(&sm.bar[G_D + st]);
+                    }
                 }
-                mma_commit(&sm.bar[G_E + st]);
-                mma_commit(&sm.bar[G_D + st]);
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
         if (elect_one()) mma_commit(&sm.bar[G_END]);
         __syncwarp();
