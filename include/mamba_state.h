@@ -631,11 +631,11 @@ size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total
  *   y                (total_tokens, nheads, head_dim) act_dtype, dense.
  *   workspace        at least la_chunk_scan_workspace_bytes(...) bytes (MAMBA_ENOSPACE otherwise); two calls
  *                    that may run at the same time need one each.
- * Layers of bf16 activations with head_dim and d_state each 64 or 128 run on the tensor cores in chunks
- * of 128 tokens from each sequence's start: products of bf16 operands (the scores and the state read by the
- * queries are rounded to bf16, 2^-9 of each), sums and the state itself in fp32; the decayed keys that enter the
- * state are held to 16 bits under a bf16 pool and 24 under an fp32 pool.  A NaN or an infinity of one token also reaches the outputs
- * of earlier tokens of its chunk there.  Other layers run token by token in fp32.
+ * Layers of bf16 activations with head_dim 64 or 128 run on the tensor cores in chunks of 128 tokens from
+ * each sequence's start: products of bf16 operands (the scores and the state read by the queries are rounded
+ * to bf16, 2^-9 of each), sums and the state itself in fp32; the decayed keys that enter the state are held
+ * to 16 bits under a bf16 pool and 24 under an fp32 pool.  A NaN or an infinity of one token also reaches the
+ * outputs of earlier tokens of its chunk there.  Other layers run token by token in fp32.
  * Limits: nseq <= 65535.  Alignment: the pool, workspace, v, k, q and y 16 bytes; the slot stride and the
  * token strides in bytes multiples of 16.
  */

@@ -58,7 +58,7 @@ __device__ __forceinline__ int32_t ckpt_slot(const ScanParams &p, int s, int don
     return cs;
 }
 
-// Whether the layer runs in chunks: bf16 activations, head_dim and d_state each 64 or 128.
+// Whether a layer of a compiled shape runs in chunks: bf16 activations, head_dim 64 or 128.
 bool chunked_eligible(const mamba_layer_desc *d);
 // Tokens of a segment of the chunked form for a batch of these sizes.
 int chunked_segment_tokens(int H, int T, int nseq);

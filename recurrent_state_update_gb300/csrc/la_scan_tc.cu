@@ -215,13 +215,14 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
 
 template <int P, int N, bool F32S>
 struct ChainSmem {
+    static_assert(N == 128 || P == 64, "compiled state shapes");
     // Parts of K' past the first, and stages of queries and values: what the parts leave room for.  Keys are needed first and
     // read last, so that they always have two.
     static constexpr int MORE = F32S ? 2 : 1, NQ = P == 64 && !F32S ? 2 : 1, NV = P == 128 && F32S ? 1 : 2;
     // Where the outputs stand on their way to memory: in a place of their own, where there is room for one, or over the chunk's
     // values, which are used by then, or its K' where values have one stage.  (Over K' the next keys come late: a ragged batch
     // took 209 us so.)
-    static constexpr bool OWN_OUT = P == 64 || N == 64, OUT_ON_V = !OWN_OUT && NV == 2, OUT_ON_K = !OWN_OUT && !OUT_ON_V;
+    static constexpr bool OWN_OUT = P == 64, OUT_ON_V = !OWN_OUT && NV == 2, OUT_ON_K = !OWN_OUT && !OUT_ON_V;
     static constexpr uint32_t kQ = N * 256, kSb = P * N * 2, kOut = OWN_OUT ? P * 256 : 1024;
     unsigned char q[NQ][kQ], k[2][kTile], v[NV][P * 256], sb[kSb], rest[MORE][kTile], out[kOut];
     float diag[4][32];  // d^m, for each of the scores' warps
@@ -932,6 +933,7 @@ int launch(const ScanParams &p, cudaStream_t st) {
         !tile_map(&vmap, p.v, (int64_t)p.H * P, p.T, p.vs) || !tile_map(&ymap, p.y, (int64_t)p.H * P, p.T, (int64_t)p.H * P))
         return MAMBA_ECUDA;
     const int64_t units = (int64_t)p.max_segs * p.H;
+    if (units > INT32_MAX) return MAMBA_EINVAL;
     if (p.seg_tokens < kWhole) {
         auto kern = k_la_segment<P, N, F32S>;
         constexpr size_t smem = sizeof(SegSmem<P, F32S>) + 1024;
@@ -949,14 +951,14 @@ int launch(const ScanParams &p, cudaStream_t st) {
 
 template <bool F32S>
 int dispatch(const ScanParams &p, int P, int N, cudaStream_t st) {
-    if (P == 128) return N == 128 ? launch<128, 128, F32S>(p, st) : launch<128, 64, F32S>(p, st);
+    if (P == 128) return launch<128, 128, F32S>(p, st);
     return N == 128 ? launch<64, 128, F32S>(p, st) : launch<64, 64, F32S>(p, st);
 }
 
 }  // namespace
 
 bool chunked_eligible(const mamba_layer_desc *d) {
-    return d->act_dtype == MAMBA_BF16 && (d->head_dim == 64 || d->head_dim == 128) && (d->d_state == 64 || d->d_state == 128);
+    return d->act_dtype == MAMBA_BF16 && (d->head_dim == 64 || d->head_dim == 128);  // (of the compiled shapes)
 }
 
 // Sequences are cut where their heads alone are fewer than the SMs: into as many segments as make one block an SM, at
@@ -965,8 +967,8 @@ int chunked_segment_tokens(int H, int T, int nseq) {
     const int64_t blocks = kSMs / H;
     if (blocks < 2 * (int64_t)nseq) return kWhole;
     const int64_t chunks = ((int64_t)T + C - 1) / C, spare = blocks - nseq / 2;
-    const int64_t per = (chunks + spare - 1) / spare;
-    return (int)((per < 4 ? 4 : per) * C);
+    const int64_t even = (chunks + spare - 1) / spare, per = even < 4 ? 4 : even;
+    return per < chunks ? (int)(per * C) : kWhole;
 }
 
 size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq, int seg_tokens) {

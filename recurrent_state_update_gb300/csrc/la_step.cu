@@ -284,6 +284,7 @@ extern "C" int la_qk_norm_rope(const mamba_layer_desc *d, const void *k, int64_t
     const int64_t strides[4] = {k_stride, q_stride, k_out_stride, q_out_stride};
     for (int64_t s : strides)
         if (s < (int64_t)G * N) return MAMBA_EINVAL;
+    if ((k_out == k && k_out_stride != k_stride) || (q_out == q && q_out_stride != q_stride)) return MAMBA_EINVAL;
     if (N != 16 && N != 32 && N != 64 && N != 128 && N != 256) return MAMBA_EUNSUPPORTED;
     if ((rc = check_prep(N, qk_norm, eps, positions, inv_freq, rot_dim)) != MAMBA_OK) return rc;
     const size_t ab = dtype_bytes(d->act_dtype);
