@@ -145,7 +145,7 @@ int dispatch_step(StepArgs &a, int batch, int P, int N, cudaStream_t st) {
 
 // ---- norm and rotation on their own ----
 
-constexpr int kPrepThreads = 128, kPrepAhead = 2;  // threads a block; rows of a lane on their way at a time
+constexpr int kPrepThreads = 128, kPrepAhead = 3;  // threads a block; rows of a lane on their way at a time
 
 struct PrepArgs {
     const void *k, *q;
@@ -156,8 +156,9 @@ struct PrepArgs {
 };
 
 // Streaming: 2 G N values a token in and out.  A warp takes a token's rows, or a part of them: its lanes' angles are then
-// the same for all of them and stay in registers, and warps need nothing of one another.
-template <typename ActT, int N>
+// the same for all of them and stay in registers, each times the weights it meets, and warps need nothing of one another.
+// Arithmetic goes two values an instruction: a lane's pairs (u, v) are held as eight u and eight v (see LaneRow).
+template <typename ActT, int N, bool INTER>
 __global__ void __launch_bounds__(kPrepThreads) k_la_qk_prep(const PrepArgs p) {
     constexpr int V = 8, LPR = N / (2 * V), RPW = 32 / LPR;
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_la_qk_prep(const PrepArgs p) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
         turn[e] = own.turns ? turned(turns(p.prep.inv_freq[own.angle + e]), pos) : make_float2(1.0f, 0.0f);
-    float w[2 * V];
+    // u' = uc u - us v, v' = vc v + vs u: cosines and sines times the weights
+    uint64_t uc[V / 2], us[V / 2], vc[V / 2], vs[V / 2];
     int kind = -1;
     for (int base = begin; base - sub < end; base += kPrepAhead * RPW) {  // (the same for all lanes of a warp)
 #pragma unroll
@@ -193,15 +195,54 @@ __global__ void __launch_bounds__(kPrepThreads) k_la_qk_prep(const PrepArgs p) {
             fetch(i, r + kPrepAhead * RPW);
             if (kind != (r >= p.G)) {
                 kind = r >= p.G;
+                float w[2 * V], c[4][V];
                 norm_weights(kind ? p.prep.qw : p.prep.kw, own, w);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float wu = INTER ? w[2 * e] : w[e], wv = INTER ? w[2 * e + 1] : w[V + e];
+                    c[0][e] = wu * turn[e].x, c[1][e] = -wv * turn[e].y, c[2][e] = wv * turn[e].x, c[3][e] = wu * turn[e].y;
+                }
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) {
+                    uc[e] = pair(c[0][2 * e], c[0][2 * e + 1]), us[e] = pair(c[1][2 * e], c[1][2 * e + 1]);
+                    vc[e] = pair(c[2][2 * e], c[2][2 * e + 1]), vs[e] = pair(c[3][2 * e], c[3][2 * e + 1]);
+                }
             }
-            norm_rotate<N, V>(x, w, p.prep, turn, own);
+            uint64_t u[V / 2], v[V / 2];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                u[e] = INTER ? pair(x[4 * e], x[4 * e + 2]) : pair(x[2 * e], x[2 * e + 1]);
+                v[e] = INTER ? pair(x[4 * e + 1], x[4 * e + 3]) : pair(x[V + 2 * e], x[V + 2 * e + 1]);
+            }
+            if (p.prep.norm) {
+                uint64_t ss = mul2(u[0], u[0]);
+#pragma unroll
+                for (int e = 1; e < V / 2; ++e) ss = fma2(u[e], u[e], ss);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) ss = fma2(v[e], v[e], ss);
+                float s0, s1;
+                unpair(ss, s0, s1);
+                const float f = rsqrtf(sum_lanes<LPR>(s0 + s1) * (1.0f / N) + p.prep.eps);
+                const uint64_t f2 = pair(f, f);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) u[e] = mul2(u[e], f2), v[e] = mul2(v[e], f2);
+            }
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                const uint64_t a = mul2(u[e], uc[e]), b = mul2(v[e], vc[e]);
+                const uint64_t at = own.turns ? fma2(v[e], us[e], a) : a, bt = own.turns ? fma2(u[e], vs[e], b) : b;
+                float y[4];
+                unpair(at, y[0], y[1]);
+                unpair(bt, y[2], y[3]);
+                x[INTER ? 4 * e : 2 * e] = y[0], x[INTER ? 4 * e + 2 : 2 * e + 1] = y[1];
+                x[INTER ? 4 * e + 1 : V + 2 * e] = y[2], x[INTER ? 4 * e + 3 : V + 2 * e + 1] = y[3];
+            }
             if (r < end) {
                 ActT *to = r < p.G ? ko + r * N : qo + (r - p.G) * N;
-                const float u[V] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]},
-                            v[V] = {x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]};
-                store8_stream(to + own.a, u);
-                store8_stream(to + own.b, v);
+                const float first[V] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]},
+                            second[V] = {x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]};
+                store8_stream(to + own.a, first);
+                store8_stream(to + own.b, second);
             }
         }
     }
@@ -219,7 +260,8 @@ int launch_prep(PrepArgs &a, cudaStream_t st) {
     a.parts = (int)((passes + per - 1) / per);
     const int64_t blocks = ((int64_t)a.T * a.parts + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
     if (blocks > INT32_MAX) return MAMBA_EINVAL;
-    if (launch_pdl(k_la_qk_prep<ActT, N>, dim3((unsigned)blocks), dim3(kPrepThreads), 0, st, a) != cudaSuccess) return MAMBA_ECUDA;
+    auto kern = a.prep.inter ? k_la_qk_prep<ActT, N, true> : k_la_qk_prep<ActT, N, false>;
+    if (launch_pdl(kern, dim3((unsigned)blocks), dim3(kPrepThreads), 0, st, a) != cudaSuccess) return MAMBA_ECUDA;
     return launch_status();
 }
 
