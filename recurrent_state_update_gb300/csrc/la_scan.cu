@@ -240,7 +240,7 @@ int dispatch_tokens(const ScanParams &p, int P, int N, cudaStream_t st) {
 }
 
 int segment_tokens(const mamba_layer_desc *d, int T, int nseq) {
-    return chunked_eligible(d) ? chunked_segment_tokens(d->nheads, T, nseq) : 1 << 30;
+    return chunked_eligible(d) ? chunked_segment_tokens(d->nheads, T, nseq) : kWhole;
 }
 
 }  // namespace

@@ -29,7 +29,6 @@ namespace {
 
 constexpr int C = kChunk;
 constexpr int kSMs = 152;
-constexpr int kWhole = 1 << 30;               // tokens of a segment where sequences are not cut
 constexpr uint32_t kPolls = umma::kWaitPolls;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint32_t kBlk = 128 * 128;          // bytes of a swizzled block: 128 tokens, 64 values each
