@@ -135,9 +135,9 @@ __device__ __forceinline__ void other_parts(const uint4 &k, const uint4 &first, 
 #pragma unroll
     for (int m = 0; m < MORE; ++m) out[m] = make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
 }
-// The other parts of blocks B0 .. B1 - 1 of a row of K into the tiles at rest, and the first parts to registers.  Four pieces are
+// The other parts of blocks B0 .. B1 - 1 of a row of K (or V) into the tiles at rest, REST bytes apart, and the first parts to registers.  Four pieces are
 // read before the first is worked on.
-template <int MORE, int B0, int B1>
+template <int MORE, int B0, int B1, uint32_t REST>
 __device__ __forceinline__ void other_parts(const unsigned char *k, unsigned char *rest, int row, const Weight &w, uint4 *first) {
 #pragma unroll
     for (int i = 8 * B0; i < 8 * B1; i += 4) {
@@ -152,7 +152,7 @@ __device__ __forceinline__ void other_parts(const unsigned char *k, unsigned cha
             other_parts<MORE>(x[c], hi, w, out);
             first[i - 8 * B0 + c] = hi;
 #pragma unroll
-            for (int m = 0; m < MORE; ++m) *reinterpret_cast<uint4 *>(rest + m * kTile + at) = out[m];
+            for (int m = 0; m < MORE; ++m) *reinterpret_cast<uint4 *>(rest + m * REST + at) = out[m];
         }
     }
 }
@@ -215,15 +215,20 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
 template <int P, int N, bool F32S>
 struct ChainSmem {
     static_assert(N == 128 || P == 64, "compiled state shapes");
-    // Parts of K' past the first, and stages of queries and values: what the parts leave room for.  Keys are needed first and
-    // read last, so that they always have two.
+    // The weights of a chunk's tokens in the state meet its keys (K', in place of K) or its values (V', beside V): these, where
+    // they are half as many and leave room.
+    static constexpr bool ON_V = P == 64;
+    // Parts of K' past the first, or of V' past V; stages of queries and values: what the parts leave room for.  Keys are needed
+    // first and read last, so that they always have two.
     static constexpr int MORE = F32S ? 2 : 1, NQ = P == 64 && !F32S ? 2 : 1, NV = P == 128 && F32S ? 1 : 2;
+    static constexpr int RESTS = ON_V ? MORE + 1 : MORE;
+    static constexpr uint32_t kRest = ON_V ? kBlk : kTile;
     // Where the outputs stand on their way to memory: in a place of their own, where there is room for one, or over the chunk's
     // values, which are used by then, or its K' where values have one stage.  (Over K' the next keys come late: a ragged batch
     // took 209 us so.)
     static constexpr bool OWN_OUT = P == 64, OUT_ON_V = !OWN_OUT && NV == 2, OUT_ON_K = !OWN_OUT && !OUT_ON_V;
     static constexpr uint32_t kQ = N * 256, kSb = P * N * 2, kOut = OWN_OUT ? P * 256 : 1024;
-    unsigned char q[NQ][kQ], k[2][kTile], v[NV][P * 256], sb[kSb], rest[MORE][kTile], out[kOut];
+    unsigned char q[NQ][kQ], k[2][kTile], v[NV][P * 256], sb[kSb], rest[RESTS][kRest], out[kOut];
     float diag[4][32];  // d^m, for each of the scores' warps
     int32_t ring[kRing];   // units given out, by turn
     uint64_t bar[kBars];
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     constexpr int NP = P == 64 && NQ == 2 ? 2 : 1;
     constexpr uint32_t T_P = 0, T_Y2 = NP * 128, T_Y = T_Y2 + P, T_D = T_Y + P;
     static_assert(T_D + P <= 512, "tensor memory");
-    constexpr bool HELP = MORE == 2 && NB == 2;  // whether the scores' group takes half of the other parts
+    constexpr bool ON_V = Smem::ON_V, HELP = MORE == 2 && !ON_V;  // HELP: whether the scores' group takes half of the other parts
     extern __shared__ __align__(1024) unsigned char chain_smem[];
     Smem &sm = *align1024<Smem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -284,8 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
         for (int i = tid; i < (int)kBlk / 16; i += kThreads) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) reinterpret_cast<uint4 *>(sm.k[s] + kBlk)[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int m = 0; m < MORE; ++m) reinterpret_cast<uint4 *>(sm.rest[m] + kBlk)[i] = make_uint4(0, 0, 0, 0);
         }
     if (warp == 16 && elect_one()) {
         tma_prefetch_desc(&qmap), tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap), tma_prefetch_desc(&ymap);
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                     const int L = min(C, left);
                     uint4 part[8];
                     if (row < L) {
-                        other_parts<MORE, NB / 2, NB>(sm.k[g & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part);
+                        other_parts<MORE, NB / 2, NB, kTile>(sm.k[g & 1], sm.rest[0], row, Weight(power(l2, L - 1 - row)), part);
                     } else {
 #pragma unroll
                         for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, NB / 2, NB);
@@ -575,8 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     } else if (warp < 16) {
         more_registers<kKeyRegs>();
         // K', token j a thread: its other parts (with the scores' group, see there) once the chunk before is through with theirs,
-        // while the scores are formed, and the first in place of K when these have read it.  Past the segment's end zeros, in V as
-        // well: the tiles hold another's tokens there.
+        // while the scores are formed, and the first in place of K when these have read it.  Or V', all parts beside V, which waits
+        // for no scores.  Past the segment's end zeros, in V and K as well: the tiles hold another's tokens there (whose scores
+        // nothing reads).
         do {
             const float l2 = p.log_decay[units.h] * LOG2E;
             for (int left = job.len; left > 0; left -= C, ++g) {
@@ -584,23 +588,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 unsigned char *tile = sm.k[g & 1];
                 const Weight w(power(l2, max(L - 1 - row, 0)));
                 if (!(ok = wait(B_KF + (g & 1), g >> 1) && (!g || wait(B_S, g - 1)))) break;
-                constexpr int OWN = HELP ? NB / 2 : NB;
-                uint4 first[8 * OWN];
-                if (row < L) {
-                    other_parts<MORE, 0, OWN>(tile, sm.rest[0], row, w, first);
-                } else {
-#pragma unroll
-                    for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, 0, OWN);
-#pragma unroll
-                    for (int i = 0; i < 8 * OWN; ++i) first[i] = make_uint4(0, 0, 0, 0);
-                }
-                __syncwarp();
-                if (!(ok = wait(B_P + g % NP, g / NP))) break;
-#pragma unroll
-                for (int i = 0; i < 8 * OWN; ++i) *reinterpret_cast<uint4 *>(tile + piece_at(row, i)) = first[i];
-                if (L < C) {
+                if constexpr (ON_V) {
                     if (!(ok = wait(B_VF + g % NV, g / NV))) break;
-                    if (row >= L) clear_row(sm.v[g % NV], row, 0, PB);
+                    unsigned char *values = sm.v[g % NV];
+                    if (row < L) {
+                        uint4 first[8];
+                        other_parts<MORE, 0, 1, kBlk>(values, sm.rest[1], row, w, first);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(sm.rest[0] + piece_at(row, i)) = first[i];
+                    } else {
+#pragma unroll
+                        for (int m = 0; m <= MORE; ++m) clear_row(sm.rest[m], row, 0, 1);
+                        clear_row(values, row, 0, 1);
+                        clear_row(tile, row, 0, NB);
+                    }
+                } else {
+                    constexpr int OWN = HELP ? NB / 2 : NB;
+                    uint4 first[8 * OWN];
+                    if (row < L) {
+                        other_parts<MORE, 0, OWN, kTile>(tile, sm.rest[0], row, w, first);
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < MORE; ++m) clear_row(sm.rest[m], row, 0, OWN);
+#pragma unroll
+                        for (int i = 0; i < 8 * OWN; ++i) first[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                    if (!(ok = wait(B_P + g % NP, g / NP))) break;
+#pragma unroll
+                    for (int i = 0; i < 8 * OWN; ++i) *reinterpret_cast<uint4 *>(tile + piece_at(row, i)) = first[i];
+                    if (L < C) {
+                        if (!(ok = wait(B_VF + g % NV, g / NV))) break;
+                        if (row >= L) clear_row(sm.v[g % NV], row, 0, PB);
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -677,10 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 if (elect_one()) {
 #pragma unroll
                     for (int m = MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
-                        const uint32_t part = m ? smem_u32(sm.rest[m - 1]) : k;
+                        const uint32_t keys = ON_V || !m ? k : smem_u32(sm.rest[m - 1]), values = ON_V ? smem_u32(sm.rest[m]) : v;
 #pragma unroll
                         for (int kk = 0; kk < C / 16; ++kk)
-                            mma_bf16(tm + T_D, desc_mnmajor(part, kBlk, kk), desc_mnmajor(v, kBlk, kk), ID_S, m < MORE || kk > 0);
+                            mma_bf16(tm + T_D, desc_mnmajor(keys, kBlk, kk), desc_mnmajor(values, kBlk, kk), ID_S, m < MORE || kk > 0);
                     }
                     mma_commit(&sm.bar[B_S]);
                     if (!Smem::OUT_ON_K) mma_commit(&sm.bar[B_KE + st]);  // (else the outputs go there first)
