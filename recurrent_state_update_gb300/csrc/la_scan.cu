@@ -5,6 +5,8 @@
 // head are independent, so a block takes a few rows of one head.  A token is one update and one dot product a
 // row, and only the update's multiply-add follows the token before.  Keys and queries of 16 tokens are staged
 // in shared memory in fp32 for all warps of the block, the next 16 tokens' loads being in flight meanwhile.
+// What bounds it is the issue of its instructions where there are many rows (16 sequences of 500 tokens of 32 heads of
+// 128 x 128, 21 G operations, 767 us), and their latency, 0.23 us a token, where there are few.
 #include "la_scan.h"
 
 namespace ms {
@@ -14,7 +16,7 @@ using namespace la;
 namespace {
 
 constexpr int kStage = 16;            // tokens staged in shared memory at a time
-constexpr int64_t kManyRows = 32768;  // rows of all states together from which a lane takes most of them
+constexpr int64_t kManyRows = 32768;  // rows of all states together from which a lane takes more of them
 
 constexpr int kPlanThreads = 1024;
 
@@ -216,25 +218,23 @@ int launch_tokens(const ScanParams &p, cudaStream_t st) {
     return launch_status();
 }
 
+// Rows a lane, pieces of 8 columns and warps a block.  A token costs a warp its keys and queries whatever its rows, so many
+// rows keep the SMs' issue slots for the rows and few make many warps.  Measured with fp32 states and activations: 16 sequences
+// of 500 tokens of 32 heads of 128 x 128 767 us with 8 rows, 818 with 4, 1230 with 2; one of 1000 tokens 329, 232 and 264; 8 of
+// 500 of 128 heads of 64 x 128 760, 815, 1217; two of 1000 of 24 such heads 488, 340, 392.  Of 64 x 64 two pieces of 2 rows
+// served 4 sequences of 500 tokens of 8 heads in 190 us and 24 of 40 heads in 371; one row 189 and 557, 4 rows of one piece
+// 218 and 386.  Of 32 x 64, 12 heads, two pieces of 2 rows took 150 us for 100 sequences of 200 tokens and 198 for 4 of 500,
+// of one row 185 and 188.
 template <typename StateT, typename ActT>
 int dispatch_tokens(const ScanParams &p, int P, int N, cudaStream_t st) {
-    const int64_t rows = (int64_t)p.nseq * p.H * P;
-    if (P == 128 && N == 128) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 128, 128, 8, 1, 4>(p, st);
-        return launch_tokens<StateT, ActT, 128, 128, 2, 1, 8>(p, st);
-    }
-    if (P == 64 && N == 128) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 128, 8, 1, 4>(p, st);
-        return launch_tokens<StateT, ActT, 64, 128, 2, 1, 8>(p, st);
-    }
-    if (P == 64 && N == 64) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 64, 64, 2, 2, 4>(p, st);
-        return launch_tokens<StateT, ActT, 64, 64, 1, 2, 4>(p, st);
-    }
-    if (P == 32 && N == 64) {
-        if (rows >= kManyRows) return launch_tokens<StateT, ActT, 32, 64, 2, 2, 2>(p, st);
-        return launch_tokens<StateT, ActT, 32, 64, 1, 2, 4>(p, st);
-    }
+    const bool many = (int64_t)p.nseq * p.H * P >= kManyRows;
+    if (P == 128 && N == 128)
+        return many ? launch_tokens<StateT, ActT, 128, 128, 8, 1, 4>(p, st) : launch_tokens<StateT, ActT, 128, 128, 4, 1, 4>(p, st);
+    if (P == 64 && N == 128)
+        return many ? launch_tokens<StateT, ActT, 64, 128, 8, 1, 4>(p, st) : launch_tokens<StateT, ActT, 64, 128, 4, 1, 4>(p, st);
+    if (P == 64 && N == 64) return launch_tokens<StateT, ActT, 64, 64, 2, 2, 4>(p, st);
+    if (P == 32 && N == 64)
+        return many ? launch_tokens<StateT, ActT, 32, 64, 2, 2, 2>(p, st) : launch_tokens<StateT, ActT, 32, 64, 1, 2, 4>(p, st);
     if (P == 16 && N == 16) return launch_tokens<StateT, ActT, 16, 16, 1, 1, 1>(p, st);
     return MAMBA_EUNSUPPORTED;
 }

@@ -4,14 +4,16 @@
 // before it:
 //   A = (Q K^T) . D,  D_ij = d^(i-j) for j <= i, else 0
 //   Y = A V + diag(d^(i+1)) Q S^T
-//   S <- d^L S + V^T K',  K'_j = d^(L-1-j) k_j
-// Four products of 128 x 128 x 128, none of which waits for another one's result but A V for A, and Q S^T for
-// the state before: only the state's own update, elementwise, follows from chunk to chunk.  Everything else of the next
-// chunk is under way meanwhile, in warps of its own: loads, products, A's decays, the keys' decays, the state, and the outputs.
+//   S <- d^L S + V^T K',  K'_j = d^(L-1-j) k_j   (or V'^T K with the weights on V, which heads of 64 values do)
+// Four products, none of which waits for another one's result but A V for A, and Q S^T for the state before: only the state's
+// own update, elementwise, follows from chunk to chunk.  Everything else of the next chunk is under way meanwhile, in warps
+// of its own: loads, products, A's decays, the weights, the state, and the outputs.
 // The state stands in registers in fp32, a key index a thread, and takes each chunk's product with one rounding to nearest: the
-// tensor cores' own sums cut bits off, in one direction, and would add up over the chunks.  Its copy for the queries, and A, are rounded to bf16, the type of the V, K and Q that they meet: an output is off by about
-// as much as its own rounding to bf16 takes.  K', whose rounding would stay in the state, is held as the sum of two bf16 numbers
-// (16 bits) under a bf16 pool and of three (24) under an fp32 pool, in as many products.
+// tensor cores' own sums cut bits off, in one direction, and would add up over the chunks (1.3e-6 of a state after 8192 tokens;
+// 1.4e-7 so).  Its copy for the queries, and A, are rounded to bf16, the type of the V, K and Q that they meet: an output is off
+// by about as much as its own rounding to bf16 takes (2.3e-3 rms together, 1.7e-3 for that rounding alone).  K', whose rounding
+// would stay in the state, is held as the sum of two bf16 numbers (16 bits) under a bf16 pool, without which outputs are 2.7e-3
+// off, and of three (24) under an fp32 pool, in as many products.
 //
 // A sequence's state is linear in what came before, so a long sequence of few heads is cut into segments that are
 // worked on side by side: k_la_segment forms what each but the last adds to the state, and a segment's block
@@ -135,8 +137,8 @@ __device__ __forceinline__ void other_parts(const uint4 &k, const uint4 &first, 
 #pragma unroll
     for (int m = 0; m < MORE; ++m) out[m] = make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
 }
-// The other parts of blocks B0 .. B1 - 1 of a row of K (or V) into the tiles at rest, REST bytes apart, and the first parts to registers.  Four pieces are
-// read before the first is worked on.
+// The other parts of blocks B0 .. B1 - 1 of a row of K (or V) into the tiles at rest, REST bytes apart, and the first parts to
+// registers.  Four pieces are read before the first is worked on.
 template <int MORE, int B0, int B1, uint32_t REST>
 __device__ __forceinline__ void other_parts(const unsigned char *k, unsigned char *rest, int row, const Weight &w, uint4 *first) {
 #pragma unroll
@@ -173,11 +175,11 @@ enum {
     B_QE = 6, B_KE = 8, B_VE = 10,  // the products have read it
     B_P = 12,  // Q K^T is there, by place
     B_A = 14,       // A is in tensor memory
-    B_K2,      // K' is in place of K
+    B_K2,      // K' is in place of K, or V' beside V
     B_Y2,      // Q S^T is there
     B_M,       // ... scaled, and in the place where A V adds to it
     B_Y,       // the outputs are there
-    B_S,       // V^T K' is there
+    B_S,       // the state's update is there
     B_SB,      // ... and added, and the state's copy is written (phase 0: before the first chunk)
     B_END,     // every product has finished
     B_U,       // a unit is given out, by turn
@@ -262,6 +264,13 @@ struct Units {
     }
 };
 
+// A block an SM, each with one segment of one head after the other.  What bounds a chunk is shared memory: of 128 x 128 heads in
+// bf16 the products read 288 KB of operands from it, the warps move 160 KB through it, loads and outputs 128 KB, 4600 cycles
+// at 128 bytes a cycle (5300 under an fp32 pool), and a chunk takes 5000 to 6000; of 64 x 128 heads 400 KB, 3100 cycles, in about
+// 3400.  Where all SMs work on heads of 128 x 128 device memory is as slow: 8 ragged prompts of 32768 tokens of 32 heads, 1.11 GB,
+// take 197 us, 0.84 of a copy's rate.  29 seeded sequences of 4001 tokens, a chunk or two each, take 72 us (their states alone are
+// 122 MB), 8192 tokens of 128 heads of 64 x 128 122 us, one prompt of 8192 tokens 113 us: 33 for its segments' sums, 55 for 16 chunks
+// of 128 blocks.
 template <int P, int N, bool F32S>
 __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, const __grid_constant__ CUtensorMap qmap,
                                                           const __grid_constant__ CUtensorMap kmap,
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
             for (int e = 0; e < 8; ++e) col[e] = pair(power(l2, 15 - 2 * e), power(l2, 14 - 2 * e));
             const float step = power(l2, 16), first = power(l2, lane + 1);
             for (int left = job.len; left > 0; left -= C, ++g) {
-                if (HELP) {  // three parts of K' take the keys' group longer than the scores take to come: the second block is done here
+                if (HELP) {  // (three parts of K' take the keys' group longer than the scores take to come: half is done here)
                     if (!(ok = wait(B_KF + (g & 1), g >> 1) && (!g || wait(B_S, g - 1)))) break;
                     const int L = min(C, left);
                     uint4 part[8];
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 }
                 __syncwarp();
                 if (++st == stages) st = 0, ++use;
-                if (warp == 18 && t + C >= job.t0 + job.len) {  // the next unit, for all warps.  (None is as many as kRing behind this one.)
+                if (warp == 18 && t + C >= job.t0 + job.len) {  // the next unit, for all warps (none is kRing units behind)
                     const int k = units.k % kRing;
                     if (elect_one()) {
                         sm.ring[k] = gridDim.x + atomicAdd(&p.meta[1], 1);
@@ -964,7 +973,8 @@ int launch(const ScanParams &p, cudaStream_t st) {
     constexpr size_t smem = sizeof(ChainSmem<P, N, F32S>) + 1024;
     static_assert(smem <= 232448, "shared memory of a block");
     if (!ready(reinterpret_cast<const void *>(kern), smem, kRegs)) return MAMBA_ECUDA;
-    if (launch_pdl(kern, dim3((unsigned)(units < kSMs ? units : kSMs)), dim3(kThreads), smem, st, p, qmap, kmap, vmap, ymap) != cudaSuccess) return MAMBA_ECUDA;
+    const dim3 grid((unsigned)(units < kSMs ? units : kSMs));
+    if (launch_pdl(kern, grid, dim3(kThreads), smem, st, p, qmap, kmap, vmap, ymap) != cudaSuccess) return MAMBA_ECUDA;
     return launch_status();
 }
 

@@ -158,6 +158,8 @@ struct PrepArgs {
 // Streaming: 2 G N values a token in and out.  A warp takes a token's rows, or a part of them: its lanes' angles are then
 // the same for all of them and stay in registers, each times the weights it meets, and warps need nothing of one another.
 // Arithmetic goes two values an instruction: a lane's pairs (u, v) are held as eight u and eight v (see LaneRow).
+// 16384 tokens of 32 + 32 heads of 128, 537 MB, take 93 us, 0.87 of what a copy takes; with one value an instruction 108 us, half
+// of the issue slots, and with 4 values from each half, which are twice as many loads, 116.
 template <typename ActT, int N, bool INTER>
 __global__ void __launch_bounds__(kPrepThreads) k_la_qk_prep(const PrepArgs p) {
     constexpr int V = 8, LPR = N / (2 * V), RPW = 32 / LPR;
