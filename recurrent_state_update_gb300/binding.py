@@ -467,7 +467,7 @@ def _gdn_pointers(what, tensors):
         if t is None:
             out.append(None)
             continue
-        if t.dtype is not want or not t.is_cuda or t.numel() < least or (dense and not t.is_contiguous()):
+        if t.dtype is not want or not t.is_cuda or (least > 0 and t.numel() < least) or (dense and not t.is_contiguous()):
             _gdn_refuse(what, tensors)
         out.append(t.data_ptr())
     return out

@@ -30,7 +30,7 @@ struct QkPrep {
 // takes by that many.  The logarithm's own error is relative to l, so that it is no larger than one such rounding over that time.
 __device__ __forceinline__ float2 decay_of(float l) {
     const float hi = expf(l);
-    return make_float2(hi, hi > 1e-30f && hi < 1.0f ? hi * (l - logf(hi)) : 0.0f);
+    return make_float2(hi, hi > 1e-30f && hi <= 1.0f ? hi * (l - logf(hi)) : 0.0f);
 }
 // S <- d S + v k on two of a row's values at a time.
 __device__ __forceinline__ uint64_t decayed_add(uint64_t hi, uint64_t lo, uint64_t S, uint64_t v, uint64_t k) {

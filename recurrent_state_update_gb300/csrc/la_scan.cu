@@ -290,6 +290,7 @@ extern "C" int la_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t 
     p.y = y; p.err = err_word;
     p.seg_tokens = segment_tokens(d, total_tokens, nseq);
     p.max_segs = (int)scan_max_segments(total_tokens, nseq, p.seg_tokens);
+    if ((int64_t)p.max_segs * H > INT32_MAX) return MAMBA_EINVAL;
     p.meta = static_cast<int32_t *>(workspace);
     p.ws = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + scan_meta_bytes(p.max_segs));
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -174,7 +174,7 @@ enum {
     B_QF = 0, B_KF = 2, B_VF = 4,   // loaded, by stage
     B_QE = 6, B_KE = 8, B_VE = 10,  // the products have read it
     B_P = 12,  // Q K^T is there, by place
-    B_A = 14,       // A is in tensor memory
+    B_A = 14,  // A is in tensor memory
     B_K2,      // K' is in place of K, or V' beside V
     B_Y2,      // Q S^T is there
     B_M,       // ... scaled, and in the place where A V adds to it
@@ -961,7 +961,6 @@ int launch(const ScanParams &p, cudaStream_t st) {
         !tile_map(&vmap, p.v, (int64_t)p.H * P, p.T, p.vs) || !tile_map(&ymap, p.y, (int64_t)p.H * P, p.T, (int64_t)p.H * P))
         return MAMBA_ECUDA;
     const int64_t units = (int64_t)p.max_segs * p.H;
-    if (units > INT32_MAX) return MAMBA_EINVAL;
     if (p.seg_tokens < kWhole) {
         auto kern = k_la_segment<P, N, F32S>;
         constexpr size_t smem = sizeof(SegSmem<P, F32S>) + 1024;
