@@ -659,8 +659,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 if (warp == 18 && t + C >= job.t0 + job.len) {  // the next unit, for all warps (none is kRing units behind)
                     const int k = units.k % kRing;
                     if (elect_one()) {
-                        sm.ring[k] = gridDim.x + atomicAdd(&p.meta[1], 1);
+                        const int i = gridDim.x + atomicAdd(&p.meta[1], 1);
+                        sm.ring[k] = i;
                         arrive(&sm.bar[B_U + k]);
+                        if (i < units.total) {  // and its state on the way into L2
+                            const Segment &next = meta_segments(p)[i / p.H];
+                            if (next.seeded && !next.last)
+                                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                                 static_cast<const StateT *>(p.pool) + next.slot * p.stride + (int64_t)(i % p.H) * P * N),
+                                             "r"((uint32_t)(P * N * sizeof(StateT)))
+                                             : "memory");
+                        }
                     }
                     __syncwarp();
                 }
