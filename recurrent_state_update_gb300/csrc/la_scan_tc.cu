@@ -266,11 +266,11 @@ struct Units {
 
 // A block an SM, each with one segment of one head after the other.  What bounds a chunk is shared memory: of 128 x 128 heads in
 // bf16 the products read 288 KB of operands from it, the warps move 160 KB through it, loads and outputs 128 KB, 4600 cycles
-// at 128 bytes a cycle (5300 under an fp32 pool), and a chunk takes 5000 to 6000; of 64 x 128 heads 400 KB, 3100 cycles, in about
-// 3400.  Where all SMs work on heads of 128 x 128 device memory is as slow: 8 ragged prompts of 32768 tokens of 32 heads, 1.11 GB,
-// take 197 us, 0.84 of a copy's rate.  29 seeded sequences of 4001 tokens, a chunk or two each, take 72 us (their states alone are
-// 122 MB), 8192 tokens of 128 heads of 64 x 128 122 us, one prompt of 8192 tokens 113 us: 33 for its segments' sums, 55 for 16 chunks
-// of 128 blocks.
+// at 128 bytes a cycle (5300 under an fp32 pool), and a chunk takes 5000 to 6000; of 64 x 128 heads 368 KB, 2900 cycles, in about
+// 3300 (3600 with a product for each part of V', 4100 with the weights on K).  Where all SMs work on heads of 128 x 128 device
+// memory is as slow: 8 ragged prompts of 32768 tokens of 32 heads, 1.11 GB, take 197 us, 0.84 of a copy's rate.  29 seeded sequences of
+// 4001 tokens, a chunk or two each, take 69 us (their states alone are 122 MB), 8192 tokens of 128 heads of 64 x 128 113 us, one
+// prompt of 8192 tokens 112 us: 33 for its segments' sums, 55 for 16 chunks of 128 blocks.
 template <int P, int N, bool F32S>
 __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, const __grid_constant__ CUtensorMap qmap,
                                                           const __grid_constant__ CUtensorMap kmap,
@@ -283,8 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     // state's update.  A takes the second half of its scores' columns.
     constexpr int NP = P == 64 && NQ == 2 ? 2 : 1;
     constexpr uint32_t T_P = 0, T_Y2 = NP * 128, T_Y = T_Y2 + P, T_D = T_Y + P;
-    static_assert(T_D + P <= 512, "tensor memory");
-    constexpr bool ON_V = Smem::ON_V, HELP = MORE == 2 && !ON_V;  // HELP: whether the scores' group takes half of the other parts
+    constexpr bool ON_V = Smem::ON_V;
+    constexpr int PARTS = ON_V ? MORE + 1 : 1;  // of the state's update, side by side: those of V' meet K in one product
+    static_assert(T_D + PARTS * P <= 512, "tensor memory");
+    constexpr bool HELP = MORE == 2 && !ON_V;  // HELP: whether the scores' group takes half of the other parts
     extern __shared__ __align__(1024) unsigned char chain_smem[];
     Smem &sm = *align1024<Smem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
@@ -539,11 +541,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                     tc_fence_after();
                     const float over = c + 1 == nc ? part : whole;
                     const uint64_t over2 = pair(over, over);
-                    tmem_pieces<P / 16>(lanes + T_D, [&](int i, const uint32_t (&d)[16]) {
+                    if constexpr (PARTS == 1) {
+                        tmem_pieces<P / 16>(lanes + T_D, [&](int i, const uint32_t (&d)[16]) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            S[8 * i + e] = fma2(over2, S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-                    });
+                            for (int e = 0; e < 8; ++e)
+                                S[8 * i + e] = fma2(over2, S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+                        });
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < P / 16; ++i) {
+                            uint32_t d[PARTS][16];
+#pragma unroll
+                            for (int m = 0; m < PARTS; ++m) tmem_get(lanes + T_D + m * P + 16 * i, d[m]);
+#pragma unroll
+                            for (int m = 0; m < PARTS; ++m) tmem_got(d[m]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                uint64_t sum = pair(__uint_as_float(d[MORE][2 * e]), __uint_as_float(d[MORE][2 * e + 1]));
+#pragma unroll
+                                for (int m = MORE - 1; m >= 0; --m)  // (the smallest first)
+                                    sum = add2(sum, pair(__uint_as_float(d[m % PARTS][2 * e]), __uint_as_float(d[m % PARTS][2 * e + 1])));
+                                S[8 * i + e] = fma2(over2, S[8 * i + e], sum);
+                            }
+                        }
+                    }
                 }
                 if (c + 1 < nc) {
                     if (n < N) {
@@ -678,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
         in_flight = full, of = stages;
     } else {
         fewer_registers<kIssueRegs>();
-        constexpr uint32_t ID_P = idesc_bf16(128, 128, false, false), ID_S = idesc_bf16(128, P, true, true),
+        constexpr uint32_t ID_P = idesc_bf16(128, 128, false, false), ID_S = idesc_bf16(128, PARTS * P, true, true),
                            ID_Y = idesc_bf16(128, P, false, true);
         constexpr bool AHEAD = NP == 2;  // whether the next chunk's scores go before this one's outputs
         auto scores = [&](int c) {
@@ -714,11 +735,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int m = MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
-                        const uint32_t keys = ON_V || !m ? k : smem_u32(sm.rest[m - 1]), values = ON_V ? smem_u32(sm.rest[m]) : v;
+                    for (int m = ON_V ? 0 : MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
+                        const uint32_t keys = m ? smem_u32(sm.rest[m - 1]) : k, values = ON_V ? smem_u32(sm.rest[0]) : v;
 #pragma unroll
                         for (int kk = 0; kk < C / 16; ++kk)
-                            mma_bf16(tm + T_D, desc_mnmajor(keys, kBlk, kk), desc_mnmajor(values, kBlk, kk), ID_S, m < MORE || kk > 0);
+                            mma_bf16(tm + T_D, desc_mnmajor(keys, kBlk, kk), desc_mnmajor(values, kBlk, kk), ID_S,
+                                     (!ON_V && m < MORE) || kk > 0);
                     }
                     mma_commit(&sm.bar[B_S]);
                     if (!Smem::OUT_ON_K) mma_commit(&sm.bar[B_KE + st]);  // (else the outputs go there first)
