@@ -268,7 +268,7 @@ struct Units {
 // bf16 the products read 288 KB of operands from it, the warps move 160 KB through it, loads and outputs 128 KB, 4600 cycles
 // at 128 bytes a cycle (5300 under an fp32 pool), and a chunk takes 5000 to 6000; of 64 x 128 heads 368 KB, 2900 cycles, in about
 // 3300 (3600 with a product for each part of V', 4100 with the weights on K).  Where all SMs work on heads of 128 x 128 device
-// memory is as slow: 8 ragged prompts of 32768 tokens of 32 heads, 1.11 GB, take 197 us, 0.84 of a copy's rate.  29 seeded sequences of
+// memory is as slow: 8 ragged prompts of 32768 tokens of 32 heads, 1.11 GB, take 200 us, 0.83 of a copy's rate.  29 seeded sequences of
 // 4001 tokens, a chunk or two each, take 69 us (their states alone are 122 MB), 8192 tokens of 128 heads of 64 x 128 113 us, one
 // prompt of 8192 tokens 112 us: 33 for its segments' sums, 55 for 16 chunks of 128 blocks.
 template <int P, int N, bool F32S>

@@ -361,6 +361,14 @@ def test_scan_of_many_sequences():
     assert run_scan(37, small, wl.F32, wl.F32, lens) == 0
 
 
+@pytest.mark.parametrize("shape", SHAPES[:2], ids=ids)
+@pytest.mark.parametrize("st", [wl.BF16, wl.F32])
+def test_scan_of_more_sequences_than_blocks(shape, st):
+    """Two or three sequences a block, one after the other, whose last chunks are of every length."""
+    lens = wl.rng(39, 0).integers(1, 161, 90 * 4 // shape.nheads).tolist()
+    assert run_scan(39, shape, st, wl.BF16, lens + [128, 256]) == 0
+
+
 def test_scan_scale_and_no_tokens():
     import torch
     assert run_scan(38, FULL, wl.F32, wl.BF16, [40], scale=1.0) == 0
