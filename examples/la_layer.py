@@ -136,7 +136,7 @@ def serve(layer, x, prompt, chunk, decode, drafts, accept):
         for i in range(n):
             out[i].append(y[i].clone())
             at[i] += 1
-    if drafts:
+    if drafts:  # (they end in the block they begin in: a commit leaves the state in the page that they were planned to)
         new.fill_(drafts)
         fill = layer.plan(new, past, table[:n], n * drafts)
         yd = torch.zeros(n, drafts, s.nheads * s.head_dim, dtype=layer.act, device=dev)

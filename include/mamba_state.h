@@ -670,6 +670,8 @@ int la_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot
  *                    is a multiple of block and k*block < n; else -1.  (Checkpoints of the scans count from a
  *                    sequence's first new token: cut a prompt's chunks at multiples of block to have them.)
  *                    A table entry of -1 skips its checkpoint.
+ * (Drafts are planned like other tokens; let them end in the block they begin in, because mamba_spec_commit leaves the
+ * state in slot_ids' page however many are kept.)
  *   positions, token_rows (max_tokens): position (c + its place) and row of each token; -1 behind the last one.
  * Errors: lengths that are negative, sum to more than max_tokens, or positions of 2^31 and more:
  * MAMBA_ERR_SEQLENS, and the outputs are those of a batch of padding rows.  A page that is needed but not
