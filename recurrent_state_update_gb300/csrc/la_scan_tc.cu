@@ -83,6 +83,11 @@ __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
+// The warp's index, in a form that the compiler knows to be the same of all lanes: what the warps of one group do apart then
+// needs no copies in registers of what stays the same (at most 20 bytes of spills in any form; without, up to 500, and 140 us
+// instead of 115 for 8192 tokens of 128 heads of 64 x 128).
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+
 template <typename T>
 __device__ __forceinline__ T *align1024(unsigned char *p) {
     return reinterpret_cast<T *>(p + (-smem_u32(p) & 1023u));  // (an offset, so that accesses stay shared-memory ones)
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
     Smem &sm = *align1024<Smem>(chain_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
     volatile int *failed = &sm.failed;
     Units units(p, sm.ring, &sm.bar[B_U], failed);
     Segment job;
@@ -657,113 +662,114 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                 if (lane == 0) arrive(&sm.bar[B_K2]);
             }
         } while (ok && units.next(job));
-    } else if (warp != 17) {
-        fewer_registers<kIssueRegs>();
-        // loads: of queries, keys and values, a warp each
-        const int stages = warp == 16 ? NQ : warp == 18 ? 2 : NV, full = warp == 16 ? B_QF : warp == 18 ? B_KF : B_VF,
-                  empty = warp == 16 ? B_QE : warp == 18 ? B_KE : B_VE, blocks = warp == 19 ? PB : NB;
-        unsigned char *tiles = warp == 16 ? sm.q[0] : warp == 18 ? sm.k[0] : sm.v[0];
-        const uint32_t size = warp == 16 ? Smem::kQ : warp == 18 ? kTile : P * 256;
-        const CUtensorMap *map = warp == 16 ? &qmap : warp == 18 ? &kmap : &vmap;
-        int st = 0, use = 0;
-        do {
-            const int x = warp == 19 ? units.h * P : units.h / p.HG * N;
-            for (int t = job.t0; t < job.t0 + job.len; t += C, ++loaded) {
-                if (use && !(ok = wait(empty + st, use - 1))) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.bar[full + st], blocks * kBlk);
-                    for (int b = 0; b < blocks; ++b)
-                        tma_load_2d(tiles + st * size + b * kBlk, map, x + 64 * b, t, &sm.bar[full + st]);
-                }
-                __syncwarp();
-                if (++st == stages) st = 0, ++use;
-                if (warp == 18 && t + C >= job.t0 + job.len) {  // the next unit, for all warps (none is kRing units behind)
-                    const int k = units.k % kRing;
+    } else {
+        fewer_registers<kIssueRegs>();  // (before the group's warps part: all of them have to execute the same one)
+        if (warp != 17) {
+            // loads: of queries, keys and values, a warp each
+            const int stages = warp == 16 ? NQ : warp == 18 ? 2 : NV, full = warp == 16 ? B_QF : warp == 18 ? B_KF : B_VF,
+                      empty = warp == 16 ? B_QE : warp == 18 ? B_KE : B_VE, blocks = warp == 19 ? PB : NB;
+            unsigned char *tiles = warp == 16 ? sm.q[0] : warp == 18 ? sm.k[0] : sm.v[0];
+            const uint32_t size = warp == 16 ? Smem::kQ : warp == 18 ? kTile : P * 256;
+            const CUtensorMap *map = warp == 16 ? &qmap : warp == 18 ? &kmap : &vmap;
+            int st = 0, use = 0;
+            do {
+                const int x = warp == 19 ? units.h * P : units.h / p.HG * N;
+                for (int t = job.t0; t < job.t0 + job.len; t += C, ++loaded) {
+                    if (use && !(ok = wait(empty + st, use - 1))) break;
                     if (elect_one()) {
-                        const int i = gridDim.x + atomicAdd(&p.meta[1], 1);
-                        sm.ring[k] = i;
-                        arrive(&sm.bar[B_U + k]);
-                        if (i < units.total) {  // and its state on the way into L2
-                            const Segment &next = meta_segments(p)[i / p.H];
-                            if (next.seeded && !next.last)
-                                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                                 static_cast<const StateT *>(p.pool) + next.slot * p.stride + (int64_t)(i % p.H) * P * N),
-                                             "r"((uint32_t)(P * N * sizeof(StateT)))
-                                             : "memory");
-                        }
+                        mbar_arrive_expect_tx(&sm.bar[full + st], blocks * kBlk);
+                        for (int b = 0; b < blocks; ++b)
+                            tma_load_2d(tiles + st * size + b * kBlk, map, x + 64 * b, t, &sm.bar[full + st]);
                     }
                     __syncwarp();
-                }
-            }
-        } while (ok && units.next(job));
-        in_flight = full, of = stages;
-    } else {
-        fewer_registers<kIssueRegs>();
-        constexpr uint32_t ID_P = idesc_bf16(128, 128, false, false), ID_S = idesc_bf16(128, PARTS * P, true, true),
-                           ID_Y = idesc_bf16(128, P, false, true);
-        constexpr bool AHEAD = NP == 2;  // whether the next chunk's scores go before this one's outputs
-        auto scores = [&](int c) {
-            const int st = c & 1, qs = c % NQ;
-            if (!wait(B_KF + st, c >> 1) || !wait(B_QF + qs, c / NQ)) return false;
-            if (c >= NP && !wait(B_Y, c - NP)) return false;  // A, which lies where the scores go, is read
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), to = tm + T_P + (NP == 2 ? (c & 1) * 128 : 0);
-#pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) mma_bf16(to, desc_kmajor(q, kBlk, kk), desc_kmajor(k, kBlk, kk), ID_P, kk > 0);
-                mma_commit(&sm.bar[B_P + c % NP]);
-            }
-            __syncwarp();
-            return true;
-        };
-        ok = scores(0);
-        for (bool more = true; ok && more;) {
-            for (int left = job.len; left > 0; left -= C, ++g) {
-                const int st = g & 1, qs = g % NQ, vs = g % NV;
-                const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), v = smem_u32(sm.v[vs]), sb = smem_u32(sm.sb);
-                if (!(ok = wait(B_SB, g) && (!g || wait(B_M, g - 1)))) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < N / 16; ++kk)
-                        mma_bf16(tm + T_Y2, desc_kmajor(q, kBlk, kk), desc_mnmajor(sb, N * 128, kk), ID_Y, kk > 0);
-                    mma_commit(&sm.bar[B_QE + qs]);
-                    mma_commit(&sm.bar[B_Y2]);
-                }
-                __syncwarp();
-                if (!(ok = wait(B_K2, g) && wait(B_VF + vs, g / NV))) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int m = ON_V ? 0 : MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
-                        const uint32_t keys = m ? smem_u32(sm.rest[m - 1]) : k, values = ON_V ? smem_u32(sm.rest[0]) : v;
-#pragma unroll
-                        for (int kk = 0; kk < C / 16; ++kk)
-                            mma_bf16(tm + T_D, desc_mnmajor(keys, kBlk, kk), desc_mnmajor(values, kBlk, kk), ID_S,
-                                     (!ON_V && m < MORE) || kk > 0);
+                    if (++st == stages) st = 0, ++use;
+                    if (warp == 18 && t + C >= job.t0 + job.len) {  // the next unit, for all warps (none is kRing units behind)
+                        const int k = units.k % kRing;
+                        if (elect_one()) {
+                            const int i = gridDim.x + atomicAdd(&p.meta[1], 1);
+                            sm.ring[k] = i;
+                            arrive(&sm.bar[B_U + k]);
+                            if (i < units.total) {  // and its state on the way into L2
+                                const Segment &next = meta_segments(p)[i / p.H];
+                                if (next.seeded && !next.last)
+                                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                                     static_cast<const StateT *>(p.pool) + next.slot * p.stride + (int64_t)(i % p.H) * P * N),
+                                                 "r"((uint32_t)(P * N * sizeof(StateT)))
+                                                 : "memory");
+                            }
+                        }
+                        __syncwarp();
                     }
-                    mma_commit(&sm.bar[B_S]);
-                    if (!Smem::OUT_ON_K) mma_commit(&sm.bar[B_KE + st]);  // (else the outputs go there first)
                 }
-                __syncwarp();
-                if (left <= C) more = units.next(job);  // (given out when the chunk's keys were loaded)
-                if (AHEAD && (left > C || more) && !(ok = scores(g + 1))) break;
-                if (!(ok = wait(B_A, g) && wait(B_M, g))) break;
+            } while (ok && units.next(job));
+            in_flight = full, of = stages;
+        } else {
+            constexpr uint32_t ID_P = idesc_bf16(128, 128, false, false), ID_S = idesc_bf16(128, PARTS * P, true, true),
+                               ID_Y = idesc_bf16(128, P, false, true);
+            constexpr bool AHEAD = NP == 2;  // whether the next chunk's scores go before this one's outputs
+            auto scores = [&](int c) {
+                const int st = c & 1, qs = c % NQ;
+                if (!wait(B_KF + st, c >> 1) || !wait(B_QF + qs, c / NQ)) return false;
+                if (c >= NP && !wait(B_Y, c - NP)) return false;  // A, which lies where the scores go, is read
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t a = tm + T_P + (NP == 2 ? (g & 1) * 128 : 0) + 64;
-#pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ts(tm + T_Y, a + 8 * kk, desc_mnmajor(v, kBlk, kk), ID_Y, 1);
-                    mma_commit(&sm.bar[B_Y]);
-                    if (!Smem::OUT_ON_V) mma_commit(&sm.bar[B_VE + vs]);
+                    const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), to = tm + T_P + (NP == 2 ? (c & 1) * 128 : 0);
+    #pragma unroll
+                    for (int kk = 0; kk < N / 16; ++kk) mma_bf16(to, desc_kmajor(q, kBlk, kk), desc_kmajor(k, kBlk, kk), ID_P, kk > 0);
+                    mma_commit(&sm.bar[B_P + c % NP]);
                 }
                 __syncwarp();
-                if (!AHEAD && (left > C || more) && !(ok = scores(g + 1))) break;
+                return true;
+            };
+            ok = scores(0);
+            for (bool more = true; ok && more;) {
+                for (int left = job.len; left > 0; left -= C, ++g) {
+                    const int st = g & 1, qs = g % NQ, vs = g % NV;
+                    const uint32_t q = smem_u32(sm.q[qs]), k = smem_u32(sm.k[st]), v = smem_u32(sm.v[vs]), sb = smem_u32(sm.sb);
+                    if (!(ok = wait(B_SB, g) && (!g || wait(B_M, g - 1)))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+    #pragma unroll
+                        for (int kk = 0; kk < N / 16; ++kk)
+                            mma_bf16(tm + T_Y2, desc_kmajor(q, kBlk, kk), desc_mnmajor(sb, N * 128, kk), ID_Y, kk > 0);
+                        mma_commit(&sm.bar[B_QE + qs]);
+                        mma_commit(&sm.bar[B_Y2]);
+                    }
+                    __syncwarp();
+                    if (!(ok = wait(B_K2, g) && wait(B_VF + vs, g / NV))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+    #pragma unroll
+                        for (int m = ON_V ? 0 : MORE; m >= 0; --m) {  // (the smallest first: their sums cut off less)
+                            const uint32_t keys = m ? smem_u32(sm.rest[m - 1]) : k, values = ON_V ? smem_u32(sm.rest[0]) : v;
+    #pragma unroll
+                            for (int kk = 0; kk < C / 16; ++kk)
+                                mma_bf16(tm + T_D, desc_mnmajor(keys, kBlk, kk), desc_mnmajor(values, kBlk, kk), ID_S,
+                                         (!ON_V && m < MORE) || kk > 0);
+                        }
+                        mma_commit(&sm.bar[B_S]);
+                        if (!Smem::OUT_ON_K) mma_commit(&sm.bar[B_KE + st]);  // (else the outputs go there first)
+                    }
+                    __syncwarp();
+                    if (left <= C) more = units.next(job);  // (given out when the chunk's keys were loaded)
+                    if (AHEAD && (left > C || more) && !(ok = scores(g + 1))) break;
+                    if (!(ok = wait(B_A, g) && wait(B_M, g))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t a = tm + T_P + (NP == 2 ? (g & 1) * 128 : 0) + 64;
+    #pragma unroll
+                        for (int kk = 0; kk < C / 16; ++kk) mma_bf16_ts(tm + T_Y, a + 8 * kk, desc_mnmajor(v, kBlk, kk), ID_Y, 1);
+                        mma_commit(&sm.bar[B_Y]);
+                        if (!Smem::OUT_ON_V) mma_commit(&sm.bar[B_VE + vs]);
+                    }
+                    __syncwarp();
+                    if (!AHEAD && (left > C || more) && !(ok = scores(g + 1))) break;
+                }
             }
+            if (elect_one()) mma_commit(&sm.bar[B_END]);
+            __syncwarp();
+            drain(&sm.bar[B_END], 0);
         }
-        if (elect_one()) mma_commit(&sm.bar[B_END]);
-        __syncwarp();
-        drain(&sm.bar[B_END], 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -809,7 +815,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
     Smem &sm = *align1024<Smem>(seg_smem);
     pdl_wait();  // see pdl_wait: no global access before the previous grid is complete
     pdl_launch_dependents();
-    const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & 127;
+    const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31, row = tid & 127;
     const int which = blockIdx.x / p.H;
     const Segment job = meta_segments(p)[min(which, p.max_segs - 1)];
     if (which >= p.meta[0] || job.index == job.last) return;
@@ -899,59 +905,58 @@ __global__ void __launch_bounds__(kSegThreads, 1) k_la_segment(const ScanParams 
 #pragma unroll
             for (int e = 0; e < P / 2; ++e) unpair(S[e], to[2 * e * 128], to[(2 * e + 1) * 128]);
         }
-    } else if (warp == 12) {
+    } else {
         fewer_registers<kSegIssueRegs>();
-        const int g = h / p.HG;
-        int c = 0;
-        for (; c < nc; ++c) {
-            const int st = c & 1, use = c >> 1, t = job.t0 + c * C;
-            if (use && !wait(G_E + st, use - 1)) break;
-            if (elect_one()) {
-                uint64_t *bar = &sm.bar[G_F + st];
-                mbar_arrive_expect_tx(bar, (NB + PB) * kBlk);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) tma_load_2d(sm.k[st] + b * kBlk, &kmap, g * N + 64 * b, t, bar);
-#pragma unroll
-                for (int b = 0; b < PB; ++b) tma_load_2d(sm.v[st] + b * kBlk, &vmap, h * P + 64 * b, t, bar);
-            }
-            __syncwarp();
-        }
-        loaded = c;
-    } else if (warp == 13) {
-        fewer_registers<kSegIssueRegs>();
-        constexpr uint32_t ID_S = idesc_bf16(128, P, true, true);
-        for (int c = 0; c < nc; ++c) {
-            const int st = c & 1, use = c >> 1;
-            const uint32_t k = smem_u32(sm.k[st]), v = smem_u32(sm.v[st]);
-            if (!wait(G_F + st, use) || (use && !wait(G_DE + st, use - 1))) break;
-            bool ok = true;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!(ok = wait(G_K2 + 2 * half + st, use))) break;
-                tc_fence_after();
+        if (warp == 12) {
+            const int g = h / p.HG;
+            int c = 0;
+            for (; c < nc; ++c) {
+                const int st = c & 1, use = c >> 1, t = job.t0 + c * C;
+                if (use && !wait(G_E + st, use - 1)) break;
                 if (elect_one()) {
-#pragma unroll
-                    for (int m = MORE; m >= 0; --m)  // (the smallest first: their sums cut off less)
-#pragma unroll
-                        for (int kk = 0; kk < C / 32; ++kk)
-                            mma_bf16(tm + 128 * st,
-                                     m ? desc_mnmajor(smem_u32(sm.rest[half][m - 1]), kBlk / 2, kk) : desc_mnmajor(k, kBlk, 4 * half + kk),
-                                     desc_mnmajor(v, kBlk, 4 * half + kk), ID_S, half > 0 || m < MORE || kk > 0);
-                    mma_commit(&sm.bar[G_R + half]);
-                    if (half == 1) {
-                        mma_commit(&sm.bar[G_E + st]);
-                        mma_commit(&sm.bar[G_D + st]);
-                    }
+                    uint64_t *bar = &sm.bar[G_F + st];
+                    mbar_arrive_expect_tx(bar, (NB + PB) * kBlk);
+    #pragma unroll
+                    for (int b = 0; b < NB; ++b) tma_load_2d(sm.k[st] + b * kBlk, &kmap, g * N + 64 * b, t, bar);
+    #pragma unroll
+                    for (int b = 0; b < PB; ++b) tma_load_2d(sm.v[st] + b * kBlk, &vmap, h * P + 64 * b, t, bar);
                 }
                 __syncwarp();
             }
-            if (!ok) break;
+            loaded = c;
+        } else if (warp == 13) {
+            constexpr uint32_t ID_S = idesc_bf16(128, P, true, true);
+            for (int c = 0; c < nc; ++c) {
+                const int st = c & 1, use = c >> 1;
+                const uint32_t k = smem_u32(sm.k[st]), v = smem_u32(sm.v[st]);
+                if (!wait(G_F + st, use) || (use && !wait(G_DE + st, use - 1))) break;
+                bool ok = true;
+    #pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait(G_K2 + 2 * half + st, use))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+    #pragma unroll
+                        for (int m = MORE; m >= 0; --m)  // (the smallest first: their sums cut off less)
+    #pragma unroll
+                            for (int kk = 0; kk < C / 32; ++kk)
+                                mma_bf16(tm + 128 * st,
+                                         m ? desc_mnmajor(smem_u32(sm.rest[half][m - 1]), kBlk / 2, kk) : desc_mnmajor(k, kBlk, 4 * half + kk),
+                                         desc_mnmajor(v, kBlk, 4 * half + kk), ID_S, half > 0 || m < MORE || kk > 0);
+                        mma_commit(&sm.bar[G_R + half]);
+                        if (half == 1) {
+                            mma_commit(&sm.bar[G_E + st]);
+                            mma_commit(&sm.bar[G_D + st]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+            if (elect_one()) mma_commit(&sm.bar[G_END]);
+            __syncwarp();
+            drain(&sm.bar[G_END], 0);
         }
-        if (elect_one()) mma_commit(&sm.bar[G_END]);
-        __syncwarp();
-        drain(&sm.bar[G_END], 0);
-    } else {
-        fewer_registers<kSegIssueRegs>();
     }
     tc_fence_before();
     __syncthreads();

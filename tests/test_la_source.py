@@ -52,3 +52,36 @@ def test_the_ring_of_units_counts_its_phases():
         assert (completed[slot] - 1) & 1 != use & 1  # not yet given out: the wait holds
         completed[slot] += 1
         assert (completed[slot] - 1) & 1 == use & 1  # given out: it passes
+
+
+def braces(text, at):
+    """The text within the braces that open first from `at` on, and where they end."""
+    a = text.index("{", at)
+    depth = 0
+    for i in range(a, len(text)):
+        depth += (text[i] == "{") - (text[i] == "}")
+        if depth == 0:
+            return text[a + 1:i], i + 1
+
+
+def test_a_warpgroup_changes_its_registers_in_one_instruction():
+    """All warps of a warpgroup have to execute the same setmaxnreg, before anything they do not do together; what a group of
+    four asks for is free only once every group has given up its share."""
+    text = source()
+    sites = r"\b(?:fewer|more)_registers<\w+>\(\);"
+    for kernel, groups in (("k_la_chain", 5), ("k_la_segment", 4)):
+        body, _ = braces(text, re.search(r"\b%s\(const ScanParams p" % kernel, text).end())
+        at, warps, shared = re.search(r"\n    if \(warp < \d+\) \{", body).start(), 0, 0
+        while True:
+            head = re.match(r"\s*(?:else )?(?:if \(warp < (\d+)\) |(?=\{))", body[at:])
+            assert head, (kernel, "a warpgroup's warps go different ways", body[at:at + 40])
+            branch, end = braces(body, at)
+            upto = int(head.group(1)) if head.group(1) else 4 * groups
+            assert upto % 4 == 0 and warps < upto  # whole warpgroups
+            assert len(re.findall(sites, branch)) == 1 and re.match(r"\s*" + sites, branch), (kernel, warps)
+            warps, shared = upto, shared + 1
+            tail = re.match(r"\s*else ", body[end:])
+            if not tail:
+                break
+            at = end
+        assert warps == 4 * groups and len(re.findall(sites, body)) == shared
