@@ -1029,7 +1029,7 @@ bool chunked_eligible(const mamba_layer_desc *d) {
 // least 4 chunks each (what a segment adds to the state costs about half of its pass).
 int chunked_segment_tokens(int H, int T, int nseq) {
     const int64_t blocks = kSMs / H;
-    if (blocks < 2 * (int64_t)nseq) return kWhole;
+    if (nseq == 0 || blocks < 2 * (int64_t)nseq) return kWhole;
     const int64_t chunks = ((int64_t)T + C - 1) / C, spare = blocks - nseq / 2;
     const int64_t even = (chunks + spare - 1) / spare, per = even < 4 ? 4 : even;
     return per < chunks ? (int)(per * C) : kWhole;

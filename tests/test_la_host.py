@@ -133,3 +133,14 @@ def test_each_call_opens_and_closes_its_nvtx_range(lib, tmp_path):
                        env=dict(os.environ, NVTX_INJECTION64_PATH=probe))
     assert r.returncode == 0, r.stderr
     assert [x for x in r.stdout.splitlines() if x] == [e for n in calls for e in ("+" + n, "-")]
+
+
+def test_the_workspace_of_no_sequences(tmp_path):
+    """Of any layer, in a process of its own, which a division by no blocks would end."""
+    script = (f"import sys\nsys.path.insert(0, {ROOT!r})\nfrom recurrent_state_update_gb300 import binding as bd, workloads as wl\n"
+              "for heads in (1, 76, 152, 153, 160, 1000):\n"
+              "    d = bd.layer_desc(wl.LayerShape(nheads=heads, head_dim=64, d_state=128, n_groups=1))\n"
+              "    for tokens in (0, 1, 100, 1 << 20):\n"
+              "        assert 0 < bd.la_chunk_scan_workspace_bytes(d, tokens, 0) <= 4096\n")
+    r = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
