@@ -636,8 +636,8 @@ size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total
  * to bf16, 2^-9 of each), sums and the state itself in fp32; the decayed keys that enter the state are held
  * to 16 bits under a bf16 pool and 24 under an fp32 pool.  A NaN or an infinity of one token also reaches the
  * outputs of earlier tokens of its chunk there.  Other layers run token by token in fp32.
- * Limits: nseq <= 65535.  Alignment: the pool, workspace, v, k, q and y 16 bytes; the slot stride and the
- * token strides in bytes multiples of 16.
+ * Limits: nseq <= 65535, total_tokens <= 2^31 - 128.  Alignment: the pool, workspace, v, k, q and y 16 bytes; the
+ * slot stride and the token strides in bytes multiples of 16.
  */
 int la_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slot_stride,
                   int64_t num_slots, const int32_t *cu_seqlens, int32_t nseq, int32_t total_tokens,

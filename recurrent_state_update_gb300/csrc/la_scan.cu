@@ -249,7 +249,7 @@ int segment_tokens(const mamba_layer_desc *d, int T, int nseq) {
 using namespace ms;
 
 extern "C" size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *d, int32_t total_tokens, int32_t nseq) {
-    if (check_layer(d) != MAMBA_OK || total_tokens < 0 || nseq < 0) return 0;
+    if (check_layer(d) != MAMBA_OK || total_tokens < 0 || total_tokens > kWhole || nseq < 0) return 0;
     const int tokens = segment_tokens(d, total_tokens, nseq);
     const int64_t segs = scan_max_segments(total_tokens, nseq, tokens);
     return scan_meta_bytes(segs) + (chunked_eligible(d) ? chunked_workspace_bytes(d, segs, nseq, tokens) : 0);
@@ -264,7 +264,7 @@ extern "C" int la_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t 
     MS_TRACE("la_chunk_scan");
     int rc = check_desc(d);
     if (rc != MAMBA_OK) return rc;
-    if (nseq < 0 || nseq > 65535 || total_tokens < 0) return MAMBA_EINVAL;
+    if (nseq < 0 || nseq > 65535 || total_tokens < 0 || total_tokens > kWhole) return MAMBA_EINVAL;
     if (nseq == 0) return MAMBA_OK;
     if (!ssm_pool || !cu_seqlens || !slot_ids || !log_decay || !workspace) return MAMBA_EINVAL;
     if (total_tokens > 0 && (!v || !k || !q || !y)) return MAMBA_EINVAL;

@@ -7,7 +7,9 @@ namespace ms {
 namespace la {
 
 constexpr int kChunk = 128;  // tokens of one chunk of the chunked form
-constexpr int kWhole = 0x7fffff80;  // tokens of a segment where sequences are not cut
+// Tokens of a segment where sequences are not cut, and the most of a call: a whole chunk below 2^31, since loops step that far past
+// the last token.
+constexpr int kWhole = 0x7fffff80;
 
 // A run of whole chunks of a sequence (the sequence's last one ends with it), worked on from start to end by one block a head: all
 // that its block has to know, in one load.

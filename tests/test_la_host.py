@@ -144,3 +144,14 @@ def test_the_workspace_of_no_sequences(tmp_path):
               "        assert 0 < bd.la_chunk_scan_workspace_bytes(d, tokens, 0) <= 4096\n")
     r = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+def test_more_tokens_than_their_counters_hold_are_refused(lib):
+    """Loops step 16 or 128 tokens past the last one and sequences of more than a whole segment are not expected, so that the most
+    tokens are 2^31 - 128.  (The workspace given here is too small, which is checked after that.)"""
+    d, most = bd.layer_desc(SHAPE), 2 ** 31 - 128
+    assert bd.la_chunk_scan_workspace_bytes(d, most, 1) > 0
+    assert _call(lib, "la_chunk_scan", d, T=most, ws_bytes=0) == bd.MAMBA_ENOSPACE
+    for tokens in (most + 1, 2 ** 31 - 1):
+        assert bd.la_chunk_scan_workspace_bytes(d, tokens, 1) == 0
+        assert _call(lib, "la_chunk_scan", d, T=tokens, ws_bytes=0) == E
