@@ -32,9 +32,10 @@ __device__ __forceinline__ float2 decay_of(float l) {
     const float hi = expf(l);
     return make_float2(hi, hi > 1e-30f && hi <= 1.0f ? hi * (l - logf(hi)) : 0.0f);
 }
-// S <- d S + v k on two of a row's values at a time.
+// S <- d S + x, and d S + v k, on two of a row's values at a time.
+__device__ __forceinline__ uint64_t decayed(uint64_t hi, uint64_t lo, uint64_t S, uint64_t x) { return fma2(hi, S, fma2(lo, S, x)); }
 __device__ __forceinline__ uint64_t decayed_add(uint64_t hi, uint64_t lo, uint64_t S, uint64_t v, uint64_t k) {
-    return fma2(hi, S, fma2(lo, S, mul2(v, k)));
+    return decayed(hi, lo, S, mul2(v, k));
 }
 
 // Turns a position, as a fraction of 2^64 (0 <= f; exact to 2^-62 of itself or 2^-64).

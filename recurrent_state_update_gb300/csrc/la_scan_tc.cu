@@ -8,12 +8,13 @@
 // Four products, none of which waits for another one's result but A V for A, and Q S^T for the state before: only the state's
 // own update, elementwise, follows from chunk to chunk.  Everything else of the next chunk is under way meanwhile, in warps
 // of its own: loads, products, A's decays, the weights, the state, and the outputs.
-// The state stands in registers in fp32, a key index a thread, and takes each chunk's product with one rounding to nearest: the
-// tensor cores' own sums cut bits off, in one direction, and would add up over the chunks (1.3e-6 of a state after 8192 tokens;
-// 1.4e-7 so).  Its copy for the queries, and A, are rounded to bf16, the type of the V, K and Q that they meet: an output is off
-// by about as much as its own rounding to bf16 takes (2.3e-3 rms together, 1.7e-3 for that rounding alone).  K', whose rounding
-// would stay in the state, is held as the sum of two bf16 numbers (16 bits) under a bf16 pool, without which outputs are 2.7e-3
-// off, and of three (24) under an fp32 pool, in as many products.
+// The state stands in registers in fp32, a key index a thread, and takes each chunk's product with a rounding to nearest: the
+// tensor cores' own sums cut bits off, in one direction, and would add up over the chunks.  Heads that remember 1 to 500 tokens
+// hold a state to 1.6e-7 after 8192 tokens so, and to 1.3e-6 otherwise; one that remembers 1e5 tokens and more holds it to 5.5e-7
+// after 65536.  Its copy for the queries, and A, are rounded to bf16, the type of the V, K and Q that they meet: an output is
+// off by about as much as its own rounding to bf16 takes (2.3e-3 rms together, 1.7e-3 for that rounding alone).  K', whose
+// rounding would stay in the state, is held as the sum of two bf16 numbers (16 bits) under a bf16 pool, without which outputs
+// are 2.7e-3 off, and of three (24) under an fp32 pool, in as many products.
 //
 // A sequence's state is linear in what came before, so a long sequence of few heads is cut into segments that are
 // worked on side by side: k_la_segment forms what each but the last adds to the state, and a segment's block
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
         const int n = row;
         do {
             const int h = units.h, nc = (job.len + C - 1) / C;
-            const float l2 = p.log_decay[h] * LOG2E;
+            const float l = p.log_decay[h];
             StateT *pool = static_cast<StateT *>(p.pool) + (int64_t)h * P * N + n;
             const bool seeded = n < N && job.seeded;
             uint64_t S[P / 2];  // values 2 e and 2 e + 1
@@ -528,29 +529,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
                         S[e] = pair(to_f32(pool[job.slot * p.stride + 2 * e * N]), to_f32(pool[job.slot * p.stride + (2 * e + 1) * N]));
                 }
                 if (n < N && job.index) {
-                    const float over = power(l2, p.seg_tokens);
-                    const uint64_t over2 = pair(over, over);
+                    const float2 over = decay_of(l * (float)p.seg_tokens);
+                    const uint64_t over2 = pair(over.x, over.x), rest2 = pair(over.y, over.y);
 #pragma unroll 1
                     for (int r = 1; r <= job.index; ++r) {
                         from += (int64_t)p.H * (128 * P);
 #pragma unroll
-                        for (int e = 0; e < P / 2; ++e) S[e] = fma2(over2, S[e], pair(from[2 * e * 128], from[(2 * e + 1) * 128]));
+                        for (int e = 0; e < P / 2; ++e)
+                            S[e] = decayed(over2, rest2, S[e], pair(from[2 * e * 128], from[(2 * e + 1) * 128]));
                     }
                 }
             }
-            const float whole = power(l2, C), part = power(l2, job.len - (nc - 1) * C);  // over a chunk, and the last one
+            // Over a chunk, and over the last one: two numbers, since what one loses to rounding is lost anew every chunk (up to
+            // 2^-25 each, 1.5e-5 of a state after 512, and all of a decay of less than that).
+            const float2 whole = decay_of(l * (float)C), part = decay_of(l * (float)(job.len - (nc - 1) * C));
             for (int c = -1; c < nc; ++c) {  // (from -1: only the copy for the first chunk)
                 if (c >= 0) {
                     if (!(ok = wait(B_S, g))) break;
                     ++g;
                     tc_fence_after();
-                    const float over = c + 1 == nc ? part : whole;
-                    const uint64_t over2 = pair(over, over);
+                    const float2 over = c + 1 == nc ? part : whole;
+                    const uint64_t over2 = pair(over.x, over.x), rest2 = pair(over.y, over.y);
                     if constexpr (PARTS == 1) {
                         tmem_pieces<P / 16>(lanes + T_D, [&](int i, const uint32_t (&d)[16]) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                S[8 * i + e] = fma2(over2, S[8 * i + e], pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+                                S[8 * i + e] = decayed(over2, rest2, S[8 * i + e],
+                                                       pair(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
                         });
                     } else {
 #pragma unroll
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, co
 #pragma unroll
                                 for (int m = MORE - 1; m >= 0; --m)  // (the smallest first)
                                     sum = add2(sum, pair(__uint_as_float(d[m % PARTS][2 * e]), __uint_as_float(d[m % PARTS][2 * e + 1])));
-                                S[8 * i + e] = fma2(over2, S[8 * i + e], sum);
+                                S[8 * i + e] = decayed(over2, rest2, S[8 * i + e], sum);
                             }
                         }
                     }
