@@ -51,7 +51,8 @@ __device__ __forceinline__ uint64_t turns(float f) {
 }
 // Cosine and sine of `pos` steps of t.
 __device__ __forceinline__ float2 turned(uint64_t t, int32_t pos) {
-    const int32_t a = (int32_t)((uint64_t)((int64_t)pos * (int64_t)t) >> 32);  // in 2^-32 of a turn, from -1/2 to 1/2
+    // in 2^-32 of a turn, from -1/2 to 1/2; without signs, since the product passes 2^63 and is meant to wrap
+    const int32_t a = (int32_t)(uint32_t)(((uint64_t)(int64_t)pos * t) >> 32);
     float2 r;
     sincospif((float)a * 4.656612873077393e-10f, &r.y, &r.x);                  // (2^-31: half turns)
     return r;
