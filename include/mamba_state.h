@@ -562,8 +562,9 @@ int gdn_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slo
  * A linear attention layer with a fixed decay for each head keeps one (head_dim, d_state) state a head
  * in a slot of the same pool and is described by the same mamba_layer_desc, read as for a gated delta
  * rule layer: values of head_dim, keys and queries of d_state in n_groups groups, channels [v | k | q].
- * It has no convolution and no steps (conv_kernel, conv_dtype and dt_dtype are not used);
- * mamba_spec_commit, mamba_slot_copy and the int8 store serve it as they are, with conv_pool NULL.
+ * It has no convolution and no steps: the calls below do not look at conv_kernel, num_spec, conv_dtype and
+ * dt_dtype.  mamba_spec_commit, mamba_slot_copy and the int8 store serve it as they are, with conv_pool NULL; they
+ * check all fields (conv_kernel 2..8, num_spec >= 0, valid types).
  * Per head h (group g = h / (H / G)) and token:
  *     S <- exp(log_decay[h]) * S + v k^T,   y = scale * S q            (S q sums over d_state)
  * The method's domain is log_decay <= 0.

@@ -136,6 +136,26 @@ template <int V> struct Some<float, V> {
     }
 };
 
+// The checks of a layer (check_desc's, and check_layer's for the compiled shapes) with what belongs to a convolution and to steps
+// replaced: these layers have neither.
+inline mamba_layer_desc without_conv(const mamba_layer_desc &d) {
+    mamba_layer_desc u = d;
+    u.conv_kernel = 2;
+    u.num_spec = 0;
+    u.conv_dtype = u.dt_dtype = d.act_dtype;
+    return u;
+}
+inline int check_la_desc(const mamba_layer_desc *d) {
+    if (!d) return MAMBA_EINVAL;
+    const mamba_layer_desc u = without_conv(*d);
+    return check_desc(&u);
+}
+inline int check_la_layer(const mamba_layer_desc *d) {
+    if (!d) return MAMBA_EINVAL;
+    const mamba_layer_desc u = without_conv(*d);
+    return check_layer(&u);
+}
+
 // The checks of a call's norm and rotation.
 inline int check_prep(int N, int32_t qk_norm, float eps, const int32_t *pos, const float *inv_freq, int32_t rot_dim) {
     if (rot_dim < 0 || (rot_dim && (!pos || !inv_freq)) || (qk_norm && !(eps >= 0.0f))) return MAMBA_EINVAL;

@@ -249,7 +249,7 @@ int segment_tokens(const mamba_layer_desc *d, int T, int nseq) {
 using namespace ms;
 
 extern "C" size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *d, int32_t total_tokens, int32_t nseq) {
-    if (check_layer(d) != MAMBA_OK || total_tokens < 0 || total_tokens > kWhole || nseq < 0) return 0;
+    if (check_la_layer(d) != MAMBA_OK || total_tokens < 0 || total_tokens > kWhole || nseq < 0) return 0;
     const int tokens = segment_tokens(d, total_tokens, nseq);
     const int64_t segs = scan_max_segments(total_tokens, nseq, tokens);
     return scan_meta_bytes(segs) + (chunked_eligible(d) ? chunked_workspace_bytes(d, segs, nseq, tokens) : 0);
@@ -262,7 +262,7 @@ extern "C" int la_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t 
                              const void *q, int64_t q_stride, const float *log_decay, float scale, void *y, void *workspace,
                              size_t workspace_bytes, int32_t *err_word, void *stream) {
     MS_TRACE("la_chunk_scan");
-    int rc = check_desc(d);
+    int rc = check_la_desc(d);
     if (rc != MAMBA_OK) return rc;
     if (nseq < 0 || nseq > 65535 || total_tokens < 0 || total_tokens > kWhole) return MAMBA_EINVAL;
     if (nseq == 0) return MAMBA_OK;
@@ -273,7 +273,7 @@ extern "C" int la_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t 
     if (total_tokens > 0 && (v_stride < (int64_t)H * P || k_stride < (int64_t)G * N || q_stride < (int64_t)G * N))
         return MAMBA_EINVAL;
     if (ckpt_slots && (max_ckpt <= 0 || ckpt_interval <= 0 || ckpt_interval % kChunk)) return MAMBA_EINVAL;
-    if ((rc = check_layer(d)) != MAMBA_OK) return rc;
+    if ((rc = check_la_layer(d)) != MAMBA_OK) return rc;
     if (workspace_bytes < la_chunk_scan_workspace_bytes(d, total_tokens, nseq)) return MAMBA_ENOSPACE;
     const size_t ab = dtype_bytes(d->act_dtype);
     if (!aligned16(ssm_pool) || ((size_t)ssm_slot_stride * dtype_bytes(d->state_dtype)) % 16 != 0 || !aligned16(workspace) ||

@@ -288,14 +288,14 @@ extern "C" int la_state_update(const mamba_layer_desc *d, void *ssm_pool, int64_
                                const float *q_weight, float eps, const int32_t *positions, const float *inv_freq,
                                int32_t rot_dim, int32_t interleaved, float scale, void *y, int32_t *err_word, void *stream) {
     MS_TRACE("la_state_update");
-    int rc = check_desc(d);
+    int rc = check_la_desc(d);
     if (rc != MAMBA_OK) return rc;
     if (batch < 0 || batch > 65535 || ntok < 1 || ntok > kMaxTok) return MAMBA_EINVAL;
     if (batch == 0) return MAMBA_OK;
     if (!ssm_pool || !slot_ids || !xbc || !log_decay || !y) return MAMBA_EINVAL;
     const int H = d->nheads, P = d->head_dim, N = d->d_state, G = d->n_groups;
     if (num_slots <= 0 || ssm_slot_stride < (int64_t)H * P * N) return MAMBA_EINVAL;
-    if ((rc = check_layer(d)) != MAMBA_OK) return rc;
+    if ((rc = check_la_layer(d)) != MAMBA_OK) return rc;
     if ((rc = check_prep(N, qk_norm, eps, positions, inv_freq, rot_dim)) != MAMBA_OK) return rc;
     if (!aligned16(ssm_pool) || ((size_t)ssm_slot_stride * dtype_bytes(d->state_dtype)) % 16 != 0 || !aligned16(xbc) ||
         (uintptr_t)y % dtype_bytes(d->act_dtype) != 0)
@@ -305,7 +305,7 @@ extern "C" int la_state_update(const mamba_layer_desc *d, void *ssm_pool, int64_
     a.slot = slot_ids; a.scratch = scratch_slots; a.ntok = ntok;
     a.xbc = xbc; a.log_decay = log_decay; a.scale = scale;
     a.prep = make_prep(qk_norm, k_weight, q_weight, eps, positions, inv_freq, rot_dim, interleaved);
-    a.y = y; a.err = err_word; a.H = H; a.G = G; a.HG = H / G; a.Cd = mamba_conv_dim(d);
+    a.y = y; a.err = err_word; a.H = H; a.G = G; a.HG = H / G; a.Cd = H * P + 2 * G * N;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool sbf = d->state_dtype == MAMBA_BF16, abf = d->act_dtype == MAMBA_BF16;
     if (sbf && abf) return dispatch_step<bf16, bf16>(a, batch, P, N, st);
@@ -319,7 +319,7 @@ extern "C" int la_qk_norm_rope(const mamba_layer_desc *d, const void *k, int64_t
                                const int32_t *positions, const float *inv_freq, int32_t rot_dim, int32_t interleaved,
                                void *k_out, int64_t k_out_stride, void *q_out, int64_t q_out_stride, void *stream) {
     MS_TRACE("la_qk_norm_rope");
-    int rc = check_desc(d);
+    int rc = check_la_desc(d);
     if (rc != MAMBA_OK) return rc;
     if (tokens < 0) return MAMBA_EINVAL;
     if (tokens == 0) return MAMBA_OK;

@@ -155,3 +155,25 @@ def test_more_tokens_than_their_counters_hold_are_refused(lib):
     for tokens in (most + 1, 2 ** 31 - 1):
         assert bd.la_chunk_scan_workspace_bytes(d, tokens, 1) == 0
         assert _call(lib, "la_chunk_scan", d, T=tokens, ws_bytes=0) == E
+
+
+@pytest.mark.parametrize("field,value", [("conv_kernel", 0), ("conv_kernel", 99), ("num_spec", -1), ("conv_dtype", 7),
+                                         ("conv_dtype", bd.MAMBA_F32), ("dt_dtype", -1)])
+def test_fields_of_the_convolution_and_the_steps_are_not_looked_at(lib, field, value):
+    """These layers have neither.  Each call gets as far as an argument that it refuses with another status."""
+    d, plain = bd.layer_desc(SHAPE), bd.layer_desc(SHAPE)
+    setattr(d, field, value)
+    assert bd.la_chunk_scan_workspace_bytes(d, 5000, 2) == bd.la_chunk_scan_workspace_bytes(plain, 5000, 2) > 0
+    assert _call(lib, "la_state_update", d, y=P + 1) == A
+    assert _call(lib, "la_chunk_scan", d, ws_bytes=0) == bd.MAMBA_ENOSPACE
+    assert _call(lib, "la_qk_norm_rope", d, k=3 * P + 8) == A
+    assert _call(lib, "la_state_update", d, batch=0) == _call(lib, "la_chunk_scan", d, nseq=0) == _call(lib, "la_qk_norm_rope", d, tokens=0) == 0
+
+
+@pytest.mark.parametrize("field", ["state_dtype", "act_dtype", "nheads", "head_dim", "d_state", "n_groups"])
+def test_the_other_fields_are(lib, field):
+    d = bd.layer_desc(SHAPE)
+    setattr(d, field, -1)
+    for name in CASES:
+        assert _call(lib, name, d) == E
+    assert bd.la_chunk_scan_workspace_bytes(d, 5000, 2) == 0
