@@ -616,7 +616,8 @@ int la_qk_norm_rope(const mamba_layer_desc *desc, const void *k, int64_t k_strid
                     int32_t rot_dim, int32_t interleaved, void *k_out, int64_t k_out_stride, void *q_out,
                     int64_t q_out_stride, void *stream);
 
-/* Bytes of device workspace la_chunk_scan needs for these sizes (0 on a bad argument). */
+/* Bytes of device workspace la_chunk_scan needs for these sizes (0 on a bad argument).  They serve fewer tokens too, but not
+ * fewer sequences, which may be cut into more pieces. */
 size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total_tokens, int32_t nseq);
 
 /*

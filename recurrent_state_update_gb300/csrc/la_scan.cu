@@ -250,9 +250,9 @@ using namespace ms;
 
 extern "C" size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *d, int32_t total_tokens, int32_t nseq) {
     if (check_la_layer(d) != MAMBA_OK || total_tokens < 0 || total_tokens > kWhole || nseq < 0) return 0;
-    const int tokens = segment_tokens(d, total_tokens, nseq);
-    const int64_t segs = scan_max_segments(total_tokens, nseq, tokens);
-    return scan_meta_bytes(segs) + (chunked_eligible(d) ? chunked_workspace_bytes(d, segs, nseq, tokens) : 0);
+    // of the most segments that a batch of this many tokens or fewer is cut into: more tokens can be fewer, longer segments
+    const int64_t segs = chunked_eligible(d) ? chunked_most_segments(d->nheads, total_tokens, nseq) : nseq;
+    return scan_meta_bytes(segs) + (chunked_eligible(d) ? chunked_workspace_bytes(d, segs, nseq) : 0);
 }
 
 extern "C" int la_chunk_scan(const mamba_layer_desc *d, void *ssm_pool, int64_t ssm_slot_stride, int64_t num_slots,

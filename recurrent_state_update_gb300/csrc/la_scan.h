@@ -41,7 +41,10 @@ struct ScanParams {
     float *ws;       // workspace of the chunked form, past meta
 };
 
-__host__ __device__ inline int64_t scan_max_segments(int T, int nseq, int seg_tokens) { return (int64_t)(T / seg_tokens) + nseq; }
+// Segments of a batch, at most: a sequence's last one, and one for each whole one that more tokens follow.
+__host__ __device__ inline int64_t scan_max_segments(int T, int nseq, int seg_tokens) {
+    return (int64_t)((T > 0 ? T - 1 : 0) / seg_tokens) + nseq;
+}
 inline size_t scan_meta_bytes(int64_t max_segs) {
     return ((size_t)(4 * sizeof(int32_t)) + (size_t)max_segs * sizeof(Segment) + 1023) / 1024 * 1024;
 }
@@ -65,8 +68,10 @@ __device__ __forceinline__ int32_t ckpt_slot(const ScanParams &p, int s, int don
 bool chunked_eligible(const mamba_layer_desc *d);
 // Tokens of a segment of the chunked form for a batch of these sizes.
 int chunked_segment_tokens(int H, int T, int nseq);
+// The most segments of a batch of T tokens or fewer.
+int64_t chunked_most_segments(int H, int T, int nseq);
 // Workspace past the plan.
-size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq, int seg_tokens);
+size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq);
 // Launches the chunked form after the plan; MAMBA_OK or a negative status.
 int chunked_launch(const ScanParams &p, const mamba_layer_desc *d, cudaStream_t stream);
 

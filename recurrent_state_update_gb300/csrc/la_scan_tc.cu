@@ -1032,16 +1032,25 @@ bool chunked_eligible(const mamba_layer_desc *d) {
 
 // Sequences are cut where their heads alone are fewer than the SMs: into as many segments as make one block an SM, at
 // least 4 chunks each (what a segment adds to the state costs about half of its pass).
-int chunked_segment_tokens(int H, int T, int nseq) {
+constexpr int kLeastChunks = 4;
+int64_t spare_blocks(int H, int nseq) {  // segments that sequences are cut into, but for one each; 0: they are not
     const int64_t blocks = kSMs / H;
-    if (nseq == 0 || blocks < 2 * (int64_t)nseq) return kWhole;
-    const int64_t chunks = ((int64_t)T + C - 1) / C, spare = blocks - nseq / 2;
-    const int64_t even = (chunks + spare - 1) / spare, per = even < 4 ? 4 : even;
+    return nseq == 0 || blocks < 2 * (int64_t)nseq ? 0 : blocks - nseq / 2;
+}
+int chunked_segment_tokens(int H, int T, int nseq) {
+    const int64_t chunks = ((int64_t)T + C - 1) / C, spare = spare_blocks(H, nseq);
+    if (spare == 0) return kWhole;
+    const int64_t even = (chunks + spare - 1) / spare, per = even < kLeastChunks ? kLeastChunks : even;
     return per < chunks ? (int)(per * C) : kWhole;
 }
+// Segments make T / (per C) + nseq, and per is at least chunks / spare and kLeastChunks whatever T.
+int64_t chunked_most_segments(int H, int T, int nseq) {
+    const int64_t spare = spare_blocks(H, nseq), least = T / (kLeastChunks * C);
+    return (spare < least ? spare : least) + nseq;
+}
 
-size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq, int seg_tokens) {
-    return seg_tokens == kWhole ? 0 : (size_t)(max_segs + nseq) * d->nheads * 128 * d->head_dim * sizeof(float);
+size_t chunked_workspace_bytes(const mamba_layer_desc *d, int64_t max_segs, int nseq) {
+    return max_segs == nseq ? 0 : (size_t)(max_segs + nseq) * d->nheads * 128 * d->head_dim * sizeof(float);
 }
 
 int chunked_launch(const ScanParams &p, const mamba_layer_desc *d, cudaStream_t st) {

@@ -177,3 +177,16 @@ def test_the_other_fields_are(lib, field):
     for name in CASES:
         assert _call(lib, name, d) == E
     assert bd.la_chunk_scan_workspace_bytes(d, 5000, 2) == 0
+
+
+@pytest.mark.parametrize("heads,head_dim,d_state", [(1, 64, 64), (8, 128, 128), (32, 128, 128), (40, 64, 128), (12, 32, 64)])
+def test_a_workspace_of_the_most_tokens_serves_fewer(lib, heads, head_dim, d_state):
+    """A program asks once, for the most tokens of a batch."""
+    d = bd.layer_desc(wl.LayerShape(nheads=heads, head_dim=head_dim, d_state=d_state, n_groups=1), state=wl.F32)
+    row = heads * (head_dim + 2 * d_state)
+    for nseq in (1, 2, 5, 30):
+        sizes = [bd.la_chunk_scan_workspace_bytes(d, t, nseq) for t in range(0, 120000, 37)]
+        assert sizes == sorted(sizes)
+        for t in (1, 511, 513, 2433, 19457, 77777):  # refused for its keys' address, not for its workspace
+            assert _call(lib, "la_chunk_scan", d, T=t, nseq=nseq, vs=row, ks=row, qs=row, k=P + 8, stride=heads * head_dim * d_state,
+                         ws_bytes=max(bd.la_chunk_scan_workspace_bytes(d, u, nseq) for u in range(t, t + 2000, 100))) == A
