@@ -567,7 +567,7 @@ int gdn_chunk_scan(const mamba_layer_desc *desc, void *ssm_pool, int64_t ssm_slo
  * check all fields (conv_kernel 2..8, num_spec >= 0, valid types).
  * Per head h (group g = h / (H / G)) and token:
  *     S <- exp(log_decay[h]) * S + v k^T,   y = scale * S q            (S q sums over d_state)
- * The method's domain is log_decay <= 0.
+ * The method's domain is log_decay <= 0.  An infinite state stays infinite unless its decay is zero in fp32.
  *
  * Norm and rotation of keys and queries, in this order, each on request, in fp32 with one rounding:
  *     x <- x / sqrt(mean(x^2) + eps) * weight            over the d_state values of a head   (qk_norm)
@@ -637,7 +637,8 @@ size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total
  * each sequence's start: products of bf16 operands (the scores and the state read by the queries are rounded
  * to bf16, 2^-9 of each), sums and the state itself in fp32; the decayed keys that enter the state are held
  * to 16 bits under a bf16 pool and 24 under an fp32 pool.  A NaN or an infinity of one token also reaches the
- * outputs of earlier tokens of its chunk there.  Other layers run token by token in fp32.
+ * outputs of earlier tokens of its chunk there, an infinite key or value counts as a NaN, and a state decays by
+ * whole chunks at once (exp(128 log_decay)).  Other layers run token by token in fp32.
  * Limits: nseq <= 65535, total_tokens <= 2^31 - 128.  Alignment: the pool, workspace, v, k, q and y 16 bytes; the
  * slot stride and the token strides in bytes multiples of 16.
  */

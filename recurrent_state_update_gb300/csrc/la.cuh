@@ -27,10 +27,15 @@ struct QkPrep {
 };
 
 // e^l as the sum of two fp32 numbers: a head that remembers 1 / |l| tokens multiplies what rounding a single one to 24 bits
-// takes by that many.  The logarithm's own error is relative to l, so that it is no larger than one such rounding over that time.
+// takes by that many.  The logarithm's own error is 2^-24 of l, no larger than one such rounding over that time, or 2^-45.
+// The first is taken from below and the second is never zero, unless e^l is, so that an infinite state stays infinite: of
+// numbers of opposite signs, or of a zero, it would make NaN.
 __device__ __forceinline__ float2 decay_of(float l) {
-    const float hi = expf(l);
-    return make_float2(hi, hi > 1e-30f && hi <= 1.0f ? hi * (l - logf(hi)) : 0.0f);
+    const float e = expf(l);
+    if (!(e > 0.0f && e <= 1.0f)) return make_float2(e, 0.0f);
+    const float hi = e - e * 0x1p-21f;                                // (expf is off by 2^-22 of itself at most)
+    const float d = l - logf(hi);                                     // e^l = hi e^d
+    return make_float2(hi, fmaxf(hi * fmaf(0.5f * d, d, d), 0x1p-149f));
 }
 // S <- d S + x, and d S + v k, on two of a row's values at a time.
 __device__ __forceinline__ uint64_t decayed(uint64_t hi, uint64_t lo, uint64_t S, uint64_t x) { return fma2(hi, S, fma2(lo, S, x)); }
