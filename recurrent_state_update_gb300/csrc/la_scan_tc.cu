@@ -10,7 +10,7 @@
 // of its own: loads, products, A's decays, the weights, the state, and the outputs.
 // The state stands in registers in fp32, a key index a thread, and takes each chunk's product with a rounding to nearest: the
 // tensor cores' own sums cut bits off, in one direction, and would add up over the chunks.  Heads that remember 1 to 500 tokens
-// hold a state to 1.6e-7 after 8192 tokens so, and to 1.3e-6 otherwise; one that remembers 1e5 tokens and more holds it to 5.5e-7
+// hold a state to 1.8e-7 after 8192 tokens so, and to 1.3e-6 otherwise; one that remembers 1e4 tokens and more holds it to 5.6e-7
 // after 65536.  Its copy for the queries, and A, are rounded to bf16, the type of the V, K and Q that they meet: an output is
 // off by about as much as its own rounding to bf16 takes (2.3e-3 rms together, 1.7e-3 for that rounding alone).  K', whose
 // rounding would stay in the state, is held as the sum of two bf16 numbers (16 bits) under a bf16 pool, without which outputs
@@ -270,13 +270,15 @@ struct Units {
     }
 };
 
-// A block an SM, each with one segment of one head after the other.  What bounds a chunk is shared memory: of 128 x 128 heads in
-// bf16 the products read 288 KB of operands from it, the warps move 160 KB through it, loads and outputs 128 KB, 4600 cycles
-// at 128 bytes a cycle (5300 under an fp32 pool), and a chunk takes 5000 to 6000; of 64 x 128 heads 368 KB, 2900 cycles, in about
-// 3300 (3600 with a product for each part of V', 4100 with the weights on K).  Where all SMs work on heads of 128 x 128 device
-// memory is as slow: 8 ragged prompts of 32768 tokens of 32 heads, 1.11 GB, take 200 us, 0.83 of a copy's rate.  29 seeded sequences of
-// 4001 tokens, a chunk or two each, take 69 us (their states alone are 122 MB), 8192 tokens of 128 heads of 64 x 128 113 us, one
-// prompt of 8192 tokens 112 us: 33 for its segments' sums, 55 for 16 chunks of 128 blocks.
+// A block an SM, each with one segment of one head after the other.  What bounds a chunk in bf16 is shared memory: of 128 x 128
+// heads the products read 288 KB of operands from it, the warps move 160 KB through it, loads and outputs 128 KB, 4600 cycles at
+// 128 bytes a cycle, and a chunk takes about 5000; of 64 x 128 heads 368 KB, 2900 cycles, in about 3300 (3600 with a product for
+// each part of V', 4100 with the weights on K).  Under an fp32 pool it is 5300 of 6200 cycles, and a chunk's steps follow one another:
+// the keys' three parts, of which the scores' warps make half before they turn to the scores (2700 cycles), A (1400), A V (900)
+// and the outputs (1600).  Where all SMs work on heads of 128 x 128 device memory is as slow: 8 ragged prompts of 32768 tokens of 32
+// heads, 1.11 GB, take 193 us, 0.86 of a copy's rate.  29 seeded sequences of 4001 tokens, a chunk or two each, take 68 us (their
+// states alone are 122 MB), 8192 tokens of 128 heads of 64 x 128 115 us, one prompt of 8192 tokens 105 us: 8 for the plan and the
+// launches, 34 for its segments' sums, 2 to 9 until a block has the state before its segment, 53 for 16 chunks of 128 blocks.
 template <int P, int N, bool F32S>
 __global__ void __launch_bounds__(kThreads, 1) k_la_chain(const ScanParams p, const __grid_constant__ CUtensorMap qmap,
                                                           const __grid_constant__ CUtensorMap kmap,
@@ -1030,8 +1032,10 @@ bool chunked_eligible(const mamba_layer_desc *d) {
     return d->act_dtype == MAMBA_BF16 && (d->head_dim == 64 || d->head_dim == 128);  // (of the compiled shapes)
 }
 
-// Sequences are cut where their heads alone are fewer than the SMs: into as many segments as make one block an SM, at
-// least 4 chunks each (what a segment adds to the state costs about half of its pass).
+// Sequences are cut where twice their heads are no more than the SMs: into as many segments as make one block an SM, at least 4
+// chunks each (what a segment adds to the state costs about half of its pass).  The host knows how many tokens and sequences there
+// are (those of padding among them), not a sequence's length: with more than 152 / (2 H) sequences a long prompt among short ones
+// is not cut (8192 tokens of 32 heads beside two sequences of 64 tokens 200 us, alone 105).
 constexpr int kLeastChunks = 4;
 int64_t spare_blocks(int H, int nseq) {  // segments that sequences are cut into, but for one each; 0: they are not
     const int64_t blocks = kSMs / H;
