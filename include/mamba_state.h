@@ -635,10 +635,10 @@ size_t la_chunk_scan_workspace_bytes(const mamba_layer_desc *desc, int32_t total
  *                    that may run at the same time need one each.
  * Layers of bf16 activations with head_dim 64 or 128 run on the tensor cores in chunks of 128 tokens from
  * each sequence's start: products of bf16 operands (the scores and the state read by the queries are rounded
- * to bf16, 2^-9 of each), sums and the state itself in fp32; the decayed keys that enter the state are held
- * to 16 bits under a bf16 pool and 24 under an fp32 pool.  A NaN or an infinity of one token also reaches the
- * outputs of earlier tokens of its chunk there, an infinite key or value counts as a NaN, and a state decays by
- * whole chunks at once (exp(128 log_decay)).  Other layers run token by token in fp32.
+ * to bf16, off by 2^-8 of each at most), sums and the state itself in fp32; the decayed keys (or values) that
+ * enter the state are held to 16 bits under a bf16 pool and 24 under an fp32 pool.  A NaN or an infinity of one
+ * token also reaches the outputs of earlier tokens of its chunk there, an infinite key or value counts as a NaN,
+ * and a state decays by whole chunks at once (exp(128 log_decay)).  Other layers run token by token in fp32.
  * Limits: nseq <= 65535, total_tokens <= 2^31 - 128.  Alignment: the pool, workspace, v, k, q and y 16 bytes; the
  * slot stride and the token strides in bytes multiples of 16.
  */

@@ -276,7 +276,7 @@ struct Units {
 // each part of V', 4100 with the weights on K).  Under an fp32 pool it is 5300 of 6200 cycles, and a chunk's steps follow one another:
 // the keys' three parts, of which the scores' warps make half before they turn to the scores (2700 cycles), A (1400), A V (900)
 // and the outputs (1600).  Where all SMs work on heads of 128 x 128 device memory is as slow: 8 ragged prompts of 32768 tokens of 32
-// heads, 1.11 GB, take 193 us, 0.86 of a copy's rate.  29 seeded sequences of 4001 tokens, a chunk or two each, take 68 us (their
+// heads, 1.11 GB, take 193 to 197 us, 0.84 to 0.86 of a copy's rate.  29 seeded sequences of 4001 tokens, a chunk or two each, take 68 us (their
 // states alone are 122 MB), 8192 tokens of 128 heads of 64 x 128 115 us, one prompt of 8192 tokens 105 us: 8 for the plan and the
 // launches, 34 for its segments' sums, 2 to 9 until a block has the state before its segment, 53 for 16 chunks of 128 blocks.
 template <int P, int N, bool F32S>
